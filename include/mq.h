@@ -89,8 +89,18 @@ enum {
     MQ_ERR_WORKSPACE = -6, /* workspace missing or smaller than mq_gemm_workspace_bytes */
     MQ_ERR_SPLIT = -7,     /* split_k outside 0..MQ_MAX_SPLIT_K */
     MQ_ERR_HIP = -8,       /* the HIP runtime rejected a launch; see mq_last_hip_error */
-    MQ_ERR_SCRATCH = -9    /* mq_gemm_fused_noalloc: the plan's partial tiles exceed
+    MQ_ERR_SCRATCH = -9,   /* mq_gemm_fused_noalloc: the plan's partial tiles exceed
                               MQ_NOALLOC_SCRATCH_BYTES */
+    MQ_ERR_TYPE = -10,     /* an element type that is not MQ_F32 or MQ_F16 */
+    MQ_ERR_EPS = -11,      /* a norm's eps that is negative or not finite */
+    MQ_ERR_OVERLAP = -12   /* an output that overlaps another buffer of the call where
+                              the entry point does not allow it */
+};
+
+/* Element types of activations, residuals and outputs, numbered as GGUF types. */
+enum {
+    MQ_F32 = 0,
+    MQ_F16 = 1
 };
 
 /* Limits checked by every entry point. */
@@ -311,6 +321,43 @@ int64_t mq_gemm_mmq_workspace_bytes(int fmt, int M, int N, int K, int split_k);
 int mq_gemm_mmq(int fmt, const int8_t *Xq, int ldq, const float *ds, const void *wq, float *Y,
                 int ldy, int M, int N, int K, void *ws, size_t ws_bytes, int split_k,
                 void *stream);
+
+/* Residual addition and root-mean-square norm of M activation rows, the step
+ * between two layers' products, with the output in the type the next product
+ * reads.  Per row, in f32 (sums included):
+ *   h = x + r, rounded once to r's type and written to H (without r: h = x);
+ *   y = (h · 1/sqrt(Σ_k h²/K + eps)) · w, rounded once to the output type.
+ *   X      : device, x_type (MQ_F32 / MQ_F16), row stride ldx >= K.
+ *   R, H   : device, r_type, row strides ldr, ldh >= K: the residual stream in
+ *            and out.  H may be R itself (same pointer and stride).  R == NULL:
+ *            no residual; H is then not used (pass NULL) and r_type ignored.
+ *   w      : device f32, K norm weights.
+ *   eps    : finite, >= 0.
+ *   Y      : device, y_type, row stride ldy >= K.
+ * H and Y may each be X or R itself (same pointer, stride and type); they may
+ * not overlap each other, w, or X or R in any other way.  Interleaved rows of
+ * one buffer (equal strides, disjoint columns) do not overlap.
+ *   K      : any, 1 .. MQ_MAX_K; M >= 1.
+ * Pointers are aligned to their element; rows need no further alignment (odd K
+ * and odd strides included).  Columns >= K of H and Y are not written.  One
+ * kernel, each row read once (rows of more than 32768 elements twice).
+ * Errors: MQ_ERR_NULL, MQ_ERR_TYPE, MQ_ERR_SHAPE, MQ_ERR_LD, MQ_ERR_ALIGN,
+ * MQ_ERR_EPS, MQ_ERR_OVERLAP, MQ_ERR_HIP. */
+int mq_add_rms_norm(int x_type, const void *X, int ldx, int r_type, const void *R, int ldr,
+                    const float *w, float eps, void *H, int ldh, int y_type, void *Y, int ldy,
+                    int M, int K, void *stream);
+
+/* The same with the Q8_1-style int8 blocks of mq_quantize_q8_1 as output: the
+ * codes and (d, s) are the ones it gives for the f32 y, bit for bit.
+ *   Xq, ldq, ds : as mq_quantize_q8_1 writes them (Xq and ds 16-byte aligned,
+ *                 ldq a multiple of 16).
+ *                 Neither may overlap another buffer of the call.
+ *   K           : a multiple of 32; y finite (finite x and r whose squares
+ *                 do not overflow f32).
+ *   other arguments and errors as mq_add_rms_norm. */
+int mq_add_rms_norm_q8_1(int x_type, const void *X, int ldx, int r_type, const void *R, int ldr,
+                         const float *w, float eps, void *H, int ldh, int8_t *Xq, int ldq,
+                         float *ds, int M, int K, void *stream);
 
 /* The launch plan of a GEMM call, as the host computes it (no GPU needed, no
  * device call made).  For callers that size workspaces ahead and for tests

@@ -35,6 +35,7 @@ from .api import (
     row_bytes,
     workspace_bytes,
 )
+from .layers import add_rms_norm, add_rms_norm_q8_1
 
 __all__ = [
     "FORMATS",
@@ -47,6 +48,8 @@ __all__ = [
     "MQ_Q6_K",
     "MQ_Q8_0",
     "MQError",
+    "add_rms_norm",
+    "add_rms_norm_q8_1",
     "block_bytes",
     "block_elems",
     "cache_ld",

@@ -20,6 +20,9 @@ MQ_ERR_WORKSPACE = -6
 MQ_ERR_SPLIT = -7
 MQ_ERR_HIP = -8
 MQ_ERR_SCRATCH = -9
+MQ_ERR_TYPE = -10
+MQ_ERR_EPS = -11
+MQ_ERR_OVERLAP = -12
 MQ_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 MQ_Q4_0 = 2
@@ -30,6 +33,11 @@ MQ_Q4_K = 12
 MQ_Q5_K = 13
 MQ_Q6_K = 14
 
+# element types of activations, residuals and outputs
+MQ_F32 = 0
+MQ_F16 = 1
+
+_c_float = ctypes.c_float
 _c_int, _c_i64, _c_size, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 
 
@@ -73,6 +81,10 @@ SIGNATURES = {
     "mq_gemm_mmq_workspace_bytes": (_c_i64, [_c_int, _c_int, _c_int, _c_int, _c_int]),
     "mq_gemm_mmq": (_c_int, [_c_int, _vp, _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                              _vp, _c_size, _c_int, _vp]),
+    "mq_add_rms_norm": (_c_int, [_c_int, _vp, _c_int, _c_int, _vp, _c_int, _vp, _c_float, _vp,
+                                 _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _vp]),
+    "mq_add_rms_norm_q8_1": (_c_int, [_c_int, _vp, _c_int, _c_int, _vp, _c_int, _vp, _c_float,
+                                      _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _vp]),
     "mq_gemm_plan_query": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                     ctypes.POINTER(MqGemmPlanInfo)]),
     "mq_strerror": (ctypes.c_char_p, [_c_int]),

@@ -94,37 +94,11 @@ __global__ __launch_bounds__(256) void quantize_q8_1_kernel(const float *__restr
         const f32x4 *src = reinterpret_cast<const f32x4 *>(X + row * ldx + 8 * c);
         const f32x4 lo = src[0], hi = src[1];
         const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        float a = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[j]));
-        a = fmaxf(a, __shfl_xor(a, 1));
-        a = fmaxf(a, __shfl_xor(a, 2));
-        const float d = a / 127.0f;
-        int q[8], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            int qj = 0;
-            if (d != 0.0f) {
-                const float t = v[j] / d;
-                float r = truncf(t);
-                if (fabsf(t - r) >= 0.5f) r += copysignf(1.0f, t);   // halves away from zero
-                qj = (int)r;
-            }
-            q[j] = qj;
-            sum += qj;
-        }
-        sum += __shfl_xor(sum, 1);
-        sum += __shfl_xor(sum, 2);
         uint2 packed;
-        packed.x = (q[0] & 255) | ((q[1] & 255) << 8) | ((q[2] & 255) << 16) | ((uint32_t)q[3] << 24);
-        packed.y = (q[4] & 255) | ((q[5] & 255) << 8) | ((q[6] & 255) << 16) | ((uint32_t)q[7] << 24);
+        float2 out;
+        quantize8(v, packed, out);
         *reinterpret_cast<uint2 *>(Xq + row * ldq + 8 * c) = packed;
-        if ((c & 3) == 0) {
-            float2 out;
-            out.x = d;
-            out.y = d * (float)sum;
-            *reinterpret_cast<float2 *>(ds + 2 * (row * nblk + (c >> 2))) = out;
-        }
+        if ((c & 3) == 0) *reinterpret_cast<float2 *>(ds + 2 * (row * nblk + (c >> 2))) = out;
     }
 }
 

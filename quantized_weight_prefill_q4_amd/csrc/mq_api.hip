@@ -57,6 +57,90 @@ int check_dequant(int fmt, const void *wq, int N, int K, const uint16_t *w16, in
     return MQ_OK;
 }
 
+// An element type of the norm and the linear layers, and a pointer aligned to it.
+bool type_ok(int type) { return type == MQ_F32 || type == MQ_F16; }
+bool elem_aligned(const void *p, int type) {
+    return ((uintptr_t)p & (type == MQ_F32 ? 3 : 1)) == 0;
+}
+
+// The rows of a buffer that a call reads or writes.
+struct Span {
+    const char *p;
+    int64_t stride, row, rows;   // bytes, bytes, count
+};
+Span span(const void *p, int64_t ld, int64_t K, int64_t elem, int64_t rows) {
+    return Span{(const char *)p, ld * elem, K * elem, rows};
+}
+bool same_span(const Span &a, const Span &b) {
+    return a.p == b.p && a.row == b.row && (a.stride == b.stride || a.rows == 1);
+}
+// Rows at one stride with disjoint columns (slices of one buffer) do not
+// overlap; ranges that meet at different strides count as overlapping.
+bool overlap(const Span &a, const Span &b) {
+    if (a.p + (a.rows - 1) * a.stride + a.row <= b.p ||
+        b.p + (b.rows - 1) * b.stride + b.row <= a.p)
+        return false;
+    if (a.stride != b.stride && a.rows > 1 && b.rows > 1) return true;
+    const int64_t s = a.rows > 1 ? a.stride : b.stride;
+    if (s <= 0 || (a.rows == 1 && b.rows == 1)) return true;
+    const int64_t d = ((b.p - a.p) % s + s) % s;
+    return d < a.row || d + b.row > s;
+}
+
+// The overlap rules of the norm: an output is elementwise the input itself or
+// disjoint from it, and disjoint from the other output and the weights.
+int check_norm_overlap(const mq::NormSpec &n, int64_t y_elem) {
+    auto bytes = [](int type) { return (int64_t)(type == MQ_F32 ? 4 : 2); };
+    const Span x = span(n.x, n.ldx, n.K, bytes(n.x_type), n.M);
+    const Span y = span(n.y, n.ldy, n.K, y_elem, n.M);
+    const Span w = span(n.w, n.K, n.K, 4, 1);
+    const bool q8 = n.y_type == mq::kTypeI8;
+    auto clash = [](const Span &out, const Span &in, bool may_be_same) {
+        return overlap(out, in) && !(may_be_same && same_span(out, in));
+    };
+    if (clash(y, x, !q8) || clash(y, w, false)) return MQ_ERR_OVERLAP;
+    const Span ds = span(n.ds, n.K / 16, n.K / 16, 4, n.M);
+    if (q8 && (clash(ds, x, false) || clash(ds, w, false) || clash(ds, y, false)))
+        return MQ_ERR_OVERLAP;
+    if (n.r) {
+        const Span r = span(n.r, n.ldr, n.K, bytes(n.r_type), n.M);
+        const Span h = span(n.h, n.ldh, n.K, bytes(n.r_type), n.M);
+        if (clash(y, r, !q8) || clash(y, h, false) || clash(h, x, true) || clash(h, r, true) ||
+            clash(h, w, false))
+            return MQ_ERR_OVERLAP;
+        if (q8 && (clash(ds, r, false) || clash(ds, h, false))) return MQ_ERR_OVERLAP;
+    }
+    return MQ_OK;
+}
+
+// Checks of the norm's inputs and residual stream; fills their part of `n`.
+int check_norm(int x_type, const void *X, int ldx, int r_type, const void *R, int ldr,
+               const float *w, float eps, void *H, int ldh, int M, int K, mq::NormSpec *n) {
+    if (!X || !w || (R && !H)) return MQ_ERR_NULL;
+    if (!type_ok(x_type) || (R && !type_ok(r_type))) return MQ_ERR_TYPE;
+    if (ldx < K || (R && (ldr < K || ldh < K))) return MQ_ERR_LD;
+    if (!elem_aligned(X, x_type) || !elem_aligned(w, MQ_F32) ||
+        (R && (!elem_aligned(R, r_type) || !elem_aligned(H, r_type))))
+        return MQ_ERR_ALIGN;
+    if (!(eps >= 0.0f) || eps > 3.0e38f) return MQ_ERR_EPS;
+    *n = mq::NormSpec{};
+    n->x = X;
+    n->ldx = ldx;
+    n->x_type = x_type;
+    n->w = w;
+    n->eps = eps;
+    n->M = M;
+    n->K = K;
+    if (R) {
+        n->r = R;
+        n->h = H;
+        n->ldr = ldr;
+        n->ldh = ldh;
+        n->r_type = r_type;
+    }
+    return MQ_OK;
+}
+
 // How a GEMM with f32 activations runs.  Up to kInTileMaxM rows the kernel
 // rounds X to f16 while staging its tiles; above, X is converted once into
 // the front of the workspace and the f16-activation kernel (with its own
@@ -346,6 +430,41 @@ int mq_gemm_mmq(int fmt, const int8_t *Xq, int ldq, const float *ds, const void 
                                      (float *)ws, (hipStream_t)stream));
 }
 
+int mq_add_rms_norm(int x_type, const void *X, int ldx, int r_type, const void *R, int ldr,
+                    const float *w, float eps, void *H, int ldh, int y_type, void *Y, int ldy,
+                    int M, int K, void *stream) {
+    mq::NormSpec n;
+    if (int rc = check_dims(M, 1, K)) return rc;   // an empty tensor's pointers are NULL
+    if (!Y) return MQ_ERR_NULL;
+    if (!type_ok(y_type)) return MQ_ERR_TYPE;
+    if (int rc = check_norm(x_type, X, ldx, r_type, R, ldr, w, eps, H, ldh, M, K, &n)) return rc;
+    if (ldy < K) return MQ_ERR_LD;
+    if (!elem_aligned(Y, y_type)) return MQ_ERR_ALIGN;
+    n.y = Y;
+    n.ldy = ldy;
+    n.y_type = y_type;
+    if (int rc = check_norm_overlap(n, y_type == MQ_F32 ? 4 : 2)) return rc;
+    return hip_status(mq::launch_add_rms_norm(n, (hipStream_t)stream));
+}
+
+int mq_add_rms_norm_q8_1(int x_type, const void *X, int ldx, int r_type, const void *R, int ldr,
+                         const float *w, float eps, void *H, int ldh, int8_t *Xq, int ldq,
+                         float *ds, int M, int K, void *stream) {
+    mq::NormSpec n;
+    if (int rc = check_dims(M, 1, K)) return rc;
+    if (!Xq || !ds) return MQ_ERR_NULL;
+    if (int rc = check_norm(x_type, X, ldx, r_type, R, ldr, w, eps, H, ldh, M, K, &n)) return rc;
+    if (K % 32) return MQ_ERR_SHAPE;
+    if (!ldq_ok(ldq, K)) return MQ_ERR_LD;
+    if (!aligned16(Xq) || !aligned16(ds)) return MQ_ERR_ALIGN;
+    n.y = Xq;
+    n.ldy = ldq;
+    n.ds = ds;
+    n.y_type = mq::kTypeI8;
+    if (int rc = check_norm_overlap(n, 1)) return rc;
+    return hip_status(mq::launch_add_rms_norm(n, (hipStream_t)stream));
+}
+
 int mq_gemm_plan_query(int path, int fmt, int M, int N, int K, int split_k,
                        mq_gemm_plan_info *out) {
     if (!out) return MQ_ERR_NULL;
@@ -403,6 +522,9 @@ const char *mq_strerror(int code) {
     case MQ_ERR_SPLIT: return "split_k out of range for this problem";
     case MQ_ERR_HIP: return "the HIP runtime rejected a launch";
     case MQ_ERR_SCRATCH: return "the K-split partial tiles exceed the static scratch (MQ_NOALLOC_SCRATCH_BYTES)";
+    case MQ_ERR_TYPE: return "an element type that is not f32 or f16";
+    case MQ_ERR_EPS: return "eps is negative or not finite";
+    case MQ_ERR_OVERLAP: return "an output overlaps another buffer of the call";
     default: return "unknown error code";
     }
 }

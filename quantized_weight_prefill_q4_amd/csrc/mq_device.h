@@ -60,6 +60,38 @@ __device__ __forceinline__ uint32_t shift2(uint32_t hi, uint32_t lo) {
     return __builtin_amdgcn_alignbyte(hi, lo, 2);
 }
 
+// Eight f32 values of a 32-element Q8_1-style block, whose four threads are
+// consecutive lanes 4i .. 4i + 3: their int8 codes, and the block's (d, s).
+// a = max|v|, d = fl32(a / 127), code = the integer nearest fl32(v / d), halves
+// away from zero (0 when d = 0), s = fl32(d · Σcode).
+__device__ __forceinline__ void quantize8(const float v[8], uint2 &codes, float2 &ds) {
+    float a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[j]));
+    a = fmaxf(a, __shfl_xor(a, 1));
+    a = fmaxf(a, __shfl_xor(a, 2));
+    const float d = a / 127.0f;
+    int q[8], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        int qj = 0;
+        if (d != 0.0f) {
+            const float t = v[j] / d;
+            float r = truncf(t);
+            if (fabsf(t - r) >= 0.5f) r += copysignf(1.0f, t);   // halves away from zero
+            qj = (int)r;
+        }
+        q[j] = qj;
+        sum += qj;
+    }
+    sum += __shfl_xor(sum, 1);
+    sum += __shfl_xor(sum, 2);
+    codes.x = (q[0] & 255) | ((q[1] & 255) << 8) | ((q[2] & 255) << 16) | ((uint32_t)q[3] << 24);
+    codes.y = (q[4] & 255) | ((q[5] & 255) << 8) | ((q[6] & 255) << 16) | ((uint32_t)q[7] << 24);
+    ds.x = d;
+    ds.y = d * (float)sum;
+}
+
 // Buffer resource over [base, base + bytes) for raw buffer loads: a load whose
 // offset is at or past `bytes` returns zeros instead of touching memory.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, uint32_t bytes) {

@@ -15,6 +15,11 @@ constexpr int kFmtQ4_K = 12;
 constexpr int kFmtQ5_K = 13;
 constexpr int kFmtQ6_K = 14;
 
+// Element types of activations, residuals and outputs.
+constexpr int kTypeF32 = 0;
+constexpr int kTypeF16 = 1;
+constexpr int kTypeI8 = 24;   // Q8_1-style codes (the norm's int8 output)
+
 inline int block_elems(int fmt) {
     switch (fmt) {
     case kFmtQ4_0: case kFmtQ5_0: case kFmtQ5_1: case kFmtQ8_0: return 32;
@@ -94,5 +99,20 @@ hipError_t launch_mmq(int fmt, const int8_t *Xq, int ldq, const float *ds, const
 // X16[m·ld16 + k] = f16_rne(X[m·ldx + k]) for m < M, k < K (K a multiple of 8).
 hipError_t launch_convert_f32_to_f16(const float *X, int ldx, uint16_t *X16, int ld16, int M,
                                      int K, hipStream_t stream);
+
+// Residual addition and RMS norm (arguments already validated).  r == nullptr:
+// no residual, h unused.  y_type kTypeI8: y holds int8 codes (row stride ldy
+// bytes) and ds their (d, s) pairs.
+struct NormSpec {
+    const void *x, *r;
+    const float *w;
+    void *h, *y;
+    float *ds;
+    int64_t ldx, ldr, ldh, ldy;   // elements
+    int M, K;
+    int x_type, r_type, y_type;
+    float eps;
+};
+hipError_t launch_add_rms_norm(const NormSpec &n, hipStream_t stream);
 
 }  // namespace mq

@@ -1,0 +1,133 @@
+"""Torch front end of the operators around the quantized products: the residual
+RMS norm that feeds them.
+
+As in ``api``, every step of the computation runs in the HIP library; these
+functions check dtypes, devices, shapes and strides, allocate the outputs and
+pass pointers on the current stream of the tensors' device.  All tensors of a
+call must be on one GPU; it need not be the current one.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from ._lib import MQ_F16, MQ_F32, check, lib
+
+_TYPES = {torch.float32: MQ_F32, torch.float16: MQ_F16}
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or float16, got {t.dtype}")
+    return code
+
+
+def _device(x: torch.Tensor, name: str) -> int:
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return dev
+
+
+def _matrix(t: torch.Tensor, dev: int, rows: int, cols: int, name: str) -> int:
+    """The row stride of a row-major matrix of at least rows x cols on GPU `dev`."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    if shape[0] < rows or shape[1] < cols:
+        raise ValueError(f"{name} must be at least {rows} x {cols}, got {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the same GPU as the activations")
+    # the stride of a single row is never used
+    return stride[0] if shape[0] > 1 else max(stride[0], cols)
+
+
+def _vector(t: torch.Tensor, dev: int, n: int, name: str) -> int:
+    """The address of a contiguous f32 vector of n elements on GPU `dev`."""
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be torch.float32, got {t.dtype}")
+    if t.dim() != 1 or not t.is_contiguous() or t.shape[0] < n:
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the same GPU as the activations")
+    return t.data_ptr()
+
+
+def _call(dev: int, name: str, *args) -> None:
+    """lib().name(*args, stream) on GPU `dev`'s current stream, with `dev` current."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+
+
+def _norm_inputs(x, weight, residual, residual_out):
+    """(device, M, K, the library call's arguments up to H's stride but eps, h)."""
+    dev = _device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D with unit column stride")
+    M, K = x.shape
+    ldx = _matrix(x, dev, M, K, "x")
+    w = _vector(weight, dev, K, "weight")
+    xt = _type(x, "x")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        return dev, M, K, (xt, x.data_ptr(), ldx, MQ_F32, 0, 0, w), (0, 0), None
+    rt = _type(residual, "residual")
+    ldr = _matrix(residual, dev, M, K, "residual")
+    if residual_out is None:
+        h = torch.empty((M, K), dtype=residual.dtype, device=x.device)
+        ldh = K
+    else:
+        h = residual_out
+        if h.dtype != residual.dtype:
+            raise ValueError(f"residual_out must be {residual.dtype}, got {h.dtype}")
+        ldh = _matrix(h, dev, M, K, "residual_out")
+    return (dev, M, K, (xt, x.data_ptr(), ldx, rt, residual.data_ptr(), ldr, w),
+            (h.data_ptr(), ldh), h)
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                 eps: float = 1e-6, out_dtype: torch.dtype = torch.float16,
+                 out: torch.Tensor | None = None, residual_out: torch.Tensor | None = None):
+    """(y, h): h = x + residual in the residual's type, and y [M, K] = h /
+    sqrt(mean(h^2) + eps) * weight in out_dtype (f16 or f32).
+
+    x, residual [M, K] f32 or f16, any row stride; weight f32 [K].  Without a
+    residual h is None and y the norm of x.  residual_out may be the residual
+    itself (the stream is then updated in place)."""
+    dev, M, K, head, tail, h = _norm_inputs(x, weight, residual, residual_out)
+    if out is None:
+        if out_dtype not in _TYPES:
+            raise ValueError(f"out_dtype must be float32 or float16, got {out_dtype}")
+        out = torch.empty((M, K), dtype=out_dtype, device=x.device)
+        ldy = K
+    else:
+        ldy = _matrix(out, dev, M, K, "out")
+    _call(dev, "mq_add_rms_norm", *head, eps, *tail, _type(out, "out"), out.data_ptr(), ldy, M, K)
+    return out, h
+
+
+def add_rms_norm_q8_1(x: torch.Tensor, weight: torch.Tensor,
+                      residual: torch.Tensor | None = None, eps: float = 1e-6,
+                      xq: torch.Tensor | None = None, ds: torch.Tensor | None = None,
+                      residual_out: torch.Tensor | None = None):
+    """(xq, ds, h): add_rms_norm with y as the int8 blocks that gemm_mmq reads,
+    the ones quantize_q8_1 gives for the f32 y.  K a multiple of 32."""
+    dev, M, K, head, tail, h = _norm_inputs(x, weight, residual, residual_out)
+    if xq is None:
+        xq = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=x.device)
+    elif xq.dtype != torch.int8:
+        raise ValueError(f"xq must be torch.int8, got {xq.dtype}")
+    ldq = _matrix(xq, dev, M, K, "xq")
+    if ds is None:
+        ds = torch.empty((M, K // 32, 2), dtype=torch.float32, device=x.device)
+    elif (ds.dtype != torch.float32 or not ds.is_contiguous() or ds.get_device() != dev
+          or ds.numel() < M * (K // 32) * 2):
+        raise ValueError("ds must be contiguous float32 with M*K/16 elements, on x's GPU")
+    _call(dev, "mq_add_rms_norm_q8_1", *head, eps, *tail, xq.data_ptr(), ldq, ds.data_ptr(), M, K)
+    return xq, ds, h
