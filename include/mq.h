@@ -93,14 +93,24 @@ enum {
                               MQ_NOALLOC_SCRATCH_BYTES */
     MQ_ERR_TYPE = -10,     /* an element type that is not MQ_F32 or MQ_F16 */
     MQ_ERR_EPS = -11,      /* a norm's eps that is negative or not finite */
-    MQ_ERR_OVERLAP = -12   /* an output that overlaps another buffer of the call where
+    MQ_ERR_OVERLAP = -12,  /* an output that overlaps another buffer of the call where
                               the entry point does not allow it */
+    MQ_ERR_ACT = -13       /* unknown activation */
 };
 
 /* Element types of activations, residuals and outputs, numbered as GGUF types. */
 enum {
     MQ_F32 = 0,
     MQ_F16 = 1
+};
+
+/* Activations of a linear layer. */
+enum {
+    MQ_ACT_NONE = 0,
+    MQ_ACT_RELU = 1,       /* max(v, 0) */
+    MQ_ACT_SILU = 2,       /* v / (1 + e^-v) */
+    MQ_ACT_GELU = 3,       /* 0.5·v·(1 + erf(v/√2)) */
+    MQ_ACT_GELU_TANH = 4   /* 0.5·v·(1 + tanh(√(2/π)·(v + 0.044715·v³))) */
 };
 
 /* Limits checked by every entry point. */
@@ -321,6 +331,64 @@ int64_t mq_gemm_mmq_workspace_bytes(int fmt, int M, int N, int K, int split_k);
 int mq_gemm_mmq(int fmt, const int8_t *Xq, int ldq, const float *ds, const void *wq, float *Y,
                 int ldy, int M, int N, int K, void *ws, size_t ws_bytes, int split_k,
                 void *stream);
+
+/* Linear layers: the product of mq_gemm_f16cache / mq_gemm_fused with what
+ * follows it in a layer applied to the f32 sums before they are written, so
+ * that neither the sums nor an intermediate cross memory:
+ *   Y[M×N] = act(X·Wᵀ + bias) + R.
+ * Accumulation, bias, activation and residual are f32; Y is rounded once to
+ * its type.  The sums are the ones of the matching GEMM (same products, f32
+ * accumulation in an order of the library's choice; results are deterministic).
+ *   X       : device, x_type (MQ_F32 / MQ_F16), 16-byte aligned, row stride ldx
+ *             (f16: >= K, a multiple of 8; f32: >= K, a multiple of 4).  f32
+ *             activations are rounded to f16 (to nearest even) as in the _xf32
+ *             entry points.
+ *   W16, ldw, wq, fmt, K : as mq_gemm_f16cache / mq_gemm_fused.
+ *   bias    : device f32, N values, or NULL.
+ *   act     : one of MQ_ACT_*.
+ *   R, ldr  : device, r_type, row stride ldr >= N, or NULL (no residual; r_type
+ *             and ldr are then ignored).  R may be Y itself (same pointer,
+ *             stride and type): the residual stream updated in place.
+ *   Y       : device, y_type, row stride ldy >= N.  Y may not overlap any other
+ *             buffer of the call, or R in any other way.
+ *   ws      : device, 16-byte aligned, ws_bytes >=
+ *             mq_linear_workspace_bytes(fmt or 0, x_type, M, N, K, split_k); may
+ *             be NULL when that is 0.  Calls that may overlap in time need a
+ *             workspace each.
+ *   split_k : as mq_gemm_f16cache.
+ * bias, R and Y are aligned to their element (N, ldr and ldy may be odd);
+ * columns >= N of Y are not written.
+ * Errors: those of mq_gemm_fused, MQ_ERR_TYPE, MQ_ERR_ACT, MQ_ERR_OVERLAP. */
+int64_t mq_linear_workspace_bytes(int fmt, int x_type, int M, int N, int K, int split_k);
+
+int mq_linear_f16cache(int x_type, const void *X, int ldx, const uint16_t *W16, int ldw,
+                       const float *bias, int act, int r_type, const void *R, int ldr, int y_type,
+                       void *Y, int ldy, int M, int N, int K, void *ws, size_t ws_bytes,
+                       int split_k, void *stream);
+
+int mq_linear_fused(int x_type, const void *X, int ldx, int fmt, const void *wq,
+                    const float *bias, int act, int r_type, const void *R, int ldr, int y_type,
+                    void *Y, int ldy, int M, int N, int K, void *ws, size_t ws_bytes, int split_k,
+                    void *stream);
+
+/* Gated linear layers: with W the gate's N rows followed by the up matrix's N
+ * rows (2·N rows at one stride, as two weights decoded into one cache or two
+ * quantized weights stored one after the other),
+ *   Y[M×N] = act(X·Wgᵀ + bias_g) · (X·Wuᵀ + bias_u),
+ * both products in one kernel and only Y written.
+ *   bias : device f32, 2·N values (gate's, then up's), or NULL.
+ *   N    : columns of Y; 2·N <= MQ_MAX_DIM.
+ *   ws   : ws_bytes >= mq_glu_workspace_bytes(...) of the same arguments.
+ *   other arguments and errors as the linear layers (no residual). */
+int64_t mq_glu_workspace_bytes(int fmt, int x_type, int M, int N, int K, int split_k);
+
+int mq_glu_f16cache(int x_type, const void *X, int ldx, const uint16_t *W16, int ldw,
+                    const float *bias, int act, int y_type, void *Y, int ldy, int M, int N, int K,
+                    void *ws, size_t ws_bytes, int split_k, void *stream);
+
+int mq_glu_fused(int x_type, const void *X, int ldx, int fmt, const void *wq, const float *bias,
+                 int act, int y_type, void *Y, int ldy, int M, int N, int K, void *ws,
+                 size_t ws_bytes, int split_k, void *stream);
 
 /* Residual addition and root-mean-square norm of M activation rows, the step
  * between two layers' products, with the output in the type the next product

@@ -35,9 +35,19 @@ from .api import (
     row_bytes,
     workspace_bytes,
 )
-from .layers import add_rms_norm, add_rms_norm_q8_1
+from .layers import (
+    ACTIVATIONS,
+    add_rms_norm,
+    add_rms_norm_q8_1,
+    glu_f16cache,
+    glu_fused,
+    linear_f16cache,
+    linear_fused,
+    linear_workspace_bytes,
+)
 
 __all__ = [
+    "ACTIVATIONS",
     "FORMATS",
     "LIB_PATH",
     "MQ_Q4_0",
@@ -60,7 +70,12 @@ __all__ = [
     "gemm_fused",
     "gemm_mmq",
     "gemm_plan",
+    "glu_f16cache",
+    "glu_fused",
     "lib",
+    "linear_f16cache",
+    "linear_fused",
+    "linear_workspace_bytes",
     "mmq_workspace_bytes",
     "quantize_q8_1",
     "row_bytes",

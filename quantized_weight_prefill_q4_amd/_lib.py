@@ -23,6 +23,7 @@ MQ_ERR_SCRATCH = -9
 MQ_ERR_TYPE = -10
 MQ_ERR_EPS = -11
 MQ_ERR_OVERLAP = -12
+MQ_ERR_ACT = -13
 MQ_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 MQ_Q4_0 = 2
@@ -81,6 +82,18 @@ SIGNATURES = {
     "mq_gemm_mmq_workspace_bytes": (_c_i64, [_c_int, _c_int, _c_int, _c_int, _c_int]),
     "mq_gemm_mmq": (_c_int, [_c_int, _vp, _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                              _vp, _c_size, _c_int, _vp]),
+    "mq_linear_workspace_bytes": (_c_i64, [_c_int] * 6),
+    "mq_linear_f16cache": (_c_int, [_c_int, _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _vp,
+                                    _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _c_int, _vp,
+                                    _c_size, _c_int, _vp]),
+    "mq_linear_fused": (_c_int, [_c_int, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp,
+                                 _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _c_int, _vp,
+                                 _c_size, _c_int, _vp]),
+    "mq_glu_workspace_bytes": (_c_i64, [_c_int] * 6),
+    "mq_glu_f16cache": (_c_int, [_c_int, _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _vp,
+                                 _c_int, _c_int, _c_int, _c_int, _vp, _c_size, _c_int, _vp]),
+    "mq_glu_fused": (_c_int, [_c_int, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _c_int,
+                              _c_int, _c_int, _c_int, _vp, _c_size, _c_int, _vp]),
     "mq_add_rms_norm": (_c_int, [_c_int, _vp, _c_int, _c_int, _vp, _c_int, _vp, _c_float, _vp,
                                  _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _vp]),
     "mq_add_rms_norm_q8_1": (_c_int, [_c_int, _vp, _c_int, _c_int, _vp, _c_int, _vp, _c_float,

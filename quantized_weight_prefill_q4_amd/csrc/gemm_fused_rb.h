@@ -295,8 +295,8 @@ __device__ __forceinline__ void rb_step_x(const u32x4 *Ac, const u32x4 *An, cons
     });
 }
 
-template <int FMT, int BM>
-__global__ __launch_bounds__(kThreads, 1) void gemm_q4k_rb_kernel(Args a) {
+template <int FMT, int BM, int EPI = kStore>
+__global__ __launch_bounds__(kThreads, 1) void gemm_q4k_rb_kernel(KernelArgs<EPI> a) {
     static_assert(FMT == kFmtQ4_K || FMT == kFmtQ5_K, "Q4_K or Q5_K");
     using G = KRb<FMT>;
     static_assert(BM == 64 || BM == 128 || BM == 256, "tiles of 64, 128 or 256 rows");
@@ -336,14 +336,15 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_q4k_rb_kernel(Args a) {
     constexpr int NA = decltype(la)::NPART;
     // raw weight chunks: chunk c = thread + 256·i is byte 16(c mod CH) of the
     // super-block of tile row c / CH, and lands at LDS chunk c
-    const int rows_valid = min(BN, a.N - n0);
+    const int rows_valid = EPI == kGlu ? a.N - (n0 >> 1) : min(BN, a.N - n0);
     const __amdgpu_buffer_rsrc_t rsb =
-        make_rsrc(a.W + (int64_t)n0 * a.ldw, (uint32_t)(rows_valid * a.ldw));
+        make_rsrc(a.W + (int64_t)(EPI == kGlu ? n0 >> 1 : n0) * a.ldw,
+                  (uint32_t)(rows_valid * a.ldw));
     uint32_t goff[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int c = (int)threadIdx.x + kThreads * i, r = c / G::CH;
-        goff[i] = (uint32_t)(r * a.ldw + 16 * (c - G::CH * r));
+        goff[i] = (uint32_t)(tile_row<EPI>(r, a.N >> 1) * a.ldw + 16 * (c - G::CH * r));
     }
     u32x4 bv[2][G::PER];
     RbRaw raw[2];   // raw bytes of the current and the next k-step (index P, 1 − P)
@@ -442,7 +443,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_q4k_rb_kernel(Args a) {
         step(std::integral_constant<int, 3>(), kt + 3);
     }
 
-    store_tile<BM, BN, FM, FN, TM, TN, 4, (int)sizeof(A0), (int)sizeof(Bq0)>(
+    finish_tile<EPI, BM, BN, FM, FN, TM, TN, 4, (int)sizeof(A0), (int)sizeof(Bq0)>(
         a, acc, tail, part, tile, m0, n0, wm, wn, lane, wave, A0, A1, Bq0, Bq1);
 }
 
@@ -660,8 +661,8 @@ __device__ __forceinline__ void rb6_step_x(const u32x4 *Ac, const u32x4 *Bc, con
     });
 }
 
-template <int FMT, int BM>
-__global__ __launch_bounds__(kThreads, 1) void gemm_q6k_rb_kernel(Args a) {
+template <int FMT, int BM, int EPI = kStore>
+__global__ __launch_bounds__(kThreads, 1) void gemm_q6k_rb_kernel(KernelArgs<EPI> a) {
     static_assert(FMT == kFmtQ6_K, "Q6_K only");
     static_assert(BM == 64 || BM == 128 || BM == 256, "tiles of 64, 128 or 256 rows");
     constexpr int BN = 256, BK = 64, CPR = 8;
@@ -698,8 +699,8 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_q6k_rb_kernel(Args a) {
     constexpr int NA = decltype(la)::NPART;
     // raw weight chunks: the resource starts at the 16-byte boundary at or
     // below the tile's first row; chunk p = thread mod 8 of rows r0 + 32i
-    const int rows_valid = min(BN, a.N - n0);
-    const int64_t start = (int64_t)n0 * a.ldw;
+    const int rows_valid = EPI == kGlu ? a.N - (n0 >> 1) : min(BN, a.N - n0);
+    const int64_t start = (int64_t)(EPI == kGlu ? n0 >> 1 : n0) * a.ldw;
     const uint32_t shift0 = (uint32_t)(((uintptr_t)a.W + start) & 15);
     const int64_t extent = shift0 + (int64_t)rows_valid * a.ldw;
     const __amdgpu_buffer_rsrc_t rsb =
@@ -709,7 +710,8 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_q6k_rb_kernel(Args a) {
     const uint32_t phalf = p < 4 ? 64u : (p < 6 ? 32u : 0u);   // + phalf·h for half h
     uint32_t roff[kR6PerThread];
 #pragma unroll
-    for (int i = 0; i < kR6PerThread; ++i) roff[i] = shift0 + (uint32_t)((r0 + 32 * i) * a.ldw) + psrc0;
+    for (int i = 0; i < kR6PerThread; ++i) 
+        roff[i] = shift0 + (uint32_t)(tile_row<EPI>(r0 + 32 * i, a.N >> 1) * a.ldw) + psrc0;
     uint32_t bv[2][4][5], bsh[2][4];
     // load chunk i of half hx into slot (set, j)
     auto bload = [&](int set, int j, int i, int hx) MQ_INLINE {
@@ -808,7 +810,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_q6k_rb_kernel(Args a) {
         step(std::integral_constant<int, 0>(), kt);
         step(std::integral_constant<int, 1>(), kt + 1);
     }
-    store_tile<BM, BN, FM, FN, TM, TN, 4, (int)sizeof(A0), (int)sizeof(Bq0)>(
+    finish_tile<EPI, BM, BN, FM, FN, TM, TN, 4, (int)sizeof(A0), (int)sizeof(Bq0)>(
         a, acc, tail, part, tile, m0, n0, wm, wn, lane, wave, A0, A1, Bq0, Bq1);
 }
 
@@ -1042,8 +1044,8 @@ __device__ __forceinline__ void b32_step_x(const u32x4 *Ac, const u32x4 *An, con
     });
 }
 
-template <int FMT, int BM>
-__global__ __launch_bounds__(kThreads, 1) void gemm_b32_rb_kernel(Args a) {
+template <int FMT, int BM, int EPI = kStore>
+__global__ __launch_bounds__(kThreads, 1) void gemm_b32_rb_kernel(KernelArgs<EPI> a) {
     using G = B32Rb<FMT>;
     static_assert(BM == 64 || BM == 128 || BM == 256, "tiles of 64, 128 or 256 rows");
     constexpr int BN = 256, BK = 64, CPR = 8;
@@ -1082,16 +1084,17 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_b32_rb_kernel(Args a) {
     constexpr int NA = decltype(la)::NPART;
     // raw weight chunks (rows 16-byte aligned): chunk c = t + 256i of the
     // tile's 256 × CH is row c / CH, chunk c mod CH, LDS chunk S·row + that
-    const int rows_valid = min(BN, a.N - n0);
+    const int rows_valid = EPI == kGlu ? a.N - (n0 >> 1) : min(BN, a.N - n0);
     const __amdgpu_buffer_rsrc_t rsb =
-        make_rsrc(a.W + (int64_t)n0 * a.ldw, (uint32_t)(rows_valid * a.ldw));
+        make_rsrc(a.W + (int64_t)(EPI == kGlu ? n0 >> 1 : n0) * a.ldw,
+                  (uint32_t)(rows_valid * a.ldw));
     const int t = (int)threadIdx.x;
     uint32_t roff[G::CH];
     int lpos[G::CH];
 #pragma unroll
     for (int i = 0; i < G::CH; ++i) {
         const int c = t + kThreads * i, row = c / G::CH, ch = c - row * G::CH;
-        roff[i] = (uint32_t)(row * a.ldw) + 16u * (uint32_t)ch;
+        roff[i] = (uint32_t)(tile_row<EPI>(row, a.N >> 1) * a.ldw) + 16u * (uint32_t)ch;
         lpos[i] = row * G::S + ch;
     }
     constexpr int NSET = G::P0 > G::CH - G::P0 ? G::P0 : G::CH - G::P0;
@@ -1215,7 +1218,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_b32_rb_kernel(Args a) {
         step(std::integral_constant<int, 0>(), kt);
         step(std::integral_constant<int, 1>(), kt + 1);
     }
-    store_tile<BM, BN, FM, FN, TM, TN, 4, (int)sizeof(A0), (int)sizeof(Bq0)>(
+    finish_tile<EPI, BM, BN, FM, FN, TM, TN, 4, (int)sizeof(A0), (int)sizeof(Bq0)>(
         a, acc, tail, part, tile, m0, n0, wm, wn, lane, wave, A0, A1, Bq0, Bq1);
 }
 

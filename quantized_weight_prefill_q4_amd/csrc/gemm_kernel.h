@@ -41,6 +41,7 @@
 
 #pragma once
 
+#include "epilogue.h"
 #include "mq_device.h"
 #include "mq_internal.h"
 
@@ -80,6 +81,52 @@ struct Args {
     int tiles_m, tiles_n, k_steps, steps_per_split;
     int dp_tiles, tail_tiles;
 };
+
+// What the tile kernels do with a finished tile.
+constexpr int kStore = 0;    // write the f32 sums
+constexpr int kLinear = 1;   // bias, activation, residual, rounding
+constexpr int kGlu = 2;      // the gate's and the up matrix's sums combined
+
+// The kernels' arguments with an epilogue.  Gated products: N counts the
+// weight's 2·F rows, gate rows first.  A tile's BN columns are then blocks of
+// 32 taken alternately from the two halves — columns 64p .. 64p + 31 are gate
+// rows h0 + 32p .. + 31 and columns 64p + 32 .. 64p + 63 the up rows of the
+// same numbers, h0 = n0/2 — so that both sums of an output sit in one lane's
+// accumulators (or, K-split, in one partial tile) and only the products'
+// result is written: F columns of y instead of 2·F of f32 sums.  The weight
+// keeps the layout of two matrices stacked; only row addresses change.
+struct EpiArgs : Args {
+    const float *bias;
+    const void *res;
+    int64_t ldr;
+    int act, res_type, y_type;
+};
+template <int EPI>
+using KernelArgs = std::conditional_t<EPI == kStore, Args, EpiArgs>;
+
+// Row of its half that tile row r is, and which half (1: up).
+__device__ __forceinline__ int glu_row(int r) { return ((r >> 6) << 5) | (r & 31); }
+__device__ __forceinline__ int glu_half(int r) { return (r >> 5) & 1; }
+// The weight row (relative to the tile's first) of tile row r; F: rows per half.
+template <int EPI>
+__device__ __forceinline__ int64_t tile_row(int r, int F) {
+    if constexpr (EPI == kGlu)
+        return (int64_t)glu_half(r) * F + glu_row(r);
+    else
+        return r;
+}
+
+// The fused loaders take the weight rows of a gated tile wave by wave: two
+// threads per row and 64 per wave make a wave's part one 32-row block, gate
+// for even waves and up for odd ones.  Their init then receives the first row
+// of the wave's half and numbers rows within it.
+template <int EPI>
+__device__ __forceinline__ int loader_row(int r) {
+    if constexpr (EPI == kGlu)
+        return glu_row(r);
+    else
+        return r;
+}
 
 // LDS tiles are rows of CPR 16-byte chunks (CPR = k-step / 8: 8 for a 64-wide
 // step, 4 for a 32-wide one); chunk c of row r is stored at position
@@ -164,6 +211,54 @@ struct F16Loader {
     }
 };
 
+// The f16 weight tile of a gated product: F16Loader's thread map, with the
+// tile's 32-row blocks taken alternately from gate and up.  256 threads: a
+// thread's parts are 32 rows apart, so even parts are gate rows and odd ones
+// up rows.  512 threads: parts are 64 rows apart, so waves 0-3 hold gate rows
+// and waves 4-7 up rows.  Each half has its own resource (their distance may
+// exceed a resource's range).
+template <int ROWS, int NTH>
+struct F16GluLoader {
+    static_assert(NTH == 256 || NTH == 512, "4 or 8 waves");
+    static constexpr int NPART = ROWS * 8 / NTH;
+    static constexpr int RSTEP = NTH / 8;
+    static constexpr bool BOTH = NTH == 256;
+    __amdgpu_buffer_rsrc_t rs[BOTH ? 2 : 1];
+    uint32_t off0, stride, kc;
+    int lds0;
+    int K;
+    uint32_t obase[2];
+    u32x4 v[2][NPART];
+
+    __device__ void init(const uint16_t *W, int F, int h0, int64_t ld, int K_) {
+        K = K_;
+        const int valid = min(ROWS / 2, F - h0);
+        const uint32_t bytes = (uint32_t)((valid - 1) * ld * 2 + (int64_t)K_ * 2);
+        const int t = threadIdx.x, r0 = t >> 3, c = t & 7;
+        if constexpr (BOTH) {
+            rs[0] = make_rsrc(W + h0 * ld, bytes);
+            rs[1] = make_rsrc(W + ((int64_t)F + h0) * ld, bytes);
+        } else {
+            const int half = __builtin_amdgcn_readfirstlane(t >> 8);
+            rs[0] = make_rsrc(W + ((int64_t)half * F + h0) * ld, bytes);
+        }
+        off0 = (uint32_t)((r0 & 31) * ld * 2 + c * 16);
+        stride = (uint32_t)(32 * ld * 2);
+        kc = (uint32_t)(c * 8);
+        lds0 = r0 * 8 + (c ^ swz<8>(r0));
+    }
+    __device__ __forceinline__ void begin(int set, int k0, bool live) {
+        obase[set] = live && (uint32_t)k0 + kc < (uint32_t)K ? off0 + (uint32_t)k0 * 2 : kOOB;
+    }
+    __device__ __forceinline__ void load(int set, int i) {
+        v[set][i] = buf_load16(rs[BOTH ? i & 1 : 0],
+                               obase[set] + (uint32_t)(BOTH ? i >> 1 : i) * stride);
+    }
+    __device__ __forceinline__ void store(int set, int i, u32x4 *lds) const {
+        lds[lds0 + i * RSTEP * 8] = v[set][i];
+    }
+};
+
 // Eight f32 values to one 16-byte chunk of f16.
 __device__ __forceinline__ u32x4 pack8(float v0, float v1, float v2, float v3, float v4, float v5,
                                        float v6, float v7) {
@@ -235,11 +330,12 @@ struct Q4KLoader {
     int c4[2];
     u32x4 hdr[2][NPART], qs[2][NPART];
 
-    __device__ void init(const uint8_t *W, int64_t row_bytes, int n0, int rows_valid, int) {
+    template <int EPI = kStore>
+    __device__ void init(const uint8_t *W, int64_t row_bytes, int64_t n0, int rows_valid, int) {
         rs = make_rsrc(W + (int64_t)n0 * row_bytes, (uint32_t)(rows_valid * row_bytes));
 #pragma unroll
         for (int i = 0; i < NPART; ++i) {
-            const int r = (i * kThreads + (int)threadIdx.x) >> 1;
+            const int r = loader_row<EPI>((i * kThreads + (int)threadIdx.x) >> 1);
             roff[i] = (uint32_t)(r * row_bytes);
         }
     }
@@ -340,14 +436,15 @@ struct Q6KLoader {
     mutable uint32_t wa[2][NPART][5], wb[2][NPART][5], wh[2][NPART][5], odd[2][NPART];
     uint32_t wsa[2][NPART], wsb[2][NPART], wd[2][NPART], osc[2][NPART];
 
-    __device__ void init(const uint8_t *W, int64_t row_bytes, int n0, int rows_valid, int) {
+    template <int EPI = kStore>
+    __device__ void init(const uint8_t *W, int64_t row_bytes, int64_t n0, int rows_valid, int) {
         const int64_t start = (int64_t)n0 * row_bytes;
         const uint32_t shift0 = (uint32_t)(((uintptr_t)W + start) & 15);
         const int64_t extent = shift0 + (int64_t)rows_valid * row_bytes;
         rs = make_rsrc(W + start - shift0, (uint32_t)((extent + 3) & ~(int64_t)3));
 #pragma unroll
         for (int i = 0; i < NPART; ++i) {
-            const int r = (i * kThreads + (int)threadIdx.x) >> 1;
+            const int r = loader_row<EPI>((i * kThreads + (int)threadIdx.x) >> 1);
             roff[i] = shift0 + (uint32_t)(r * row_bytes);
         }
     }
@@ -430,7 +527,8 @@ struct Q80Loader {
     int nb, blk[2];
     bool live_[2];
 
-    __device__ void init(const uint8_t *W, int64_t row_bytes, int n0, int rows_valid, int K) {
+    template <int EPI = kStore>
+    __device__ void init(const uint8_t *W, int64_t row_bytes, int64_t n0, int rows_valid, int K) {
         nb = K >> 5;
         const int64_t start = (int64_t)n0 * row_bytes;
         const uint32_t shift0 = (uint32_t)(((uintptr_t)W + start) & 15);
@@ -438,7 +536,7 @@ struct Q80Loader {
         rs = make_rsrc(W + start - shift0, (uint32_t)((extent + 3) & ~(int64_t)3));
 #pragma unroll
         for (int i = 0; i < NPART; ++i) {
-            const int r = (i * kThreads + (int)threadIdx.x) >> 1;
+            const int r = loader_row<EPI>((i * kThreads + (int)threadIdx.x) >> 1);
             roff[i] = shift0 + (uint32_t)(r * row_bytes);
         }
     }
@@ -502,7 +600,8 @@ struct Q32Loader {
     int nb, blk[2];
     bool live_[2];
 
-    __device__ void init(const uint8_t *W, int64_t row_bytes, int n0, int rows_valid, int K) {
+    template <int EPI = kStore>
+    __device__ void init(const uint8_t *W, int64_t row_bytes, int64_t n0, int rows_valid, int K) {
         nb = K >> 5;
         const int64_t start = (int64_t)n0 * row_bytes;
         const uint32_t shift0 = (uint32_t)(((uintptr_t)W + start) & 15);
@@ -510,7 +609,7 @@ struct Q32Loader {
         rs = make_rsrc(W + start - shift0, (uint32_t)((extent + 3) & ~(int64_t)3));
 #pragma unroll
         for (int i = 0; i < NPART; ++i) {
-            const int r = (i * kThreads + (int)threadIdx.x) >> 1;
+            const int r = loader_row<EPI>((i * kThreads + (int)threadIdx.x) >> 1);
             roff[i] = shift0 + (uint32_t)(r * row_bytes);
         }
     }
@@ -615,11 +714,12 @@ struct Q5KLoader {
     int c4[2];
     u32x4 hdr[2][NPART], qh[2][NPART], qs[2][NPART];
 
-    __device__ void init(const uint8_t *W, int64_t row_bytes, int n0, int rows_valid, int) {
+    template <int EPI = kStore>
+    __device__ void init(const uint8_t *W, int64_t row_bytes, int64_t n0, int rows_valid, int) {
         rs = make_rsrc(W + (int64_t)n0 * row_bytes, (uint32_t)(rows_valid * row_bytes));
 #pragma unroll
         for (int i = 0; i < NPART; ++i) {
-            const int r = (i * kThreads + (int)threadIdx.x) >> 1;
+            const int r = loader_row<EPI>((i * kThreads + (int)threadIdx.x) >> 1);
             roff[i] = (uint32_t)(r * row_bytes);
         }
     }
@@ -920,6 +1020,130 @@ __device__ __forceinline__ void store_tile(const Args &a, f32x16 (&acc)[FM][FN],
         }
 }
 
+// A whole tile's epilogue and output.  The wave takes its tile 16 rows at a
+// time through a private LDS patch of 16 × (TN + 4) floats (in the idle
+// stages, as store_tile): written in the MFMA layout (a column per lane), read
+// back as 8 consecutive columns of a row per lane, so that bias, residual and
+// y are 16-byte accesses and the activation runs once per output in a loop
+// that is not unrolled over the tile.  The residual rows of the next 16 are
+// loaded while the current ones are finished.
+template <int EPI, int BM, int BN, int FM, int FN, int TM, int TN, int NW, int SA, int SB>
+__device__ __forceinline__ void store_tile_epi(const EpiArgs &a, f32x16 (&acc)[FM][FN], int m0,
+                                               int n0, int wm, int wn, int lane, int wave,
+                                               u32x4 *S0, u32x4 *S1, u32x4 *S2, u32x4 *S3) {
+    constexpr bool GLU = EPI == kGlu;
+    static_assert(!GLU || FN % 2 == 0, "a gated wave tile holds whole gate / up block pairs");
+    constexpr int PS = TN + 4, PB = 16 * PS * 4;
+    constexpr int PA = SA / PB, PBB = SB / PB;
+    static_assert(2 * (PA + PBB) >= NW, "a patch per wave in the idle stages");
+    u32x4 *buf;
+    int slot;
+    if (wave < PA) {
+        buf = S0;
+        slot = wave;
+    } else if (wave < 2 * PA) {
+        buf = S1;
+        slot = wave - PA;
+    } else if (wave < 2 * PA + PBB) {
+        buf = S2;
+        slot = wave - 2 * PA;
+    } else {
+        buf = S3;
+        slot = wave - 2 * PA - PBB;
+    }
+    float *patch = reinterpret_cast<float *>(buf) + slot * (16 * PS);
+
+    constexpr int OC = GLU ? TN / 2 : TN;          // output columns of the wave
+    constexpr int LPR = OC / 8, RPI = 64 / LPR;    // lanes per row, rows per pass
+    constexpr int QN = 16 / RPI;                   // passes per 16 rows
+    static_assert(QN >= 1 && QN * RPI == 16, "whole passes");
+    const int rr = lane / LPR, cc = 8 * (lane % LPR);
+    const int F = GLU ? a.N >> 1 : a.N;
+    const int col = (GLU ? (n0 >> 1) + wn * (TN / 2) : n0 + wn * TN) + cc;
+    const int n = min(8, F - col);                 // columns this lane writes (<= 0: none)
+    const int pc = GLU ? (cc >> 5) * 64 + (cc & 31) : cc;
+    float b0[8] = {}, b1[8] = {};
+    if (a.bias && n > 0) {
+        load_upto8(a.bias, kTypeF32, col, n, b0);
+        if constexpr (GLU) load_upto8(a.bias, kTypeF32, (int64_t)F + col, n, b1);
+    }
+    const int64_t ye = a.y_type == kTypeF32 ? 4 : 2, re = a.res_type == kTypeF32 ? 4 : 2;
+    const int row0 = m0 + wm * TM + rr;
+    float res[2][QN][8] = {};
+    auto load_res = [&](int set, int g) MQ_INLINE {
+        if constexpr (!GLU) {
+            if (a.res) {
+#pragma unroll
+                for (int q = 0; q < QN; ++q) {
+                    const int64_t row = row0 + 16 * g + RPI * q;
+                    if (row < a.M && n > 0)
+                        load_upto8((const char *)a.res + row * a.ldr * re, a.res_type, col, n,
+                                   res[set][q]);
+                }
+            }
+        }
+    };
+    const int col_l = lane & 31, row_l = (lane >> 5) * 4;
+    load_res(0, 0);
+    sync_lds();   // every wave is done reading the stages
+    static_for<2 * FM>([&](auto G) MQ_INLINE {
+        constexpr int g = G, i = g >> 1, h = g & 1;
+        if constexpr (g + 1 < 2 * FM) load_res((g + 1) & 1, g + 1);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int r = 8 * h; r < 8 * h + 8; ++r)
+                patch[((r >> 2) * 8 - 16 * h + row_l + (r & 3)) * PS + j * 32 + col_l] =
+                    acc[i][j][r];
+        // lanes read what other lanes wrote: the LDS runs one wave's
+        // instructions in order, so only the compiler must keep them
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int q = 0; q < QN; ++q) {
+            const int64_t row = row0 + 16 * g + RPI * q;
+            const float *p = patch + (rr + RPI * q) * PS + pc;
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(p);
+            const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + 4);
+            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += b0[j];
+            apply_act(a.act, v);
+            if constexpr (GLU) {
+                const f32x4 ul = *reinterpret_cast<const f32x4 *>(p + 32);
+                const f32x4 uh = *reinterpret_cast<const f32x4 *>(p + 36);
+                const float u[8] = {ul.x, ul.y, ul.z, ul.w, uh.x, uh.y, uh.z, uh.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= u[j] + b1[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += res[g & 1][q][j];
+            }
+            if (row < a.M && n > 0)
+                store_upto8((char *)a.Y + row * a.ldy * ye, a.y_type, col, n, v);
+        }
+        asm volatile("" ::: "memory");
+    });
+}
+
+// A workgroup's last step: the tile's output, or a K range's partial tile.
+template <int EPI, int BM, int BN, int FM, int FN, int TM, int TN, int NW, int SA, int SB>
+__device__ __forceinline__ void finish_tile(const KernelArgs<EPI> &a, f32x16 (&acc)[FM][FN],
+                                            bool tail, int part, int tile, int m0, int n0, int wm,
+                                            int wn, int lane, int wave, u32x4 *S0, u32x4 *S1,
+                                            u32x4 *S2, u32x4 *S3) {
+    if constexpr (EPI == kStore) {
+        store_tile<BM, BN, FM, FN, TM, TN, NW, SA, SB>(a, acc, tail, part, tile, m0, n0, wm, wn,
+                                                       lane, wave, S0, S1, S2, S3);
+    } else {
+        if (tail)
+            store_tile<BM, BN, FM, FN, TM, TN, NW, SA, SB>(a, acc, true, part, tile, m0, n0, wm,
+                                                           wn, lane, wave, S0, S1, S2, S3);
+        else
+            store_tile_epi<EPI, BM, BN, FM, FN, TM, TN, NW, SA, SB>(a, acc, m0, n0, wm, wn, lane,
+                                                                    wave, S0, S1, S2, S3);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // The GEMM kernel.  Two LDS stages and two register sets per operand:
 // during step j (MFMAs from LDS stage j%2) each thread issues the global
@@ -945,8 +1169,8 @@ __device__ __forceinline__ void store_tile(const Args &a, f32x16 (&acc)[FM][FN],
 // a tail tile (see the plan); the latter writes its f32 partial tile to the
 // workspace.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int FMT, bool XF32, int NWV = 4>
-__global__ __launch_bounds__(64 * NWV, 1) void gemm_kernel(Args a) {
+template <int BM, int BN, int FMT, bool XF32, int NWV = 4, int EPI = kStore>
+__global__ __launch_bounds__(64 * NWV, 1) void gemm_kernel(KernelArgs<EPI> a) {
     static_assert(NWV == 4 || (NWV == 8 && BN == 128 && !XF32), "8 waves: tiles of 128 columns");
     constexpr int BK = 64;
     constexpr int WN = NWV == 4 ? 2 : (BM >= 128 ? 2 : 4), WM = NWV / WN;
@@ -993,12 +1217,22 @@ __global__ __launch_bounds__(64 * NWV, 1) void gemm_kernel(Args a) {
     // compiler's wait counts had to cover both paths and made the decoding
     // waves wait for the loads of the current step (M = 128: 14336 x 4096
     // Q8_0 41 -> 52 us).
-    std::conditional_t<NWV == 4 || FMT != kFmtF16, typename BLoaderFor<BN, FMT>::T,
-                       F16Loader<BN, 64 * NWV>>
+    std::conditional_t<EPI == kGlu && FMT == kFmtF16, F16GluLoader<BN, 64 * NWV>,
+                       std::conditional_t<NWV == 4 || FMT != kFmtF16,
+                                          typename BLoaderFor<BN, FMT>::T,
+                                          F16Loader<BN, 64 * NWV>>>
         lb;
     const bool bw = NWV == 4 || FMT == kFmtF16 ||
                     __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) < kThreads / 64;
-    if constexpr (FMT == kFmtF16)
+    if constexpr (EPI == kGlu) {
+        const int F = a.N >> 1, h0 = n0 >> 1;
+        if constexpr (FMT == kFmtF16) {
+            lb.init((const uint16_t *)a.W, F, h0, a.ldw, a.K);
+        } else {
+            const int half = __builtin_amdgcn_readfirstlane(((int)threadIdx.x >> 6) & 1);
+            lb.template init<EPI>(a.W, a.ldw, (int64_t)half * F + h0, min(BN / 2, F - h0), a.K);
+        }
+    } else if constexpr (FMT == kFmtF16)
         lb.init((const uint16_t *)a.W + n0 * a.ldw, min(BN, a.N - n0), a.ldw, a.K);
     else
         lb.init(a.W, a.ldw, n0, min(BN, a.N - n0), a.K);
@@ -1113,7 +1347,7 @@ __global__ __launch_bounds__(64 * NWV, 1) void gemm_kernel(Args a) {
     }
     if (kt < kt_end) step(std::integral_constant<int, 0>(), kt);
 
-    store_tile<BM, BN, FM, FN, TM, TN, NWV, BM * CPR * 16, BN * CPR * 16>(
+    finish_tile<EPI, BM, BN, FM, FN, TM, TN, NWV, BM * CPR * 16, BN * CPR * 16>(
         a, acc, tail, part, tile, m0, n0, wm, wn, lane, wave, A0, A1, B0, B1);
 }
 
@@ -1180,39 +1414,163 @@ hipError_t launch_splitk_reduce(int split, dim3 grid, hipStream_t stream, const 
     return hipErrorInvalidValue;
 }
 
-template <int BM, int BN, int FMT, bool XF32>
-hipError_t launch_tile(const Args &a, int grid, hipStream_t stream, bool dry) {
+// The reduce with an epilogue: the same fixed-order sums, then bias,
+// activation, residual (or gate · up) and the output's rounding.  A thread owns
+// four consecutive outputs; for a gated product their up sums are 32 columns
+// further in the partial tile.
+template <int EPI, int S>
+__global__ __launch_bounds__(256) void splitk_reduce_epi(EpiArgs a, int bm, int bn) {
+    constexpr bool GLU = EPI == kGlu;
+    const int ocols = GLU ? bn / 2 : bn;
+    const int chunks = bm * ocols / 1024;
+    const int tt = blockIdx.x / chunks;
+    const int e = (blockIdx.x - tt * chunks) * 1024 + threadIdx.x * 4;
+    const int r = e / ocols, c = e - r * ocols;
+    int tm, tn;
+    tile_coords(a.dp_tiles + tt, a.tiles_m, a.tiles_n, tm, tn);
+    const int F = GLU ? a.N >> 1 : a.N;
+    const int row = tm * bm + r, col = tn * ocols + c;
+    if (row >= a.M || col >= F) return;
+    const int64_t tile_elems = (int64_t)bm * bn, stride = tile_elems * a.tail_tiles;
+    const int pc = GLU ? (c >> 5) * 64 + (c & 31) : c;
+    const float *p = a.ws + tt * tile_elems + (int64_t)r * bn + pc;
+    f32x4 v[S], u[GLU ? S : 1];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        v[s] = __builtin_nontemporal_load((const f32x4 *)(p + s * stride));
+        if constexpr (GLU) u[s] = __builtin_nontemporal_load((const f32x4 *)(p + s * stride + 32));
+    }
+    const int n = min(4, F - col);
+    float b0[4] = {}, b1[4] = {}, res[4] = {};
+    if (a.bias) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n) {
+                b0[j] = a.bias[col + j];
+                if constexpr (GLU) b1[j] = a.bias[F + col + j];
+            }
+    }
+    if constexpr (!GLU) {
+        if (a.res) {
+            const int64_t at = (int64_t)row * a.ldr + col;
+            if (a.res_type == kTypeF32) {
+                const float *q = (const float *)a.res + at;
+                if (n == 4) {
+                    const f32x4 t = *(const f32x4_a4 *)q;
+                    res[0] = t.x; res[1] = t.y; res[2] = t.z; res[3] = t.w;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < n) res[j] = q[j];
+                }
+            } else {
+                const uint16_t *q = (const uint16_t *)a.res + at;
+                if (n == 4) {
+                    const u32x2 t = *(const u32x2_a2 *)q;
+                    res[0] = f16_bits_to_f32(t.x); res[1] = f16_bits_to_f32(t.x >> 16);
+                    res[2] = f16_bits_to_f32(t.y); res[3] = f16_bits_to_f32(t.y >> 16);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < n) res[j] = f16_bits_to_f32(q[j]);
+                }
+            }
+        }
+    }
+    f32x4 sum = v[0];
+#pragma unroll
+    for (int s = 1; s < S; ++s) sum += v[s];
+    float y[4] = {sum.x + b0[0], sum.y + b0[1], sum.z + b0[2], sum.w + b0[3]};
+    apply_act(a.act, y);
+    if constexpr (GLU) {
+        f32x4 us = u[0];
+#pragma unroll
+        for (int s = 1; s < S; ++s) us += u[s];
+        y[0] *= us.x + b1[0];
+        y[1] *= us.y + b1[1];
+        y[2] *= us.z + b1[2];
+        y[3] *= us.w + b1[3];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] += res[j];
+    }
+    const int64_t at = (int64_t)row * a.ldy + col;
+    if (a.y_type == kTypeF32) {
+        float *o = (float *)a.Y + at;
+        if (n == 4) {
+            *(f32x4_a4 *)o = f32x4{y[0], y[1], y[2], y[3]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) o[j] = y[j];
+        }
+    } else {
+        uint16_t *o = (uint16_t *)a.Y + at;
+        if (n == 4) {
+            *(u32x2_a2 *)o = u32x2{pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3])};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) o[j] = (uint16_t)pack_f16x2(y[j], 0.0f);
+        }
+    }
+}
+
+template <int EPI, int S = 2>
+hipError_t launch_splitk_reduce_epi(const GemmPlan &plan, hipStream_t stream, const EpiArgs &a) {
+    if constexpr (S <= 16) {
+        if (plan.split != S) return launch_splitk_reduce_epi<EPI, S + 1>(plan, stream, a);
+        const int ocols = EPI == kGlu ? plan.bn / 2 : plan.bn;
+        const int blocks = plan.tail_tiles * (plan.bm * ocols / 1024);
+        hipLaunchKernelGGL((splitk_reduce_epi<EPI, S>), dim3(blocks), dim3(256), 0, stream, a,
+                           plan.bm, plan.bn);
+        return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
+}
+
+template <int BM, int BN, int FMT, bool XF32, int EPI = kStore>
+hipError_t launch_tile(const KernelArgs<EPI> &a, int grid, hipStream_t stream, bool dry) {
     if (dry) return hipSuccess;
     // Tiles of 128 columns on 8 waves: two waves per SIMD double the LDS
     // throughput a step can draw on.  f16 cache: 1.5-4% faster at M = 128
     // and on the 7B q/o shape, no slower elsewhere.  Fused, with 128 or 256
     // rows: 2-5% faster at M = 2048 (q/o, 4096 x 4096; Q4_K, Q6_K, Q8_0),
     // 2-18% at M = 128, no slower elsewhere.  Fused 64-row tiles keep 4
-    // waves (8 gained nothing on k/v and lost 3% at N = 1024).
-    constexpr int NWV = (BN == 128 && !XF32 && (FMT == kFmtF16 || BM >= 128)) ? 8 : 4;
-    hipLaunchKernelGGL((gemm_kernel<BM, BN, FMT, XF32, NWV>), dim3(grid), dim3(64 * NWV), 0, stream,
-                       a);
+    // waves (8 gained nothing on k/v and lost 3% at N = 1024).  A gated 64-row
+    // tile takes 4 waves too: with 8 a wave holds one 32-column block, not a
+    // gate / up pair.
+    constexpr int NWV =
+        (BN == 128 && !XF32 && (BM >= 128 || (FMT == kFmtF16 && EPI != kGlu))) ? 8 : 4;
+    hipLaunchKernelGGL((gemm_kernel<BM, BN, FMT, XF32, NWV, EPI>), dim3(grid), dim3(64 * NWV), 0,
+                       stream, a);
     return hipGetLastError();
 }
 
 // The register-expansion fused kernel of format FMT on BM × 256 tiles
 // (Q4_K and Q5_K, Q6_K, and the 32-element block formats when K is a
 // multiple of 256); hipErrorNotSupported when there is none.
-template <int FMT, int BM>
-hipError_t launch_rb(const Args &a, int grid, hipStream_t stream, bool dry) {
+template <int FMT, int BM, int EPI = kStore>
+hipError_t launch_rb(const KernelArgs<EPI> &a, int grid, hipStream_t stream, bool dry) {
+    // a gated tile's rows are reached through one resource from the gate rows
+    // to the weight's end, whose offsets must stay below the masked-off one
+    if (EPI == kGlu && (int64_t)a.N * a.ldw + 16 > (int64_t)kOOB) return hipErrorNotSupported;
     if constexpr (FMT == kFmtQ4_K || FMT == kFmtQ5_K) {
         if (dry) return hipSuccess;
-        hipLaunchKernelGGL((gemm_q4k_rb_kernel<FMT, BM>), dim3(grid), dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((gemm_q4k_rb_kernel<FMT, BM, EPI>), dim3(grid), dim3(kThreads), 0, stream,
+                           a);
         return hipGetLastError();
     } else if constexpr (FMT == kFmtQ6_K) {
         if (dry) return hipSuccess;
-        hipLaunchKernelGGL((gemm_q6k_rb_kernel<FMT, BM>), dim3(grid), dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((gemm_q6k_rb_kernel<FMT, BM, EPI>), dim3(grid), dim3(kThreads), 0, stream,
+                           a);
         return hipGetLastError();
     } else if constexpr (FMT == kFmtQ8_0 || FMT == kFmtQ4_0 || FMT == kFmtQ5_0 ||
                          FMT == kFmtQ5_1) {
         if (a.K % 256 != 0) return hipErrorNotSupported;   // rows of whole 8-block runs only
         if (dry) return hipSuccess;
-        hipLaunchKernelGGL((gemm_b32_rb_kernel<FMT, BM>), dim3(grid), dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((gemm_b32_rb_kernel<FMT, BM, EPI>), dim3(grid), dim3(kThreads), 0, stream,
+                           a);
         return hipGetLastError();
     }
     return hipErrorNotSupported;
@@ -1222,35 +1580,35 @@ hipError_t launch_rb(const Args &a, int grid, hipStream_t stream, bool dry) {
 // error, never a launch with a mismatched tile (its grid would address tiles
 // past the matrix).  dry: only report whether a kernel exists (hipSuccess)
 // or not (hipErrorInvalidValue), launching nothing.
-template <int FMT, bool XF32>
-hipError_t launch_fmt(const Args &a, int bm, int bn, int grid, hipStream_t stream, bool dry) {
+template <int FMT, bool XF32, int EPI = kStore>
+hipError_t launch_fmt(const KernelArgs<EPI> &a, int bm, int bn, int grid, hipStream_t stream, bool dry) {
     if (bm == 256 && bn == 256) {
         if constexpr (!XF32 && FMT != kFmtF16) {
-            if (hipError_t e = launch_rb<FMT, 256>(a, grid, stream, dry); e != hipErrorNotSupported)
+            if (hipError_t e = launch_rb<FMT, 256, EPI>(a, grid, stream, dry);
+                e != hipErrorNotSupported)
                 return e;
         }
-        if constexpr (!XF32) return launch_tile<256, 256, FMT, XF32>(a, grid, stream, dry);
+        // an ungated linear layer's K-quants always have the kernel above
+        constexpr bool always_rb = EPI == kLinear && (FMT == kFmtQ4_K || FMT == kFmtQ5_K ||
+                                                      FMT == kFmtQ6_K);
+        if constexpr (!XF32 && !always_rb)
+            return launch_tile<256, 256, FMT, XF32, EPI>(a, grid, stream, dry);
     } else if (bm == 256 && bn == 128) {
-        return launch_tile<256, 128, FMT, XF32>(a, grid, stream, dry);
+        return launch_tile<256, 128, FMT, XF32, EPI>(a, grid, stream, dry);
     } else if (bm == 128 && bn == 128) {
-        return launch_tile<128, 128, FMT, XF32>(a, grid, stream, dry);
+        return launch_tile<128, 128, FMT, XF32, EPI>(a, grid, stream, dry);
     } else if (bm == 64 && bn == 128) {
-        return launch_tile<64, 128, FMT, XF32>(a, grid, stream, dry);
+        return launch_tile<64, 128, FMT, XF32, EPI>(a, grid, stream, dry);
     }
     return hipErrorInvalidValue;
 }
 
-// The plan's kernel for format `fmt` (kFmtF16: the f16 cache), then, for a
-// K split, the fixed-order reduction of the tail tiles' partial planes.
-// dry: check that the plan has a kernel and launch nothing.
-template <bool XF32>
-hipError_t launch_gemm_t(int fmt, const void *X, int ldx, const void *W, int64_t ldw, float *Y,
-                         int ldy, int M, int N, int K, const GemmPlan &plan, float *ws,
-                         hipStream_t stream, bool dry = false) {
-    Args a;
+// Fills the kernels' arguments from a plan.
+inline void fill_args(Args &a, const void *X, int ldx, const void *W, int64_t ldw, void *Y,
+                      int ldy, int M, int N, int K, const GemmPlan &plan, float *ws) {
     a.X = X;
     a.W = (const uint8_t *)W;
-    a.Y = Y;
+    a.Y = (float *)Y;
     a.ws = ws;
     a.ldw = ldw;
     a.ldx = ldx;
@@ -1264,24 +1622,60 @@ hipError_t launch_gemm_t(int fmt, const void *X, int ldx, const void *W, int64_t
     a.steps_per_split = plan.steps_per_split;
     a.dp_tiles = plan.dp_tiles;
     a.tail_tiles = plan.tail_tiles;
-    const int grid = plan.dp_tiles + plan.tail_tiles * plan.split;
-    hipError_t e;
+}
+
+// launch_fmt of the format `fmt`.
+template <bool XF32, int EPI>
+hipError_t launch_any(int fmt, const KernelArgs<EPI> &a, const GemmPlan &plan, hipStream_t stream,
+                      bool dry) {
+    const int bm = plan.bm, bn = plan.bn, grid = plan.dp_tiles + plan.tail_tiles * plan.split;
     switch (fmt) {
-    case kFmtQ4_K: e = launch_fmt<kFmtQ4_K, XF32>(a, plan.bm, plan.bn, grid, stream, dry); break;
-    case kFmtQ6_K: e = launch_fmt<kFmtQ6_K, XF32>(a, plan.bm, plan.bn, grid, stream, dry); break;
-    case kFmtQ8_0: e = launch_fmt<kFmtQ8_0, XF32>(a, plan.bm, plan.bn, grid, stream, dry); break;
-    case kFmtQ4_0: e = launch_fmt<kFmtQ4_0, XF32>(a, plan.bm, plan.bn, grid, stream, dry); break;
-    case kFmtQ5_0: e = launch_fmt<kFmtQ5_0, XF32>(a, plan.bm, plan.bn, grid, stream, dry); break;
-    case kFmtQ5_1: e = launch_fmt<kFmtQ5_1, XF32>(a, plan.bm, plan.bn, grid, stream, dry); break;
-    case kFmtQ5_K: e = launch_fmt<kFmtQ5_K, XF32>(a, plan.bm, plan.bn, grid, stream, dry); break;
-    case kFmtF16: e = launch_fmt<kFmtF16, XF32>(a, plan.bm, plan.bn, grid, stream, dry); break;
-    default: e = hipErrorInvalidValue; break;
+    case kFmtQ4_K: return launch_fmt<kFmtQ4_K, XF32, EPI>(a, bm, bn, grid, stream, dry);
+    case kFmtQ6_K: return launch_fmt<kFmtQ6_K, XF32, EPI>(a, bm, bn, grid, stream, dry);
+    case kFmtQ8_0: return launch_fmt<kFmtQ8_0, XF32, EPI>(a, bm, bn, grid, stream, dry);
+    case kFmtQ4_0: return launch_fmt<kFmtQ4_0, XF32, EPI>(a, bm, bn, grid, stream, dry);
+    case kFmtQ5_0: return launch_fmt<kFmtQ5_0, XF32, EPI>(a, bm, bn, grid, stream, dry);
+    case kFmtQ5_1: return launch_fmt<kFmtQ5_1, XF32, EPI>(a, bm, bn, grid, stream, dry);
+    case kFmtQ5_K: return launch_fmt<kFmtQ5_K, XF32, EPI>(a, bm, bn, grid, stream, dry);
+    case kFmtF16: return launch_fmt<kFmtF16, XF32, EPI>(a, bm, bn, grid, stream, dry);
+    default: return hipErrorInvalidValue;
     }
+}
+
+// The plan's kernel for format `fmt` (kFmtF16: the f16 cache), then, for a
+// K split, the fixed-order reduction of the tail tiles' partial planes.
+// dry: check that the plan has a kernel and launch nothing.
+template <bool XF32>
+hipError_t launch_gemm_t(int fmt, const void *X, int ldx, const void *W, int64_t ldw, float *Y,
+                         int ldy, int M, int N, int K, const GemmPlan &plan, float *ws,
+                         hipStream_t stream, bool dry = false) {
+    Args a;
+    fill_args(a, X, ldx, W, ldw, Y, ldy, M, N, K, plan, ws);
+    const hipError_t e = launch_any<XF32, kStore>(fmt, a, plan, stream, dry);
     if (e != hipSuccess || plan.split == 1 || dry) return e;
     const int blocks = plan.tail_tiles * (plan.bm * plan.bn / 1024);
     return launch_splitk_reduce(plan.split, dim3(blocks), stream, ws, plan.tail_tiles,
                                 plan.dp_tiles, plan.bm, plan.bn, plan.tiles_m, plan.tiles_n, Y,
                                 ldy, M, N);
+}
+
+// The plan's kernel with an epilogue; with a K split the whole tiles finish in
+// the kernel and the split ones in the reduce.
+template <int EPI>
+hipError_t launch_gemm_epi(int fmt, const uint16_t *X, int ldx, const void *W, int64_t ldw,
+                           void *Y, int ldy, int M, int N, int K, const GemmPlan &plan, float *ws,
+                           const EpiSpec &epi, hipStream_t stream) {
+    EpiArgs a;
+    fill_args(a, X, ldx, W, ldw, Y, ldy, M, EPI == kGlu ? 2 * N : N, K, plan, ws);
+    a.bias = epi.bias;
+    a.res = epi.res;
+    a.ldr = epi.ldr;
+    a.act = epi.act;
+    a.res_type = epi.res_type;
+    a.y_type = epi.y_type;
+    const hipError_t e = launch_any<false, EPI>(fmt, a, plan, stream, false);
+    if (e != hipSuccess || plan.split == 1) return e;
+    return launch_splitk_reduce_epi<EPI>(plan, stream, a);
 }
 
 }  // namespace

@@ -246,6 +246,97 @@ int run_xf32(int fmt, const float *X, int ldx, const void *W, int64_t ldw, float
                                       (float *)((char *)ws + xp.x16_bytes), stream));
 }
 
+// How a linear layer runs: f32 activations are rounded to f16 into the front of
+// the workspace, as xf32_plan does; the product's planes follow.
+struct LinearPlan {
+    int ld16;               // row stride of the converted X, 0 when X is f16
+    int64_t x16_bytes;
+    mq::GemmPlan gemm;
+    int64_t ws_bytes;
+};
+
+LinearPlan linear_plan(int fmt, int x_type, int M, int rows, int K, int split_k) {
+    LinearPlan p;
+    p.ld16 = 0;
+    p.x16_bytes = 0;
+    if (x_type == MQ_F32) {
+        p.ld16 = (int)mq_f16cache_ld(K);
+        p.x16_bytes = ((int64_t)M * p.ld16 * 2 + 255) / 256 * 256;
+    }
+    p.gemm = mq::plan_gemm(fmt, M, rows, K, split_k);
+    p.ws_bytes = p.x16_bytes + p.gemm.ws_bytes;
+    return p;
+}
+
+// Sizes, format and split of a linear layer (`rows` rows of weights).
+int check_linear_shape(int fmt, int x_type, int M, int rows, int K, int split_k) {
+    if (fmt != mq::kFmtF16 && !quant_fmt(fmt)) return MQ_ERR_FORMAT;
+    if (!type_ok(x_type)) return MQ_ERR_TYPE;
+    if (int rc = check_dims(M, rows, K)) return rc;
+    if (K % (fmt == mq::kFmtF16 ? 8 : mq::block_elems(fmt))) return MQ_ERR_SHAPE;
+    if (split_k < 0 || split_k > MQ_MAX_SPLIT_K) return MQ_ERR_SPLIT;
+    if (split_k > 1 && (int64_t)M * rows >= ((int64_t)1 << 31)) return MQ_ERR_SPLIT;
+    return MQ_OK;
+}
+
+// Rows of weights of a layer with N output columns; -1 (a bad shape) for an N
+// that has none.
+int weight_rows(int N, bool glu) { return N <= 0 || N > MQ_MAX_DIM ? -1 : glu ? 2 * N : N; }
+
+int64_t linear_workspace(int fmt, int x_type, int M, int N, int K, int split_k, bool glu) {
+    const int rows = weight_rows(N, glu);
+    if (int rc = check_linear_shape(fmt, x_type, M, rows, K, split_k)) return rc;
+    return linear_plan(fmt, x_type, M, rows, K, split_k).ws_bytes;
+}
+
+// Checks and runs a linear layer; ldw in halves for the f16 cache, unused else.
+int run_linear(int fmt, int x_type, const void *X, int ldx, const void *W, int64_t ldw, int y_type,
+               void *Y, int ldy, int M, int N, int K, const mq::EpiSpec &epi, void *ws,
+               size_t ws_bytes, int split_k, hipStream_t stream) {
+    const int rows = weight_rows(N, epi.glu);
+    if (int rc = check_linear_shape(fmt, x_type, M, rows, K, split_k)) return rc;
+    if (!X || !W || !Y) return MQ_ERR_NULL;
+    if (!type_ok(y_type) || (epi.res && !type_ok(epi.res_type))) return MQ_ERR_TYPE;
+    if (epi.act < MQ_ACT_NONE || epi.act > MQ_ACT_GELU_TANH) return MQ_ERR_ACT;
+    if (!(x_type == MQ_F32 ? ld32_ok(ldx, K) : ld_ok(ldx, K)) || ldy < N ||
+        (epi.res && epi.ldr < N))
+        return MQ_ERR_LD;
+    if (fmt == mq::kFmtF16 ? !ld_ok(ldw, K) : false) return MQ_ERR_LD;
+    if (!aligned16(X) || !aligned16(W) || !elem_aligned(Y, y_type) ||
+        !elem_aligned(epi.bias, MQ_F32) || (epi.res && !elem_aligned(epi.res, epi.res_type)))
+        return MQ_ERR_ALIGN;
+    const LinearPlan p = linear_plan(fmt, x_type, M, rows, K, split_k);
+    if (p.ws_bytes > 0 && (!ws || !aligned16(ws) || ws_bytes < (size_t)p.ws_bytes))
+        return MQ_ERR_WORKSPACE;
+    const int64_t wbytes =
+        fmt == mq::kFmtF16 ? ldw * 2 : (int64_t)K / mq::block_elems(fmt) * mq::block_bytes(fmt);
+    auto bytes = [](int type) { return (int64_t)(type == MQ_F32 ? 4 : 2); };
+    const Span y = span(Y, ldy, N, bytes(y_type), M);
+    const Span others[] = {span(X, ldx, K, bytes(x_type), M),
+                           Span{(const char *)W, wbytes, fmt == mq::kFmtF16 ? 2 * (int64_t)K : wbytes, rows},
+                           span(epi.bias, rows, epi.bias ? rows : 0, 4, 1),
+                           span(ws, p.ws_bytes, p.ws_bytes, 1, 1)};
+    for (const Span &o : others)
+        if (o.p && o.row > 0 && overlap(y, o)) return MQ_ERR_OVERLAP;
+    if (epi.res) {
+        const Span r = span(epi.res, epi.ldr, N, bytes(epi.res_type), M);
+        if (overlap(y, r) && !same_span(y, r)) return MQ_ERR_OVERLAP;
+    }
+    const uint16_t *x16 = (const uint16_t *)X;
+    if (p.ld16) {
+        uint16_t *to = (uint16_t *)ws;
+        if (int rc = hip_status(
+                mq::launch_convert_f32_to_f16((const float *)X, ldx, to, p.ld16, M, K, stream)))
+            return rc;
+        x16 = to;
+        ldx = p.ld16;
+    }
+    float *planes = (float *)((char *)ws + p.x16_bytes);
+    return hip_status((epi.glu ? mq::launch_gemm_glu : mq::launch_gemm_linear)(
+        fmt, x16, ldx, W, fmt == mq::kFmtF16 ? ldw : wbytes, Y, ldy, M, N, K, p.gemm, planes, epi,
+        stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -430,6 +521,50 @@ int mq_gemm_mmq(int fmt, const int8_t *Xq, int ldq, const float *ds, const void 
                                      (float *)ws, (hipStream_t)stream));
 }
 
+int64_t mq_linear_workspace_bytes(int fmt, int x_type, int M, int N, int K, int split_k) {
+    return linear_workspace(fmt, x_type, M, N, K, split_k, false);
+}
+
+int64_t mq_glu_workspace_bytes(int fmt, int x_type, int M, int N, int K, int split_k) {
+    return linear_workspace(fmt, x_type, M, N, K, split_k, true);
+}
+
+int mq_linear_f16cache(int x_type, const void *X, int ldx, const uint16_t *W16, int ldw,
+                       const float *bias, int act, int r_type, const void *R, int ldr, int y_type,
+                       void *Y, int ldy, int M, int N, int K, void *ws, size_t ws_bytes,
+                       int split_k, void *stream) {
+    const mq::EpiSpec epi{bias, R, ldr, act, r_type, y_type, false};
+    return run_linear(mq::kFmtF16, x_type, X, ldx, W16, ldw, y_type, Y, ldy, M, N, K, epi, ws,
+                      ws_bytes, split_k, (hipStream_t)stream);
+}
+
+int mq_linear_fused(int x_type, const void *X, int ldx, int fmt, const void *wq,
+                    const float *bias, int act, int r_type, const void *R, int ldr, int y_type,
+                    void *Y, int ldy, int M, int N, int K, void *ws, size_t ws_bytes, int split_k,
+                    void *stream) {
+    if (!quant_fmt(fmt)) return MQ_ERR_FORMAT;
+    const mq::EpiSpec epi{bias, R, ldr, act, r_type, y_type, false};
+    return run_linear(fmt, x_type, X, ldx, wq, 0, y_type, Y, ldy, M, N, K, epi, ws, ws_bytes,
+                      split_k, (hipStream_t)stream);
+}
+
+int mq_glu_f16cache(int x_type, const void *X, int ldx, const uint16_t *W16, int ldw,
+                    const float *bias, int act, int y_type, void *Y, int ldy, int M, int N, int K,
+                    void *ws, size_t ws_bytes, int split_k, void *stream) {
+    const mq::EpiSpec epi{bias, nullptr, 0, act, MQ_F32, y_type, true};
+    return run_linear(mq::kFmtF16, x_type, X, ldx, W16, ldw, y_type, Y, ldy, M, N, K, epi, ws,
+                      ws_bytes, split_k, (hipStream_t)stream);
+}
+
+int mq_glu_fused(int x_type, const void *X, int ldx, int fmt, const void *wq, const float *bias,
+                 int act, int y_type, void *Y, int ldy, int M, int N, int K, void *ws,
+                 size_t ws_bytes, int split_k, void *stream) {
+    if (!quant_fmt(fmt)) return MQ_ERR_FORMAT;
+    const mq::EpiSpec epi{bias, nullptr, 0, act, MQ_F32, y_type, true};
+    return run_linear(fmt, x_type, X, ldx, wq, 0, y_type, Y, ldy, M, N, K, epi, ws, ws_bytes,
+                      split_k, (hipStream_t)stream);
+}
+
 int mq_add_rms_norm(int x_type, const void *X, int ldx, int r_type, const void *R, int ldr,
                     const float *w, float eps, void *H, int ldh, int y_type, void *Y, int ldy,
                     int M, int K, void *stream) {
@@ -525,6 +660,7 @@ const char *mq_strerror(int code) {
     case MQ_ERR_TYPE: return "an element type that is not f32 or f16";
     case MQ_ERR_EPS: return "eps is negative or not finite";
     case MQ_ERR_OVERLAP: return "an output overlaps another buffer of the call";
+    case MQ_ERR_ACT: return "unknown activation";
     default: return "unknown error code";
     }
 }

@@ -20,6 +20,13 @@ constexpr int kTypeF32 = 0;
 constexpr int kTypeF16 = 1;
 constexpr int kTypeI8 = 24;   // Q8_1-style codes (the norm's int8 output)
 
+// Activations of a linear layer's epilogue.
+constexpr int kActNone = 0;
+constexpr int kActRelu = 1;
+constexpr int kActSilu = 2;
+constexpr int kActGelu = 3;       // 0.5·v·(1 + erf(v/√2))
+constexpr int kActGeluTanh = 4;   // 0.5·v·(1 + tanh(√(2/π)·(v + 0.044715·v³)))
+
 inline int block_elems(int fmt) {
     switch (fmt) {
     case kFmtQ4_0: case kFmtQ5_0: case kFmtQ5_1: case kFmtQ8_0: return 32;
@@ -99,6 +106,27 @@ hipError_t launch_mmq(int fmt, const int8_t *Xq, int ldq, const float *ds, const
 // X16[m·ld16 + k] = f16_rne(X[m·ldx + k]) for m < M, k < K (K a multiple of 8).
 hipError_t launch_convert_f32_to_f16(const float *X, int ldx, uint16_t *X16, int ld16, int M,
                                      int K, hipStream_t stream);
+
+// What a linear layer does with the f32 sums before they are written; glu: the
+// weight has 2·N rows (gate, then up) and y = act(gate)·up.
+struct EpiSpec {
+    const float *bias;     // N (glu: 2·N) values, or null
+    const void *res;       // residual rows, or null
+    int64_t ldr;
+    int act;
+    int res_type, y_type;
+    bool glu;
+};
+
+// The tile GEMM with an epilogue: launch_gemm's plan and products, y of type
+// epi.y_type (gemm_linear.hip); for a gated layer the plan is the one of a
+// weight of 2·N rows (gemm_glu.hip).  N: columns of y.
+hipError_t launch_gemm_linear(int fmt, const uint16_t *X, int ldx, const void *W, int64_t ldw,
+                              void *Y, int ldy, int M, int N, int K, const GemmPlan &plan,
+                              float *ws, const EpiSpec &epi, hipStream_t stream);
+hipError_t launch_gemm_glu(int fmt, const uint16_t *X, int ldx, const void *W, int64_t ldw,
+                           void *Y, int ldy, int M, int N, int K, const GemmPlan &plan, float *ws,
+                           const EpiSpec &epi, hipStream_t stream);
 
 // Residual addition and RMS norm (arguments already validated).  r == nullptr:
 // no residual, h unused.  y_type kTypeI8: y holds int8 codes (row stride ldy

@@ -1,5 +1,6 @@
-"""Torch front end of the operators around the quantized products: the residual
-RMS norm that feeds them.
+"""Torch front end of the operators around the quantized products: linear layers
+(the product with bias, activation and residual in its epilogue), gated pairs of
+them, and the residual RMS norm that feeds them.
 
 As in ``api``, every step of the computation runs in the HIP library; these
 functions check dtypes, devices, shapes and strides, allocate the outputs and
@@ -9,11 +10,17 @@ call must be on one GPU; it need not be the current one.
 
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from ._lib import MQ_F16, MQ_F32, check, lib
+from .api import _fmt, _need_quant
 
 _TYPES = {torch.float32: MQ_F32, torch.float16: MQ_F16}
+
+# activations of a linear layer (include/mq.h)
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
 def _type(t: torch.Tensor, name: str) -> int:
@@ -62,6 +69,128 @@ def _call(dev: int, name: str, *args) -> None:
     else:
         with torch.cuda.device(dev):
             check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+
+
+def _act(act) -> int:
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"unknown activation {act!r}: one of {list(ACTIVATIONS)}")
+    return code
+
+
+@functools.lru_cache(maxsize=4096)
+def _layer_workspace(f: int, xt: int, M: int, N: int, K: int, split_k: int, glu: bool) -> int:
+    name = "mq_glu_workspace_bytes" if glu else "mq_linear_workspace_bytes"
+    return check(getattr(lib(), name)(f, xt, M, N, K, split_k), name)
+
+
+def linear_workspace_bytes(fmt, M: int, N: int, K: int, split_k: int = 0, x_f32: bool = False,
+                           glu: bool = False) -> int:
+    """Workspace bytes of a linear layer (fmt 0 / "f16": the f16 cache), or with
+    ``glu`` of a gated one with N output columns; x_f32 for f32 activations."""
+    f = 0 if fmt in (0, None, "f16") else _fmt(fmt)
+    return _layer_workspace(f, MQ_F32 if x_f32 else MQ_F16, int(M), int(N), int(K), int(split_k),
+                            bool(glu))
+
+
+def _layer(x, weight, f, N, K, act, bias, residual, glu, out_dtype, split_k, out, ws):
+    """One linear (or gated) layer: f is 0 for an f16 cache, else the format of
+    the quantized weight."""
+    dev = _device(x, "x")
+    xt = _type(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D with unit column stride")
+    M = x.shape[0]
+    rows = 2 * N if glu else N
+    ldx = _matrix(x, dev, M, K, "x")
+    if f:
+        _need_quant(weight, f, rows, K)
+        if weight.get_device() != dev:
+            raise ValueError("wq must be on the same GPU as the activations")
+        w = (f, weight.data_ptr())
+    else:
+        if weight.dtype != torch.float16:
+            raise ValueError(f"w16 must be torch.float16, got {weight.dtype}")
+        w = (weight.data_ptr(), _matrix(weight, dev, rows, K, "w16"))
+    b = 0 if bias is None else _vector(bias, dev, rows, "bias")
+    if glu:
+        r = ()
+    elif residual is None:
+        r = (MQ_F32, 0, 0)
+    else:
+        ldr = _matrix(residual, dev, M, N, "residual")
+        r = (_type(residual, "residual"), residual.data_ptr(), ldr)
+    if out is None:
+        if out_dtype not in _TYPES:
+            raise ValueError(f"out_dtype must be float32 or float16, got {out_dtype}")
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        ldy = N
+    else:
+        ldy = _matrix(out, dev, M, N, "out")
+    yt = _type(out, "out")
+    if ws is None:
+        nbytes = _layer_workspace(f, xt, M, N, K, split_k, glu)
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous, on the same GPU as the activations")
+    wsp = (0, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    name = ("mq_glu_" if glu else "mq_linear_") + ("fused" if f else "f16cache")
+    _call(dev, name, xt, x.data_ptr(), ldx, *w, b, _act(act), *r, yt, out.data_ptr(), ldy, M, N,
+          K, *wsp, split_k)
+    return out
+
+
+def linear_f16cache(x: torch.Tensor, w16: torch.Tensor, K: int | None = None,
+                    bias: torch.Tensor | None = None, act: str | None = None,
+                    residual: torch.Tensor | None = None,
+                    out_dtype: torch.dtype = torch.float32, split_k: int = 0,
+                    out: torch.Tensor | None = None,
+                    ws: torch.Tensor | None = None) -> torch.Tensor:
+    """y[M, N] = act(x[:, :K] @ w16[:, :K]^T + bias) + residual, in out_dtype
+    (f32 or f16): gemm_f16cache with the layer's epilogue.
+
+    x [M, >=K] f16 (or f32, rounded to f16), w16 the f16 cache [N, ld], bias
+    f32 [N], act one of ACTIVATIONS, residual [M, N] f32 or f16.  out may be
+    the residual itself (the stream is then updated in place)."""
+    K = x.shape[-1] if K is None else K
+    return _layer(x, w16, 0, w16.shape[0], K, act, bias, residual, False, out_dtype, split_k, out,
+                  ws)
+
+
+def linear_fused(x: torch.Tensor, wq: torch.Tensor, fmt, N: int, K: int | None = None,
+                 bias: torch.Tensor | None = None, act: str | None = None,
+                 residual: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                 split_k: int = 0, out: torch.Tensor | None = None,
+                 ws: torch.Tensor | None = None) -> torch.Tensor:
+    """linear_f16cache straight from the quantized weight wq [N rows of K]."""
+    K = x.shape[-1] if K is None else K
+    return _layer(x, wq, _fmt(fmt), N, K, act, bias, residual, False, out_dtype, split_k, out, ws)
+
+
+def glu_f16cache(x: torch.Tensor, w16: torch.Tensor, K: int | None = None,
+                 act: str | None = "silu", bias: torch.Tensor | None = None,
+                 out_dtype: torch.dtype = torch.float16, split_k: int = 0,
+                 out: torch.Tensor | None = None,
+                 ws: torch.Tensor | None = None) -> torch.Tensor:
+    """y[M, N] = act(x @ wg^T + bias_g) * (x @ wu^T + bias_u), in out_dtype (f16
+    or f32), with w16 [2N, ld] the f16 caches of gate and up one after the
+    other and bias f32 [2N] likewise; x as in linear_f16cache."""
+    if w16.shape[0] % 2:
+        raise ValueError(f"w16 must have an even number of rows, got {w16.shape[0]}")
+    K = x.shape[-1] if K is None else K
+    return _layer(x, w16, 0, w16.shape[0] // 2, K, act, bias, None, True, out_dtype, split_k, out,
+                  ws)
+
+
+def glu_fused(x: torch.Tensor, wq: torch.Tensor, fmt, N: int, K: int | None = None,
+              act: str | None = "silu", bias: torch.Tensor | None = None,
+              out_dtype: torch.dtype = torch.float16, split_k: int = 0,
+              out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """glu_f16cache straight from the quantized weights: wq holds the gate's N
+    rows of K, then the up matrix's."""
+    K = x.shape[-1] if K is None else K
+    return _layer(x, wq, _fmt(fmt), N, K, act, bias, None, True, out_dtype, split_k, out, ws)
 
 
 def _norm_inputs(x, weight, residual, residual_out):

@@ -72,3 +72,94 @@ def test_norm_q8_1_refuses(L, bad, code):
 def test_error_texts(L):
     known = {L.mq_strerror(c) for c in range(_lib.MQ_ERR_OVERLAP, 1)}
     assert len(known) == 1 - _lib.MQ_ERR_OVERLAP and b"unknown error code" not in known
+
+
+LIN = dict(xt=F16, X=FAKE, ldx=512, W=W, ldw=512, b=H, act=2, rt=F32, R=R, ldr=96, yt=F32, Y=Y,
+           ldy=96, M=300, N=96, K=512, ws=None, wsb=0, split=1)
+
+
+def _linear(L, fmt=0, **kw):
+    a = {**LIN, **kw}
+    w = (a["W"], a["ldw"]) if fmt == 0 else (fmt, a["W"])
+    f = L.mq_linear_f16cache if fmt == 0 else L.mq_linear_fused
+    return f(a["xt"], a["X"], a["ldx"], *w, a["b"], a["act"], a["rt"], a["R"], a["ldr"], a["yt"],
+             a["Y"], a["ldy"], a["M"], a["N"], a["K"], a["ws"], a["wsb"], a["split"], None)
+
+
+def _glu(L, fmt=0, **kw):
+    a = {**LIN, **kw}
+    w = (a["W"], a["ldw"]) if fmt == 0 else (fmt, a["W"])
+    f = L.mq_glu_f16cache if fmt == 0 else L.mq_glu_fused
+    return f(a["xt"], a["X"], a["ldx"], *w, a["b"], a["act"], a["yt"], a["Y"], a["ldy"], a["M"],
+             a["N"], a["K"], a["ws"], a["wsb"], a["split"], None)
+
+
+LAYER_BAD = [
+    (dict(X=None), _lib.MQ_ERR_NULL), (dict(W=None), _lib.MQ_ERR_NULL),
+    (dict(Y=None), _lib.MQ_ERR_NULL),
+    (dict(xt=2), _lib.MQ_ERR_TYPE), (dict(yt=-1), _lib.MQ_ERR_TYPE),
+    (dict(act=5), _lib.MQ_ERR_ACT), (dict(act=-1), _lib.MQ_ERR_ACT),
+    (dict(M=0), _lib.MQ_ERR_SHAPE), (dict(N=0), _lib.MQ_ERR_SHAPE),
+    (dict(N=-(1 << 31)), _lib.MQ_ERR_SHAPE), (dict(N=(1 << 31) - 1), _lib.MQ_ERR_SHAPE),
+    (dict(K=500), _lib.MQ_ERR_SHAPE), (dict(K=0), _lib.MQ_ERR_SHAPE),
+    (dict(ldx=508), _lib.MQ_ERR_LD), (dict(ldx=504), _lib.MQ_ERR_LD),
+    (dict(xt=F32, ldx=514, ws=D, wsb=1 << 30), _lib.MQ_ERR_LD),
+    (dict(ldy=95), _lib.MQ_ERR_LD),
+    (dict(X=FAKE + 8), _lib.MQ_ERR_ALIGN), (dict(W=W + 2), _lib.MQ_ERR_ALIGN),
+    (dict(Y=Y + 2), _lib.MQ_ERR_ALIGN), (dict(b=H + 2), _lib.MQ_ERR_ALIGN),
+    (dict(split=17), _lib.MQ_ERR_SPLIT), (dict(split=-1), _lib.MQ_ERR_SPLIT),
+    (dict(split=4), _lib.MQ_ERR_WORKSPACE),
+    (dict(split=4, ws=D, wsb=100), _lib.MQ_ERR_WORKSPACE),
+    (dict(split=4, ws=D + 8, wsb=1 << 30), _lib.MQ_ERR_WORKSPACE),
+    (dict(split=4, ws=Y + 64, wsb=1 << 30), _lib.MQ_ERR_OVERLAP),
+    (dict(Y=FAKE, ldx=512, ldy=96), _lib.MQ_ERR_OVERLAP),      # x's place
+    (dict(Y=W), _lib.MQ_ERR_OVERLAP), (dict(Y=H), _lib.MQ_ERR_OVERLAP),
+]
+
+
+@pytest.mark.parametrize("bad,code", LAYER_BAD + [
+    (dict(ldw=520 + 4), _lib.MQ_ERR_LD), (dict(ldw=504), _lib.MQ_ERR_LD)])
+def test_f16cache_layers_refuse(L, bad, code):
+    assert _linear(L, **bad) == code
+    assert _glu(L, **bad) == code
+
+
+@pytest.mark.parametrize("bad,code", LAYER_BAD + [(dict(K=384), _lib.MQ_ERR_SHAPE)])
+@pytest.mark.parametrize("fmt", [12, 14])
+def test_fused_layers_refuse(L, fmt, bad, code):
+    assert _linear(L, fmt, **bad) == code
+    assert _glu(L, fmt, **bad) == code
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(rt=3), _lib.MQ_ERR_TYPE), (dict(ldr=95), _lib.MQ_ERR_LD),
+    (dict(R=R + 2), _lib.MQ_ERR_ALIGN),
+    (dict(R=Y + 4), _lib.MQ_ERR_OVERLAP),               # the stream, shifted
+    (dict(R=Y, rt=F16), _lib.MQ_ERR_OVERLAP),           # in another type
+    (dict(R=Y, ldr=104), _lib.MQ_ERR_OVERLAP),          # at another stride
+])
+def test_residuals_refused(L, bad, code):
+    assert _linear(L, **bad) == code and _linear(L, 12, **bad) == code
+
+
+def test_unknown_formats(L):
+    for fmt in (1, 5, 99, -1):
+        for f in (L.mq_linear_fused, L.mq_glu_fused):
+            n = 19 if f is L.mq_linear_fused else 16
+            assert f(*([F16, FAKE, 512, fmt, W] + [0] * (n - 5) + [None])) == _lib.MQ_ERR_FORMAT
+        assert L.mq_linear_workspace_bytes(fmt, F16, 1, 64, 256, 0) == _lib.MQ_ERR_FORMAT
+    assert L.mq_linear_fused(F16, FAKE, 512, 0, W, None, 0, 0, None, 0, F32, Y, 96, 4, 96, 512,
+                             None, 0, 0, None) == _lib.MQ_ERR_FORMAT
+    assert L.mq_glu_workspace_bytes(12, 9, 1, 64, 256, 0) == _lib.MQ_ERR_TYPE
+    assert L.mq_glu_workspace_bytes(12, F16, 1, (1 << 23) + 1, 256, 0) == _lib.MQ_ERR_SHAPE
+
+
+def test_layer_workspaces(L):
+    """The planes of the matching product, after the converted f32 activations."""
+    for M, N, K in ((2048, 3584, 18944), (300, 96, 512), (2048, 512, 3584)):
+        planes = L.mq_gemm_workspace_bytes(0, M, N, K, 0)
+        assert L.mq_linear_workspace_bytes(0, F16, M, N, K, 0) == planes
+        x16 = (M * (K + (64 if K % 1024 == 0 else 0)) * 2 + 255) // 256 * 256
+        assert L.mq_linear_workspace_bytes(0, F32, M, N, K, 0) == x16 + planes
+        assert L.mq_glu_workspace_bytes(12, F16, M, N, 3584, 0) == \
+            L.mq_gemm_workspace_bytes(12, M, 2 * N, 3584, 0)
