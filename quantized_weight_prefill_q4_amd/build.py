@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libmq.so")
 SOURCES = ("mq_api.hip", "dequant.hip", "gemm.hip", "gemm_xf32.hip", "mmq.hip", "rms_norm.hip",
-           "gemm_linear.hip", "gemm_glu.hip")
+           "gemm_linear.hip", "gemm_glu.hip", "linear_rows.hip")
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 
@@ -41,9 +41,11 @@ CFLAGS = [
 ]
 
 
-# Per-file additions.  mmq.hip: MFMA results in VGPRs, where the VALU that
-# scales each block's integer dot reads them (instead of AGPR copies).
-EXTRA = {"mmq.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# Per-file additions.  MFMA results in VGPRs, where the VALU reads them (instead
+# of AGPR copies): mmq.hip scales each block's integer dot, linear_rows.hip has
+# few accumulators.
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+EXTRA = {"mmq.hip": _VGPR_FORM, "linear_rows.hip": _VGPR_FORM}
 
 
 def _compile(src: str, verbose: bool) -> str:

@@ -117,5 +117,48 @@ __device__ __forceinline__ void store_upto8(void *row, int type, int64_t col, in
         }
 }
 
+// load_upto8 / store_upto8 for groups of four.
+__device__ __forceinline__ void load_upto4(const void *row, int type, int64_t col, int n,
+                                           float (&v)[4]) {
+    if (n >= 4) {
+        if (type == kTypeF32) {
+            const f32x4 a = *reinterpret_cast<const f32x4_a4 *>((const float *)row + col);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        } else {
+            const u32x2 a = *reinterpret_cast<const u32x2_a2 *>((const uint16_t *)row + col);
+            v[0] = f16_bits_to_f32(a.x); v[1] = f16_bits_to_f32(a.x >> 16);
+            v[2] = f16_bits_to_f32(a.y); v[3] = f16_bits_to_f32(a.y >> 16);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = 0.0f;
+        if (j < n)
+            v[j] = type == kTypeF32 ? ((const float *)row)[col + j]
+                                    : f16_bits_to_f32(((const uint16_t *)row)[col + j]);
+    }
+}
+
+__device__ __forceinline__ void store_upto4(void *row, int type, int64_t col, int n,
+                                            const float (&v)[4]) {
+    if (n >= 4) {
+        if (type == kTypeF32)
+            *reinterpret_cast<f32x4_a4 *>((float *)row + col) = f32x4{v[0], v[1], v[2], v[3]};
+        else
+            *reinterpret_cast<u32x2_a2 *>((uint16_t *)row + col) =
+                u32x2{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < n) {
+            if (type == kTypeF32)
+                ((float *)row)[col + j] = v[j];
+            else
+                ((uint16_t *)row)[col + j] = (uint16_t)pack_f16x2(v[j], 0.0f);
+        }
+}
+
 }  // namespace
 }  // namespace mq

@@ -1443,40 +1443,12 @@ __global__ __launch_bounds__(256) void splitk_reduce_epi(EpiArgs a, int bm, int 
     const int n = min(4, F - col);
     float b0[4] = {}, b1[4] = {}, res[4] = {};
     if (a.bias) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < n) {
-                b0[j] = a.bias[col + j];
-                if constexpr (GLU) b1[j] = a.bias[F + col + j];
-            }
+        load_upto4(a.bias, kTypeF32, col, n, b0);
+        if constexpr (GLU) load_upto4(a.bias, kTypeF32, (int64_t)F + col, n, b1);
     }
-    if constexpr (!GLU) {
-        if (a.res) {
-            const int64_t at = (int64_t)row * a.ldr + col;
-            if (a.res_type == kTypeF32) {
-                const float *q = (const float *)a.res + at;
-                if (n == 4) {
-                    const f32x4 t = *(const f32x4_a4 *)q;
-                    res[0] = t.x; res[1] = t.y; res[2] = t.z; res[3] = t.w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j < n) res[j] = q[j];
-                }
-            } else {
-                const uint16_t *q = (const uint16_t *)a.res + at;
-                if (n == 4) {
-                    const u32x2 t = *(const u32x2_a2 *)q;
-                    res[0] = f16_bits_to_f32(t.x); res[1] = f16_bits_to_f32(t.x >> 16);
-                    res[2] = f16_bits_to_f32(t.y); res[3] = f16_bits_to_f32(t.y >> 16);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j < n) res[j] = f16_bits_to_f32(q[j]);
-                }
-            }
-        }
-    }
+    if (!GLU && a.res)
+        load_upto4((const char *)a.res + row * a.ldr * (a.res_type == kTypeF32 ? 4 : 2),
+                   a.res_type, col, n, res);
     f32x4 sum = v[0];
 #pragma unroll
     for (int s = 1; s < S; ++s) sum += v[s];
@@ -1494,26 +1466,8 @@ __global__ __launch_bounds__(256) void splitk_reduce_epi(EpiArgs a, int bm, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] += res[j];
     }
-    const int64_t at = (int64_t)row * a.ldy + col;
-    if (a.y_type == kTypeF32) {
-        float *o = (float *)a.Y + at;
-        if (n == 4) {
-            *(f32x4_a4 *)o = f32x4{y[0], y[1], y[2], y[3]};
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < n) o[j] = y[j];
-        }
-    } else {
-        uint16_t *o = (uint16_t *)a.Y + at;
-        if (n == 4) {
-            *(u32x2_a2 *)o = u32x2{pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3])};
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < n) o[j] = (uint16_t)pack_f16x2(y[j], 0.0f);
-        }
-    }
+    store_upto4((char *)a.Y + (int64_t)row * a.ldy * (a.y_type == kTypeF32 ? 4 : 2), a.y_type, col,
+                n, y);
 }
 
 template <int EPI, int S = 2>

@@ -1,0 +1,576 @@
+// Linear and gated layers for a few activation rows (one generated token, or a
+// handful of sequences decoded together): Y = epilogue(X·Wᵀ) with M <= 16.
+//
+// Mathematics and bound.  Every weight is used M times and read once, so the
+// product is bound by the weight's bytes (0.56 to 2 per weight) and, for the
+// block formats, by the instructions that expand them (about 3 per weight, as
+// in the fused GEMM: the same f16 values feed the matrix cores).  Tiles of
+// 64 × 128 outputs would need a K split with partial planes and a second
+// kernel to fill the chip, and stage X and W in LDS that nothing shares.
+//
+// Layout.  The matrix instruction is v_mfma_f32_16x16x32_f16 with the weight
+// rows as its 16 rows and the activation rows as its 16 columns: lane l holds
+// weight row l % 16 and, with g = l / 16, a quarter of the k range, and feeds
+// its weights straight from the registers that loaded them — no LDS, no
+// barrier in the loop.  Since a sum does not care in which order its k are
+// taken, a lane's quarter is what is contiguous in the block format (64
+// elements: two 32-element blocks, or a quarter of a super-block with one pair
+// of scales), and the activations are loaded for the same k.  A wave takes RT
+// tiles of 16 weight rows (for a gated layer a gate tile and its up tile) on
+// the same activations; the waves of a workgroup take the units of 256 k in
+// turn, and their sums are joined in LDS in a fixed order, so one launch does
+// the whole layer and results are deterministic.  A wave has one unit's raw
+// bytes in registers: as soon as a tile's bytes are unpacked into the form its
+// fragments are made from, the next unit's loads go into the same registers
+// and are in flight while the fragments are expanded and multiplied.
+
+#include "epilogue.h"
+#include "mq_device.h"
+#include "mq_internal.h"
+
+#include <type_traits>
+
+namespace mq {
+namespace {
+
+struct RowsArgs {
+    const void *X;
+    const uint8_t *W;
+    void *Y;
+    const float *bias;
+    const void *res;
+    int64_t ldw;       // bytes per weight row
+    int64_t ldr;
+    int ldx, ldy;
+    int M, N, K;       // N: output columns (a gated layer's weight has 2·N rows)
+    int act, res_type, y_type;
+};
+
+// Eight expanded weights (one MFMA operand) from two dwords of 4..6-bit codes.
+__device__ __forceinline__ half8 frag_fma(uint32_t w0, uint32_t w1, float A, float C) {
+    w0 = opaque(w0);
+    w1 = opaque(w1);
+    auto f = [&](float q) { return __builtin_fmaf(A, q, C); };
+    const u32x4 v = {pack_f16x2(f(ubyte_f32<0>(w0)), f(ubyte_f32<1>(w0))),
+                     pack_f16x2(f(ubyte_f32<2>(w0)), f(ubyte_f32<3>(w0))),
+                     pack_f16x2(f(ubyte_f32<0>(w1)), f(ubyte_f32<1>(w1))),
+                     pack_f16x2(f(ubyte_f32<2>(w1)), f(ubyte_f32<3>(w1)))};
+    return __builtin_bit_cast(half8, v);
+}
+
+__device__ __forceinline__ uint32_t spread4(uint32_t b) {
+    return ((b * 0x00204081u) & 0x01010101u) << 4;
+}
+
+// ---------------------------------------------------------------------------
+// What a lane holds of its weight row for one unit of k.  load(): the raw
+// bytes from row offset `row` (a dword-aligned resource), zeros when the unit
+// is not live; unpack(): the form the fragments are made from; frag<S>(): the
+// eight weights of fragment S, whose k is kofs(g, S) within the unit.
+// ---------------------------------------------------------------------------
+template <int FMT>
+struct RowUnit;
+
+template <>
+struct RowUnit<kFmtF16> {
+    static constexpr int NF = 4, UK = 128;
+    u32x4 v[NF];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t row, int u, int g,
+                                         int K, bool live) {
+#pragma unroll
+        for (int s = 0; s < NF; ++s) {
+            const int k = u * UK + kofs(g, s);
+            v[s] = buf_load16(rs, live && k < K ? row + 2 * k : kOOB);
+        }
+    }
+    struct Unpacked {
+        u32x4 v[NF];
+        template <int S>
+        __device__ __forceinline__ half8 frag() const {
+            return __builtin_bit_cast(half8, v[S]);
+        }
+    };
+    __device__ __forceinline__ Unpacked unpack(int) const {
+        Unpacked p;
+#pragma unroll
+        for (int s = 0; s < NF; ++s) p.v[s] = v[s];
+        return p;
+    }
+    static __device__ __forceinline__ int kofs(int g, int s) { return 32 * s + 8 * g; }
+};
+
+// Q4_K, Q5_K: quarter g of the super-block, sub-blocks 2g (low nibbles) and
+// 2g + 1 (high nibbles).
+template <int FMT>
+struct KUnit {
+    static constexpr int NF = 8, UK = 256;
+    static constexpr bool Q5 = FMT == kFmtQ5_K;
+    static constexpr uint32_t BB = Q5 ? 176 : 144, QS = Q5 ? 48 : 16;
+    u32x4 hdr, q[2], h[Q5 ? 2 : 1];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t row, int u, int g,
+                                         int, bool live) {
+        const uint32_t o = live ? row + (uint32_t)u * BB : kOOB;
+        hdr = buf_load16(rs, o);
+        q[0] = buf_load16(rs, o + QS + 32 * g);
+        q[1] = buf_load16(rs, o + QS + 32 * g + 16);
+        if constexpr (Q5) {
+            h[0] = buf_load16(rs, o + 16);
+            h[1] = buf_load16(rs, o + 32);
+        }
+    }
+    struct Unpacked {
+        float A[2], C[2];
+        u32x4 q[2], h[Q5 ? 2 : 1];
+        template <int S>
+        __device__ __forceinline__ half8 frag() const {
+            constexpr int c = S & 3;             // 8 of the 32 quant bytes
+            constexpr int high = S >= 4;
+            const u32x4 w = q[c >> 1];
+            uint32_t w0 = (c & 1) ? w.z : w.x, w1 = (c & 1) ? w.w : w.y;
+            w0 = (high ? w0 >> 4 : w0) & 0x0F0F0F0Fu;
+            w1 = (high ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
+            if constexpr (Q5) {
+                const u32x4 b = h[c >> 1];
+                const uint32_t b0 = (c & 1) ? b.z : b.x, b1 = (c & 1) ? b.w : b.y;
+                w0 |= ((high ? b0 >> 1 : b0) & 0x01010101u) << 4;
+                w1 |= ((high ? b1 >> 1 : b1) & 0x01010101u) << 4;
+            }
+            return frag_fma(w0, w1, A[high], C[high]);
+        }
+    };
+    __device__ __forceinline__ Unpacked unpack(int g) const {
+        Unpacked p;
+        // sub-blocks 2g, 2g + 1: bytes 2(g & 1) and the next of the scale dwords
+        const uint32_t sh = 16 * (g & 1);
+        const uint32_t lo = hdr.y >> sh, mid = hdr.z >> sh, hi = hdr.w >> sh;
+        const bool first = g < 2;
+        const uint32_t sc0 = first ? lo & 63 : (hi & 15) | ((lo >> 2) & 48);
+        const uint32_t m0 = first ? mid & 63 : ((hi >> 4) & 15) | ((mid >> 2) & 48);
+        const uint32_t sc1 = first ? (lo >> 8) & 63 : ((hi >> 8) & 15) | ((lo >> 10) & 48);
+        const uint32_t m1 = first ? (mid >> 8) & 63 : ((hi >> 12) & 15) | ((mid >> 10) & 48);
+        const float d = f16_bits_to_f32(hdr.x), dmin = f16_bits_to_f32(hdr.x >> 16);
+        p.A[0] = d * (float)sc0;
+        p.C[0] = -(dmin * (float)m0);
+        p.A[1] = d * (float)sc1;
+        p.C[1] = -(dmin * (float)m1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            p.q[i] = q[i];
+            if constexpr (Q5) p.h[i] = h[i] >> (2 * g);   // bit 2g to bit 0 of each byte
+        }
+        return p;
+    }
+    static __device__ __forceinline__ int kofs(int g, int s) { return 64 * g + 8 * s; }
+};
+template <> struct RowUnit<kFmtQ4_K> : KUnit<kFmtQ4_K> {};
+template <> struct RowUnit<kFmtQ5_K> : KUnit<kFmtQ5_K> {};
+
+// Q6_K: half h = g / 2 of the super-block, elements 16p .. 16p + 15 (p = g % 2)
+// of its four 32-element groups.  Blocks are 2-byte aligned: fields are read
+// as the aligned dwords that cover them.
+template <>
+struct RowUnit<kFmtQ6_K> {
+    static constexpr int NF = 8, UK = 256;
+    uint32_t a[5], b[5], hh[5], sc[3], dd, sh;
+    static __device__ __forceinline__ void load5(__amdgpu_buffer_rsrc_t rs, uint32_t o,
+                                                 uint32_t (&w)[5]) {
+        const u32x4 v = buf_load16(rs, o);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        w[4] = buf_load4(rs, o + 16);
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t row, int u, int g,
+                                         int, bool live) {
+        const uint32_t o = row + (uint32_t)u * 210u, al = live ? o & ~3u : kOOB;
+        const uint32_t h = g >> 1, p = g & 1;
+        sh = o & 2;
+        load5(rs, al + 64 * h + 16 * p, a);
+        load5(rs, al + 64 * h + 32 + 16 * p, b);
+        load5(rs, al + 128 + 32 * h + 16 * p, hh);
+        const uint32_t s = al + 192 + 8 * h;
+        sc[0] = buf_load4(rs, s);
+        sc[1] = buf_load4(rs, s + 4);
+        sc[2] = buf_load4(rs, s + 8);
+        dd = buf_load4(rs, al + 208);
+    }
+    static __device__ __forceinline__ u32x4 realign(const uint32_t (&w)[5], uint32_t s) {
+        return u32x4{__builtin_amdgcn_alignbyte(w[1], w[0], s),
+                     __builtin_amdgcn_alignbyte(w[2], w[1], s),
+                     __builtin_amdgcn_alignbyte(w[3], w[2], s),
+                     __builtin_amdgcn_alignbyte(w[4], w[3], s)};
+    }
+    struct Unpacked {
+        u32x4 a, b, h;
+        float A[4];
+        template <int S>
+        __device__ __forceinline__ half8 frag() const {
+            constexpr int grp = S >> 1, c = S & 1;
+            const u32x4 l = (grp & 1) ? b : a;
+            uint32_t w0 = c ? l.z : l.x, w1 = c ? l.w : l.y;
+            const uint32_t h0 = c ? h.z : h.x, h1 = c ? h.w : h.y;
+            w0 = (grp >= 2 ? w0 >> 4 : w0) & 0x0F0F0F0Fu;
+            w1 = (grp >= 2 ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
+            w0 |= ((h0 >> (2 * grp)) & 0x03030303u) << 4;
+            w1 |= ((h1 >> (2 * grp)) & 0x03030303u) << 4;
+            // (d·s)·(q − 32): ds·q and 32·ds are exact, so one fma is
+            return frag_fma(w0, w1, A[grp], -32.0f * A[grp]);
+        }
+    };
+    __device__ __forceinline__ Unpacked unpack(int g) const {
+        Unpacked p;
+        p.a = realign(a, sh);
+        p.b = realign(b, sh);
+        p.h = realign(hh, sh);
+        // the half's eight scales; this lane's are bytes p, p + 2, p + 4, p + 6
+        uint32_t s0 = __builtin_amdgcn_alignbyte(sc[1], sc[0], sh);
+        uint32_t s1 = __builtin_amdgcn_alignbyte(sc[2], sc[1], sh);
+        s0 >>= 8 * (g & 1);
+        s1 >>= 8 * (g & 1);
+        const float d = f16_bits_to_f32(dd >> (8 * sh));
+        p.A[0] = d * sbyte_f32<0>(s0);
+        p.A[1] = d * sbyte_f32<2>(s0);
+        p.A[2] = d * sbyte_f32<0>(s1);
+        p.A[3] = d * sbyte_f32<2>(s1);
+        return p;
+    }
+    static __device__ __forceinline__ int kofs(int g, int s) {
+        return 128 * (g >> 1) + 32 * (s >> 1) + 16 * (g & 1) + 8 * (s & 1);
+    }
+};
+
+// The 32-element formats: blocks 2g and 2g + 1 of the unit's eight, read as
+// the aligned dwords that cover them.  A block past the row's last has its
+// factors cleared (its bytes are the next row's).
+template <int FMT>
+struct BUnit {
+    static constexpr int NF = 8, UK = 256;
+    static constexpr int BB = FMT == kFmtQ4_0 ? 18 : FMT == kFmtQ5_0 ? 22 : FMT == kFmtQ5_1 ? 24 : 34;
+    // dwords that cover two blocks at a 2-byte offset (Q5_1 blocks are aligned)
+    static constexpr int NW = FMT == kFmtQ5_1 ? 12 : (2 * BB + 2 + 3) / 4;
+    uint32_t w[NW], sh;
+    int exist;                           // blocks of this lane that exist
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t row, int u, int g,
+                                         int K, bool live) {
+        const int blk = 8 * u + 2 * g;
+        exist = live ? (K >> 5) - blk : 0;
+        const uint32_t o = row + (uint32_t)blk * BB;
+        sh = o & 2;
+        const uint32_t al = exist > 0 ? o & ~3u : kOOB;
+#pragma unroll
+        for (int i = 0; i + 4 <= NW; i += 4) {
+            const u32x4 v = buf_load16(rs, al + 4 * i);
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = NW / 4 * 4; i < NW; ++i) w[i] = buf_load4(rs, al + 4 * i);
+    }
+    struct Unpacked {
+        static constexpr int NC = 2 * BB / 4;
+        uint32_t c[NC];                  // the two blocks from byte 0
+        float A[2], C[2];
+        // the dword at even byte offset T of the two blocks
+        template <int TO>
+        __device__ __forceinline__ uint32_t dw() const {
+            if constexpr (TO % 4 == 0)
+                return c[TO / 4];
+            else
+                return __builtin_amdgcn_alignbyte(c[TO / 4 + 1], c[TO / 4], 2);
+        }
+        template <int S>
+        __device__ __forceinline__ half8 frag() const {
+            constexpr int b = S >> 2, ch = S & 3, base = b * BB;   // block, 8-element chunk
+            if constexpr (FMT == kFmtQ8_0) {
+                const uint32_t w0 = dw<base + 2 + 8 * ch>(), w1 = dw<base + 6 + 8 * ch>();
+                const float d = A[b];
+                const u32x4 v = {pack_f16x2(d * sbyte_f32<0>(w0), d * sbyte_f32<1>(w0)),
+                                 pack_f16x2(d * sbyte_f32<2>(w0), d * sbyte_f32<3>(w0)),
+                                 pack_f16x2(d * sbyte_f32<0>(w1), d * sbyte_f32<1>(w1)),
+                                 pack_f16x2(d * sbyte_f32<2>(w1), d * sbyte_f32<3>(w1))};
+                return __builtin_bit_cast(half8, v);
+            } else {
+                constexpr int QS = FMT == kFmtQ4_0 ? 2 : FMT == kFmtQ5_0 ? 6 : 8;
+                uint32_t w0 = dw<base + QS + 8 * (ch & 1)>(), w1 = dw<base + QS + 4 + 8 * (ch & 1)>();
+                w0 = (ch >= 2 ? w0 >> 4 : w0) & 0x0F0F0F0Fu;
+                w1 = (ch >= 2 ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
+                if constexpr (FMT != kFmtQ4_0) {
+                    constexpr int QH = FMT == kFmtQ5_0 ? 2 : 4;
+                    const uint32_t hb = dw<base + QH>() >> (8 * ch);
+                    w0 |= spread4(hb & 15);
+                    w1 |= spread4((hb >> 4) & 15);
+                }
+                return frag_fma(w0, w1, A[b], C[b]);
+            }
+        }
+    };
+    __device__ __forceinline__ Unpacked unpack(int) const {
+        Unpacked p;
+#pragma unroll
+        for (int i = 0; i < Unpacked::NC; ++i) {
+            if constexpr (FMT == kFmtQ5_1)
+                p.c[i] = w[i];
+            else
+                p.c[i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], sh);
+        }
+        const uint32_t h0 = p.c[0], h1 = BB % 4 ? p.c[BB / 4] >> 16 : p.c[BB / 4];
+        const float d0 = f16_bits_to_f32(h0), d1 = f16_bits_to_f32(h1);
+        p.A[0] = exist > 0 ? d0 : 0.0f;
+        p.A[1] = exist > 1 ? d1 : 0.0f;
+        if constexpr (FMT == kFmtQ5_1) {
+            const float m0 = f16_bits_to_f32(h0 >> 16), m1 = f16_bits_to_f32(h1 >> 16);
+            p.C[0] = exist > 0 ? m0 : 0.0f;
+            p.C[1] = exist > 1 ? m1 : 0.0f;
+        } else if constexpr (FMT != kFmtQ8_0) {
+            p.C[0] = (FMT == kFmtQ4_0 ? -8.0f : -16.0f) * p.A[0];
+            p.C[1] = (FMT == kFmtQ4_0 ? -8.0f : -16.0f) * p.A[1];
+        }
+        return p;
+    }
+    static __device__ __forceinline__ int kofs(int g, int s) { return 64 * g + 8 * s; }
+};
+template <> struct RowUnit<kFmtQ4_0> : BUnit<kFmtQ4_0> {};
+template <> struct RowUnit<kFmtQ5_0> : BUnit<kFmtQ5_0> {};
+template <> struct RowUnit<kFmtQ5_1> : BUnit<kFmtQ5_1> {};
+template <> struct RowUnit<kFmtQ8_0> : BUnit<kFmtQ8_0> {};
+
+// A unit's activations: MR rows of UK elements, loaded in whole row segments
+// (64 lanes cover RPI rows of UK / 8 chunks of 8 elements) one unit ahead,
+// rounded to f16 when they are f32, and handed through a strip of LDS that
+// belongs to the wave alone, so without a barrier.  Fragment loads straight
+// from global memory touch a cache line per lane instead (M = 16, gated
+// 14336 x 4096 Q4_K: 46 us).  Chunk c of row r is stored at c ^ (r mod 16):
+// the 16 rows that a ds_read_b128 serves together then lie in distinct banks.
+template <class U, int MR, bool XF32>
+struct XUnit {
+    static constexpr int CH = U::UK / 8;          // chunks per row: 32 or 16
+    static constexpr int RPI = 64 / CH;           // rows per load
+    static constexpr int NX = MR / RPI;
+    static_assert(NX >= 1 && NX * RPI == MR, "whole loads");
+    u32x4 v[NX][XF32 ? 2 : 1];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t ldb, int u, int lane,
+                                         int M, int K, bool live) {
+        const int c = lane & (CH - 1), r0 = lane / CH, k = u * U::UK + 8 * c;
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int r = r0 + RPI * i;
+            const uint32_t o = live && k < K && r < M ? (uint32_t)r * ldb + (XF32 ? 4 : 2) * k : kOOB;
+            v[i][0] = buf_load16(rs, o);
+            if constexpr (XF32) v[i][1] = buf_load16(rs, o + 16);
+        }
+    }
+    __device__ __forceinline__ void store(u32x4 *lds, int lane) const {
+        const int c = lane & (CH - 1), r0 = lane / CH;
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int r = r0 + RPI * i;
+            u32x4 h = v[i][0];
+            if constexpr (XF32) {
+                auto f = [](uint32_t w) { return __builtin_bit_cast(float, w); };
+                const u32x4 p = v[i][0], q = v[i][1];
+                h = u32x4{pack_f16x2(f(p.x), f(p.y)), pack_f16x2(f(p.z), f(p.w)),
+                          pack_f16x2(f(q.x), f(q.y)), pack_f16x2(f(q.z), f(q.w))};
+            }
+            lds[r * CH + (c ^ (r & 15))] = h;
+        }
+    }
+    // Fragment s of lane (row, g).  Columns of the product past M are never
+    // written out, so rows past MR may read any row's chunk.
+    static __device__ __forceinline__ half8 frag(const u32x4 *lds, int row, int g, int s) {
+        const int r = row & (MR - 1), c = U::kofs(g, s) >> 3;
+        return __builtin_bit_cast(half8, lds[r * CH + (c ^ (r & 15))]);
+    }
+};
+
+template <int I, int N, class F>
+__device__ __forceinline__ void for_const(F &&f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        for_const<I + 1, N>(f);
+    }
+}
+
+// The LDS strip of a wave: its activations, then its sums.
+template <class Unit, int RT, int MR>
+constexpr int strip_chunks() {
+    return MR * Unit::UK / 8 > RT * 64 ? MR * Unit::UK / 8 : RT * 64;
+}
+
+// RT tiles of 16 weight rows per workgroup of blockDim.x / 64 waves, at least
+// RT (gated: a gate tile and its up tile, RT = 2); MR: activation rows held.
+// Registers are capped so that 4 waves share a SIMD (with half of them the
+// loads in flight do not cover the memory's latency), 3 where the 16 rows'
+// activations take 32 or 64 of them.
+template <int MR>
+constexpr int kMaxWaves = MR > 4 ? 8 : 16;
+template <int FMT, int RT, bool GLU, bool XF32, int MR>
+__global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_rows_kernel(RowsArgs a) {
+    static_assert(!GLU || RT == 2, "a gate tile and an up tile");
+    using Unit = RowUnit<FMT>;
+    using XU = XUnit<Unit, MR, XF32>;
+    constexpr int NF = Unit::NF, SC = strip_chunks<Unit, RT, MR>();
+    extern __shared__ u32x4 strips[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int NW = (int)blockDim.x >> 6;
+    const int r16 = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * (GLU ? 16 : 16 * RT);   // first output column
+
+    // what the epilogue needs, requested first: thread (tile t, lane) finishes
+    // row r16 of y, columns n0 + 16t + 4g .. + 3
+    constexpr int OT = GLU ? 1 : RT;
+    const int col = n0 + 16 * wave + 4 * g;
+    const int n = wave < OT && r16 < a.M ? min(4, a.N - col) : 0;
+    float b0[4] = {}, b1[4] = {}, res[4] = {};
+    if (n > 0) {
+        if (a.bias) {
+            load_upto4(a.bias, kTypeF32, col, n, b0);
+            if constexpr (GLU) load_upto4(a.bias, kTypeF32, (int64_t)a.N + col, n, b1);
+        }
+        if (!GLU && a.res)
+            load_upto4((const char *)a.res + r16 * a.ldr * (a.res_type == kTypeF32 ? 4 : 2),
+                       a.res_type, col, n, res);
+    }
+
+    __amdgpu_buffer_rsrc_t rsw[RT];
+    uint32_t wrow[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int first = n0 + (GLU ? 0 : 16 * t);
+        const int valid = min(16, a.N - first);
+        const int64_t start = ((int64_t)first + (GLU && t ? a.N : 0)) * a.ldw;
+        const uint32_t lead = FMT == kFmtF16 ? 0 : (uint32_t)(((uintptr_t)a.W + start) & 15);
+        const int64_t row = FMT == kFmtF16 ? 2 * (int64_t)a.K : a.ldw;
+        // a tile past N reads nothing
+        const int64_t bytes = valid > 0 ? (lead + (valid - 1) * a.ldw + row + 3) & ~(int64_t)3 : 0;
+        rsw[t] = make_rsrc(valid > 0 ? a.W + start - lead : a.W, (uint32_t)bytes);
+        wrow[t] = lead + (uint32_t)(r16 * a.ldw);
+    }
+    constexpr int XE = XF32 ? 4 : 2;
+    const __amdgpu_buffer_rsrc_t rsx =
+        make_rsrc(a.X, (uint32_t)(((int64_t)(a.M - 1) * a.ldx + a.K) * XE));
+    const uint32_t ldb = (uint32_t)a.ldx * XE;
+
+    const int units = (a.K + Unit::UK - 1) / Unit::UK;
+    f32x4 acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = f32x4{};
+    Unit w[RT];
+    XU x;
+    u32x4 *const xl = strips + wave * SC;
+    // Look-aheads past the last unit load zeros: a branch around the loads
+    // would make the compiler wait for all of them at its join.
+    auto load_w = [&](int t, int u) { w[t].load(rsw[t], wrow[t], u, g, a.K, u < units); };
+    int u = wave;
+    x.load(rsx, ldb, u, lane, a.M, a.K, u < units);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) load_w(t, u);
+    for (; u < units; u += NW) {
+        // the previous unit's reads of the strip come before in the wave's LDS
+        // order; only the compiler must keep both
+        asm volatile("" ::: "memory");
+        x.store(xl, lane);
+        asm volatile("" ::: "memory");
+        x.load(rsx, ldb, u + NW, lane, a.M, a.K, u + NW < units);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const auto p = w[t].unpack(g);
+            load_w(t, u + NW);
+            for_const<0, NF>([&](auto f) {
+                constexpr int S = decltype(f)::value;
+                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    p.template frag<S>(), XU::frag(xl, r16, g, S), acc[t], 0, 0, 0);
+            });
+        }
+    }
+
+    asm volatile("" ::: "memory");
+    f32x4 *const sums = reinterpret_cast<f32x4 *>(strips);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) sums[wave * SC + t * 64 + lane] = acc[t];
+    __syncthreads();
+    if (n <= 0) return;
+    const int ot = GLU ? 0 : wave;
+    f32x4 s = sums[ot * 64 + lane];
+    for (int i = 1; i < NW; ++i) s += sums[i * SC + ot * 64 + lane];
+    float y[4] = {s.x + b0[0], s.y + b0[1], s.z + b0[2], s.w + b0[3]};
+    apply_act(a.act, y);
+    if constexpr (GLU) {
+        f32x4 v = sums[64 + lane];
+        for (int i = 1; i < NW; ++i) v += sums[i * SC + 64 + lane];
+        y[0] *= v.x + b1[0];
+        y[1] *= v.y + b1[1];
+        y[2] *= v.z + b1[2];
+        y[3] *= v.w + b1[3];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] += res[j];
+    }
+    store_upto4((char *)a.Y + (int64_t)r16 * a.ldy * (a.y_type == kTypeF32 ? 4 : 2), a.y_type, col,
+                n, y);
+}
+
+template <int FMT, int RT, bool GLU, bool XF32, int MR>
+hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
+    using Unit = RowUnit<FMT>;
+    const int cols = GLU ? 16 : 16 * RT;
+    const int tiles = (a.N + cols - 1) / cols;
+    const int units = (a.K + Unit::UK - 1) / Unit::UK;
+    int nw = MR <= 4 && tiles * 16 <= 4096 ? 16 : tiles * 8 <= 4096 ? 8 : 4;
+    while (nw > 4 && nw / 2 >= units) nw /= 2;
+    const size_t lds = nw * (size_t)(strip_chunks<Unit, RT, MR>()) * 16;
+    hipLaunchKernelGGL((linear_rows_kernel<FMT, RT, GLU, XF32, MR>), dim3(tiles), dim3(64 * nw),
+                       lds, stream, a);
+    return hipGetLastError();
+}
+
+template <int FMT, bool XF32, int MR>
+hipError_t launch_rows_fmt(const RowsArgs &a, bool glu, hipStream_t stream) {
+    if (glu) return launch_rows<FMT, 2, true, XF32, MR>(a, stream);
+    if constexpr (MR > 4) {
+        if (a.N > 16 * 512) return launch_rows<FMT, 2, false, XF32, MR>(a, stream);
+    }
+    return launch_rows<FMT, 1, false, XF32, MR>(a, stream);
+}
+
+template <bool XF32, int MR>
+hipError_t launch_rows_any(int fmt, const RowsArgs &a, bool glu, hipStream_t stream) {
+    switch (fmt) {
+    case kFmtF16: return launch_rows_fmt<kFmtF16, XF32, MR>(a, glu, stream);
+    case kFmtQ4_0: return launch_rows_fmt<kFmtQ4_0, XF32, MR>(a, glu, stream);
+    case kFmtQ5_0: return launch_rows_fmt<kFmtQ5_0, XF32, MR>(a, glu, stream);
+    case kFmtQ5_1: return launch_rows_fmt<kFmtQ5_1, XF32, MR>(a, glu, stream);
+    case kFmtQ8_0: return launch_rows_fmt<kFmtQ8_0, XF32, MR>(a, glu, stream);
+    case kFmtQ4_K: return launch_rows_fmt<kFmtQ4_K, XF32, MR>(a, glu, stream);
+    case kFmtQ5_K: return launch_rows_fmt<kFmtQ5_K, XF32, MR>(a, glu, stream);
+    case kFmtQ6_K: return launch_rows_fmt<kFmtQ6_K, XF32, MR>(a, glu, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_linear_rows(int fmt, bool x_f32, const void *X, int ldx, const void *W,
+                              int64_t ldw, void *Y, int ldy, int M, int N, int K,
+                              const EpiSpec &epi, hipStream_t stream) {
+    RowsArgs a;
+    a.X = X;
+    a.W = (const uint8_t *)W;
+    a.Y = Y;
+    a.bias = epi.bias;
+    a.res = epi.res;
+    a.ldw = fmt == kFmtF16 ? 2 * ldw : ldw;
+    a.ldr = epi.ldr;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.act = epi.act;
+    a.res_type = epi.res_type;
+    a.y_type = epi.y_type;
+    if (M <= 4)
+        return x_f32 ? launch_rows_any<true, 4>(fmt, a, epi.glu, stream)
+                     : launch_rows_any<false, 4>(fmt, a, epi.glu, stream);
+    return x_f32 ? launch_rows_any<true, 16>(fmt, a, epi.glu, stream)
+                 : launch_rows_any<false, 16>(fmt, a, epi.glu, stream);
+}
+
+}  // namespace mq

@@ -246,9 +246,12 @@ int run_xf32(int fmt, const float *X, int ldx, const void *W, int64_t ldw, float
                                       (float *)((char *)ws + xp.x16_bytes), stream));
 }
 
-// How a linear layer runs: f32 activations are rounded to f16 into the front of
-// the workspace, as xf32_plan does; the product's planes follow.
+// How a linear layer runs.  Few rows with the split left to the library: one
+// kernel that needs no workspace.  Else the tile GEMM: f32 activations are
+// rounded to f16 into the front of the workspace, as xf32_plan does; the
+// product's planes follow.
 struct LinearPlan {
+    bool rows;              // the few-row kernel
     int ld16;               // row stride of the converted X, 0 when X is f16
     int64_t x16_bytes;
     mq::GemmPlan gemm;
@@ -257,8 +260,11 @@ struct LinearPlan {
 
 LinearPlan linear_plan(int fmt, int x_type, int M, int rows, int K, int split_k) {
     LinearPlan p;
+    p.rows = M <= mq::kRowsMaxM && split_k == 0;
     p.ld16 = 0;
     p.x16_bytes = 0;
+    p.ws_bytes = 0;
+    if (p.rows) return p;
     if (x_type == MQ_F32) {
         p.ld16 = (int)mq_f16cache_ld(K);
         p.x16_bytes = ((int64_t)M * p.ld16 * 2 + 255) / 256 * 256;
@@ -322,6 +328,10 @@ int run_linear(int fmt, int x_type, const void *X, int ldx, const void *W, int64
         const Span r = span(epi.res, epi.ldr, N, bytes(epi.res_type), M);
         if (overlap(y, r) && !same_span(y, r)) return MQ_ERR_OVERLAP;
     }
+    if (p.rows)
+        return hip_status(mq::launch_linear_rows(fmt, x_type == MQ_F32, X, ldx, W,
+                                                 fmt == mq::kFmtF16 ? ldw : wbytes, Y, ldy, M, N,
+                                                 K, epi, stream));
     const uint16_t *x16 = (const uint16_t *)X;
     if (p.ld16) {
         uint16_t *to = (uint16_t *)ws;

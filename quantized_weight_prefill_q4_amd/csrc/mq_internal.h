@@ -128,6 +128,13 @@ hipError_t launch_gemm_glu(int fmt, const uint16_t *X, int ldx, const void *W, i
                            void *Y, int ldy, int M, int N, int K, const GemmPlan &plan, float *ws,
                            const EpiSpec &epi, hipStream_t stream);
 
+// The same for at most kRowsMaxM activation rows, f32 or f16 (linear_rows.hip):
+// one kernel, no workspace.
+constexpr int kRowsMaxM = 16;
+hipError_t launch_linear_rows(int fmt, bool x_f32, const void *X, int ldx, const void *W,
+                              int64_t ldw, void *Y, int ldy, int M, int N, int K,
+                              const EpiSpec &epi, hipStream_t stream);
+
 // Residual addition and RMS norm (arguments already validated).  r == nullptr:
 // no residual, h unused.  y_type kTypeI8: y holds int8 codes (row stride ldy
 // bytes) and ds their (d, s) pairs.

@@ -185,6 +185,19 @@ def test_glu_shapes(fmt, shape):
               yt=("f32", "f16")[(i // 2) % 2], seed=i)
 
 
+@pytest.mark.parametrize("fmt", [0, synth.Q4_0, synth.Q5_0, synth.Q5_1, synth.Q8_0])
+@pytest.mark.parametrize("K", [32, 64, 96, 160, 224, 288, 1056, 2016])
+def test_part_units(fmt, K):
+    """Rows that end inside a unit of 256 and inside a lane's pair of blocks;
+    the last weight row's end is the buffer's."""
+    for M in (1, 4, 5, 16):
+        check_linear(fmt, M, 47, K, act="silu", rt="f32", yt="f32", seed=K)
+        check_glu(fmt, M, 31, K, yt="f32", seed=K)
+    if fmt == 0:
+        check_linear(fmt, 3, 47, K - 24, yt="f32", seed=K)      # 8 halves
+        check_linear(fmt, 9, 33, K + 8, xt="f32", yt="f32", seed=K)
+
+
 @pytest.mark.parametrize("fmt", [0] + FMTS)
 def test_wide_outputs(fmt):
     """256 x 256 tiles, the last ones ragged in rows and columns."""
