@@ -46,16 +46,36 @@ struct RowsArgs {
     int act, res_type, y_type;
 };
 
-// Eight expanded weights (one MFMA operand) from two dwords of 4..6-bit codes.
-__device__ __forceinline__ half8 frag_fma(uint32_t w0, uint32_t w1, float A, float C) {
-    w0 = opaque(w0);
-    w1 = opaque(w1);
-    auto f = [&](float q) { return __builtin_fmaf(A, q, C); };
-    const u32x4 v = {pack_f16x2(f(ubyte_f32<0>(w0)), f(ubyte_f32<1>(w0))),
-                     pack_f16x2(f(ubyte_f32<2>(w0)), f(ubyte_f32<3>(w0))),
-                     pack_f16x2(f(ubyte_f32<0>(w1)), f(ubyte_f32<1>(w1))),
-                     pack_f16x2(f(ubyte_f32<2>(w1)), f(ubyte_f32<3>(w1)))};
+// Eight expanded weights (one MFMA operand), fl32(A·q + C) rounded to f16, from
+// four dwords of two codes each: e0, e1 hold elements 0 and 2, 1 and 3 in their
+// 16-bit halves, e2, e3 elements 4 and 6, 5 and 7.  A code q in the low bits of
+// a half is the f16 subnormal q·2^-24, which v_fma_mix_f32 widens while it
+// multiplies: with A scaled by 2^24 (exact) the fma's one rounding is the
+// decode's, and no separate integer conversion is spent (2.1 instructions per
+// Q4_K weight instead of 2.9).  Codes 4 bits up are scaled by 2^20 instead.
+constexpr float kCode = 16777216.0f;        // 2^24
+constexpr float kCodeHigh = 1048576.0f;     // 2^20
+__device__ __forceinline__ half8 frag_codes(uint32_t e0, uint32_t e1, uint32_t e2, uint32_t e3,
+                                            float A, float C) {
+    auto lo = [&](uint32_t e) { return __builtin_fmaf(A, f16_bits_to_f32(e), C); };
+    auto hi = [&](uint32_t e) { return __builtin_fmaf(A, f16_bits_to_f32(e >> 16), C); };
+    const u32x4 v = {pack_f16x2(lo(e0), lo(e1)), pack_f16x2(hi(e0), hi(e1)),
+                     pack_f16x2(lo(e2), lo(e3)), pack_f16x2(hi(e2), hi(e3))};
     return __builtin_bit_cast(half8, v);
+}
+
+// The same from two dwords of byte codes (at most 8 bits each).
+__device__ __forceinline__ half8 frag_bytes(uint32_t w0, uint32_t w1, float A, float C) {
+    constexpr uint32_t B = 0x00FF00FFu;
+    return frag_codes(w0 & B, (w0 >> 8) & B, w1 & B, (w1 >> 8) & B, A, C);
+}
+
+// The same from the low (HIGH = 0) or high nibbles of two dwords; A scaled by
+// kCode or kCodeHigh accordingly.
+template <int HIGH>
+__device__ __forceinline__ half8 frag_nibbles(uint32_t w0, uint32_t w1, float A, float C) {
+    constexpr uint32_t L = HIGH ? 0x00F000F0u : 0x000F000Fu;
+    return frag_codes(w0 & L, (w0 >> 8) & L, w1 & L, (w1 >> 8) & L, A, C);
 }
 
 __device__ __forceinline__ uint32_t spread4(uint32_t b) {
@@ -63,24 +83,32 @@ __device__ __forceinline__ uint32_t spread4(uint32_t b) {
 }
 
 // ---------------------------------------------------------------------------
-// What a lane holds of its weight row for one unit of k.  load(): the raw
-// bytes from row offset `row` (a dword-aligned resource), zeros when the unit
-// is not live; unpack(): the form the fragments are made from; frag<S>(): the
+// One unit of k of a tile of 16 weight rows, as a wave holds it.  load(): the
+// raw bytes into registers, zeros when the unit is not live; unpack(): the
+// form that lane (row r, quarter g) makes its fragments from; frag<S>(): the
 // eight weights of fragment S, whose k is kofs(g, S) within the unit.
 // ---------------------------------------------------------------------------
 template <int FMT>
 struct RowUnit;
 
+// f16: the fragments are loaded as they are used, 64 contiguous bytes of each
+// row per load.
 template <>
 struct RowUnit<kFmtF16> {
-    static constexpr int NF = 4, UK = 128;
+    static constexpr int NF = 4, UK = 128, STRIP = 0;
     u32x4 v[NF];
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t row, int u, int g,
-                                         int K, bool live) {
+    struct Place {
+        uint32_t row;
+        __device__ __forceinline__ void init(int lane, int64_t ldw) {
+            row = (uint32_t)((lane & 15) * ldw);
+        }
+    };
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t, const Place &at, int u,
+                                         int lane, int K, bool live) {
 #pragma unroll
         for (int s = 0; s < NF; ++s) {
-            const int k = u * UK + kofs(g, s);
-            v[s] = buf_load16(rs, live && k < K ? row + 2 * k : kOOB);
+            const int k = u * UK + kofs(lane >> 4, s);
+            v[s] = buf_load16(rs, live && k < K ? at.row + 2 * k : kOOB);
         }
     }
     struct Unpacked {
@@ -90,7 +118,7 @@ struct RowUnit<kFmtF16> {
             return __builtin_bit_cast(half8, v[S]);
         }
     };
-    __device__ __forceinline__ Unpacked unpack(int) const {
+    __device__ __forceinline__ Unpacked unpack(u32x4 *, uint32_t, int64_t, int, int, int) const {
         Unpacked p;
 #pragma unroll
         for (int s = 0; s < NF; ++s) p.v[s] = v[s];
@@ -99,25 +127,65 @@ struct RowUnit<kFmtF16> {
     static __device__ __forceinline__ int kofs(int g, int s) { return 32 * s + 8 * g; }
 };
 
+// The block formats' bytes: UB bytes per row and unit, loaded as the WB / 16
+// chunks of 16 bytes that cover them from the 16-byte boundary at or below
+// their start (the 18, 22, 34 and 210-byte blocks are only 2-byte aligned),
+// chunk by chunk of row after row over the 64 lanes, and handed to the lanes
+// that expand them through a strip of LDS of the wave's own.  Loading each
+// lane's bytes directly touches every cache line several times and is bound by
+// the first-level cache (gated 14336 x 4096 at M = 1: Q8_0 36 us, Q6_K 36 us);
+// chunks at dword alignment cost the address unit twice the cycles.
+template <int UB_, int WB_>
+struct Staged {
+    static constexpr int UB = UB_, WB = WB_, CPR = WB / 16, NCH = 16 * CPR, NJ = (NCH + 63) / 64;
+    static constexpr int STRIP = NJ * 64;   // chunks of LDS
+    static_assert(WB % 16 == 0 && WB >= UB, "whole chunks");
+    // The chunks' alignment: where UB bytes at any even start fit, the 16-byte
+    // boundary below it; Q4_K's and Q5_K's rows start on one anyway, and Q5_1's
+    // on 8 bytes (a 13th chunk for their other half costs a fourth load:
+    // gated 14336 x 4096 at M = 1 25.4 -> 28.3 us).
+    static constexpr uint32_t kAlign = WB >= UB + 14 ? 16 : 4;
+    u32x4 v[NJ];
+    struct Place {
+        uint32_t o[NJ];
+        __device__ __forceinline__ void init(int lane, int64_t ldw) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int id = 64 * j + lane, r = id / CPR;
+                o[j] = id < NCH ? (uint32_t)(r * ldw) + 16u * (id - r * CPR) : kOOB;
+            }
+        }
+    };
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t lead, const Place &at,
+                                         int u, int, int, bool live) {
+        const uint32_t base = lead + (uint32_t)u * UB;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            v[j] = buf_load16(rs, live && at.o[j] < kOOB ? (at.o[j] + base) & ~(kAlign - 1) : kOOB);
+    }
+    // to the strip; returns row lane % 16 of it
+    __device__ __forceinline__ const uint32_t *stage(u32x4 *strip, int lane) const {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) strip[64 * j + lane] = v[j];
+        asm volatile("" ::: "memory");
+        return reinterpret_cast<const uint32_t *>(strip + (lane & 15) * CPR);
+    }
+    // where in the strip's row the bytes of row lane % 16 start (even)
+    static __device__ __forceinline__ uint32_t shift(uint32_t lead, int64_t ldw, int u, int lane) {
+        return (lead + (uint32_t)((lane & 15) * ldw) + (uint32_t)u * UB) & 15;
+    }
+    static __device__ __forceinline__ u32x4 chunk(const uint32_t *w, int i) {
+        return reinterpret_cast<const u32x4 *>(w)[i];
+    }
+};
+
 // Q4_K, Q5_K: quarter g of the super-block, sub-blocks 2g (low nibbles) and
 // 2g + 1 (high nibbles).
 template <int FMT>
-struct KUnit {
+struct KUnit : Staged<FMT == kFmtQ5_K ? 176 : 144, FMT == kFmtQ5_K ? 176 : 144> {
     static constexpr int NF = 8, UK = 256;
     static constexpr bool Q5 = FMT == kFmtQ5_K;
-    static constexpr uint32_t BB = Q5 ? 176 : 144, QS = Q5 ? 48 : 16;
-    u32x4 hdr, q[2], h[Q5 ? 2 : 1];
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t row, int u, int g,
-                                         int, bool live) {
-        const uint32_t o = live ? row + (uint32_t)u * BB : kOOB;
-        hdr = buf_load16(rs, o);
-        q[0] = buf_load16(rs, o + QS + 32 * g);
-        q[1] = buf_load16(rs, o + QS + 32 * g + 16);
-        if constexpr (Q5) {
-            h[0] = buf_load16(rs, o + 16);
-            h[1] = buf_load16(rs, o + 32);
-        }
-    }
     struct Unpacked {
         float A[2], C[2];
         u32x4 q[2], h[Q5 ? 2 : 1];
@@ -127,37 +195,43 @@ struct KUnit {
             constexpr int high = S >= 4;
             const u32x4 w = q[c >> 1];
             uint32_t w0 = (c & 1) ? w.z : w.x, w1 = (c & 1) ? w.w : w.y;
-            w0 = (high ? w0 >> 4 : w0) & 0x0F0F0F0Fu;
-            w1 = (high ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
             if constexpr (Q5) {
+                w0 = (high ? w0 >> 4 : w0) & 0x0F0F0F0Fu;
+                w1 = (high ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
                 const u32x4 b = h[c >> 1];
                 const uint32_t b0 = (c & 1) ? b.z : b.x, b1 = (c & 1) ? b.w : b.y;
                 w0 |= ((high ? b0 >> 1 : b0) & 0x01010101u) << 4;
                 w1 |= ((high ? b1 >> 1 : b1) & 0x01010101u) << 4;
+                return frag_bytes(w0, w1, A[high], C[high]);
+            } else {
+                return frag_nibbles<high>(w0, w1, A[high], C[high]);
             }
-            return frag_fma(w0, w1, A[high], C[high]);
         }
     };
-    __device__ __forceinline__ Unpacked unpack(int g) const {
+    __device__ __forceinline__ Unpacked unpack(u32x4 *strip, uint32_t, int64_t, int, int lane,
+                                               int) const {
+        const int g = lane >> 4;
+        const uint32_t *w = this->stage(strip, lane);
+        const u32x4 hdr = this->chunk(w, 0);
         Unpacked p;
-        // sub-blocks 2g, 2g + 1: bytes 2(g & 1) and the next of the scale dwords
-        const uint32_t sh = 16 * (g & 1);
-        const uint32_t lo = hdr.y >> sh, mid = hdr.z >> sh, hi = hdr.w >> sh;
-        const bool first = g < 2;
-        const uint32_t sc0 = first ? lo & 63 : (hi & 15) | ((lo >> 2) & 48);
-        const uint32_t m0 = first ? mid & 63 : ((hi >> 4) & 15) | ((mid >> 2) & 48);
-        const uint32_t sc1 = first ? (lo >> 8) & 63 : ((hi >> 8) & 15) | ((lo >> 10) & 48);
-        const uint32_t m1 = first ? (mid >> 8) & 63 : ((hi >> 12) & 15) | ((mid >> 10) & 48);
-        const float d = f16_bits_to_f32(hdr.x), dmin = f16_bits_to_f32(hdr.x >> 16);
-        p.A[0] = d * (float)sc0;
-        p.C[0] = -(dmin * (float)m0);
-        p.A[1] = d * (float)sc1;
-        p.C[1] = -(dmin * (float)m1);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            p.q[i] = q[i];
-            if constexpr (Q5) p.h[i] = h[i] >> (2 * g);   // bit 2g to bit 0 of each byte
+            p.q[i] = this->chunk(w, (Q5 ? 3 : 1) + 2 * g + i);
+            if constexpr (Q5) p.h[i] = this->chunk(w, 1 + i) >> (2 * g);   // bit 2g to bit 0
         }
+        // Sub-blocks 2g, 2g + 1: bytes 2(g & 1) and the next of the scale dwords.
+        // Of the first four the 6 bits lie together; of the last four the low 4
+        // are nibbles of the third dword and the top 2 the first four's top bits.
+        const uint32_t sh = 16 * (g & 1);
+        const uint32_t lo = hdr.y >> sh, mid = hdr.z >> sh, hi = hdr.w >> sh;
+        const uint32_t low = g < 2 ? 0x3F3Fu : 0x0F0Fu, top = g < 2 ? 0u : 0x3030u;
+        const uint32_t sc = ((g < 2 ? lo : hi) & low) | ((lo >> 2) & top);
+        const uint32_t mn = ((g < 2 ? mid : hi >> 4) & low) | ((mid >> 2) & top);
+        const float d = kCode * f16_bits_to_f32(hdr.x), dmin = f16_bits_to_f32(hdr.x >> 16);
+        p.A[0] = d * ubyte_f32<0>(sc);
+        p.C[0] = -(dmin * ubyte_f32<0>(mn));
+        p.A[1] = (Q5 ? d : d * (kCodeHigh / kCode)) * ubyte_f32<1>(sc);
+        p.C[1] = -(dmin * ubyte_f32<1>(mn));
         return p;
     }
     static __device__ __forceinline__ int kofs(int g, int s) { return 64 * g + 8 * s; }
@@ -166,41 +240,13 @@ template <> struct RowUnit<kFmtQ4_K> : KUnit<kFmtQ4_K> {};
 template <> struct RowUnit<kFmtQ5_K> : KUnit<kFmtQ5_K> {};
 
 // Q6_K: half h = g / 2 of the super-block, elements 16p .. 16p + 15 (p = g % 2)
-// of its four 32-element groups.  Blocks are 2-byte aligned: fields are read
-// as the aligned dwords that cover them.
+// of its four 32-element groups.
 template <>
-struct RowUnit<kFmtQ6_K> {
+struct RowUnit<kFmtQ6_K> : Staged<210, 224> {
     static constexpr int NF = 8, UK = 256;
-    uint32_t a[5], b[5], hh[5], sc[3], dd, sh;
-    static __device__ __forceinline__ void load5(__amdgpu_buffer_rsrc_t rs, uint32_t o,
-                                                 uint32_t (&w)[5]) {
-        const u32x4 v = buf_load16(rs, o);
-        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-        w[4] = buf_load4(rs, o + 16);
-    }
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t row, int u, int g,
-                                         int, bool live) {
-        const uint32_t o = row + (uint32_t)u * 210u, al = live ? o & ~3u : kOOB;
-        const uint32_t h = g >> 1, p = g & 1;
-        sh = o & 2;
-        load5(rs, al + 64 * h + 16 * p, a);
-        load5(rs, al + 64 * h + 32 + 16 * p, b);
-        load5(rs, al + 128 + 32 * h + 16 * p, hh);
-        const uint32_t s = al + 192 + 8 * h;
-        sc[0] = buf_load4(rs, s);
-        sc[1] = buf_load4(rs, s + 4);
-        sc[2] = buf_load4(rs, s + 8);
-        dd = buf_load4(rs, al + 208);
-    }
-    static __device__ __forceinline__ u32x4 realign(const uint32_t (&w)[5], uint32_t s) {
-        return u32x4{__builtin_amdgcn_alignbyte(w[1], w[0], s),
-                     __builtin_amdgcn_alignbyte(w[2], w[1], s),
-                     __builtin_amdgcn_alignbyte(w[3], w[2], s),
-                     __builtin_amdgcn_alignbyte(w[4], w[3], s)};
-    }
     struct Unpacked {
         u32x4 a, b, h;
-        float A[4];
+        float A[4], C[4];
         template <int S>
         __device__ __forceinline__ half8 frag() const {
             constexpr int grp = S >> 1, c = S & 1;
@@ -212,24 +258,39 @@ struct RowUnit<kFmtQ6_K> {
             w0 |= ((h0 >> (2 * grp)) & 0x03030303u) << 4;
             w1 |= ((h1 >> (2 * grp)) & 0x03030303u) << 4;
             // (d·s)·(q − 32): ds·q and 32·ds are exact, so one fma is
-            return frag_fma(w0, w1, A[grp], -32.0f * A[grp]);
+            return frag_bytes(w0, w1, A[grp], C[grp]);
         }
     };
-    __device__ __forceinline__ Unpacked unpack(int g) const {
+    // the 16 bytes at w[4i] + s bytes (s = 0 or 2)
+    static __device__ __forceinline__ u32x4 realign(const uint32_t *w, int i, uint32_t s) {
+        const uint32_t *q = w + 4 * i;
+        const uint32_t t[5] = {q[0], q[1], q[2], q[3], q[4]};
+        return u32x4{__builtin_amdgcn_alignbyte(t[1], t[0], s), __builtin_amdgcn_alignbyte(t[2], t[1], s),
+                     __builtin_amdgcn_alignbyte(t[3], t[2], s), __builtin_amdgcn_alignbyte(t[4], t[3], s)};
+    }
+    __device__ __forceinline__ Unpacked unpack(u32x4 *strip, uint32_t lead, int64_t ldw, int u,
+                                               int lane, int) const {
+        const int g = lane >> 4, h = g >> 1, pp = g & 1;
+        const uint32_t off = shift(lead, ldw, u, lane), sh = off & 2;
+        const uint32_t *w = stage(strip, lane) + (off >> 2);
         Unpacked p;
-        p.a = realign(a, sh);
-        p.b = realign(b, sh);
-        p.h = realign(hh, sh);
-        // the half's eight scales; this lane's are bytes p, p + 2, p + 4, p + 6
+        p.a = realign(w, 4 * h + pp, sh);
+        p.b = realign(w, 4 * h + 2 + pp, sh);
+        p.h = realign(w, 8 + 2 * h + pp, sh);
+        // the half's eight scales; this lane's are bytes pp, pp + 2, pp + 4, pp + 6
+        const uint32_t *sc = w + 48 + 2 * h;
         uint32_t s0 = __builtin_amdgcn_alignbyte(sc[1], sc[0], sh);
         uint32_t s1 = __builtin_amdgcn_alignbyte(sc[2], sc[1], sh);
-        s0 >>= 8 * (g & 1);
-        s1 >>= 8 * (g & 1);
-        const float d = f16_bits_to_f32(dd >> (8 * sh));
-        p.A[0] = d * sbyte_f32<0>(s0);
-        p.A[1] = d * sbyte_f32<2>(s0);
-        p.A[2] = d * sbyte_f32<0>(s1);
-        p.A[3] = d * sbyte_f32<2>(s1);
+        s0 >>= 8 * pp;
+        s1 >>= 8 * pp;
+        const float d = f16_bits_to_f32(w[52] >> (8 * sh));
+        const float ds[4] = {d * sbyte_f32<0>(s0), d * sbyte_f32<2>(s0), d * sbyte_f32<0>(s1),
+                             d * sbyte_f32<2>(s1)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p.A[i] = kCode * ds[i];
+            p.C[i] = -32.0f * ds[i];
+        }
         return p;
     }
     static __device__ __forceinline__ int kofs(int g, int s) {
@@ -237,32 +298,15 @@ struct RowUnit<kFmtQ6_K> {
     }
 };
 
-// The 32-element formats: blocks 2g and 2g + 1 of the unit's eight, read as
-// the aligned dwords that cover them.  A block past the row's last has its
-// factors cleared (its bytes are the next row's).
+// The 32-element formats: blocks 2g and 2g + 1 of the unit's eight.  A block
+// past the row's last has its factors cleared (its bytes are the next row's).
+constexpr int b32_bytes(int fmt) {
+    return fmt == kFmtQ4_0 ? 18 : fmt == kFmtQ5_0 ? 22 : fmt == kFmtQ5_1 ? 24 : 34;
+}
 template <int FMT>
-struct BUnit {
-    static constexpr int NF = 8, UK = 256;
-    static constexpr int BB = FMT == kFmtQ4_0 ? 18 : FMT == kFmtQ5_0 ? 22 : FMT == kFmtQ5_1 ? 24 : 34;
-    // dwords that cover two blocks at a 2-byte offset (Q5_1 blocks are aligned)
-    static constexpr int NW = FMT == kFmtQ5_1 ? 12 : (2 * BB + 2 + 3) / 4;
-    uint32_t w[NW], sh;
-    int exist;                           // blocks of this lane that exist
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t row, int u, int g,
-                                         int K, bool live) {
-        const int blk = 8 * u + 2 * g;
-        exist = live ? (K >> 5) - blk : 0;
-        const uint32_t o = row + (uint32_t)blk * BB;
-        sh = o & 2;
-        const uint32_t al = exist > 0 ? o & ~3u : kOOB;
-#pragma unroll
-        for (int i = 0; i + 4 <= NW; i += 4) {
-            const u32x4 v = buf_load16(rs, al + 4 * i);
-            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
-        }
-#pragma unroll
-        for (int i = NW / 4 * 4; i < NW; ++i) w[i] = buf_load4(rs, al + 4 * i);
-    }
+struct BUnit : Staged<8 * b32_bytes(FMT),
+                      FMT == kFmtQ5_1 ? 192 : (8 * b32_bytes(FMT) + 14 + 15) / 16 * 16> {
+    static constexpr int NF = 8, UK = 256, BB = b32_bytes(FMT);
     struct Unpacked {
         static constexpr int NC = 2 * BB / 4;
         uint32_t c[NC];                  // the two blocks from byte 0
@@ -279,48 +323,65 @@ struct BUnit {
         __device__ __forceinline__ half8 frag() const {
             constexpr int b = S >> 2, ch = S & 3, base = b * BB;   // block, 8-element chunk
             if constexpr (FMT == kFmtQ8_0) {
-                const uint32_t w0 = dw<base + 2 + 8 * ch>(), w1 = dw<base + 6 + 8 * ch>();
-                const float d = A[b];
-                const u32x4 v = {pack_f16x2(d * sbyte_f32<0>(w0), d * sbyte_f32<1>(w0)),
-                                 pack_f16x2(d * sbyte_f32<2>(w0), d * sbyte_f32<3>(w0)),
-                                 pack_f16x2(d * sbyte_f32<0>(w1), d * sbyte_f32<1>(w1)),
-                                 pack_f16x2(d * sbyte_f32<2>(w1), d * sbyte_f32<3>(w1))};
-                return __builtin_bit_cast(half8, v);
+                // q + 128 as an unsigned byte; d·(q + 128) − 128·d is exact
+                constexpr uint32_t S8 = 0x80808080u;
+                return frag_bytes(dw<base + 2 + 8 * ch>() ^ S8, dw<base + 6 + 8 * ch>() ^ S8, A[b],
+                                  C[b]);
             } else {
                 constexpr int QS = FMT == kFmtQ4_0 ? 2 : FMT == kFmtQ5_0 ? 6 : 8;
                 uint32_t w0 = dw<base + QS + 8 * (ch & 1)>(), w1 = dw<base + QS + 4 + 8 * (ch & 1)>();
-                w0 = (ch >= 2 ? w0 >> 4 : w0) & 0x0F0F0F0Fu;
-                w1 = (ch >= 2 ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
-                if constexpr (FMT != kFmtQ4_0) {
+                if constexpr (FMT == kFmtQ4_0) {
+                    return frag_nibbles<(ch >> 1)>(w0, w1, ch >= 2 ? A[b] * (kCodeHigh / kCode) : A[b],
+                                                   C[b]);
+                } else {
+                    w0 = (ch >= 2 ? w0 >> 4 : w0) & 0x0F0F0F0Fu;
+                    w1 = (ch >= 2 ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
                     constexpr int QH = FMT == kFmtQ5_0 ? 2 : 4;
                     const uint32_t hb = dw<base + QH>() >> (8 * ch);
                     w0 |= spread4(hb & 15);
                     w1 |= spread4((hb >> 4) & 15);
+                    return frag_bytes(w0, w1, A[b], C[b]);
                 }
-                return frag_fma(w0, w1, A[b], C[b]);
             }
         }
     };
-    __device__ __forceinline__ Unpacked unpack(int) const {
+    __device__ __forceinline__ Unpacked unpack(u32x4 *strip, uint32_t lead, int64_t ldw, int u,
+                                               int lane, int K) const {
+        const int g = lane >> 4, exist = (K >> 5) - (8 * u + 2 * g);
+        const uint32_t *w = this->stage(strip, lane);
         Unpacked p;
+        if constexpr (FMT == kFmtQ5_1) {
 #pragma unroll
-        for (int i = 0; i < Unpacked::NC; ++i) {
-            if constexpr (FMT == kFmtQ5_1)
-                p.c[i] = w[i];
-            else
-                p.c[i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], sh);
+            for (int i = 0; i < 3; ++i) {
+                const u32x4 v = this->chunk(w, 3 * g + i);
+                p.c[4 * i] = v.x; p.c[4 * i + 1] = v.y; p.c[4 * i + 2] = v.z; p.c[4 * i + 3] = v.w;
+            }
+        } else {
+            // the lane's two blocks start 2·BB·g bytes into the row's, a whole
+            // number of dwords
+            const uint32_t off = this->shift(lead, ldw, u, lane), sh = off & 2;
+            const uint32_t *b = w + (off >> 2) + (2 * BB / 4) * g;
+            uint32_t t[Unpacked::NC + 1];
+#pragma unroll
+            for (int i = 0; i <= Unpacked::NC; ++i) t[i] = b[i];
+#pragma unroll
+            for (int i = 0; i < Unpacked::NC; ++i)
+                p.c[i] = __builtin_amdgcn_alignbyte(t[i + 1], t[i], sh);
         }
         const uint32_t h0 = p.c[0], h1 = BB % 4 ? p.c[BB / 4] >> 16 : p.c[BB / 4];
         const float d0 = f16_bits_to_f32(h0), d1 = f16_bits_to_f32(h1);
-        p.A[0] = exist > 0 ? d0 : 0.0f;
-        p.A[1] = exist > 1 ? d1 : 0.0f;
+        const float e0 = exist > 0 ? d0 : 0.0f, e1 = exist > 1 ? d1 : 0.0f;
+        p.A[0] = kCode * e0;
+        p.A[1] = kCode * e1;
         if constexpr (FMT == kFmtQ5_1) {
             const float m0 = f16_bits_to_f32(h0 >> 16), m1 = f16_bits_to_f32(h1 >> 16);
             p.C[0] = exist > 0 ? m0 : 0.0f;
             p.C[1] = exist > 1 ? m1 : 0.0f;
-        } else if constexpr (FMT != kFmtQ8_0) {
-            p.C[0] = (FMT == kFmtQ4_0 ? -8.0f : -16.0f) * p.A[0];
-            p.C[1] = (FMT == kFmtQ4_0 ? -8.0f : -16.0f) * p.A[1];
+        } else {
+            // the codes' offset; d times it is exact
+            constexpr float off = FMT == kFmtQ8_0 ? -128.0f : FMT == kFmtQ4_0 ? -8.0f : -16.0f;
+            p.C[0] = off * e0;
+            p.C[1] = off * e1;
         }
         return p;
     }
@@ -387,10 +448,12 @@ __device__ __forceinline__ void for_const(F &&f) {
     }
 }
 
-// The LDS strip of a wave: its activations, then its sums.
+// The LDS strip of a wave: its activations and a tile's raw bytes, then its
+// sums.
 template <class Unit, int RT, int MR>
 constexpr int strip_chunks() {
-    return MR * Unit::UK / 8 > RT * 64 ? MR * Unit::UK / 8 : RT * 64;
+    const int need = MR * Unit::UK / 8 + Unit::STRIP;
+    return need > RT * 64 ? need : RT * 64;
 }
 
 // RT tiles of 16 weight rows per workgroup of blockDim.x / 64 waves, at least
@@ -430,19 +493,20 @@ __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_row
     }
 
     __amdgpu_buffer_rsrc_t rsw[RT];
-    uint32_t wrow[RT];
+    uint32_t lead[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int first = n0 + (GLU ? 0 : 16 * t);
         const int valid = min(16, a.N - first);
         const int64_t start = ((int64_t)first + (GLU && t ? a.N : 0)) * a.ldw;
-        const uint32_t lead = FMT == kFmtF16 ? 0 : (uint32_t)(((uintptr_t)a.W + start) & 15);
+        lead[t] = FMT == kFmtF16 ? 0 : (uint32_t)(((uintptr_t)a.W + start) & 15);
         const int64_t row = FMT == kFmtF16 ? 2 * (int64_t)a.K : a.ldw;
         // a tile past N reads nothing
-        const int64_t bytes = valid > 0 ? (lead + (valid - 1) * a.ldw + row + 3) & ~(int64_t)3 : 0;
-        rsw[t] = make_rsrc(valid > 0 ? a.W + start - lead : a.W, (uint32_t)bytes);
-        wrow[t] = lead + (uint32_t)(r16 * a.ldw);
+        const int64_t bytes = valid > 0 ? (lead[t] + (valid - 1) * a.ldw + row + 3) & ~(int64_t)3 : 0;
+        rsw[t] = make_rsrc(valid > 0 ? a.W + start - lead[t] : a.W, (uint32_t)bytes);
     }
+    typename Unit::Place place;
+    place.init(lane, a.ldw);
     constexpr int XE = XF32 ? 4 : 2;
     const __amdgpu_buffer_rsrc_t rsx =
         make_rsrc(a.X, (uint32_t)(((int64_t)(a.M - 1) * a.ldx + a.K) * XE));
@@ -454,10 +518,10 @@ __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_row
     for (int t = 0; t < RT; ++t) acc[t] = f32x4{};
     Unit w[RT];
     XU x;
-    u32x4 *const xl = strips + wave * SC;
+    u32x4 *const xl = strips + wave * SC, *const wl = xl + MR * XU::CH;
     // Look-aheads past the last unit load zeros: a branch around the loads
     // would make the compiler wait for all of them at its join.
-    auto load_w = [&](int t, int u) { w[t].load(rsw[t], wrow[t], u, g, a.K, u < units); };
+    auto load_w = [&](int t, int u) { w[t].load(rsw[t], lead[t], place, u, lane, a.K, u < units); };
     int u = wave;
     x.load(rsx, ldb, u, lane, a.M, a.K, u < units);
 #pragma unroll
@@ -471,7 +535,7 @@ __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_row
         x.load(rsx, ldb, u + NW, lane, a.M, a.K, u + NW < units);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            const auto p = w[t].unpack(g);
+            const auto p = w[t].unpack(wl, lead[t], a.ldw, u, lane, a.K);
             load_w(t, u + NW);
             for_const<0, NF>([&](auto f) {
                 constexpr int S = decltype(f)::value;

@@ -198,6 +198,21 @@ def test_part_units(fmt, K):
         check_linear(fmt, 9, 33, K + 8, xt="f32", yt="f32", seed=K)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_few_rows_see_the_cache_weights(fmt):
+    """One-hot activations read every weight back: the few-row kernels expand
+    the values of the f16 cache (an exact zero's sign aside)."""
+    N, K = 50, 512
+    announce("one-hot", fmt)
+    q, bits = _weight(fmt, N, K, 30)
+    want = torch.from_numpy(bits.view(np.float16).astype(np.float32)).to(dev())
+    eye = torch.eye(K, dtype=torch.float16, device=dev())
+    got = torch.cat([mq.linear_fused(eye[k:k + 16], q, fmt, N, K) for k in range(0, K, 16)])
+    assert torch.equal(got.t(), want)
+    got = torch.cat([mq.linear_fused(eye[k:k + 3].float(), q, fmt, N, K) for k in range(0, K, 3)])
+    assert torch.equal(got.t(), want)
+
+
 @pytest.mark.parametrize("fmt", [0] + FMTS)
 def test_wide_outputs(fmt):
     """256 x 256 tiles, the last ones ragged in rows and columns."""
