@@ -1,8 +1,10 @@
-"""Compile libmq.so for gfx950 in-tree with hipcc.
+"""Compile libmq.so for gfx950 in-tree with hipcc, and the torch binding of the
+layer operators with the host compiler.
 
 Usage: ``python -m quantized_weight_prefill_q4_amd.build`` (or ``build_lib()``).
 Each ``csrc/*.hip`` file is compiled to an object under ``_build/`` in
-parallel, then linked into ``quantized_weight_prefill_q4_amd/libmq.so``.
+parallel, then linked into ``quantized_weight_prefill_q4_amd/libmq.so``;
+``csrc/binding.cpp`` becomes the extension module ``_binding.so`` beside it.
 """
 
 from __future__ import annotations
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,9 +22,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libmq.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 SOURCES = ("mq_api.hip", "dequant.hip", "gemm.hip", "gemm_xf32.hip", "mmq.hip", "rms_norm.hip",
            "gemm_linear.hip", "gemm_glu.hip", "linear_rows.hip")
 
+CXX = os.environ.get("CXX", shutil.which("g++") or "c++")
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 
 # Device code: gfx950 only; keep IEEE denormals (f16 subnormal weights must
@@ -59,11 +64,37 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_binding(verbose: bool) -> str:
+    """csrc/binding.cpp as a CPython extension against the installed torch."""
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = os.path.join(root, "include")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build_lib(verbose: bool = False) -> str:
-    """Compile every HIP source and link libmq.so; returns the library path."""
+    """Compile every HIP source and link libmq.so, and build the torch binding;
+    returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_build_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        binding.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

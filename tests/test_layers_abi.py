@@ -163,3 +163,37 @@ def test_layer_workspaces(L):
         assert L.mq_linear_workspace_bytes(0, F32, M, N, K, 0) == x16 + planes
         assert L.mq_glu_workspace_bytes(12, F16, M, N, 3584, 0) == \
             L.mq_gemm_workspace_bytes(12, M, 2 * N, 3584, 0)
+
+
+def test_native_binding_refuses_without_a_gpu():
+    """The native side's own checks: CPU tensors, non-tensors, wrong counts."""
+    import torch
+
+    import quantized_weight_prefill_q4_amd as mq
+    from quantized_weight_prefill_q4_amd import layers
+
+    b = layers._binding()
+    x, w = torch.zeros(2, 32), torch.zeros(32)
+    for call, args in ((b.norm, (0, x, w, None, 1e-6, 0, None, None, None)),
+                       (b.layer, (0, x, w, 0, -1, -1, None, 0, None, False, 0, 0, None, None))):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call(*args)
+        with pytest.raises(ValueError, match="x must be a tensor"):
+            call(0, 7, *args[2:])
+        with pytest.raises(TypeError, match="arguments"):
+            call(*args[:-1])
+        with pytest.raises(TypeError):
+            call("stream", *args[1:])
+    with pytest.raises(ValueError, match="missing"):
+        b.bind({})
+    layers._binding.cache_clear()
+    layers._binding()                                   # bound again
+    for f, args in ((mq.add_rms_norm, (x, w)), (mq.add_rms_norm_q8_1, (x, w)),
+                    (mq.linear_f16cache, (x, x.half())), (mq.glu_f16cache, (x, x.half())),
+                    (mq.linear_fused, (x, x, "q8_0", 2)), (mq.glu_fused, (x, x, "q8_0", 1))):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            f(*args)
+    with pytest.raises(ValueError, match="unknown activation"):
+        mq.linear_f16cache(x, x.half(), act="swish")
+    with pytest.raises(ValueError, match="out_dtype"):
+        mq.add_rms_norm(x, w, out_dtype=torch.bfloat16)
