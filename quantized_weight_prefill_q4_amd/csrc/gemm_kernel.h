@@ -1020,13 +1020,46 @@ __device__ __forceinline__ void store_tile(const Args &a, f32x16 (&acc)[FM][FN],
         }
 }
 
+// Writes 16 rows (half H of block row I) of a wave's accumulators to its patch.
+template <int I, int H, int PS, int FM, int FN>
+__device__ __forceinline__ void patch_rows(float *patch, const f32x16 (&acc)[FM][FN], int row_l,
+                                           int col_l) {
+    // The compiler would otherwise merge the cases below into one with a
+    // computed index, for which the accumulators have to lie in memory: the
+    // statements differ from case to case, so it keeps them apart.
+    asm volatile("; rows %0" ::"n"(2 * I + H) : "memory");
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int r = 8 * H; r < 8 * H + 8; ++r)
+            patch[((r >> 2) * 8 - 16 * H + row_l + (r & 3)) * PS + j * 32 + col_l] = acc[I][j][r];
+    asm volatile("; rows %0 done" ::"n"(2 * I + H) : "memory");
+}
+
+// patch_rows of group g = 2·i + h, g known at run time: the accumulators are
+// registers, so each group is a case of its own.
+template <int G, int PS, int FM, int FN>
+__device__ __forceinline__ void patch_group(int g, float *patch, const f32x16 (&acc)[FM][FN],
+                                            int row_l, int col_l) {
+    if constexpr (G < 2 * FM) {
+        if (g == G)
+            patch_rows<(G >> 1), (G & 1), PS>(patch, acc, row_l, col_l);
+        else
+            patch_group<G + 1, PS>(g, patch, acc, row_l, col_l);
+    }
+}
+
 // A whole tile's epilogue and output.  The wave takes its tile 16 rows at a
 // time through a private LDS patch of 16 × (TN + 4) floats (in the idle
 // stages, as store_tile): written in the MFMA layout (a column per lane), read
-// back as 8 consecutive columns of a row per lane, so that bias, residual and
-// y are 16-byte accesses and the activation runs once per output in a loop
-// that is not unrolled over the tile.  The residual rows of the next 16 are
-// loaded while the current ones are finished.
+// back as eight columns of a row per lane, so that bias, residual and y are
+// 16-byte accesses (f32 y: two groups of four columns half the wave's columns
+// apart, so that each store instruction writes whole row segments).  The
+// residual rows of the next pass are loaded while the current one is finished.
+// The loop over the rows is not unrolled: the activations' code would be
+// repeated for every register of the tile, and fetching it once per tile costs
+// more than running it (2048 x 37888 x 3584 with f32 y: 592 us unrolled, 511
+// for the product alone).
 template <int EPI, int BM, int BN, int FM, int FN, int TM, int TN, int NW, int SA, int SB>
 __device__ __forceinline__ void store_tile_epi(const EpiArgs &a, f32x16 (&acc)[FM][FN], int m0,
                                                int n0, int wm, int wn, int lane, int wave,
@@ -1057,72 +1090,104 @@ __device__ __forceinline__ void store_tile_epi(const EpiArgs &a, f32x16 (&acc)[F
     constexpr int LPR = OC / 8, RPI = 64 / LPR;    // lanes per row, rows per pass
     constexpr int QN = 16 / RPI;                   // passes per 16 rows
     static_assert(QN >= 1 && QN * RPI == 16, "whole passes");
-    const int rr = lane / LPR, cc = 8 * (lane % LPR);
+    const bool wide = a.y_type == kTypeF32;
+    const int rr = lane / LPR, cl = lane % LPR;
     const int F = GLU ? a.N >> 1 : a.N;
-    const int col = (GLU ? (n0 >> 1) + wn * (TN / 2) : n0 + wn * TN) + cc;
-    const int n = min(8, F - col);                 // columns this lane writes (<= 0: none)
-    const int pc = GLU ? (cc >> 5) * 64 + (cc & 31) : cc;
-    float b0[8] = {}, b1[8] = {};
-    if (a.bias && n > 0) {
-        load_upto8(a.bias, kTypeF32, col, n, b0);
-        if constexpr (GLU) load_upto8(a.bias, kTypeF32, (int64_t)F + col, n, b1);
-    }
-    const int64_t ye = a.y_type == kTypeF32 ? 4 : 2, re = a.res_type == kTypeF32 ? 4 : 2;
-    const int row0 = m0 + wm * TM + rr;
-    float res[2][QN][8] = {};
-    auto load_res = [&](int set, int g) MQ_INLINE {
-        if constexpr (!GLU) {
-            if (a.res) {
+    const int64_t ye = wide ? 4 : 2, re = a.res_type == kTypeF32 ? 4 : 2;
+    int c[2], n[2], pc[2];                         // first column of each four, how many exist
+    float b0[2][4] = {}, b1[2][4] = {};
 #pragma unroll
-                for (int q = 0; q < QN; ++q) {
-                    const int64_t row = row0 + 16 * g + RPI * q;
-                    if (row < a.M && n > 0)
-                        load_upto8((const char *)a.res + row * a.ldr * re, a.res_type, col, n,
-                                   res[set][q]);
-                }
+    for (int k = 0; k < 2; ++k) {
+        const int cc = wide ? 4 * cl + k * (OC / 2) : 8 * cl + 4 * k;
+        c[k] = (GLU ? (n0 >> 1) + wn * (TN / 2) : n0 + wn * TN) + cc;
+        n[k] = min(4, F - c[k]);
+        pc[k] = GLU ? (cc >> 5) * 64 + (cc & 31) : cc;
+        if (a.bias && n[k] > 0) {
+            load_upto4(a.bias, kTypeF32, c[k], n[k], b0[k]);
+            if constexpr (GLU) load_upto4(a.bias, kTypeF32, (int64_t)F + c[k], n[k], b1[k]);
+        }
+    }
+    const int row0 = m0 + wm * TM + rr;
+    const int col_l = lane & 31, row_l = (lane >> 5) * 4;
+    // A group's eight values per pass and lane, all passes together: the LDS
+    // reads, the activations and the stores of QN rows overlap.
+    float next[QN][8] = {};
+    auto load_res = [&](int g) MQ_INLINE {
+#pragma unroll
+        for (int q = 0; q < QN; ++q) {
+            const int row = row0 + 16 * g + RPI * q;
+            if (row >= a.M) continue;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (n[k] <= 0) continue;
+                float t[4];
+                load_upto4((const char *)a.res + (int64_t)row * a.ldr * re, a.res_type, c[k], n[k],
+                           t);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) next[q][4 * k + j] = t[j];
             }
         }
     };
-    const int col_l = lane & 31, row_l = (lane >> 5) * 4;
-    load_res(0, 0);
+    if (!GLU && a.res) load_res(0);
     sync_lds();   // every wave is done reading the stages
-    static_for<2 * FM>([&](auto G) MQ_INLINE {
-        constexpr int g = G, i = g >> 1, h = g & 1;
-        if constexpr (g + 1 < 2 * FM) load_res((g + 1) & 1, g + 1);
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int r = 8 * h; r < 8 * h + 8; ++r)
-                patch[((r >> 2) * 8 - 16 * h + row_l + (r & 3)) * PS + j * 32 + col_l] =
-                    acc[i][j][r];
+#pragma clang loop unroll(disable)
+    for (int g = 0; g < 2 * FM; ++g) {
+        asm volatile("" ::: "memory");
+        patch_group<0, PS>(g, patch, acc, row_l, col_l);
         // lanes read what other lanes wrote: the LDS runs one wave's
         // instructions in order, so only the compiler must keep them
         asm volatile("" ::: "memory");
+        float v[8 * QN], u[GLU ? 8 * QN : 1], res[QN][8];
+#pragma unroll
+        for (int q = 0; q < QN; ++q)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float *p = patch + (rr + RPI * q) * PS + pc[k];
+                const f32x4 t = *reinterpret_cast<const f32x4 *>(p);
+                float *w = v + 8 * q + 4 * k;
+                w[0] = t.x + b0[k][0];
+                w[1] = t.y + b0[k][1];
+                w[2] = t.z + b0[k][2];
+                w[3] = t.w + b0[k][3];
+                if constexpr (GLU) {
+                    const f32x4 s = *reinterpret_cast<const f32x4 *>(p + 32);
+                    float *x = u + 8 * q + 4 * k;
+                    x[0] = s.x + b1[k][0];
+                    x[1] = s.y + b1[k][1];
+                    x[2] = s.z + b1[k][2];
+                    x[3] = s.w + b1[k][3];
+                }
+            }
+        if constexpr (!GLU) {
+#pragma unroll
+            for (int q = 0; q < QN; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) res[q][j] = next[q][j];
+            if (a.res && g + 1 < 2 * FM) load_res(g + 1);
+        }
+        apply_act(a.act, v);
 #pragma unroll
         for (int q = 0; q < QN; ++q) {
-            const int64_t row = row0 + 16 * g + RPI * q;
-            const float *p = patch + (rr + RPI * q) * PS + pc;
-            const f32x4 lo = *reinterpret_cast<const f32x4 *>(p);
-            const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + 4);
-            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const int row = row0 + 16 * g + RPI * q;
+            float y[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += b0[j];
-            apply_act(a.act, v);
-            if constexpr (GLU) {
-                const f32x4 ul = *reinterpret_cast<const f32x4 *>(p + 32);
-                const f32x4 uh = *reinterpret_cast<const f32x4 *>(p + 36);
-                const float u[8] = {ul.x, ul.y, ul.z, ul.w, uh.x, uh.y, uh.z, uh.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] *= u[j] + b1[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += res[g & 1][q][j];
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (GLU)
+                    y[j] = v[8 * q + j] * u[8 * q + j];
+                else
+                    y[j] = v[8 * q + j] + res[q][j];
             }
-            if (row < a.M && n > 0)
-                store_upto8((char *)a.Y + row * a.ldy * ye, a.y_type, col, n, v);
+            if (row >= a.M) continue;
+            char *yr = (char *)a.Y + (int64_t)row * a.ldy * ye;
+            const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+            if (!wide && n[1] >= 4) {
+                store8_f16(yr, c[0], y);
+            } else {
+                store_upto4(yr, a.y_type, c[0], n[0], lo);
+                store_upto4(yr, a.y_type, c[1], n[1], hi);
+            }
         }
-        asm volatile("" ::: "memory");
-    });
+    }
 }
 
 // A workgroup's last step: the tile's output, or a K range's partial tile.
