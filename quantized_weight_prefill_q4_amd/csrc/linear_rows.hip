@@ -1,5 +1,5 @@
 // Linear and gated layers for a few activation rows (one generated token, or a
-// handful of sequences decoded together): Y = epilogue(X·Wᵀ) with M <= 16.
+// handful of sequences decoded together): Y = epilogue(X·Wᵀ) with M <= 32.
 //
 // Mathematics and bound.  Every weight is used M times and read once, so the
 // product is bound by the weight's bytes (0.56 to 2 per weight) and, for the
@@ -86,7 +86,9 @@ __device__ __forceinline__ uint32_t spread4(uint32_t b) {
 // One unit of k of a tile of 16 weight rows, as a wave holds it.  load(): the
 // raw bytes into registers, zeros when the unit is not live; unpack(): the
 // form that lane (row r, quarter g) makes its fragments from; frag<S>(): the
-// eight weights of fragment S, whose k is kofs(g, S) within the unit.
+// eight weights of fragment S, whose k is kofs(g, S) within the unit.  The
+// fragments of half h of a unit, S = 4h .. 4h + 3, cover 16 of its 32 chunks of
+// 8 elements: half_chunk(h, i), i = 0 .. 15; half_slot(g, S) is the i of theirs.
 // ---------------------------------------------------------------------------
 template <int FMT>
 struct RowUnit;
@@ -125,6 +127,8 @@ struct RowUnit<kFmtF16> {
         return p;
     }
     static __device__ __forceinline__ int kofs(int g, int s) { return 32 * s + 8 * g; }
+    static __device__ __forceinline__ int half_chunk(int, int i) { return i; }
+    static __device__ __forceinline__ int half_slot(int, int) { return 0; }
 };
 
 // The block formats' bytes: UB bytes per row and unit, loaded as the WB / 16
@@ -235,6 +239,8 @@ struct KUnit : Staged<FMT == kFmtQ5_K ? 176 : 144, FMT == kFmtQ5_K ? 176 : 144> 
         return p;
     }
     static __device__ __forceinline__ int kofs(int g, int s) { return 64 * g + 8 * s; }
+    static __device__ __forceinline__ int half_chunk(int h, int i) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+    static __device__ __forceinline__ int half_slot(int g, int s) { return 4 * g + (s & 3); }
 };
 template <> struct RowUnit<kFmtQ4_K> : KUnit<kFmtQ4_K> {};
 template <> struct RowUnit<kFmtQ5_K> : KUnit<kFmtQ5_K> {};
@@ -295,6 +301,10 @@ struct RowUnit<kFmtQ6_K> : Staged<210, 224> {
     }
     static __device__ __forceinline__ int kofs(int g, int s) {
         return 128 * (g >> 1) + 32 * (s >> 1) + 16 * (g & 1) + 8 * (s & 1);
+    }
+    static __device__ __forceinline__ int half_chunk(int h, int i) { return 16 * (i >> 3) + 8 * h + (i & 7); }
+    static __device__ __forceinline__ int half_slot(int g, int s) {
+        return 8 * (g >> 1) + (s & 2) * 2 + 2 * (g & 1) + (s & 1);
     }
 };
 
@@ -386,29 +396,34 @@ struct BUnit : Staged<8 * b32_bytes(FMT),
         return p;
     }
     static __device__ __forceinline__ int kofs(int g, int s) { return 64 * g + 8 * s; }
+    static __device__ __forceinline__ int half_chunk(int h, int i) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+    static __device__ __forceinline__ int half_slot(int g, int s) { return 4 * g + (s & 3); }
 };
 template <> struct RowUnit<kFmtQ4_0> : BUnit<kFmtQ4_0> {};
 template <> struct RowUnit<kFmtQ5_0> : BUnit<kFmtQ5_0> {};
 template <> struct RowUnit<kFmtQ5_1> : BUnit<kFmtQ5_1> {};
 template <> struct RowUnit<kFmtQ8_0> : BUnit<kFmtQ8_0> {};
 
-// A unit's activations: MR rows of UK elements, loaded in whole row segments
-// (64 lanes cover RPI rows of UK / 8 chunks of 8 elements) one unit ahead,
-// rounded to f16 when they are f32, and handed through a strip of LDS that
-// belongs to the wave alone, so without a barrier.  Fragment loads straight
-// from global memory touch a cache line per lane instead (M = 16, gated
-// 14336 x 4096 Q4_K: 46 us).  Chunk c of row r is stored at c ^ (r mod 16):
-// the 16 rows that a ds_read_b128 serves together then lie in distinct banks.
-template <class U, int MR, bool XF32>
+// A unit's activations: MR rows of UK elements (with PH = 2 half a unit at a
+// time, so that 32 rows fit), loaded in row segments of at least 64 bytes one
+// step ahead, rounded to f16 when they are f32, and handed through a strip of
+// LDS that belongs to the wave alone, so without a barrier.  Fragment loads
+// straight from global memory touch a cache line per lane instead (M = 16,
+// gated 14336 x 4096 Q4_K: 46 us).  Slot c of row r is stored at c ^ (r mod
+// 16): the 16 rows that a ds_read_b128 serves together then lie in distinct
+// banks.
+template <class U, int MR, bool XF32, int PH>
 struct XUnit {
-    static constexpr int CH = U::UK / 8;          // chunks per row: 32 or 16
+    static constexpr int CH = U::UK / 8 / PH;     // chunks per row and step: 32 or 16
     static constexpr int RPI = 64 / CH;           // rows per load
     static constexpr int NX = MR / RPI;
     static_assert(NX >= 1 && NX * RPI == MR, "whole loads");
+    static_assert(PH == 1 || CH == 16, "halves of 16 chunks");
     u32x4 v[NX][XF32 ? 2 : 1];
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t ldb, int u, int lane,
-                                         int M, int K, bool live) {
-        const int c = lane & (CH - 1), r0 = lane / CH, k = u * U::UK + 8 * c;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t ldb, int u, int ph,
+                                         int lane, int M, int K, bool live) {
+        const int c = lane & (CH - 1), r0 = lane / CH;
+        const int k = u * U::UK + 8 * (PH == 1 ? c : U::half_chunk(ph, c));
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
             const int r = r0 + RPI * i;
@@ -432,10 +447,12 @@ struct XUnit {
             lds[r * CH + (c ^ (r & 15))] = h;
         }
     }
-    // Fragment s of lane (row, g).  Columns of the product past M are never
-    // written out, so rows past MR may read any row's chunk.
-    static __device__ __forceinline__ half8 frag(const u32x4 *lds, int row, int g, int s) {
-        const int r = row & (MR - 1), c = U::kofs(g, s) >> 3;
+    // Fragment s of lane (row, g), activation rows 16·f + row.  Columns of the
+    // product past M are never written out, so rows past MR may read any row's
+    // chunk.
+    static __device__ __forceinline__ half8 frag(const u32x4 *lds, int f, int row, int g, int s) {
+        const int r = (16 * f + row) & (MR - 1);
+        const int c = PH == 1 ? U::kofs(g, s) >> 3 : U::half_slot(g, s);
         return __builtin_bit_cast(half8, lds[r * CH + (c ^ (r & 15))]);
     }
 };
@@ -448,26 +465,33 @@ __device__ __forceinline__ void for_const(F &&f) {
     }
 }
 
+// Steps per unit: the 32-chunk units' activations in halves from 16 rows on.
+template <class Unit, int MR>
+constexpr int kPhases = Unit::UK == 256 && MR >= 16 ? 2 : 1;
+
 // The LDS strip of a wave: its activations and a tile's raw bytes, then its
 // sums.
 template <class Unit, int RT, int MR>
 constexpr int strip_chunks() {
-    const int need = MR * Unit::UK / 8 + Unit::STRIP;
-    return need > RT * 64 ? need : RT * 64;
+    const int need = MR * Unit::UK / 8 / kPhases<Unit, MR> + Unit::STRIP;
+    const int sums = RT * (MR > 16 ? MR / 16 : 1) * 64;
+    return need > sums ? need : sums;
 }
 
 // RT tiles of 16 weight rows per workgroup of blockDim.x / 64 waves, at least
-// RT (gated: a gate tile and its up tile, RT = 2); MR: activation rows held.
-// Registers are capped so that 4 waves share a SIMD (with half of them the
-// loads in flight do not cover the memory's latency), 3 where the 16 rows'
-// activations take 32 or 64 of them.
+// the RT·MF whose sums they finish (gated: a gate tile and its up tile, RT =
+// 2); MR: activation rows held.  Registers are capped so that 4 waves share a
+// SIMD (with half of them the loads in flight do not cover the memory's
+// latency), 3 with 16 rows and 2 with 32, whose activations and sums take more.
 template <int MR>
 constexpr int kMaxWaves = MR > 4 ? 8 : 16;
 template <int FMT, int RT, bool GLU, bool XF32, int MR>
-__global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_rows_kernel(RowsArgs a) {
+__global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 16 ? 2 : MR > 4 ? 3 : 4) void
+linear_rows_kernel(RowsArgs a) {
     static_assert(!GLU || RT == 2, "a gate tile and an up tile");
     using Unit = RowUnit<FMT>;
-    using XU = XUnit<Unit, MR, XF32>;
+    constexpr int PH = kPhases<Unit, MR>, MF = MR > 16 ? MR / 16 : 1;
+    using XU = XUnit<Unit, MR, XF32, PH>;
     constexpr int NF = Unit::NF, SC = strip_chunks<Unit, RT, MR>();
     extern __shared__ u32x4 strips[];
     const int lane = threadIdx.x & 63;
@@ -476,11 +500,12 @@ __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_row
     const int r16 = lane & 15, g = lane >> 4;
     const int n0 = blockIdx.x * (GLU ? 16 : 16 * RT);   // first output column
 
-    // what the epilogue needs, requested first: thread (tile t, lane) finishes
-    // row r16 of y, columns n0 + 16t + 4g .. + 3
+    // what the epilogue needs, requested first: wave (tile t, row block f)
+    // finishes rows 16f + lane % 16 of y, columns n0 + 16t + 4g .. + 3
     constexpr int OT = GLU ? 1 : RT;
-    const int col = n0 + 16 * wave + 4 * g;
-    const int n = wave < OT && r16 < a.M ? min(4, a.N - col) : 0;
+    const int ot = wave / MF, of = wave % MF, row = 16 * of + r16;
+    const int col = n0 + 16 * ot + 4 * g;
+    const int n = ot < OT && row < a.M ? min(4, a.N - col) : 0;
     float b0[4] = {}, b1[4] = {}, res[4] = {};
     if (n > 0) {
         if (a.bias) {
@@ -488,7 +513,7 @@ __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_row
             if constexpr (GLU) load_upto4(a.bias, kTypeF32, (int64_t)a.N + col, n, b1);
         }
         if (!GLU && a.res)
-            load_upto4((const char *)a.res + r16 * a.ldr * (a.res_type == kTypeF32 ? 4 : 2),
+            load_upto4((const char *)a.res + row * a.ldr * (a.res_type == kTypeF32 ? 4 : 2),
                        a.res_type, col, n, res);
     }
 
@@ -500,9 +525,10 @@ __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_row
         const int valid = min(16, a.N - first);
         const int64_t start = ((int64_t)first + (GLU && t ? a.N : 0)) * a.ldw;
         lead[t] = FMT == kFmtF16 ? 0 : (uint32_t)(((uintptr_t)a.W + start) & 15);
-        const int64_t row = FMT == kFmtF16 ? 2 * (int64_t)a.K : a.ldw;
+        const int64_t last = FMT == kFmtF16 ? 2 * (int64_t)a.K : a.ldw;
         // a tile past N reads nothing
-        const int64_t bytes = valid > 0 ? (lead[t] + (valid - 1) * a.ldw + row + 3) & ~(int64_t)3 : 0;
+        const int64_t bytes =
+            valid > 0 ? (lead[t] + (valid - 1) * a.ldw + last + 3) & ~(int64_t)3 : 0;
         rsw[t] = make_rsrc(valid > 0 ? a.W + start - lead[t] : a.W, (uint32_t)bytes);
     }
     typename Unit::Place place;
@@ -513,34 +539,68 @@ __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_row
     const uint32_t ldb = (uint32_t)a.ldx * XE;
 
     const int units = (a.K + Unit::UK - 1) / Unit::UK;
-    f32x4 acc[RT];
+    f32x4 acc[RT][MF];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) acc[t] = f32x4{};
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int f = 0; f < MF; ++f) acc[t][f] = f32x4{};
     Unit w[RT];
     XU x;
     u32x4 *const xl = strips + wave * SC, *const wl = xl + MR * XU::CH;
     // Look-aheads past the last unit load zeros: a branch around the loads
     // would make the compiler wait for all of them at its join.
     auto load_w = [&](int t, int u) { w[t].load(rsw[t], lead[t], place, u, lane, a.K, u < units); };
-    int u = wave;
-    x.load(rsx, ldb, u, lane, a.M, a.K, u < units);
-#pragma unroll
-    for (int t = 0; t < RT; ++t) load_w(t, u);
-    for (; u < units; u += NW) {
-        // the previous unit's reads of the strip come before in the wave's LDS
-        // order; only the compiler must keep both
+    // The activations' strip: the previous step's reads come before in the
+    // wave's LDS order; only the compiler must keep both.
+    auto next_x = [&](int u, int ph) {
         asm volatile("" ::: "memory");
         x.store(xl, lane);
         asm volatile("" ::: "memory");
-        x.load(rsx, ldb, u + NW, lane, a.M, a.K, u + NW < units);
+        x.load(rsx, ldb, u, ph, lane, a.M, a.K, u < units);
+    };
+    auto unpack = [&](int t, int u) {
+        const auto p = w[t].unpack(wl, lead[t], a.ldw, u, lane, a.K);
+        load_w(t, u + NW);
+        return p;
+    };
+    auto multiply = [&](int t, auto &&p, auto f, const half8 (&xf)[MF]) {
+        const half8 wf = p.template frag<decltype(f)::value>();
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const auto p = w[t].unpack(wl, lead[t], a.ldw, u, lane, a.K);
-            load_w(t, u + NW);
+        for (int i = 0; i < MF; ++i)
+            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, xf[i], acc[t][i], 0, 0, 0);
+    };
+    auto x_frags = [&](int s, half8 (&xf)[MF]) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) xf[i] = XU::frag(xl, i, r16, g, s);
+    };
+    int u = wave;
+    x.load(rsx, ldb, u, 0, lane, a.M, a.K, u < units);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) load_w(t, u);
+    for (; u < units; u += NW) {
+        if constexpr (PH == 1) {
+            next_x(u + NW, 0);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const auto p = unpack(t, u);
+                for_const<0, NF>([&](auto f) {
+                    half8 xf[MF];
+                    x_frags(decltype(f)::value, xf);
+                    multiply(t, p, f, xf);
+                });
+            }
+        } else {
+            next_x(u, 1);
+            typename Unit::Unpacked p[RT];
+#pragma unroll
+            for (int t = 0; t < RT; ++t) p[t] = unpack(t, u);
             for_const<0, NF>([&](auto f) {
                 constexpr int S = decltype(f)::value;
-                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    p.template frag<S>(), XU::frag(xl, r16, g, S), acc[t], 0, 0, 0);
+                if constexpr (S == NF / 2) next_x(u + NW, 0);
+                half8 xf[MF];
+                x_frags(S, xf);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) multiply(t, p[t], f, xf);
             });
         }
     }
@@ -548,17 +608,20 @@ __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_row
     asm volatile("" ::: "memory");
     f32x4 *const sums = reinterpret_cast<f32x4 *>(strips);
 #pragma unroll
-    for (int t = 0; t < RT; ++t) sums[wave * SC + t * 64 + lane] = acc[t];
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int f = 0; f < MF; ++f) sums[wave * SC + (t * MF + f) * 64 + lane] = acc[t][f];
     __syncthreads();
     if (n <= 0) return;
-    const int ot = GLU ? 0 : wave;
-    f32x4 s = sums[ot * 64 + lane];
-    for (int i = 1; i < NW; ++i) s += sums[i * SC + ot * 64 + lane];
+    const int at = (GLU ? of : wave) * 64 + lane;
+    f32x4 s = sums[at];
+    for (int i = 1; i < NW; ++i) s += sums[i * SC + at];
     float y[4] = {s.x + b0[0], s.y + b0[1], s.z + b0[2], s.w + b0[3]};
     apply_act(a.act, y);
     if constexpr (GLU) {
-        f32x4 v = sums[64 + lane];
-        for (int i = 1; i < NW; ++i) v += sums[i * SC + 64 + lane];
+        const int up = (MF + of) * 64 + lane;
+        f32x4 v = sums[up];
+        for (int i = 1; i < NW; ++i) v += sums[i * SC + up];
         y[0] *= v.x + b1[0];
         y[1] *= v.y + b1[1];
         y[2] *= v.z + b1[2];
@@ -567,7 +630,7 @@ __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 4 ? 3 : 4) void linear_row
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] += res[j];
     }
-    store_upto4((char *)a.Y + (int64_t)r16 * a.ldy * (a.y_type == kTypeF32 ? 4 : 2), a.y_type, col,
+    store_upto4((char *)a.Y + (int64_t)row * a.ldy * (a.y_type == kTypeF32 ? 4 : 2), a.y_type, col,
                 n, y);
 }
 
@@ -633,8 +696,11 @@ hipError_t launch_linear_rows(int fmt, bool x_f32, const void *X, int ldx, const
     if (M <= 4)
         return x_f32 ? launch_rows_any<true, 4>(fmt, a, epi.glu, stream)
                      : launch_rows_any<false, 4>(fmt, a, epi.glu, stream);
-    return x_f32 ? launch_rows_any<true, 16>(fmt, a, epi.glu, stream)
-                 : launch_rows_any<false, 16>(fmt, a, epi.glu, stream);
+    if (M <= 16)
+        return x_f32 ? launch_rows_any<true, 16>(fmt, a, epi.glu, stream)
+                     : launch_rows_any<false, 16>(fmt, a, epi.glu, stream);
+    return x_f32 ? launch_rows_any<true, 32>(fmt, a, epi.glu, stream)
+                 : launch_rows_any<false, 32>(fmt, a, epi.glu, stream);
 }
 
 }  // namespace mq

@@ -130,7 +130,7 @@ hipError_t launch_gemm_glu(int fmt, const uint16_t *X, int ldx, const void *W, i
 
 // The same for at most kRowsMaxM activation rows, f32 or f16 (linear_rows.hip):
 // one kernel, no workspace.
-constexpr int kRowsMaxM = 16;
+constexpr int kRowsMaxM = 32;
 hipError_t launch_linear_rows(int fmt, bool x_f32, const void *X, int ldx, const void *W,
                               int64_t ldw, void *Y, int ldy, int M, int N, int K,
                               const EpiSpec &epi, hipStream_t stream);

@@ -164,7 +164,8 @@ def check_glu(fmt, M, N, K, xt="f16", bias=True, act="silu", yt="f16", split=0, 
 # sizes: few rows, a row tile and one more, ragged and odd columns, wide outputs
 # that take 256 x 256 tiles (more than 192 of them), long K split over the tail
 SHAPES = [(1, 64, 256), (1, 1, 512), (2, 333, 512), (5, 130, 1024), (8, 1000, 768),
-          (13, 257, 2048), (16, 96, 512), (17, 100, 256), (33, 515, 512), (64, 128, 512),
+          (13, 257, 2048), (16, 96, 512), (17, 100, 256),
+          (24, 33, 4096), (31, 8209, 256), (32, 515, 1280), (33, 515, 512), (64, 128, 512),
           (65, 129, 256), (100, 300, 1024), (128, 256, 512), (200, 520, 768), (257, 1001, 512),
           (300, 640, 4096)]
 
@@ -190,7 +191,7 @@ def test_glu_shapes(fmt, shape):
 def test_part_units(fmt, K):
     """Rows that end inside a unit of 256 and inside a lane's pair of blocks;
     the last weight row's end is the buffer's."""
-    for M in (1, 4, 5, 16):
+    for M in (1, 4, 5, 16, 17, 32):
         check_linear(fmt, M, 47, K, act="silu", rt="f32", yt="f32", seed=K)
         check_glu(fmt, M, 31, K, yt="f32", seed=K)
     if fmt == 0:
@@ -210,6 +211,8 @@ def test_few_rows_see_the_cache_weights(fmt):
     got = torch.cat([mq.linear_fused(eye[k:k + 16], q, fmt, N, K) for k in range(0, K, 16)])
     assert torch.equal(got.t(), want)
     got = torch.cat([mq.linear_fused(eye[k:k + 3].float(), q, fmt, N, K) for k in range(0, K, 3)])
+    assert torch.equal(got.t(), want)
+    got = torch.cat([mq.linear_fused(eye[k:k + 32], q, fmt, N, K) for k in range(0, K, 32)])
     assert torch.equal(got.t(), want)
 
 
