@@ -33,6 +33,8 @@
 namespace mq {
 namespace {
 
+constexpr int kCUs = 256;   // MI355X compute units
+
 struct RowsArgs {
     const void *X;
     const uint8_t *W;
@@ -93,25 +95,27 @@ __device__ __forceinline__ uint32_t spread4(uint32_t b) {
 template <int FMT>
 struct RowUnit;
 
-// f16: the fragments are loaded as they are used, 64 contiguous bytes of each
-// row per load.
+// f16: 256 contiguous bytes of each row (four rows per load) through the wave's
+// strip of LDS; chunk c of row r lies at c ^ r, so that the 16 rows of a
+// fragment lie in distinct banks.
 template <>
 struct RowUnit<kFmtF16> {
-    static constexpr int NF = 4, UK = 128, STRIP = 0;
+    static constexpr int NF = 4, UK = 128, STRIP = 256;
     u32x4 v[NF];
     struct Place {
-        uint32_t row;
+        uint32_t o;
+        int64_t ld4;
         __device__ __forceinline__ void init(int lane, int64_t ldw) {
-            row = (uint32_t)((lane & 15) * ldw);
+            o = (uint32_t)((lane >> 4) * ldw) + 16u * (lane & 15);
+            ld4 = 4 * ldw;
         }
     };
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t, const Place &at, int u,
                                          int lane, int K, bool live) {
+        const int k = u * UK + 8 * (lane & 15);
+        const uint32_t o = live && k < K ? at.o + (uint32_t)u * (2 * UK) : kOOB;
 #pragma unroll
-        for (int s = 0; s < NF; ++s) {
-            const int k = u * UK + kofs(lane >> 4, s);
-            v[s] = buf_load16(rs, live && k < K ? at.row + 2 * k : kOOB);
-        }
+        for (int j = 0; j < NF; ++j) v[j] = buf_load16(rs, o + (uint32_t)(j * at.ld4));
     }
     struct Unpacked {
         u32x4 v[NF];
@@ -120,10 +124,19 @@ struct RowUnit<kFmtF16> {
             return __builtin_bit_cast(half8, v[S]);
         }
     };
-    __device__ __forceinline__ Unpacked unpack(u32x4 *, uint32_t, int64_t, int, int, int) const {
-        Unpacked p;
+    __device__ __forceinline__ Unpacked unpack(u32x4 *strip, uint32_t, int64_t, int, int lane,
+                                               int) const {
+        asm volatile("" ::: "memory");
 #pragma unroll
-        for (int s = 0; s < NF; ++s) p.v[s] = v[s];
+        for (int j = 0; j < NF; ++j) {
+            const int r = 4 * j + (lane >> 4);
+            strip[16 * r + ((lane & 15) ^ r)] = v[j];
+        }
+        asm volatile("" ::: "memory");
+        Unpacked p;
+        const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int s = 0; s < NF; ++s) p.v[s] = strip[16 * r + ((4 * s + g) ^ r)];
         return p;
     }
     static __device__ __forceinline__ int kofs(int g, int s) { return 32 * s + 8 * g; }
@@ -465,15 +478,17 @@ __device__ __forceinline__ void for_const(F &&f) {
     }
 }
 
-// Steps per unit: the 32-chunk units' activations in halves from 16 rows on.
-template <class Unit, int MR>
-constexpr int kPhases = Unit::UK == 256 && MR >= 16 ? 2 : 1;
+// Steps per unit: the 32-chunk units' activations in halves where a whole unit
+// of 32 rows, or of 16 in f32, would not fit the registers (16 f16 rows in
+// halves: gated 14336 x 4096 Q4_K 26 -> 31 us).
+template <class Unit, int MR, bool XF32>
+constexpr int kPhases = Unit::UK == 256 && (MR > 16 || (MR == 16 && XF32)) ? 2 : 1;
 
 // The LDS strip of a wave: its activations and a tile's raw bytes, then its
 // sums.
-template <class Unit, int RT, int MR>
+template <class Unit, int RT, int MR, bool XF32>
 constexpr int strip_chunks() {
-    const int need = MR * Unit::UK / 8 / kPhases<Unit, MR> + Unit::STRIP;
+    const int need = MR * Unit::UK / 8 / kPhases<Unit, MR, XF32> + Unit::STRIP;
     const int sums = RT * (MR > 16 ? MR / 16 : 1) * 64;
     return need > sums ? need : sums;
 }
@@ -484,15 +499,15 @@ constexpr int strip_chunks() {
 // SIMD (with half of them the loads in flight do not cover the memory's
 // latency), 3 with 16 rows and 2 with 32, whose activations and sums take more.
 template <int MR>
-constexpr int kMaxWaves = MR > 4 ? 8 : 16;
+constexpr int kMaxWaves = MR > 16 ? 8 : MR > 4 ? 12 : 16;   // per compute unit
 template <int FMT, int RT, bool GLU, bool XF32, int MR>
 __global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 16 ? 2 : MR > 4 ? 3 : 4) void
 linear_rows_kernel(RowsArgs a) {
     static_assert(!GLU || RT == 2, "a gate tile and an up tile");
     using Unit = RowUnit<FMT>;
-    constexpr int PH = kPhases<Unit, MR>, MF = MR > 16 ? MR / 16 : 1;
+    constexpr int PH = kPhases<Unit, MR, XF32>, MF = MR > 16 ? MR / 16 : 1;
     using XU = XUnit<Unit, MR, XF32, PH>;
-    constexpr int NF = Unit::NF, SC = strip_chunks<Unit, RT, MR>();
+    constexpr int NF = Unit::NF, SC = strip_chunks<Unit, RT, MR, XF32>();
     extern __shared__ u32x4 strips[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -640,9 +655,18 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
     const int cols = GLU ? 16 : 16 * RT;
     const int tiles = (a.N + cols - 1) / cols;
     const int units = (a.K + Unit::UK - 1) / Unit::UK;
-    int nw = MR <= 4 && tiles * 16 <= 4096 ? 16 : tiles * 8 <= 4096 ? 8 : 4;
-    while (nw > 4 && nw / 2 >= units) nw /= 2;
-    const size_t lds = nw * (size_t)(strip_chunks<Unit, RT, MR>()) * 16;
+    // As many waves per workgroup as let all workgroups be resident at once
+    // (a second round of a few left over costs as much as the first: 288 tiles
+    // on 256 compute units, f16 4608 x 3584 at M = 24, 15.5 us with 8 waves
+    // each, 13.8 with 4), no more than there are units, and at least the RT·MF that
+    // finish the sums.
+    const int per_cu = (tiles + kCUs - 1) / kCUs;
+    int nw = kMaxWaves<MR> / per_cu;
+    if (nw < 3) nw = 4;
+    if (nw > units) nw = units;
+    const int finish = (GLU ? 1 : RT) * (MR > 16 ? MR / 16 : 1);
+    if (nw < finish) nw = finish;
+    const size_t lds = nw * (size_t)(strip_chunks<Unit, RT, MR, XF32>()) * 16;
     hipLaunchKernelGGL((linear_rows_kernel<FMT, RT, GLU, XF32, MR>), dim3(tiles), dim3(64 * nw),
                        lds, stream, a);
     return hipGetLastError();

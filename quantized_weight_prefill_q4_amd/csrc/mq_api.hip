@@ -260,7 +260,7 @@ struct LinearPlan {
 
 LinearPlan linear_plan(int fmt, int x_type, int M, int rows, int K, int split_k) {
     LinearPlan p;
-    p.rows = M <= mq::kRowsMaxM && split_k == 0;
+    p.rows = split_k == 0 && mq::linear_rows_fit(fmt, M, rows, K);
     p.ld16 = 0;
     p.x16_bytes = 0;
     p.ws_bytes = 0;

@@ -128,12 +128,23 @@ hipError_t launch_gemm_glu(int fmt, const uint16_t *X, int ldx, const void *W, i
                            void *Y, int ldy, int M, int N, int K, const GemmPlan &plan, float *ws,
                            const EpiSpec &epi, hipStream_t stream);
 
-// The same for at most kRowsMaxM activation rows, f32 or f16 (linear_rows.hip):
-// one kernel, no workspace.
-constexpr int kRowsMaxM = 32;
+// The same for at most 32 activation rows, f32 or f16 (linear_rows.hip): one
+// kernel, no workspace.
 hipError_t launch_linear_rows(int fmt, bool x_f32, const void *X, int ldx, const void *W,
                               int64_t ldw, void *Y, int ldy, int M, int N, int K,
                               const EpiSpec &epi, hipStream_t stream);
+
+// Whether the few-row kernel is the faster one for M rows and a weight of
+// `rows` rows: always up to 16, and up to 32 (two products per expanded
+// weight, half a unit of activations at a time) except for a large f16 cache,
+// which the tile kernel streams faster.  M = 32, few-row kernel against tile
+// kernel: Q4_K 14336 x 4096 21 / 28 us, 3584 x 3584 9 / 12.6, Q6_K 3584 x 18944
+// 29 / 39; f16 3584 x 3584 9.8 / 12.8, 14336 x 4096 28 / 29.5, but 3584 x 18944
+// 38 / 32 and 28672 x 4096 52 / 46 (at M = 16 30 / 32 and 46 / 44).
+inline bool linear_rows_fit(int fmt, int M, int rows, int K) {
+    if (M <= 16) return true;
+    return M <= 32 && (fmt != kFmtF16 || (int64_t)rows * K < (int64_t)1 << 26);
+}
 
 // Residual addition and RMS norm (arguments already validated).  r == nullptr:
 // no residual, h unused.  y_type kTypeI8: y holds int8 codes (row stride ldy
