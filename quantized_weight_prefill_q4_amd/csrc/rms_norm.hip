@@ -94,11 +94,12 @@ __device__ __forceinline__ void store8(void *row, int type, int c, int K, const 
 
 __device__ __forceinline__ int64_t elem_bytes(int type) { return type == kTypeF32 ? 4 : 2; }
 
-// Sum over the T threads of a row group (T a power of two >= 64: whole waves).
+// Sum over the T threads of a row group (T a power of two: part of a wave, or
+// whole waves).
 template <int T>
 __device__ __forceinline__ float group_sum(float s, float *lds) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    for (int o = T < 64 ? T / 2 : 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
     if constexpr (T > 64) {
         const int wave = threadIdx.x >> 6, first = wave & ~(T / 64 - 1);
         if ((threadIdx.x & 63) == 0) lds[wave] = s;
@@ -245,9 +246,20 @@ hipError_t launch_add_rms_norm(const NormSpec &n, hipStream_t stream) {
     a.r_type = n.r_type;
     a.y_type = n.y_type;
     a.eps = n.eps;
+    // One chunk per thread, T the power of two that covers the row: fewer
+    // threads leave too few loads in flight (1 x 3584, f32 in, f16 out: 512
+    // threads 2.8 us, 64 threads of 8 chunks 6.6), more stand idle (4099 x 1001
+    // f16: 128 threads 9.9 us, 256 11.5; 16384 x 128 f32: 16 threads 7.7, 64
+    // 11.0).  With enough rows to fill the chip, two chunks per thread save
+    // half the cross-wave sums from 257 chunks on (2048 x 3584: 20.7 us, 4.96
+    // TB/s, against 21.7; a plain device copy reaches 4.9).
     const int chunks = (n.K + 7) / 8;
+    if (chunks <= 16) return launch_rows<16, 1, 256>(a, stream);
+    if (chunks <= 32) return launch_rows<32, 1, 256>(a, stream);
     if (chunks <= 64) return launch_rows<64, 1, 256>(a, stream);
+    if (chunks <= 128) return launch_rows<128, 1, 256>(a, stream);
     if (chunks <= 256) return launch_rows<256, 1, 256>(a, stream);
+    if (chunks <= 512 && n.M >= 1024) return launch_rows<256, 2, 256>(a, stream);
     if (chunks <= 512) return launch_rows<512, 1, 512>(a, stream);
     if (chunks <= 1024) return launch_rows<1024, 1, 1024>(a, stream);
     if (chunks <= 2048) return launch_rows<1024, 2, 1024>(a, stream);

@@ -91,11 +91,13 @@ def test_types(xt, rt, yt):
         _check(9, K, xt, rt, yt, pad, lead)
 
 
-@pytest.mark.parametrize("M", [1, 3, 4, 255, 1030, 4099])
+@pytest.mark.parametrize("M", [1, 3, 4, 17, 255, 1030, 4099])
 def test_row_counts(M):
     _check(M, 1001, "f16", "f16", "f16", 7, 0)
     _check(M, 3584, "f32", "f32", "f16", 0, 0)
     _check(M, 96, "f32", None, "f32", 0, 0)
+    _check(M, 200, "f16", "f32", "f16", 1, 1)
+    _check(M, 2300, "f16", "f32", "f32", 0, 0)
 
 
 @pytest.mark.parametrize("M,K", [(1, 32), (1, 3584), (3, 96), (7, 4096), (300, 3584), (2, 16384),
