@@ -495,13 +495,14 @@ constexpr int strip_chunks() {
 
 // RT tiles of 16 weight rows per workgroup of blockDim.x / 64 waves, at least
 // the RT·MF whose sums they finish (gated: a gate tile and its up tile, RT =
-// 2); MR: activation rows held.  Registers are capped so that 4 waves share a
-// SIMD (with half of them the loads in flight do not cover the memory's
-// latency), 3 with 16 rows and 2 with 32, whose activations and sums take more.
+// 2); MR: activation rows held (4, 8, 16 or 32).  Registers are capped so that 4
+// waves share a SIMD (with half of them the loads in flight do not cover the
+// memory's latency), 3 with 16 rows and 2 with 32, whose activations and sums
+// take more.
 template <int MR>
-constexpr int kMaxWaves = MR > 16 ? 8 : MR > 4 ? 12 : 16;   // per compute unit
+constexpr int kMaxWaves = MR > 16 ? 8 : MR > 8 ? 12 : 16;   // per compute unit
 template <int FMT, int RT, bool GLU, bool XF32, int MR>
-__global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 16 ? 2 : MR > 4 ? 3 : 4) void
+__global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 16 ? 2 : MR > 8 ? 3 : 4) void
 linear_rows_kernel(RowsArgs a) {
     static_assert(!GLU || RT == 2, "a gate tile and an up tile");
     using Unit = RowUnit<FMT>;
@@ -675,8 +676,13 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
 template <int FMT, bool XF32, int MR>
 hipError_t launch_rows_fmt(const RowsArgs &a, bool glu, hipStream_t stream) {
     if (glu) return launch_rows<FMT, 2, true, XF32, MR>(a, stream);
-    if constexpr (MR > 4) {
-        if (a.N > 16 * 512) return launch_rows<FMT, 2, false, XF32, MR>(a, stream);
+    // Two weight tiles per wave on the same activations where loading those
+    // costs more than the tile's own registers do: with 32 rows, and with 16 for
+    // the f16 cache, once one tile per workgroup would be more than two rounds of
+    // the chip (M = 32, 14336 x 4096: Q4_K 31 -> 21 us, Q8_0 38 -> 28; M = 16 f16
+    // 27 -> 25, but Q8_0 24 -> 26).
+    if constexpr (MR > 16 || (MR == 16 && FMT == kFmtF16)) {
+        if (a.N > 16 * 2 * kCUs) return launch_rows<FMT, 2, false, XF32, MR>(a, stream);
     }
     return launch_rows<FMT, 1, false, XF32, MR>(a, stream);
 }
@@ -720,6 +726,9 @@ hipError_t launch_linear_rows(int fmt, bool x_f32, const void *X, int ldx, const
     if (M <= 4)
         return x_f32 ? launch_rows_any<true, 4>(fmt, a, epi.glu, stream)
                      : launch_rows_any<false, 4>(fmt, a, epi.glu, stream);
+    if (M <= 8)
+        return x_f32 ? launch_rows_any<true, 8>(fmt, a, epi.glu, stream)
+                     : launch_rows_any<false, 8>(fmt, a, epi.glu, stream);
     if (M <= 16)
         return x_f32 ? launch_rows_any<true, 16>(fmt, a, epi.glu, stream)
                      : launch_rows_any<false, 16>(fmt, a, epi.glu, stream);
