@@ -349,8 +349,8 @@ int mq_gemm_mmq(int fmt, const int8_t *Xq, int ldq, const float *ds, const void 
  *   R, ldr  : device, r_type, row stride ldr >= N, or NULL (no residual; r_type
  *             and ldr are then ignored).  R may be Y itself (same pointer,
  *             stride and type): the residual stream updated in place.
- *   Y       : device, y_type, row stride ldy >= N.  Y may not overlap any other
- *             buffer of the call, or R in any other way.
+ *   Y       : device, y_type, row stride ldy >= N.  Neither Y nor ws may overlap
+ *             another buffer of the call (but for Y being R itself).
  *   ws      : device, 16-byte aligned, ws_bytes >=
  *             mq_linear_workspace_bytes(fmt or 0, x_type, M, N, K, split_k); may
  *             be NULL when that is 0.  Calls that may overlap in time need a

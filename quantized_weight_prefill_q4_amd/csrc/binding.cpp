@@ -85,16 +85,15 @@ void matrix_form(const at::Tensor &t, const char *name) {
     if (t.dim() != 2 || (t.stride(1) != 1 && t.size(1) > 1))
         refuse("%s must be 2-D with unit column stride", name);
 }
-// The row stride of a row-major matrix of at least rows × cols; the stride of
-// a single row is never used.
+// The row stride of a row-major matrix of at least rows × cols; for a single
+// row, whose stride is never used (a slice may carry any), its width.
 int matrix(const at::Tensor &t, int dev, int64_t rows, int64_t cols, const char *name) {
     matrix_form(t, name);
     if (t.size(0) < rows || t.size(1) < cols)
         refuse("%s must be at least %lld x %lld, got (%lld, %lld)", name, (long long)rows,
                (long long)cols, (long long)t.size(0), (long long)t.size(1));
     same_device(t, dev, name);
-    const int64_t ld = t.stride(0);
-    return to_int(t.size(0) > 1 || ld > cols ? ld : cols);
+    return to_int(t.size(0) > 1 ? t.stride(0) : cols);
 }
 
 const float *vector(const at::Tensor &t, int dev, int64_t n, const char *name) {

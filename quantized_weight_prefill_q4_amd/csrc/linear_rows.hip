@@ -667,6 +667,8 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
     if (nw > units) nw = units;
     const int finish = (GLU ? 1 : RT) * (MR > 16 ? MR / 16 : 1);
     if (nw < finish) nw = finish;
+    static_assert(kMaxWaves<MR> * strip_chunks<Unit, RT, MR, XF32>() * 16 <= 160 * 1024,
+                  "the strips of the most waves fit a compute unit's LDS");
     const size_t lds = nw * (size_t)(strip_chunks<Unit, RT, MR, XF32>()) * 16;
     hipLaunchKernelGGL((linear_rows_kernel<FMT, RT, GLU, XF32, MR>), dim3(tiles), dim3(64 * nw),
                        lds, stream, a);

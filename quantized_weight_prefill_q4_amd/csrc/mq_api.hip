@@ -259,11 +259,8 @@ struct LinearPlan {
 };
 
 LinearPlan linear_plan(int fmt, int x_type, int M, int rows, int K, int split_k) {
-    LinearPlan p;
+    LinearPlan p{};
     p.rows = split_k == 0 && mq::linear_rows_fit(fmt, M, rows, K);
-    p.ld16 = 0;
-    p.x16_bytes = 0;
-    p.ws_bytes = 0;
     if (p.rows) return p;
     if (x_type == MQ_F32) {
         p.ld16 = (int)mq_f16cache_ld(K);
@@ -318,16 +315,19 @@ int run_linear(int fmt, int x_type, const void *X, int ldx, const void *W, int64
         fmt == mq::kFmtF16 ? ldw * 2 : (int64_t)K / mq::block_elems(fmt) * mq::block_bytes(fmt);
     auto bytes = [](int type) { return (int64_t)(type == MQ_F32 ? 4 : 2); };
     const Span y = span(Y, ldy, N, bytes(y_type), M);
-    const Span others[] = {span(X, ldx, K, bytes(x_type), M),
-                           Span{(const char *)W, wbytes, fmt == mq::kFmtF16 ? 2 * (int64_t)K : wbytes, rows},
-                           span(epi.bias, rows, epi.bias ? rows : 0, 4, 1),
-                           span(ws, p.ws_bytes, p.ws_bytes, 1, 1)};
-    for (const Span &o : others)
-        if (o.p && o.row > 0 && overlap(y, o)) return MQ_ERR_OVERLAP;
-    if (epi.res) {
-        const Span r = span(epi.res, epi.ldr, N, bytes(epi.res_type), M);
-        if (overlap(y, r) && !same_span(y, r)) return MQ_ERR_OVERLAP;
-    }
+    // an absent buffer has no rows' bytes and overlaps nothing
+    auto clash = [](const Span &p, const Span &q) {
+        return p.row > 0 && q.row > 0 && overlap(p, q);
+    };
+    const Span x = span(X, ldx, K, bytes(x_type), M);
+    const Span w{(const char *)W, wbytes, fmt == mq::kFmtF16 ? 2 * (int64_t)K : wbytes, rows};
+    const Span b = span(epi.bias, rows, epi.bias ? rows : 0, 4, 1);
+    const Span r = span(epi.res, epi.ldr, epi.res ? N : 0, bytes(epi.res_type), M);
+    const Span work = span(ws, p.ws_bytes, p.ws_bytes, 1, 1);
+    if (clash(y, x) || clash(y, w) || clash(y, b) || (clash(y, r) && !same_span(y, r)))
+        return MQ_ERR_OVERLAP;
+    if (clash(work, x) || clash(work, w) || clash(work, b) || clash(work, r) || clash(work, y))
+        return MQ_ERR_OVERLAP;
     if (p.rows)
         return hip_status(mq::launch_linear_rows(fmt, x_type == MQ_F32, X, ldx, W,
                                                  fmt == mq::kFmtF16 ? ldw : wbytes, Y, ldy, M, N,

@@ -199,6 +199,34 @@ def test_part_units(fmt, K):
         check_linear(fmt, 9, 33, K + 8, xt="f32", yt="f32", seed=K)
 
 
+@pytest.mark.parametrize("fmt", [0] + FMTS)
+def test_long_rows(fmt):
+    """As many waves per workgroup as each number of rows can have (K of 16
+    units and more), their LDS up to the compute unit's; and one tile too few
+    or too many for a round of the chip."""
+    for M in (2, 8, 16, 31):
+        check_linear(fmt, M, 40, 5120, act="silu", rt="f32", yt="f32", seed=M)
+        check_glu(fmt, M, 33, 4096, xt="f32", yt="f32", seed=M)
+    check_linear(fmt, 3, 4128, 1024, rt="f16", yt="f16")
+    check_glu(fmt, 9, 2064, 768, yt="f16")
+
+
+def test_one_row_of_a_wider_buffer():
+    """The stride of a single row is of no account."""
+    K, N = 256, 48
+    announce("single row, any stride")
+    w, _ = _weight(0, N, K, 31)
+    x, _ = _x(3, K, "f16", 31)
+    buf = torch.zeros(3, K + 8, dtype=torch.float16, device=dev())
+    buf[:, :K] = x
+    odd = buf.view(-1)[:3 * (K + 8)].as_strided((1, K), (K + 3, 1))
+    assert torch.equal(mq.linear_f16cache(odd, w, K), mq.linear_f16cache(x[:1], w, K))
+    out = torch.zeros(1, N + 5, device=dev())
+    mq.linear_f16cache(x[:1], w, K, out=out[:, :N].as_strided((1, N), (3, 1)))
+    assert torch.equal(out[:, :N], mq.linear_f16cache(x[:1], w, K))
+    assert torch.equal(mq.glu_f16cache(odd, w, K), mq.glu_f16cache(x[:1], w, K))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_few_rows_see_the_cache_weights(fmt):
     """One-hot activations read every weight back: the few-row kernels expand

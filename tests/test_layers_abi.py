@@ -112,6 +112,9 @@ LAYER_BAD = [
     (dict(split=4, ws=D, wsb=100), _lib.MQ_ERR_WORKSPACE),
     (dict(split=4, ws=D + 8, wsb=1 << 30), _lib.MQ_ERR_WORKSPACE),
     (dict(split=4, ws=Y + 64, wsb=1 << 30), _lib.MQ_ERR_OVERLAP),
+    (dict(split=4, ws=FAKE + 1024, wsb=1 << 30), _lib.MQ_ERR_OVERLAP),
+    (dict(split=4, ws=W + 1024, wsb=1 << 30), _lib.MQ_ERR_OVERLAP),
+    (dict(split=4, ws=H, wsb=1 << 30), _lib.MQ_ERR_OVERLAP),
     (dict(Y=FAKE, ldx=512, ldy=96), _lib.MQ_ERR_OVERLAP),      # x's place
     (dict(Y=W), _lib.MQ_ERR_OVERLAP), (dict(Y=H), _lib.MQ_ERR_OVERLAP),
 ]
@@ -140,6 +143,20 @@ def test_fused_layers_refuse(L, fmt, bad, code):
 ])
 def test_residuals_refused(L, bad, code):
     assert _linear(L, **bad) == code and _linear(L, 12, **bad) == code
+
+
+def test_few_rows_need_no_workspace(L):
+    for xt in (F16, F32):
+        for M in (1, 4, 16):
+            assert L.mq_linear_workspace_bytes(0, xt, M, 3584, 18944, 0) == 0
+            assert L.mq_glu_workspace_bytes(14, xt, M, 14336, 4096, 0) == 0
+        assert L.mq_linear_workspace_bytes(12, xt, 32, 14336, 4096, 0) == 0
+        assert L.mq_linear_workspace_bytes(0, xt, 32, 3584, 3584, 0) == 0
+    # a split asked for is the tile kernel's, at any M
+    assert L.mq_linear_workspace_bytes(0, F16, 1, 128, 512, 2) == 2 * 64 * 128 * 4
+    # from 17 rows on a large f16 cache takes the tile kernel, too
+    assert L.mq_linear_workspace_bytes(0, F16, 17, 3584, 18944, 0) == \
+        L.mq_gemm_workspace_bytes(0, 17, 3584, 18944, 0) > 0
 
 
 def test_unknown_formats(L):
