@@ -267,6 +267,13 @@ LinearPlan linear_plan(int fmt, int x_type, int M, int rows, int K, int split_k)
         p.x16_bytes = ((int64_t)M * p.ld16 * 2 + 255) / 256 * 256;
     }
     p.gemm = mq::plan_gemm(fmt, M, rows, K, split_k);
+    // A short K over a quarter of a round of tiles or more is not worth the
+    // planes and the second kernel of a split (f16 512 x 2048 x 512: 11.5 us
+    // split two ways, 8.3 whole; Q4_K 200 x 8192 x 512 14.8 / 11.1, x 1024 17.6 /
+    // 16.0; with 48 tiles the split is ahead from K = 1024 on, 10.2 / 11.1).
+    if (split_k == 0 && p.gemm.split > 1 && p.gemm.dp_tiles == 0 && p.gemm.tail_tiles >= 64 &&
+        K <= 1024)
+        p.gemm = mq::plan_gemm(fmt, M, rows, K, 1);
     p.ws_bytes = p.x16_bytes + p.gemm.ws_bytes;
     return p;
 }

@@ -145,6 +145,14 @@ def test_residuals_refused(L, bad, code):
     assert _linear(L, **bad) == code and _linear(L, 12, **bad) == code
 
 
+def test_short_k_is_not_split_over_many_tiles(L):
+    assert L.mq_gemm_workspace_bytes(0, 512, 2048, 512, 0) > 0
+    assert L.mq_linear_workspace_bytes(0, F16, 512, 2048, 512, 0) == 0
+    assert L.mq_glu_workspace_bytes(0, F16, 512, 1024, 512, 0) == 0
+    assert L.mq_linear_workspace_bytes(0, F16, 512, 2048, 512, 2) > 0        # asked for
+    assert L.mq_linear_workspace_bytes(0, F16, 512, 2048, 1032, 0) > 0
+
+
 def test_few_rows_need_no_workspace(L):
     for xt in (F16, F32):
         for M in (1, 4, 16):
