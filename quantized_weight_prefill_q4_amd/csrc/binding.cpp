@@ -1,8 +1,9 @@
 // The torch side of the layer operators (layers.py): argument checks, output
 // and workspace allocation and the call of libmq's C entry points, in one
 // native call per operator.  A single-token layer is a few microseconds of GPU
-// time; the same checks made from Python and passed through ctypes cost about
-// as much again as the launch itself (10.5 us per call against 5 us here).
+// time; the same checks made from Python and passed through ctypes take 10.5 us
+// (linear) and 11.8 us (norm) of host time per call, here 5.8 and 6.2, of which
+// the launch itself is 3.9.
 //
 // The module holds no library of its own: layers.py hands it the addresses of
 // the entry points of the loaded libmq (bind()).  Checks that fail raise

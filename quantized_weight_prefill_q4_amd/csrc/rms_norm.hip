@@ -18,6 +18,10 @@
 // that the same thread wrote (or x).  Rows need no alignment: 16-byte
 // accesses at the element's own alignment; only a last chunk of fewer than 8
 // elements goes element by element.
+// Measured: 2048 x 3584 (f32 in, f16 or Q8_1 out) 20.7 us = 4.96 TB/s, 2048 x
+// 8192 41.7 us = 5.6 TB/s (a plain device copy: 4.9), 4099 x 1001 f16 at an odd
+// stride 9.9 us = 3.3 TB/s (one short row per two waves: latency), one row of
+// 3584 2.5 us, the least a kernel of one round trip takes.
 
 #include "mq_device.h"
 #include "mq_internal.h"
@@ -36,7 +40,7 @@ struct NormArgs {
     float *ds;
     int64_t ldx, ldr, ldh, ldy;
     int M, K;
-    int x_type, r_type, y_type;   // kF32 / kF16; y also kI8 (Q8_1 blocks)
+    int x_type, r_type, y_type;   // kTypeF32 / kTypeF16; y also kTypeI8 (Q8_1 blocks)
     float eps;
 };
 
