@@ -75,13 +75,33 @@ __device__ __forceinline__ half8 frag_codes(uint32_t e0, uint32_t e1, uint32_t e
     return __builtin_bit_cast(half8, v);
 }
 
-// The same from two dwords of byte codes (at most 8 bits each).
+// Where the value is one product of the f16 scale and a small integer, d·(u -
+// OFF), its f32 product is exact and the f16 product rounds alike: from two
+// dwords of byte codes u, as the f16 numbers 1024 + u (0x6400 | u), two
+// weights to an instruction (1.5 per weight; Q8_0 2.5 and Q4_0 2.2 by the fma
+// above.  v_fma_mixlo_f16 / mixhi, one per weight in place of fma and
+// conversion, measured 4 to 7 % slower than those).
+template <int OFF>
+__device__ __forceinline__ half8 frag_products(uint32_t w0, uint32_t w1, uint32_t d2) {
+    typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+    const half2v d = __builtin_bit_cast(half2v, d2);
+    constexpr _Float16 o = (_Float16)(1024.0f + OFF);
+    auto two = [&](uint32_t w, uint32_t bytes) {
+        const uint32_t u = __builtin_amdgcn_perm(0x64646464u, w, bytes);
+        return __builtin_bit_cast(uint32_t, (__builtin_bit_cast(half2v, u) - half2v{o, o}) * d);
+    };
+    constexpr uint32_t lo = 0x04010400u, hi = 0x04030402u;
+    const u32x4 v = {two(w0, lo), two(w0, hi), two(w1, lo), two(w1, hi)};
+    return __builtin_bit_cast(half8, v);
+}
+
+// frag_codes of two dwords of byte codes (at most 8 bits each).
 __device__ __forceinline__ half8 frag_bytes(uint32_t w0, uint32_t w1, float A, float C) {
     constexpr uint32_t B = 0x00FF00FFu;
     return frag_codes(w0 & B, (w0 >> 8) & B, w1 & B, (w1 >> 8) & B, A, C);
 }
 
-// The same from the low (HIGH = 0) or high nibbles of two dwords; A scaled by
+// frag_codes of the low (HIGH = 0) or high nibbles of two dwords; A scaled by
 // kCode or kCodeHigh accordingly.
 template <int HIGH>
 __device__ __forceinline__ half8 frag_nibbles(uint32_t w0, uint32_t w1, float A, float C) {
@@ -89,8 +109,17 @@ __device__ __forceinline__ half8 frag_nibbles(uint32_t w0, uint32_t w1, float A,
     return frag_codes(w0 & L, (w0 >> 8) & L, w1 & L, (w1 >> 8) & L, A, C);
 }
 
-__device__ __forceinline__ uint32_t spread4(uint32_t b) {
-    return ((b * 0x00204081u) & 0x01010101u) << 4;
+// The same with a byte h of fifth bits, element i's at bit i.  One pair of shifts lays the bits of
+// elements 0 and 2 beside their nibbles, and one more shift each those of 1 and
+// 3, 4 and 6, 5 and 7 (spreading a nibble's bits over a dword by a
+// multiplication costs 4 cycles' worth of instructions for each).
+template <int HIGH>
+__device__ __forceinline__ half8 frag_fifths(uint32_t w0, uint32_t w1, uint32_t h, float A,
+                                             float C) {
+    constexpr uint32_t L = HIGH ? 0x00F000F0u : 0x000F000Fu, B = HIGH ? 0x01000100u : 0x00100010u;
+    const uint32_t z = (h << (HIGH ? 8 : 4)) | (h << (HIGH ? 22 : 18));
+    return frag_codes((w0 & L) | (z & B), ((w0 >> 8) & L) | ((z >> 1) & B),
+                      (w1 & L) | ((z >> 4) & B), ((w1 >> 8) & L) | ((z >> 5) & B), A, C);
 }
 
 // ---------------------------------------------------------------------------
@@ -342,7 +371,8 @@ struct BUnit : Staged<8 * b32_bytes(FMT),
     struct Unpacked {
         static constexpr int NC = 2 * BB / 4;
         uint32_t c[NC];                  // the two blocks from byte 0
-        float A[2], C[2];
+        float A[2], C[2];                // Q5_0, Q5_1: factor and offset
+        uint32_t d2[2];                  // Q4_0, Q8_0: the f16 scale, twice
         // the dword at even byte offset T of the two blocks
         template <int TO>
         __device__ __forceinline__ uint32_t dw() const {
@@ -355,24 +385,23 @@ struct BUnit : Staged<8 * b32_bytes(FMT),
         __device__ __forceinline__ half8 frag() const {
             constexpr int b = S >> 2, ch = S & 3, base = b * BB;   // block, 8-element chunk
             if constexpr (FMT == kFmtQ8_0) {
-                // q + 128 as an unsigned byte; d·(q + 128) − 128·d is exact
+                // q + 128 as an unsigned byte
                 constexpr uint32_t S8 = 0x80808080u;
-                return frag_bytes(dw<base + 2 + 8 * ch>() ^ S8, dw<base + 6 + 8 * ch>() ^ S8, A[b],
-                                  C[b]);
+                return frag_products<128>(dw<base + 2 + 8 * ch>() ^ S8, dw<base + 6 + 8 * ch>() ^ S8,
+                                          d2[b]);
             } else {
                 constexpr int QS = FMT == kFmtQ4_0 ? 2 : FMT == kFmtQ5_0 ? 6 : 8;
-                uint32_t w0 = dw<base + QS + 8 * (ch & 1)>(), w1 = dw<base + QS + 4 + 8 * (ch & 1)>();
+                const uint32_t w0 = dw<base + QS + 8 * (ch & 1)>();
+                const uint32_t w1 = dw<base + QS + 4 + 8 * (ch & 1)>();
                 if constexpr (FMT == kFmtQ4_0) {
-                    return frag_nibbles<(ch >> 1)>(w0, w1, ch >= 2 ? A[b] * (kCodeHigh / kCode) : A[b],
-                                                   C[b]);
+                    constexpr uint32_t L = 0x0F0F0F0Fu;
+                    return frag_products<8>((ch >= 2 ? w0 >> 4 : w0) & L,
+                                            (ch >= 2 ? w1 >> 4 : w1) & L, d2[b]);
                 } else {
-                    w0 = (ch >= 2 ? w0 >> 4 : w0) & 0x0F0F0F0Fu;
-                    w1 = (ch >= 2 ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
                     constexpr int QH = FMT == kFmtQ5_0 ? 2 : 4;
-                    const uint32_t hb = dw<base + QH>() >> (8 * ch);
-                    w0 |= spread4(hb & 15);
-                    w1 |= spread4((hb >> 4) & 15);
-                    return frag_bytes(w0, w1, A[b], C[b]);
+                    return frag_fifths<(ch >> 1)>(w0, w1, (dw<base + QH>() >> (8 * ch)) & 255,
+                                                  ch >= 2 ? A[b] * (kCodeHigh / kCode) : A[b],
+                                                  C[b]);
                 }
             }
         }
@@ -401,19 +430,20 @@ struct BUnit : Staged<8 * b32_bytes(FMT),
                 p.c[i] = __builtin_amdgcn_alignbyte(t[i + 1], t[i], sh);
         }
         const uint32_t h0 = p.c[0], h1 = BB % 4 ? p.c[BB / 4] >> 16 : p.c[BB / 4];
-        const float d0 = f16_bits_to_f32(h0), d1 = f16_bits_to_f32(h1);
-        const float e0 = exist > 0 ? d0 : 0.0f, e1 = exist > 1 ? d1 : 0.0f;
-        p.A[0] = kCode * e0;
-        p.A[1] = kCode * e1;
-        if constexpr (FMT == kFmtQ5_1) {
-            const float m0 = f16_bits_to_f32(h0 >> 16), m1 = f16_bits_to_f32(h1 >> 16);
-            p.C[0] = exist > 0 ? m0 : 0.0f;
-            p.C[1] = exist > 1 ? m1 : 0.0f;
+        if constexpr (FMT == kFmtQ4_0 || FMT == kFmtQ8_0) {
+            p.d2[0] = exist > 0 ? __builtin_amdgcn_perm(h0, h0, 0x01000100u) : 0u;
+            p.d2[1] = exist > 1 ? __builtin_amdgcn_perm(h1, h1, 0x01000100u) : 0u;
         } else {
-            // the codes' offset; d times it is exact
-            constexpr float off = FMT == kFmtQ8_0 ? -128.0f : FMT == kFmtQ4_0 ? -8.0f : -16.0f;
-            p.C[0] = off * e0;
-            p.C[1] = off * e1;
+            p.A[0] = exist > 0 ? kCode * f16_bits_to_f32(h0) : 0.0f;
+            p.A[1] = exist > 1 ? kCode * f16_bits_to_f32(h1) : 0.0f;
+            if constexpr (FMT == kFmtQ5_1) {
+                p.C[0] = exist > 0 ? f16_bits_to_f32(h0 >> 16) : 0.0f;
+                p.C[1] = exist > 1 ? f16_bits_to_f32(h1 >> 16) : 0.0f;
+            } else {
+                // the codes' offset; d times it is exact
+                p.C[0] = (-16.0f / kCode) * p.A[0];
+                p.C[1] = (-16.0f / kCode) * p.A[1];
+            }
         }
         return p;
     }
