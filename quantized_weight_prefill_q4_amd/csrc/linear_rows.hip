@@ -3,7 +3,7 @@
 //
 // Mathematics and bound.  Every weight is used M times and read once, so the
 // product is bound by the weight's bytes (0.56 to 2 per weight) and, for the
-// block formats, by the instructions that expand them (2 to 3 per weight; the
+// block formats, by the instructions that expand them (3 to 5 per weight; the
 // f16 values that feed the matrix cores are the cache's, bit for bit).  Tiles
 // of 64 × 128 outputs would need a K split with partial planes and a second
 // kernel to fill the chip, and would compute mostly rows that do not exist.
@@ -25,13 +25,14 @@
 // the same registers and are in flight while the fragments are expanded and
 // multiplied.
 //
-// Measured (one token, weights cold in L2, graph replays): f16 28672 x 4096 42 us
-// = 5.6 TB/s, 14336 x 4096 23.6, 3584 x 3584 7.2; gated 2 x 14336 x 4096: f16 45
-// us, Q8_0 32.8, Q6_K 30.5, Q5_0 27.1, Q5_1 25.5, Q5_K 25.1, Q4_0 20.8, Q4_K 20.3
-// (3.3 TB/s; the expansion alone, without the loads, takes 14.7).  So the f16
-// cache and Q8_0 are bound by memory, the 4- to 6-bit formats by the vector
-// instructions of the expansion, and a small layer by the memory's first answer
-// (about 3 us from a cold start).  16 rows: Q4_K 14336 x 4096 16.7 us; 32: 21.3.
+// Measured (one token, weights cold in L2, graph replays): f16 28672 x 4096 42.9
+// us = 5.6 TB/s, 14336 x 4096 22.9, 3584 x 3584 7.4; gated 2 x 14336 x 4096: f16
+// 45 us (5.3 TB/s), Q8_0 30 (4.2), Q6_K 29, Q5_0 26, Q5_K 25, Q5_1 23.5, Q4_0 and
+// Q4_K 20.5 (3.3).  16 rows of Q4_K 14336 x 4096: 16.8 us; 32: 21.3.  The f16 cache
+// is bound by memory, the block formats by the expansion (3.2 vector
+// instructions per weight for Q8_0, 3.3 for Q4_K, 5.2 for Q6_K, all told) of the
+// last units, which no load covers, and a small layer by the memory's first
+// answer (about 3 us from a cold start).
 
 #include "epilogue.h"
 #include "mq_device.h"
@@ -532,16 +533,24 @@ constexpr int strip_chunks() {
     return need > sums ? need : sums;
 }
 
+// Waves that share a compute unit, which caps their registers: 4 per SIMD (with
+// half of them the loads in flight do not cover the memory's latency), 3 or 2
+// where more rows' activations and sums, or two tiles of a gated layer, would
+// spill (gated 9472 x 3584, 7 rows, 4 -> 3 waves: Q8_0 32 -> 22 us, f32 rows 56
+// -> 24.5, Q6_K 27 -> 24, Q4_K 17.7 -> 16.4; 14336 x 4096: Q8_0 38 -> 33, Q4_K
+// 21.7 -> 23.1).
+constexpr int max_waves(int fmt, int MR, bool GLU, bool XF32) {
+    if (MR > 16) return 8;
+    if (GLU && fmt == kFmtQ8_0) return MR > 8 && XF32 ? 8 : 12;
+    return MR > (GLU ? 4 : 8) ? 12 : 16;
+}
+
 // RT tiles of 16 weight rows per workgroup of blockDim.x / 64 waves, at least
 // the RT·MF whose sums they finish (gated: a gate tile and its up tile, RT =
-// 2); MR: activation rows held (4, 8, 16 or 32).  Registers are capped so that 4
-// waves share a SIMD (with half of them the loads in flight do not cover the
-// memory's latency), 3 with 16 rows and 2 with 32, whose activations and sums
-// take more.
-template <int MR>
-constexpr int kMaxWaves = MR > 16 ? 8 : MR > 8 ? 12 : 16;   // per compute unit
+// 2); MR: activation rows held (4, 8, 16 or 32).
 template <int FMT, int RT, bool GLU, bool XF32, int MR>
-__global__ __launch_bounds__(64 * kMaxWaves<MR>, MR > 16 ? 2 : MR > 8 ? 3 : 4) void
+__global__ __launch_bounds__(64 * max_waves(FMT, MR, GLU, XF32),
+                             max_waves(FMT, MR, GLU, XF32) / 4) void
 linear_rows_kernel(RowsArgs a) {
     static_assert(!GLU || RT == 2, "a gate tile and an up tile");
     using Unit = RowUnit<FMT>;
@@ -698,15 +707,20 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
     // As many waves per workgroup as let all workgroups be resident at once
     // (a second round of a few left over costs as much as the first: 288 tiles
     // on 256 compute units, f16 4608 x 3584 at M = 24, 15.5 us with 8 waves
-    // each, 13.8 with 4), no more than there are units, and at least the RT·MF that
-    // finish the sums.
+    // each, 13.8 with 4), but 4 where that is 5 to 7, which do not spread evenly
+    // over four SIMDs (gated 11008 x 4096 at M = 1, 5 waves -> 4: Q6_K 31 -> 24
+    // us, Q4_K 20.4 -> 16.3; 6 -> 4, gated 6144 x 4096 at M = 16: Q8_0 24.6 ->
+    // 19.7; 3 stay, all of them resident: Q8_0 gated 14336 x 4096 29 us, with 4
+    // 34), and where it is 1 or 2; no more than there are units, and at least
+    // the RT·MF that finish the sums.
     const int per_cu = (tiles + kCUs - 1) / kCUs;
-    int nw = kMaxWaves<MR> / per_cu;
-    if (nw < 3) nw = 4;
+    int nw = max_waves(FMT, MR, GLU, XF32) / per_cu;
+    if (nw < 3 || (nw > 4 && nw < 8)) nw = 4;
     if (nw > units) nw = units;
     const int finish = (GLU ? 1 : RT) * (MR > 16 ? MR / 16 : 1);
     if (nw < finish) nw = finish;
-    static_assert(kMaxWaves<MR> * strip_chunks<Unit, RT, MR, XF32>() * 16 <= 160 * 1024,
+    static_assert(max_waves(FMT, MR, GLU, XF32) * strip_chunks<Unit, RT, MR, XF32>() * 16 <=
+                      160 * 1024,
                   "the strips of the most waves fit a compute unit's LDS");
     const size_t lds = nw * (size_t)(strip_chunks<Unit, RT, MR, XF32>()) * 16;
     hipLaunchKernelGGL((linear_rows_kernel<FMT, RT, GLU, XF32, MR>), dim3(tiles), dim3(64 * nw),
