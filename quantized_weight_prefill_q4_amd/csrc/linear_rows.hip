@@ -538,11 +538,11 @@ constexpr int strip_chunks() {
 // where more rows' activations and sums, or two tiles of a gated layer, would
 // spill (gated 9472 x 3584, 7 rows, 4 -> 3 waves: Q8_0 32 -> 22 us, f32 rows 56
 // -> 24.5, Q6_K 27 -> 24, Q4_K 17.7 -> 16.4; 14336 x 4096: Q8_0 38 -> 33, Q4_K
-// 21.7 -> 23.1).
+// 21.7 -> 23.1; ungated Q8_0 6144 x 4096, 7 f32 rows, 12.5 -> 11.9).
 constexpr int max_waves(int fmt, int MR, bool GLU, bool XF32) {
     if (MR > 16) return 8;
     if (GLU && fmt == kFmtQ8_0) return MR > 8 && XF32 ? 8 : 12;
-    return MR > (GLU ? 4 : 8) ? 12 : 16;
+    return MR > (GLU || (XF32 && fmt == kFmtQ8_0) ? 4 : 8) ? 12 : 16;
 }
 
 // RT tiles of 16 weight rows per workgroup of blockDim.x / 64 waves, at least
