@@ -244,6 +244,39 @@ def test_few_rows_see_the_cache_weights(fmt):
     assert torch.equal(got.t(), want)
 
 
+@pytest.mark.parametrize("fmt", [synth.Q4_0, synth.Q5_0, synth.Q5_1, synth.Q8_0])
+def test_few_rows_see_extreme_scales(fmt):
+    """The same with block scales from the smallest subnormal to the largest
+    whose products stay finite, of both signs, and zero: what is expanded in f16
+    arithmetic rounds as the cache's values do, subnormal results included."""
+    N, K = 40, 256
+    announce("one-hot, extreme scales", fmt)
+    q = synth.weights(fmt, synth.rng(48, fmt), N, K).copy()
+    blocks = q.reshape(-1, mq.block_bytes(fmt))
+    scales = np.array([0x0001, 0x0003, 0x00FF, 0x03FF, 0x0400, 0x0401, 0x07FF, 0x1234, 0x3555,
+                       0x3C01, 0x4FFF, 0x5FFE, 0x8001, 0x83FF, 0x8401, 0xB7FD, 0xDFFE, 0x0000,
+                       0x8000], np.uint16)
+    blocks[:, :2] = scales[np.arange(len(blocks)) % len(scales)].view(np.uint8).reshape(-1, 2)
+    want = oracle.dequant_ref(fmt, q, N, K).view(np.float16).astype(np.float32)
+    assert np.isfinite(want).all()
+    w = to_dev_u8(q)
+    eye = torch.eye(K, dtype=torch.float16, device=dev())
+    for rows in (4, 16, 32):
+        got = torch.cat([mq.linear_fused(eye[k:k + rows], w, fmt, N, K)
+                         for k in range(0, K, rows)])
+        assert np.array_equal(got.t().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("fmt", [0, synth.Q6_K, synth.Q8_0])
+def test_several_tiles_per_compute_unit(fmt):
+    """Two, three and four workgroups to a compute unit, whose numbers of waves
+    differ with the rows, their type and the layer."""
+    for N in (4200, 8300, 12400):
+        check_glu(fmt, 6, N, 1024, xt="f32", yt="f16", seed=N)
+        check_linear(fmt, 13, N, 1024, rt="f16", yt="f32", seed=N)
+    check_glu(fmt, 2, 12400, 2048, yt="f32")
+
+
 @pytest.mark.parametrize("fmt", [0] + FMTS)
 def test_wide_outputs(fmt):
     """256 x 256 tiles, the last ones ragged in rows and columns."""
