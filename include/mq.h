@@ -113,9 +113,11 @@ enum {
     MQ_ACT_GELU_TANH = 4   /* 0.5·v·(1 + tanh(√(2/π)·(v + 0.044715·v³))) */
 };
 
-/* Limits checked by every entry point. */
+/* Limits checked by every entry point.  Row strides of X, of the f16 cache and of
+ * int8 codes are at most MQ_MAX_K (f16 rows: and the cache's pad, MQ_MAX_K + 64);
+ * those of Y and R, and of the norm's rows, may be any int. */
 #define MQ_MAX_DIM (1 << 24)     /* M and N */
-#define MQ_MAX_K (1 << 21)       /* K and every leading dimension */
+#define MQ_MAX_K (1 << 21)       /* K */
 #define MQ_MAX_SPLIT_K 16
 /* Static device scratch of mq_gemm_fused_noalloc, per GPU (64 MiB). */
 #define MQ_NOALLOC_SCRATCH_BYTES (64 << 20)

@@ -60,7 +60,9 @@ int64_t integer(PyObject *o) {
     if (v == -1 && PyErr_Occurred()) throw Refused{};
     return v;
 }
-// an int argument of the C ABI; sizes beyond it are out of range there anyway
+// A size, format, activation or split as an int of the C ABI, whose ranges all end
+// below INT32_MAX: what does not fit is refused there.  Not for strides, which
+// may be any int (matrix_form).
 int to_int(int64_t v) {
     if (v > INT32_MAX) return INT32_MAX;
     if (v < INT32_MIN) return INT32_MIN;
@@ -85,6 +87,10 @@ int element_type(const at::Tensor &t, const char *name) {
 void matrix_form(const at::Tensor &t, const char *name) {
     if (t.dim() != 2 || (t.stride(1) != 1 && t.size(1) > 1))
         refuse("%s must be 2-D with unit column stride", name);
+    // the C ABI takes row strides as int
+    if (t.size(0) > 1 && t.stride(0) > INT32_MAX)
+        refuse("the rows of %s must be at most %d elements apart, got %lld", name, INT32_MAX,
+               (long long)t.stride(0));
 }
 // The row stride of a row-major matrix of at least rows × cols; for a single
 // row, whose stride is never used (a slice may carry any), its width.
@@ -94,7 +100,7 @@ int matrix(const at::Tensor &t, int dev, int64_t rows, int64_t cols, const char 
         refuse("%s must be at least %lld x %lld, got (%lld, %lld)", name, (long long)rows,
                (long long)cols, (long long)t.size(0), (long long)t.size(1));
     same_device(t, dev, name);
-    return to_int(t.size(0) > 1 ? t.stride(0) : cols);
+    return t.size(0) > 1 ? (int)t.stride(0) : to_int(cols);
 }
 
 const float *vector(const at::Tensor &t, int dev, int64_t n, const char *name) {
@@ -133,9 +139,9 @@ PyObject *layer_checked(PyObject *const *a, Py_ssize_t n) {
     void *stream = PyLong_AsVoidPtr(a[0]);
     if (!stream && PyErr_Occurred()) throw Refused{};
     const at::Tensor &x = tensor(a[1], "x");
+    matrix_form(x, "x");
     const int dev = device_of(x, "x");
     const int xt = element_type(x, "x");
-    matrix_form(x, "x");
     const int fmt = to_int(integer(a[3]));
     const at::Tensor &w = tensor(a[2], fmt ? "wq" : "w16");
     const bool glu = a[9] == Py_True;
@@ -236,9 +242,9 @@ PyObject *norm_checked(PyObject *const *a, Py_ssize_t n) {
     void *stream = PyLong_AsVoidPtr(a[0]);
     if (!stream && PyErr_Occurred()) throw Refused{};
     const at::Tensor &x = tensor(a[1], "x");
+    matrix_form(x, "x");
     const int dev = device_of(x, "x");
     const int xt = element_type(x, "x");
-    matrix_form(x, "x");
     const int64_t M = x.size(0), K = x.size(1);
     const int ldx = matrix(x, dev, M, K, "x");
     const float *w = vector(tensor(a[2], "weight"), dev, K, "weight");

@@ -586,3 +586,33 @@ def test_binding_refuses():
     with pytest.raises(ValueError, match="contiguous vector"):
         mq.glu_f16cache(x, w, K, bias=b[:N // 2])
     assert mq.glu_fused(x, q, "q4_k", N // 2, K).shape == (M, N // 2)
+
+
+def test_strides_beyond_int_are_refused():
+    """Rows 2^31 elements apart, in every place a layer or a norm takes rows."""
+    K = N = 64
+    announce("strides beyond int")
+    buf = torch.empty((1 << 31) + 64, dtype=torch.float16, device=dev())
+    far = buf.as_strided((2, K), (1 << 31, 1))
+    x, r = torch.zeros(2, K, dtype=torch.float16, device=dev()), torch.zeros(2, N, device=dev())
+    w = torch.zeros(N, K, dtype=torch.float16, device=dev())
+    far_w = buf.as_strided((2, K), (1 << 31, 1))
+    q = torch.zeros(N * mq.row_bytes("q8_0", K), dtype=torch.uint8, device=dev())
+    ones = torch.ones(K, device=dev())
+    for call in (lambda: mq.linear_f16cache(far, w), lambda: mq.linear_f16cache(x, far_w),
+                 lambda: mq.linear_f16cache(x, w, residual=far),
+                 lambda: mq.linear_f16cache(x, w, out=far),
+                 lambda: mq.linear_fused(x, q, "q8_0", N, residual=far, out=far),
+                 lambda: mq.glu_f16cache(far, w), lambda: mq.glu_f16cache(x, w, out=far),
+                 lambda: mq.glu_fused(x, q, "q8_0", N // 2, out=far),
+                 lambda: mq.add_rms_norm(far, ones), lambda: mq.add_rms_norm(x, ones, out=far),
+                 lambda: mq.add_rms_norm(x, ones, residual=far, residual_out=far),
+                 lambda: mq.add_rms_norm(x, ones, residual=r.half(), residual_out=far),
+                 lambda: mq.add_rms_norm_q8_1(far, ones)):
+        with pytest.raises(ValueError, match="elements apart"):
+            call()
+    # one row of such a view has no stride
+    y = mq.linear_f16cache(x[:1], w, residual=r[:1], out=far[1:])
+    assert y.shape == (1, N) and bool((y == 0).all())
+    del buf, far, far_w
+    torch.cuda.empty_cache()

@@ -222,3 +222,25 @@ def test_native_binding_refuses_without_a_gpu():
         mq.linear_f16cache(x, x.half(), act="swish")
     with pytest.raises(ValueError, match="out_dtype"):
         mq.add_rms_norm(x, w, out_dtype=torch.bfloat16)
+
+
+def test_native_binding_refuses_strides_beyond_int():
+    """Rows further apart than the C ABI's int can say: of x, before its device is
+    looked at (meta tensors have strides without memory)."""
+    import torch
+
+    from quantized_weight_prefill_q4_amd import layers
+
+    b = layers._binding()
+    w = torch.zeros(32)
+    for stride in (1 << 31, (1 << 32) + 32):
+        x = torch.empty_strided((2, 32), (stride, 1), device="meta", dtype=torch.float16)
+        for call, args in ((b.norm, (x, w, None, 1e-6, 0, None, None, None)),
+                           (b.layer, (x, w, 0, -1, -1, None, 0, None, False, 0, 0, None, None))):
+            with pytest.raises(ValueError, match="elements apart"):
+                call(0, *args)
+    # one row has no stride, and the largest int is one
+    for shape, stride in (((1, 32), 1 << 31), ((2, 32), (1 << 31) - 1)):
+        x = torch.empty_strided(shape, (stride, 1), device="meta", dtype=torch.float16)
+        with pytest.raises(ValueError, match="GPU tensor"):
+            b.norm(0, x, w, None, 1e-6, 0, None, None, None)
