@@ -133,7 +133,7 @@ void need_bound(Py_ssize_t got, Py_ssize_t want, const char *name) {
 
 // layer(stream, x, weight, fmt, N, K, bias, act, residual, glu, y_type,
 // split_k, out, ws): fmt 0 is the f16 cache, whose N is its row count (halved
-// when glu); K < 0: x's width.
+// when glu); K None: x's width.
 PyObject *layer_checked(PyObject *const *a, Py_ssize_t n) {
     need_bound(n, 14, "layer");
     void *stream = PyLong_AsVoidPtr(a[0]);
@@ -145,9 +145,8 @@ PyObject *layer_checked(PyObject *const *a, Py_ssize_t n) {
     const int fmt = to_int(integer(a[3]));
     const at::Tensor &w = tensor(a[2], fmt ? "wq" : "w16");
     const bool glu = a[9] == Py_True;
-    int64_t N = integer(a[4]), K = integer(a[5]);
-    const int64_t M = x.size(0);
-    if (K < 0) K = x.size(1);
+    int64_t N = integer(a[4]);
+    const int64_t M = x.size(0), K = a[5] == Py_None ? x.size(1) : integer(a[5]);
     if (fmt == 0) {
         matrix_form(w, "w16");
         if (glu && w.size(0) % 2)

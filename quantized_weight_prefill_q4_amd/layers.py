@@ -101,7 +101,7 @@ def linear_f16cache(x: torch.Tensor, w16: torch.Tensor, K: int | None = None,
     f32 [N], act one of ACTIVATIONS, residual [M, N] f32 or f16.  out may be
     the residual itself (the stream is then updated in place)."""
     return _on_device(x, _binding().layer, "mq_linear_f16cache",
-                      (x, w16, 0, -1, -1 if K is None else K, bias, _act(act), residual, False,
+                      (x, w16, 0, -1, K, bias, _act(act), residual, False,
                        _out_type(out_dtype), split_k, out, ws))
 
 
@@ -112,7 +112,7 @@ def linear_fused(x: torch.Tensor, wq: torch.Tensor, fmt, N: int, K: int | None =
                  ws: torch.Tensor | None = None) -> torch.Tensor:
     """linear_f16cache straight from the quantized weight wq [N rows of K]."""
     return _on_device(x, _binding().layer, "mq_linear_fused",
-                      (x, wq, _fmt(fmt) or -1, N, -1 if K is None else K, bias, _act(act),
+                      (x, wq, _fmt(fmt) or -1, N, K, bias, _act(act),
                        residual, False, _out_type(out_dtype), split_k, out, ws))
 
 
@@ -125,7 +125,7 @@ def glu_f16cache(x: torch.Tensor, w16: torch.Tensor, K: int | None = None,
     or f32), with w16 [2N, ld] the f16 caches of gate and up one after the
     other and bias f32 [2N] likewise; x as in linear_f16cache."""
     return _on_device(x, _binding().layer, "mq_glu_f16cache",
-                      (x, w16, 0, -1, -1 if K is None else K, bias, _act(act), None, True,
+                      (x, w16, 0, -1, K, bias, _act(act), None, True,
                        _out_type(out_dtype), split_k, out, ws))
 
 
@@ -136,7 +136,7 @@ def glu_fused(x: torch.Tensor, wq: torch.Tensor, fmt, N: int, K: int | None = No
     """glu_f16cache straight from the quantized weights: wq holds the gate's N
     rows of K, then the up matrix's."""
     return _on_device(x, _binding().layer, "mq_glu_fused",
-                      (x, wq, _fmt(fmt) or -1, N, -1 if K is None else K, bias, _act(act), None,
+                      (x, wq, _fmt(fmt) or -1, N, K, bias, _act(act), None,
                        True, _out_type(out_dtype), split_k, out, ws))
 
 

@@ -616,3 +616,22 @@ def test_strides_beyond_int_are_refused():
     assert y.shape == (1, N) and bool((y == 0).all())
     del buf, far, far_w
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("K", [0, -1, -64])
+def test_sizes_below_one_are_refused(K):
+    """A K (or an N of block weights) that is not a size is refused, as the GEMM
+    entry points do; None alone stands for the activations' width."""
+    announce("K below one", K)
+    x = torch.zeros(3, 64, dtype=torch.float16, device=dev())
+    w = torch.zeros(32, 64, dtype=torch.float16, device=dev())
+    q = torch.zeros(32 * mq.row_bytes("q8_0", 64), dtype=torch.uint8, device=dev())
+    for call in (lambda: mq.linear_f16cache(x, w, K), lambda: mq.glu_f16cache(x, w, K),
+                 lambda: mq.linear_fused(x, q, "q8_0", 32, K),
+                 lambda: mq.glu_fused(x, q, "q8_0", 16, K),
+                 lambda: mq.linear_fused(x, q, "q8_0", K, 64),
+                 lambda: mq.glu_fused(x, q, "q8_0", K, 64), lambda: mq.gemm_f16cache(x, w, K)):
+        with pytest.raises(mq.MQError) as e:
+            call()
+        assert e.value.code == _lib.MQ_ERR_SHAPE
+    assert mq.linear_f16cache(x, w, None).shape == (3, 32)
