@@ -103,10 +103,12 @@ int matrix(const at::Tensor &t, int dev, int64_t rows, int64_t cols, const char 
     return t.size(0) > 1 ? (int)t.stride(0) : to_int(cols);
 }
 
+// A bias or a norm's weights: of the layer's own size (a longer vector is another
+// layer's; matrices may be wider, as parts of strided buffers are).
 const float *vector(const at::Tensor &t, int dev, int64_t n, const char *name) {
     if (t.scalar_type() != at::kFloat)
         refuse("%s must be torch.float32, got %s", name, type_name(t));
-    if (t.dim() != 1 || !t.is_contiguous() || t.size(0) < n)
+    if (t.dim() != 1 || !t.is_contiguous() || t.size(0) != n)
         refuse("%s must be a contiguous vector of %lld elements", name, (long long)n);
     same_device(t, dev, name);
     return (const float *)t.const_data_ptr();
@@ -246,12 +248,12 @@ PyObject *norm_checked(PyObject *const *a, Py_ssize_t n) {
     const int xt = element_type(x, "x");
     const int64_t M = x.size(0), K = x.size(1);
     const int ldx = matrix(x, dev, M, K, "x");
-    const float *w = vector(tensor(a[2], "weight"), dev, K, "weight");
     const double eps = PyFloat_AsDouble(a[4]);
     if (eps == -1.0 && PyErr_Occurred()) throw Refused{};
     const int want = to_int(integer(a[5]));
     const bool q8 = want < 0;
     if (M == 0 || K == 0 || (q8 && K % 32)) return status_object(MQ_ERR_SHAPE);
+    const float *w = vector(tensor(a[2], "weight"), dev, K, "weight");
 
     const at::Tensor *res = optional(a[3], "residual"), *h_t = optional(a[8], "residual_out");
     if (!res && h_t) refuse("%s", "residual_out needs a residual");

@@ -635,3 +635,25 @@ def test_sizes_below_one_are_refused(K):
             call()
         assert e.value.code == _lib.MQ_ERR_SHAPE
     assert mq.linear_f16cache(x, w, None).shape == (3, 32)
+
+
+def test_vectors_of_another_size_are_refused():
+    """A bias or a norm's weights that are longer than the layer's are another
+    layer's."""
+    K, N = 64, 32
+    announce("longer vectors")
+    x = torch.zeros(3, K, dtype=torch.float16, device=dev())
+    w = torch.zeros(N, K, dtype=torch.float16, device=dev())
+    q = torch.zeros(N * mq.row_bytes("q8_0", K), dtype=torch.uint8, device=dev())
+    v = torch.ones(K + 1, device=dev())
+    for n in (N + 1, K):
+        for call in (lambda: mq.linear_f16cache(x, w, bias=v[:n]),
+                     lambda: mq.linear_fused(x, q, "q8_0", N, bias=v[:n]),
+                     lambda: mq.glu_f16cache(x, w, bias=v[:n]),
+                     lambda: mq.glu_fused(x, q, "q8_0", N // 2, bias=v[:n])):
+            with pytest.raises(ValueError, match=f"contiguous vector of {N} elements"):
+                call()
+    for call in (mq.add_rms_norm, mq.add_rms_norm_q8_1):
+        with pytest.raises(ValueError, match=f"contiguous vector of {K} elements"):
+            call(x, v)
+    assert bool((mq.linear_f16cache(x, w, bias=v[:N]) == 1).all())
