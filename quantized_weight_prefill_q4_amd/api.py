@@ -13,7 +13,7 @@ import functools
 
 import torch
 
-from ._lib import (MQ_Q4_0, MQ_Q4_K, MQ_Q5_0, MQ_Q5_1, MQ_Q5_K, MQ_Q6_K, MQ_Q8_0,
+from ._lib import (MQ_ERR_SHAPE, MQ_Q4_0, MQ_Q4_K, MQ_Q5_0, MQ_Q5_1, MQ_Q5_K, MQ_Q6_K, MQ_Q8_0,
                    MqDequantJob, MqGemmPlanInfo, check, lib)
 
 FORMATS = {"q4_0": MQ_Q4_0, "q5_0": MQ_Q5_0, "q5_1": MQ_Q5_1, "q8_0": MQ_Q8_0,
@@ -37,15 +37,34 @@ def _need_cuda(t: torch.Tensor, name: str, dtype: torch.dtype) -> None:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+# Sizes and strides are C ints in the ABI, and ctypes keeps the low 32 bits of what
+# does not fit.  No size or split the library accepts is as large as _INT_MAX, so
+# one that does not fit is passed to a query as that, and refused; strides may be
+# any int, and beyond it are refused here.
+_INT_MAX = (1 << 31) - 1
+
+
+def _as_int(v) -> int:
+    return max(-_INT_MAX, min(int(v), _INT_MAX))
+
+
 def _row_major_2d(t: torch.Tensor, name: str) -> int:
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be 2-D with unit column stride")
-    return t.stride(0)
+    ld = t.stride(0)
+    if ld > _INT_MAX:
+        if t.shape[0] > 1:
+            raise ValueError(f"the rows of {name} must be at most {_INT_MAX} elements apart, "
+                             f"got {ld}")
+        ld = _INT_MAX   # of a single row: not used
+    return ld
 
 
 # The C ABI sees plain pointers; the sizes it cannot check are checked here,
 # so that a wrong argument is an exception rather than an access out of bounds.
 def _need_shape(t: torch.Tensor, rows: int, cols: int, name: str) -> None:
+    if rows > _INT_MAX or cols > _INT_MAX:
+        check(MQ_ERR_SHAPE, name)
     if t.shape[0] < rows or t.shape[1] < cols:
         raise ValueError(f"{name} must be at least {rows} x {cols}, got {tuple(t.shape)}")
 
@@ -76,13 +95,15 @@ def _cache_ld(K: int) -> int:
 @functools.lru_cache(maxsize=4096)
 def _workspace_bytes(f: int, M: int, N: int, K: int, split_k: int, x_f32: bool) -> int:
     fn = "mq_gemm_xf32_workspace_bytes" if x_f32 else "mq_gemm_workspace_bytes"
-    return check(getattr(lib(), fn)(f, M, N, K, split_k), fn)
+    return check(getattr(lib(), fn)(f, _as_int(M), _as_int(N), _as_int(K), _as_int(split_k)), fn)
 
 
 def _need_quant(wq: torch.Tensor, f: int, N: int, K: int) -> None:
     _need_cuda(wq, "wq", torch.uint8)
     if not wq.is_contiguous():
         raise ValueError("wq must be contiguous")
+    if N > _INT_MAX:
+        check(MQ_ERR_SHAPE, "wq")
     need = N * _row_bytes(f, K)
     if wq.numel() < need:
         raise ValueError(f"wq holds {wq.numel()} bytes; {N} rows of K = {K} need {need}")
@@ -118,8 +139,8 @@ def gemm_plan(fmt, M: int, N: int, K: int, split_k: int = 0, path: str = "f16") 
     f = 0 if fmt in (0, None, "f16") else _fmt(fmt)
     p = {"f16": 0, "f32": 1, "mmq": 2}[path]
     info = MqGemmPlanInfo()
-    check(lib().mq_gemm_plan_query(p, f, M, N, K, split_k, ctypes.byref(info)),
-          "mq_gemm_plan_query")
+    check(lib().mq_gemm_plan_query(p, f, _as_int(M), _as_int(N), _as_int(K), _as_int(split_k),
+                                   ctypes.byref(info)), "mq_gemm_plan_query")
     return {name: getattr(info, name) for name, _ in MqGemmPlanInfo._fields_}
 
 
@@ -289,7 +310,8 @@ def quantize_q8_1(x: torch.Tensor, K: int | None = None, xq: torch.Tensor | None
 
 
 def mmq_workspace_bytes(fmt, M: int, N: int, K: int, split_k: int = 0) -> int:
-    return check(lib().mq_gemm_mmq_workspace_bytes(_fmt(fmt), M, N, K, split_k),
+    return check(lib().mq_gemm_mmq_workspace_bytes(_fmt(fmt), _as_int(M), _as_int(N), _as_int(K),
+                                                   _as_int(split_k)),
                  "mq_gemm_mmq_workspace_bytes")
 
 

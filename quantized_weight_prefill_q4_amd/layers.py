@@ -19,7 +19,7 @@ import os
 import torch
 
 from ._lib import MQ_F16, MQ_F32, check, lib
-from .api import _fmt
+from .api import _as_int, _fmt
 
 _TYPES = {torch.float32: MQ_F32, torch.float16: MQ_F16}
 
@@ -85,7 +85,8 @@ def linear_workspace_bytes(fmt, M: int, N: int, K: int, split_k: int = 0, x_f32:
     ``glu`` of a gated one with N output columns; x_f32 for f32 activations."""
     f = 0 if fmt in (0, None, "f16") else _fmt(fmt)
     name = "mq_glu_workspace_bytes" if glu else "mq_linear_workspace_bytes"
-    return check(getattr(lib(), name)(f, MQ_F32 if x_f32 else MQ_F16, M, N, K, split_k), name)
+    return check(getattr(lib(), name)(f, MQ_F32 if x_f32 else MQ_F16, _as_int(M), _as_int(N),
+                                      _as_int(K), _as_int(split_k)), name)
 
 
 def linear_f16cache(x: torch.Tensor, w16: torch.Tensor, K: int | None = None,
