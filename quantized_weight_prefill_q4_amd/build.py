@@ -89,12 +89,13 @@ def _build_binding(verbose: bool) -> str:
 
 def build_lib(verbose: bool = False) -> str:
     """Compile every HIP source and link libmq.so, and build the torch binding;
-    returns the library path."""
+    returns the library path.  The library needs neither the host compiler nor
+    Python's and torch's headers: it is linked also where the binding, which
+    does, cannot be built, and that is raised afterwards."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_build_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        binding.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
@@ -103,6 +104,7 @@ def build_lib(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    binding.result()
     return LIB_PATH
 
 
