@@ -104,6 +104,8 @@ def build_lib(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    if binding.exception() and os.path.exists(BINDING_PATH):
+        os.remove(BINDING_PATH)   # an older library's
     binding.result()
     return LIB_PATH
 

@@ -40,6 +40,14 @@ def test_library_does_not_need_the_binding(fake):
     assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.BINDING_PATH)
 
 
+def test_no_binding_of_an_older_library_stays(fake):
+    build.build_lib()
+    fake.add("binding.cpp")
+    with pytest.raises(RuntimeError, match="binding.cpp"):
+        build.build_lib()
+    assert not os.path.exists(build.BINDING_PATH)
+
+
 def test_no_library_from_a_source_that_fails(fake):
     fake.add("gemm.hip")
     with pytest.raises(RuntimeError, match="gemm.hip"):
