@@ -657,3 +657,42 @@ def test_vectors_of_another_size_are_refused():
         with pytest.raises(ValueError, match=f"contiguous vector of {K} elements"):
             call(x, v)
     assert bool((mq.linear_f16cache(x, w, bias=v[:N]) == 1).all())
+
+
+@pytest.mark.parametrize("past", [False, True])
+@pytest.mark.parametrize("fmt", [synth.Q4_K, synth.Q5_K, synth.Q6_K, synth.Q5_1])
+def test_far_gated_blocks(fmt, past):
+    """Gated block weights on 256 x 256 tiles, past 2 GiB, which one buffer range
+    from the gate rows to the weight's end cannot cover, and the largest that it
+    can: rows at the edges of tiles, of 32-row blocks and of both halves, the
+    rest zero."""
+    K, M = 16384, 300
+    row = mq.row_bytes(fmt, K)
+    N = ((1 << 31) - 16) // (2 * row)
+    if past:
+        N = N // 256 * 256 + 301
+    announce("glu far blocks", fmt, N)
+    assert (2 * N * row + 16 > 1 << 31) == past
+    p = mq.gemm_plan(fmt, M, 2 * N, K)
+    assert (p["bm"], p["bn"]) == (256, 256)
+    at = [0, 1, 31, 32, 63, 64, 127, 128, 4095, N // 2, N - 128, N - 46, N - 45, N - 2, N - 1]
+    few = synth.weights(fmt, synth.rng(50, fmt), 2 * len(at), K)
+    wb = oracle.dequant_ref(fmt, few, 2 * len(at), K)
+    where = torch.tensor(at + [N + n for n in at], device=dev())
+    q = torch.zeros(2 * N, row, dtype=torch.uint8, device=dev())
+    q[where] = to_dev_u8(few).view(len(where), row)
+    x, xb = _x(M, K, "f16", 51)
+    bias = np.zeros(2 * N, np.float32)
+    b = _vec(2 * len(at), 52)
+    bias[np.array(at + [N + n for n in at])] = b
+    y, g, u, Sg, Su = layers.glu_ref(xb, wb, K, b, "silu")
+    eg, eu = 1.13 * _dv(K, Sg) + _da(g, "silu"), _dv(K, Su)
+    err = eg * np.abs(u) + np.abs(layers.act_ref(g, "silu")) * eu + eg * eu
+    tol = _out(y, err + U * (np.abs(y) + err), "f32")
+    got = mq.glu_fused(x, q.view(-1), fmt, N, K, bias=torch.from_numpy(bias).to(dev()),
+                       out_dtype=torch.float32)
+    assert _worst(got[:, at], y, tol, "f32") <= 1
+    got[:, at] = 0
+    assert not bool(got.any())
+    del q, got
+    torch.cuda.empty_cache()
