@@ -696,3 +696,67 @@ def test_far_gated_blocks(fmt, past):
     assert not bool(got.any())
     del q, got
     torch.cuda.empty_cache()
+
+
+def _far_views(M, cols, ld, dtype, count):
+    """`count` matrices of cols columns side by side in rows `ld` elements apart,
+    each followed by 8 columns of NaN."""
+    buf = torch.empty(M * ld, dtype=dtype, device=dev()).view(M, ld)
+    buf[:, :count * (cols + 8)] = float("nan")
+    return buf, [buf[:, i * (cols + 8):i * (cols + 8) + cols] for i in range(count)]
+
+
+@pytest.mark.parametrize("M,split", [(5, 0), (32, 0), (40, 1), (300, 1), (300, 3)])
+def test_outputs_and_residuals_past_2_to_31_elements(M, split):
+    """Rows of y and of the residual whose offsets pass 2^31 elements, as the last
+    token's rows of long sequences are: few-row kernels, whole tiles and the
+    reduce of a K split, in place and not."""
+    N, K = 200, 512
+    ld = ((1 << 31) // (M - 1) + 4096) | 1
+    announce("far outputs", M, split, ld)
+    w, _ = _weight(0, N, K, 60)
+    x, _ = _x(M, K, "f16", 60)
+    for dt in ("f32", "f16"):
+        r = torch.from_numpy(_vec((M, N), 61)).to(dev()).to(T[dt])
+        want = mq.linear_f16cache(x, w, K, act="gelu", residual=r, split_k=split, out_dtype=T[dt])
+        gated = mq.glu_f16cache(x, w, K, split_k=split, out_dtype=T[dt])
+        buf, (rv, yv, gv) = _far_views(M, N, ld, T[dt], 3)
+        assert (M - 1) * buf.stride(0) >= 1 << 31
+        rv.copy_(r)
+        kw = dict(act="gelu", residual=rv, split_k=split)
+        mq.linear_f16cache(x, w, K, out=yv, **kw)
+        mq.glu_f16cache(x, w, K, split_k=split, out=gv[:, :N // 2])
+        assert torch.equal(yv, want) and torch.equal(gv[:, :N // 2], gated)
+        assert torch.equal(rv, r)
+        mq.linear_f16cache(x, w, K, out=rv, **kw)
+        assert torch.equal(rv, want)
+        assert int(torch.isnan(buf[:, :3 * (N + 8)]).sum()) == M * (24 + N // 2)
+        del buf, rv, yv, gv, kw
+        torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("K", [200, 3584, 33000])
+def test_norm_rows_past_2_to_31_elements(K):
+    """The same of the norm's rows: x, the stream in and out, and y."""
+    M = 4
+    ld = ((1 << 31) // (M - 1) + 4096) | 1
+    announce("far norm rows", K)
+    w = torch.from_numpy(1 + _vec(K, 62, 0.2)).to(dev())
+    for dt in ("f32", "f16"):
+        x = torch.from_numpy(_vec((M, K), 63)).to(dev()).to(T[dt])
+        r = torch.from_numpy(_vec((M, K), 64)).to(dev()).to(T[dt])
+        y, h = mq.add_rms_norm(x, w, residual=r, out_dtype=T[dt])
+        buf, (xv, rv, hv, yv) = _far_views(M, K, ld, T[dt], 4)
+        xv.copy_(x)
+        rv.copy_(r)
+        mq.add_rms_norm(xv, w, residual=rv, out=yv, residual_out=hv)
+        assert torch.equal(yv, y) and torch.equal(hv, h) and torch.equal(rv, r)
+        mq.add_rms_norm(xv, w, residual=rv, out=yv, residual_out=rv)
+        assert torch.equal(yv, y) and torch.equal(rv, h) and torch.equal(xv, x)
+        assert int(torch.isnan(buf[:, :4 * (K + 8)]).sum()) == M * 32
+        if K % 32 == 0:
+            xq, ds, _ = mq.add_rms_norm_q8_1(xv, w, residual=hv, residual_out=rv)
+            eq, eds, eh = mq.add_rms_norm_q8_1(x, w, residual=h)
+            assert torch.equal(xq, eq) and torch.equal(ds, eds) and torch.equal(rv, eh)
+        del buf, xv, rv, hv, yv
+        torch.cuda.empty_cache()
