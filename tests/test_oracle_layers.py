@@ -1,10 +1,13 @@
 """The layers oracle against hand-derived values (CPU)."""
 
 import math
+import os
+import re
 
 import numpy as np
 import pytest
 
+from conftest import ROOT
 from oracle import layers
 
 
@@ -44,3 +47,30 @@ def test_glu_halves():
     y, S = layers.linear_ref(x, w, 2, bias=np.array([-5.0, 0, 0, 0]), act="relu",
                              residual=np.ones((1, 4)))
     assert y.tolist() == [[1, 3, 4, 7]] and S.tolist() == [[6, 2, 3, 6]]
+
+
+def test_gelu_polynomial():
+    """The kernels' polynomial for h = 0.5·e^(z²)·erfc(z), its coefficients read
+    from the source, over the z it is used for: the fit's error with the f32
+    coefficients as stored, and that of its evaluation in f32.  The latter, in
+    units of 2^-24 of h and largest towards z = 0, where t = -1 and h = 0.5: a
+    rounding of each of the eleven partial sums, which add up to 1.35 there (2.7
+    of h), and three roundings in t, with |dh/dt · t| = 0.85 (5.1 of h): 8."""
+    src = open(os.path.join(ROOT, "quantized_weight_prefill_q4_amd", "csrc", "epilogue.h")).read()
+    body = src[src.index("float gelu_f32(float v)"):]
+    body = body[:body.index("return")]
+    coeffs = re.findall(r"float h = ([-+.e0-9]+)f;", body)
+    coeffs += re.findall(r"fmaf\(h, t, ([-+.e0-9]+)f\)", body)
+    coeffs = np.array(coeffs, dtype=np.float64).astype(np.float32)
+    assert len(coeffs) == 11
+    z = np.linspace(0, 9, 9001).astype(np.float32)
+    ref = np.array([0.5 * math.exp(v * v) * math.erfc(v) for v in z.astype(np.float64)])
+    h, t = np.zeros(len(z)), (z.astype(np.float64) - 3) / (z.astype(np.float64) + 3)
+    for c in coeffs.astype(np.float64):
+        h = h * t + c
+    assert np.max(np.abs(h / ref - 1)) <= 1.25e-8
+    t = (z - np.float32(3)) / (z + np.float32(3))
+    h = np.zeros(len(z), np.float32)
+    for c in coeffs:   # a fused multiply-add: one rounding
+        h = (h.astype(np.float64) * t.astype(np.float64) + np.float64(c)).astype(np.float32)
+    assert np.max(np.abs(h / ref - 1)) <= 8 * 2.0 ** -24
