@@ -244,3 +244,12 @@ def test_native_binding_refuses_strides_beyond_int():
         x = torch.empty_strided(shape, (stride, 1), device="meta", dtype=torch.float16)
         with pytest.raises(ValueError, match="GPU tensor"):
             b.norm(0, x, w, None, 1e-6, 0, None, None, None)
+
+
+def test_every_error_has_its_text(L):
+    """All codes of the ABI, the last ones included."""
+    codes = range(_lib.MQ_ERR_ACT, 1)
+    assert min(v for k, v in vars(_lib).items() if k.startswith("MQ_ERR_")) == _lib.MQ_ERR_ACT
+    texts = [L.mq_strerror(c) for c in codes]
+    assert len(set(texts)) == len(codes) and b"unknown error code" not in texts
+    assert L.mq_strerror(_lib.MQ_ERR_ACT - 1) == b"unknown error code"
