@@ -760,3 +760,38 @@ def test_norm_rows_past_2_to_31_elements(K):
             assert torch.equal(xq, eq) and torch.equal(ds, eds) and torch.equal(rv, eh)
         del buf, xv, rv, hv, yv
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("fmt", [synth.Q4_K, synth.Q5_K, synth.Q6_K])
+def test_few_rows_see_extreme_super_block_scales(fmt):
+    """Super-block scales (and Q4_K's and Q5_K's offsets) from the smallest
+    subnormal to the largest whose values stay finite, of both signs, and zero,
+    in every pairing: the few-row kernels and the tile kernel expand the decode's
+    values."""
+    N, K = 182, 512
+    announce("one-hot, extreme super-block scales", fmt)
+    q = synth.weights(fmt, synth.rng(53, fmt), N, K).copy()
+    blocks = q.reshape(-1, mq.block_bytes(fmt))
+    scales = np.array([0x0001, 0x0003, 0x00FF, 0x03FF, 0x0400, 0x0401, 0x07FF, 0x1234, 0x3555,
+                       0x3C01, 0x47FE, 0x4BFF if fmt == synth.Q6_K else 0x4FFF, 0x8001, 0x83FF,
+                       0x8401, 0xB7FD, 0xC7FE, 0x0000, 0x8000], np.uint16)
+    n = np.arange(len(blocks))
+    d = scales[n % len(scales)].view(np.uint8).reshape(-1, 2)
+    if fmt == synth.Q6_K:
+        blocks[:, 208:] = d
+        blocks[::3, 192:208] = np.array([0x80, 0x7F] * 8, np.uint8)      # -128 and 127
+    else:
+        blocks[:, :2] = d
+        blocks[:, 2:4] = scales[n // len(scales) % len(scales)].view(np.uint8).reshape(-1, 2)
+        assert len(blocks) >= len(scales) ** 2
+        blocks[::3, 4:16] = 0xFF                                          # 63 and 63
+    want = oracle.dequant_ref(fmt, q, N, K).view(np.float16).astype(np.float32)
+    assert np.isfinite(want).all() and np.abs(want).max() > 3e4
+    w = to_dev_u8(q)
+    eye = torch.eye(K, dtype=torch.float16, device=dev())
+    for rows in (4, 8, 16, 32, 64):
+        got = torch.cat([mq.linear_fused(eye[k:k + rows], w, fmt, N, K)
+                         for k in range(0, K, rows)])
+        assert np.array_equal(got.t().cpu().numpy(), want), rows
+    got = torch.cat([mq.linear_fused(eye[k:k + 4].float(), w, fmt, N, K) for k in range(0, K, 4)])
+    assert np.array_equal(got.t().cpu().numpy(), want)
