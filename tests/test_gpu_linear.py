@@ -795,3 +795,45 @@ def test_few_rows_see_extreme_super_block_scales(fmt):
         assert np.array_equal(got.t().cpu().numpy(), want), rows
     got = torch.cat([mq.linear_fused(eye[k:k + 4].float(), w, fmt, N, K) for k in range(0, K, 4)])
     assert np.array_equal(got.t().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("fmt", [0] + FMTS)
+@pytest.mark.parametrize("xt", ["f16", "f32"])
+def test_few_rows_keep_special_values_apart(fmt, xt):
+    """NaN and infinities of one activation row stay in that row of y, and those
+    of one weight row in that column, in every few-row kernel; a part unit's
+    cleared elements bring none in."""
+    N, K = 50, 512 if fmt in (synth.Q4_K, synth.Q5_K, synth.Q6_K) else 288
+    announce("special values, few rows", fmt, xt)
+    w, _ = _weight(fmt, 2 * N, K, 70)
+    bad_w = w.clone()
+    if fmt == 0:
+        bad_w[7, :K] = float("inf")
+    else:
+        row, at = mq.row_bytes(fmt, K), 208 if fmt == synth.Q6_K else 0
+        for i in range(0, row, mq.block_bytes(fmt)):
+            bad_w.view(2 * N, row)[7, i + at:i + at + 2] = torch.tensor([0, 0x7C], device=dev())
+
+    def run(x, w, glu):
+        if fmt == 0:
+            return mq.glu_f16cache(x, w, K, act="relu", out_dtype=torch.float32) if glu else \
+                mq.linear_f16cache(x, w, K, act="relu")
+        f = mq.glu_fused if glu else mq.linear_fused
+        return f(x, w, fmt, N if glu else 2 * N, K, act="relu", out_dtype=torch.float32)
+
+    for M in (3, 4, 7, 11, 16, 19, 32):
+        x, _ = _x(M, K, xt, M)
+        bad = x.clone()
+        bad[1, 7], bad[2, K - 1] = float("nan"), float("inf")
+        keep = [i for i in range(M) if i not in (1, 2)]
+        for glu in (False, True):
+            want = run(x, w, glu)
+            assert bool(torch.isfinite(want).all())
+            y = run(bad, w, glu)
+            assert torch.equal(y[keep], want[keep]), M
+            assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[2]).all())
+            y = run(x, bad_w, glu)
+            cols = [c for c in range(want.shape[1]) if c != 7]
+            assert torch.equal(y[:, cols], want[:, cols]), M
+            if fmt == 0:                             # infinities of both signs
+                assert bool(torch.isnan(y[:, 7]).all())
