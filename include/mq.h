@@ -395,7 +395,8 @@ int mq_glu_fused(int x_type, const void *X, int ldx, int fmt, const void *wq, co
 /* Residual addition and root-mean-square norm of M activation rows, the step
  * between two layers' products, with the output in the type the next product
  * reads.  Per row, in f32 (sums included):
- *   h = x + r, rounded once to r's type and written to H (without r: h = x);
+ *   h = x + r, an f32 sum that is rounded to r's type and written to H (without
+ *   r: h = x);
  *   y = (h · 1/sqrt(Σ_k h²/K + eps)) · w, rounded once to the output type.
  *   X      : device, x_type (MQ_F32 / MQ_F16), row stride ldx >= K.
  *   R, H   : device, r_type, row strides ldr, ldh >= K: the residual stream in

@@ -708,11 +708,20 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
     // (a second round of a few left over costs as much as the first: 288 tiles
     // on 256 compute units, f16 4608 x 3584 at M = 24, 15.5 us with 8 waves
     // each, 13.8 with 4), but 4 where that is 5 to 7, which do not spread evenly
-    // over four SIMDs (gated 11008 x 4096 at M = 1, 5 waves -> 4: Q6_K 31 -> 24
-    // us, Q4_K 20.4 -> 16.3; 6 -> 4, gated 6144 x 4096 at M = 16: Q8_0 24.6 ->
-    // 19.7; 3 stay, all of them resident: Q8_0 gated 14336 x 4096 29 us, with 4
-    // 34), and where it is 1 or 2; no more than there are units, and at least
-    // the RT·MF that finish the sums.
+    // over four SIMDs, and where it is 1 or 2; no more than there are units, and
+    // at least the RT·MF that finish the sums.  Both sides, us:
+    //   6 -> 4: gated Q8_0 6144 x 4096, 1 row, 22.4 -> 17.8, 16 rows 24.5 -> 19.6;
+    //     gated Q6_K 4608 x 3584, 8 rows, 22.7 -> 18.1; 16 rows: Q8_0 6144 x 4096
+    //     14.9 -> 12.3, f16 15.2 -> 14.1, Q4_K 10.4 -> 9.8; Q4_K 4608 x 3584, 13
+    //     f32 rows, and gated 6144 x 4096, 8 rows, level;
+    //   5 -> 4: 1 row, 11008 x 4096: Q8_0 18.5 -> 13.0, Q6_K 15.7 -> 12.8, f16 and
+    //     Q4_K level; gated Q4_K 20.3 -> 15.9, Q6_K 30.7 -> 23.8, f16 37.5 -> 34;
+    //   3 stay 3, all of them resident; with 4: gated Q8_0 14336 x 4096, 1 row,
+    //     29.4 -> 33.7, 13824 x 5120, 4 rows, 38 -> 45; gated Q6_K 14336 x 4096, 8
+    //     rows, 31.4 -> 34.3; 16 rows: Q8_0 21.6 -> 23.5, Q4_K 16.7 -> 17.5, Q6_K
+    //     19.8 -> 20.2; gated 18944 x 3584, 1 row: Q6_K 33.5 -> 35.3, Q4_K 22.9 ->
+    //     23.5; ungated f16 and Q4_K level; gated Q4_K 14336 x 4096, 8 rows, 21.8 ->
+    //     21.4.
     const int per_cu = (tiles + kCUs - 1) / kCUs;
     int nw = max_waves(FMT, MR, GLU, XF32) / per_cu;
     if (nw < 3 || (nw > 4 && nw < 8)) nw = 4;

@@ -3,7 +3,8 @@
 // GEMMs), f32, or the Q8_1-style int8 blocks of the int8 product.
 //
 // Per row of K elements, everything in f32:
-//   h = x + r                     (rounded to r's type and written; without r, h = x)
+//   h = x + r                     (an f32 sum, rounded to r's type and written; without
+//                                  r, h = x)
 //   y = (h · 1/sqrt(Σh²/K + eps)) · w
 //   f16 / f32 output: y rounded once; Q8_1 output: per 32-element block the
 //   codes and (d, s) that mq_quantize_q8_1 gives for the f32 y, bit for bit
@@ -21,7 +22,7 @@
 // Measured: 2048 x 3584 (f32 in, f16 or Q8_1 out) 20.7 us = 4.96 TB/s, 2048 x
 // 8192 41.7 us = 5.6 TB/s (a plain device copy: 4.9), 4099 x 1001 f16 at an odd
 // stride 9.9 us = 3.3 TB/s (one short row per two waves: latency), one row of
-// 3584 2.5 us, the least a kernel of one round trip takes.
+// 3584 2.8 us (2.5 in a kernel trace), the least a kernel of one round trip takes.
 
 #include "mq_device.h"
 #include "mq_internal.h"
@@ -250,13 +251,15 @@ hipError_t launch_add_rms_norm(const NormSpec &n, hipStream_t stream) {
     a.r_type = n.r_type;
     a.y_type = n.y_type;
     a.eps = n.eps;
-    // One chunk per thread, T the power of two that covers the row: fewer
-    // threads leave too few loads in flight (1 x 3584, f32 in, f16 out: 512
-    // threads 2.8 us, 64 threads of 8 chunks 6.6), more stand idle (4099 x 1001
-    // f16: 128 threads 9.9 us, 256 11.5; 16384 x 128 f32: 16 threads 7.7, 64
-    // 11.0).  With enough rows to fill the chip, two chunks per thread save
-    // half the cross-wave sums from 257 chunks on (2048 x 3584: 20.7 us, 4.96
-    // TB/s, against 21.7; a plain device copy reaches 4.9).
+    // One chunk per thread, T the power of two that covers the row: for one row,
+    // fewer threads leave too few loads in flight (1 x 3584, f32 in, f16 out: 512
+    // threads 2.8 us, 256 of 2 chunks 3.5, 64 of 8 chunks 6.6); for many, more
+    // stand idle (16384 x 128 f32: 16 threads 7.7 us, 64 11.0; 4099 x 1001 f16:
+    // 128 threads 9.9, 256 11.5).  With enough rows to fill the chip, two chunks
+    // per thread save half the cross-wave sums: taken from 257 chunks on (2048 x
+    // 3584: 20.7 us against 21.5 with 512 threads of one), where they gain 4 %;
+    // below, the gain is 2 to 3 % (4099 x 1001, 64 threads of two against 128 of
+    // one: f16 9.6 / 9.9, f32 13.9 / 14.2) and one chunk serves both.
     const int chunks = (n.K + 7) / 8;
     if (chunks <= 16) return launch_rows<16, 1, 256>(a, stream);
     if (chunks <= 32) return launch_rows<32, 1, 256>(a, stream);

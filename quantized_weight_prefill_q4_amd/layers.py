@@ -6,7 +6,8 @@ As in ``api``, every step of the computation runs in the HIP library.  A layer's
 arguments are checked, its outputs allocated and the library called by one
 native function (``csrc/binding.cpp``), on the current stream of the tensors'
 device.  All tensors of a call must be on one GPU; it need not be the current
-one.
+one.  Results are not recorded by autograd: the weights are fixed after load and
+the operators have no backward pass.
 """
 
 from __future__ import annotations
@@ -99,8 +100,9 @@ def linear_f16cache(x: torch.Tensor, w16: torch.Tensor, K: int | None = None,
     (f32 or f16): gemm_f16cache with the layer's epilogue.
 
     x [M, >=K] f16 (or f32, rounded to f16), w16 the f16 cache [N, ld], bias
-    f32 [N], act one of ACTIVATIONS, residual [M, N] f32 or f16.  out may be
-    the residual itself (the stream is then updated in place)."""
+    f32 [N], act one of ACTIVATIONS, residual [M, N] f32 or f16.  With out, y is
+    of its type; out may be the residual itself (the stream is then updated in
+    place)."""
     return _on_device(x, _binding().layer, "mq_linear_f16cache",
                       (x, w16, 0, -1, K, bias, _act(act), residual, False,
                        _out_type(out_dtype), split_k, out, ws))
@@ -144,11 +146,12 @@ def glu_fused(x: torch.Tensor, wq: torch.Tensor, fmt, N: int, K: int | None = No
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
                  eps: float = 1e-6, out_dtype: torch.dtype = torch.float16,
                  out: torch.Tensor | None = None, residual_out: torch.Tensor | None = None):
-    """(y, h): h = x + residual in the residual's type, and y [M, K] = h /
-    sqrt(mean(h^2) + eps) * weight in out_dtype (f16 or f32).
+    """(y, h): h = x + residual, summed in f32 and rounded to the residual's type,
+    and y [M, K] = h / sqrt(mean(h^2) + eps) * weight in out_dtype (f16 or f32;
+    with out, in its type).
 
-    x, residual [M, K] f32 or f16, any row stride; weight f32 [K].  Without a
-    residual h is None and y the norm of x.  residual_out may be the residual
+    x, residual [M, K] f32 or f16, any row stride from K on; weight f32 [K].
+    Without a residual h is None and y the norm of x.  residual_out may be the residual
     itself (the stream is then updated in place)."""
     return _on_device(x, _binding().norm, "mq_add_rms_norm",
                       (x, weight, residual, eps, _out_type(out_dtype), out, None, residual_out))
