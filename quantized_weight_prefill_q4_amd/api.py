@@ -23,7 +23,7 @@ FORMATS = {"q4_0": MQ_Q4_0, "q5_0": MQ_Q5_0, "q5_1": MQ_Q5_1, "q8_0": MQ_Q8_0,
 def _fmt(fmt) -> int:
     if isinstance(fmt, str):
         return FORMATS[fmt.lower()]
-    return int(fmt)
+    return _as_int(fmt)
 
 
 def _stream(t: torch.Tensor) -> int:
@@ -38,9 +38,9 @@ def _need_cuda(t: torch.Tensor, name: str, dtype: torch.dtype) -> None:
 
 
 # Sizes and strides are C ints in the ABI, and ctypes keeps the low 32 bits of what
-# does not fit.  No size or split the library accepts is as large as _INT_MAX, so
-# one that does not fit is passed to a query as that, and refused; strides may be
-# any int, and beyond it are refused here.
+# does not fit.  No format, size or split the library accepts is as large as
+# _INT_MAX, so one that does not fit is passed as that, and refused; strides may
+# be any int, and beyond it are refused here.
 _INT_MAX = (1 << 31) - 1
 
 
@@ -232,7 +232,7 @@ def gemm_f16cache(x: torch.Tensor, w16: torch.Tensor, K: int | None = None, spli
     check(getattr(lib(), fn)(x.data_ptr(), ldx, w16.data_ptr(), ldw, out.data_ptr(), ldy,
                              M, N, K, 0 if ws is None else ws.data_ptr(),
                              0 if ws is None else ws.numel() * ws.element_size(),
-                             split_k, _stream(x)), fn)
+                             _as_int(split_k), _stream(x)), fn)
     return out
 
 
@@ -260,7 +260,7 @@ def gemm_fused(x: torch.Tensor, wq: torch.Tensor, fmt, N: int, K: int | None = N
     check(getattr(lib(), fn)(f, x.data_ptr(), ldx, wq.data_ptr(), out.data_ptr(), ldy, M, N, K,
                              0 if ws is None else ws.data_ptr(),
                              0 if ws is None else ws.numel() * ws.element_size(),
-                             split_k, _stream(x)), fn)
+                             _as_int(split_k), _stream(x)), fn)
     return out
 
 
@@ -342,6 +342,6 @@ def gemm_mmq(xq: torch.Tensor, ds: torch.Tensor, wq: torch.Tensor, fmt, N: int, 
         ws = torch.empty(nbytes // 4, dtype=torch.float32, device=xq.device) if nbytes else None
     check(lib().mq_gemm_mmq(f, xq.data_ptr(), ldq, ds.data_ptr(), wq.data_ptr(), out.data_ptr(),
                             ldy, M, N, K, 0 if ws is None else ws.data_ptr(),
-                            0 if ws is None else ws.numel() * ws.element_size(), split_k,
-                            _stream(xq)), "mq_gemm_mmq")
+                            0 if ws is None else ws.numel() * ws.element_size(),
+                            _as_int(split_k), _stream(xq)), "mq_gemm_mmq")
     return out

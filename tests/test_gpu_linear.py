@@ -837,3 +837,22 @@ def test_few_rows_keep_special_values_apart(fmt, xt):
             assert torch.equal(y[:, cols], want[:, cols]), M
             if fmt == 0:                             # infinities of both signs
                 assert bool(torch.isnan(y[:, 7]).all())
+
+
+def test_splits_beyond_int_are_refused():
+    """With a workspace of the caller's, which no size query precedes."""
+    K, N, split = 512, 64, (1 << 32) + 2
+    announce("splits beyond int")
+    x = torch.zeros(40, K, dtype=torch.float16, device=dev())
+    w = torch.zeros(N, K, dtype=torch.float16, device=dev())
+    q = torch.zeros(N * mq.row_bytes("q8_0", K), dtype=torch.uint8, device=dev())
+    ws = torch.empty(1 << 22, device=dev())
+    xq, ds = mq.quantize_q8_1(x.float())
+    for call in (lambda: mq.gemm_f16cache(x, w, K, split_k=split, ws=ws),
+                 lambda: mq.gemm_fused(x, q, "q8_0", N, K, split_k=split, ws=ws),
+                 lambda: mq.gemm_mmq(xq, ds, q, "q8_0", N, K, split_k=split, ws=ws),
+                 lambda: mq.linear_f16cache(x, w, K, split_k=split, ws=ws),
+                 lambda: mq.glu_fused(x, q, "q8_0", N // 2, K, split_k=split, ws=ws)):
+        with pytest.raises(mq.MQError) as e:
+            call()
+        assert e.value.code == _lib.MQ_ERR_SPLIT

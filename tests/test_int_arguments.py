@@ -53,3 +53,14 @@ def test_queries(query):
             with pytest.raises(mq.MQError) as e:
                 query(*bad)
             assert e.value.code == (_lib.MQ_ERR_SPLIT if i == 3 else _lib.MQ_ERR_SHAPE)
+
+
+def test_formats():
+    for fmt in (WRAPS + _lib.MQ_Q4_K, _lib.MQ_Q4_K - WRAPS):
+        for query in (lambda: mq.row_bytes(fmt, 256), lambda: mq.block_bytes(fmt),
+                      lambda: mq.workspace_bytes(fmt, 40, 512, 512),
+                      lambda: mq.linear_workspace_bytes(fmt, 40, 512, 512)):
+            with pytest.raises(mq.MQError) as e:
+                query()
+            assert e.value.code == _lib.MQ_ERR_FORMAT
+    assert mq.row_bytes(_lib.MQ_Q4_K, 256) == 144
