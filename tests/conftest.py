@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -13,6 +14,14 @@ GOLDEN = os.path.join(ROOT, "tests", "golden")
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (gfx950) GPU; runs the HIP library")
     config.addinivalue_line("markers", "slow: full-size shapes (minutes on CPU)")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _no_garbage_of_earlier_modules():
+    """Tensors kept by reference cycles (the traceback of an expected exception holds its
+    frames) are freed here, not by a collection in the middle of a test that compares
+    how much memory is allocated before and after its calls."""
+    gc.collect()
 
 
 @pytest.fixture(scope="session")
