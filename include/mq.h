@@ -81,7 +81,7 @@ enum {
 enum {
     MQ_OK = 0,
     MQ_ERR_NULL = -1,      /* a required pointer is NULL */
-    MQ_ERR_FORMAT = -2,    /* unknown weight format */
+    MQ_ERR_FORMAT = -2,    /* unknown weight format or rotary layout */
     MQ_ERR_SHAPE = -3,     /* M, N or K <= 0 or too large, or K not a multiple of the block */
     MQ_ERR_LD = -4,        /* a leading dimension is too small, too large or not a
                               multiple of 8 (of 4 for f32 activation rows) */
@@ -92,7 +92,8 @@ enum {
     MQ_ERR_SCRATCH = -9,   /* mq_gemm_fused_noalloc: the plan's partial tiles exceed
                               MQ_NOALLOC_SCRATCH_BYTES */
     MQ_ERR_TYPE = -10,     /* an element type that is not MQ_F32 or MQ_F16 */
-    MQ_ERR_EPS = -11,      /* a norm's eps that is negative or not finite */
+    MQ_ERR_EPS = -11,      /* a norm's eps, an attention's scale, cap or window or a rotation's
+                              magnitude that is not finite or, where it must not be, negative */
     MQ_ERR_OVERLAP = -12,  /* an output that overlaps another buffer of the call where
                               the entry point does not allow it */
     MQ_ERR_ACT = -13       /* unknown activation */
@@ -429,6 +430,135 @@ int mq_add_rms_norm(int x_type, const void *X, int ldx, int r_type, const void *
 int mq_add_rms_norm_q8_1(int x_type, const void *X, int ldx, int r_type, const void *R, int ldr,
                          const float *w, float eps, void *H, int ldh, int8_t *Xq, int ldq,
                          float *ds, int M, int K, void *stream);
+
+/* Rotary positions: in each of `heads` heads of head_dim elements, the first n_rot
+ * elements are turned pair by pair by the row's position,
+ *   a = position · freqs[j]  (f64),  c = f32(cos a · mscale),  s = f32(sin a · mscale)
+ *   (x0, x1) -> (x0·c − x1·s, x1·c + x0·s),
+ * each operation in f32, rounded once to the output type; the rest of the head
+ * is copied.  The pairs are elements (j, j + n_rot/2), or (2j, 2j + 1).
+ *   X, Y      : device, x_type and y_type, row strides ldx, ldy >= heads · head_dim,
+ *               aligned to their element.  Y may be X itself (pointer, stride and
+ *               type), else they may not overlap; nor may Y overlap the tables.
+ *   positions : device int32, M values, any (a negative one turns backwards).
+ *   freqs     : device f64, n_rot/2 values: the angle per position of each pair, with
+ *               whatever scaling a long context asks for.
+ *   layout    : MQ_ROPE_HALF or MQ_ROPE_INTERLEAVED.
+ *   mscale    : finite magnitude on cosine and sine (1 where there is none).
+ *   head_dim  : 1 .. MQ_MAX_ROPE_DIM; n_rot even, 2 .. head_dim; heads 1 ..
+ *               MQ_MAX_HEADS, heads · head_dim <= MQ_MAX_K.
+ * Errors: MQ_ERR_NULL, MQ_ERR_TYPE, MQ_ERR_SHAPE, MQ_ERR_FORMAT (layout), MQ_ERR_EPS
+ * (mscale), MQ_ERR_LD, MQ_ERR_ALIGN, MQ_ERR_OVERLAP, MQ_ERR_HIP. */
+enum {
+    MQ_ROPE_HALF = 0,
+    MQ_ROPE_INTERLEAVED = 1
+};
+#define MQ_MAX_HEADS 4096
+#define MQ_MAX_ROPE_DIM 1024
+
+int mq_rope(int x_type, const void *X, int ldx, const int32_t *positions, const double *freqs,
+            int n_rot, int layout, float mscale, int heads, int head_dim, int y_type, void *Y,
+            int ldy, int M, void *stream);
+
+/* A key/value cache in 4-bit blocks, and a batch of sequences over it.
+ *
+ * The cache is `pages` pages, each of `page` tokens (a multiple of 32) of `heads`
+ * key/value heads of head_dim (64, 96, 128 or 256) elements.  32 consecutive
+ * elements of a token's key or value are one block, d·(q − 8) with f16 d and 4-bit q
+ * as in MQ_Q4_0: 36·head_dim bytes for 32 tokens of a head.  The bytes' order is
+ * the library's (that of its kernels' operands); mq_kv_store_q4 writes them and
+ * mq_kv_load_q4 reads them back.  A cache needs no initial contents.
+ *
+ * Token t of sequence b lies in page table[b·table_ld + t / page].  Sequence b has
+ * lens[b] tokens, the batch's own rows included: its n rows are its last n tokens,
+ * at positions lens[b] − n .. lens[b] − 1.  They are rows cu_rows[b] .. cu_rows[b + 1]
+ * of the batch's M, or with cu_rows == NULL M / batch rows each, in order.
+ *
+ * table, lens and cu_rows are device memory, read by the kernels alone, so they may
+ * change between replays of a captured call.  What they hold is never taken on
+ * trust: entries of table outside 0 .. pages − 1 name no page (nothing is stored
+ * there, its tokens are not attended to and load as zeros), nor do positions at or
+ * past table_width · page; lens is cut to 0 .. 2^30; cu_rows is expected to start at
+ * 0 or more and not to descend, and is cut to 0 .. M.  Rows before cu_rows[0] and
+ * behind cu_rows[batch] are left as they were. */
+typedef struct mq_kv_q4 {
+    void *cache;             /* device, 16-byte aligned */
+    int64_t page_bytes;      /* from one page to the next: >= mq_kv_q4_page_bytes(heads,
+                                page, head_dim), a multiple of 16 */
+    int pages, heads, page, head_dim;
+    const int32_t *table;    /* device, [batch][table_width], rows table_ld apart */
+    int table_width, table_ld;
+    const int32_t *lens;     /* device, [batch] */
+    const int32_t *cu_rows;  /* device, [batch + 1], or NULL (M a multiple of batch) */
+    int batch;
+} mq_kv_q4;
+
+/* Bytes of one page, or MQ_ERR_SHAPE. */
+int64_t mq_kv_q4_page_bytes(int heads, int page, int head_dim);
+
+/* Quantizes the rows' keys and values into the cache, the keys rotated first when
+ * freqs is given, and rotates the rows' queries beside them when Q is.
+ * Per block, v its first element of largest magnitude: d = f16(v / −8), q =
+ * clamp(floor(x/d + 8.5), 0, 15), 8 where d is 0; all in f32.  A block with an
+ * infinity or NaN, or whose d overflows f16, gets NaN as its d.
+ *   K, V      : device, x_type, row strides ldk, ldv >= heads · head_dim.
+ *   freqs, n_rot, layout, mscale : as mq_rope; freqs == NULL: no rotation (the other
+ *               three ignored).
+ *   positions : device int32, M values: rotary positions of the rows, or NULL: their
+ *               positions in the sequence.
+ *   Q, QO     : device, x_type and q_type, q_heads heads of head_dim, row strides ldq,
+ *               ldqo; QO may be Q itself (pointer, stride and type).  Q == NULL: none.
+ * All are aligned to their element.  Neither QO nor the cache may overlap another
+ * buffer of the call.  Rows at negative positions (lens[b] smaller than the
+ * sequence's rows) are left out, their queries included.  Two sequences whose
+ * tables give the same page for rows of this call overwrite each other there in
+ * no particular order.
+ * Errors: those of mq_rope, MQ_ERR_SHAPE also for M not a multiple of batch without
+ * cu_rows, MQ_ERR_LD also for page_bytes and table_ld. */
+int mq_kv_store_q4(const mq_kv_q4 *cache, int x_type, const void *K, int ldk, const void *V, int ldv,
+                   const double *freqs, int n_rot, int layout, float mscale,
+                   const int32_t *positions, const void *Q, int ldq, int q_heads, int q_type,
+                   void *QO, int ldqo, int M, void *stream);
+
+/* The rows' keys and values as the cache holds them: d·(q − 8), exact in f32, rounded
+ * once in f16.
+ *   K, V : device, y_type, row strides ldk, ldv >= heads · head_dim, aligned to their
+ *          element; written.  Neither may overlap another buffer of the call.
+ * Rows at negative positions are left as they were. */
+int mq_kv_load_q4(const mq_kv_q4 *cache, int y_type, void *K, int ldk, void *V, int ldv, int M,
+                  void *stream);
+
+/* Attention of the rows over the cache.  For the row at position p of sequence b and
+ * each of q_heads heads (a multiple of heads: head h reads key/value head
+ * h / (q_heads / heads)), over the tokens j of the sequence that the row sees,
+ *   s_j = scale · q·k_j;  cap > 0: s_j = cap · tanh(s_j / cap);
+ *   slopes: s_j −= slopes[h] · |p − j|;   y = Σ_j softmax(s)_j · v_j.
+ * A row sees j where (not causal, or j <= p) and (window 0, or |p − j| < window), and
+ * every j < prefix[b].  A row that sees nothing gives zeros.
+ * q, k and v enter in f16 (f32 queries rounded to f16, d·(q − 8) rounded once),
+ * products are summed in f32 and scores and statistics are f32; the weights
+ * e^(s − max) are rounded to f16 (2^-12 of each, as far as 2^-29 of the largest) and
+ * y once to f16.  A token whose d is infinite or NaN makes the rows that see it not
+ * finite, and no others.
+ *   Q      : device, x_type, row stride ldq >= q_heads · head_dim.
+ *   Y      : device f16, row stride ldy likewise.  Q and Y are aligned to their element.
+ *   scale  : finite.  cap : finite, >= 0.  window : >= 0.
+ *   slopes : device f32, q_heads values, or NULL.
+ *   prefix : device int32, batch values, or NULL.
+ *   max_len: a bound of lens, for the launch plan alone (results do not depend on its
+ *            being one): long sequences are cut into parts that are joined after.
+ *   ws     : device, 16-byte aligned, ws_bytes >= mq_attention_q4_workspace_bytes(the
+ *            same cache, q_heads, M, max_len), or NULL when that is 0.  Calls that may
+ *            overlap in time need a workspace each.
+ * Neither Y nor ws may overlap another buffer of the call.
+ * Errors: as above, MQ_ERR_EPS (scale, cap, window), MQ_ERR_WORKSPACE. */
+int64_t mq_attention_q4_workspace_bytes(const mq_kv_q4 *cache, int q_heads, int M,
+                                        int64_t max_len);
+
+int mq_attention_q4(const mq_kv_q4 *cache, int x_type, const void *Q, int ldq, int q_heads,
+                    uint16_t *Y, int ldy, int M, float scale, int causal, int window, float cap,
+                    const float *slopes, const int32_t *prefix, int64_t max_len, void *ws,
+                    size_t ws_bytes, void *stream);
 
 /* The launch plan of a GEMM call, as the host computes it (no GPU needed, no
  * device call made).  For callers that size workspaces ahead and for tests

@@ -57,6 +57,13 @@ class MqGemmPlanInfo(ctypes.Structure):
                 ("ws_bytes", _c_i64)]
 
 
+class MqKvQ4(ctypes.Structure):
+    """struct mq_kv_q4 of include/mq.h."""
+    _fields_ = [("cache", _vp), ("page_bytes", _c_i64), ("pages", _c_int), ("heads", _c_int),
+                ("page", _c_int), ("head_dim", _c_int), ("table", _vp), ("table_width", _c_int),
+                ("table_ld", _c_int), ("lens", _vp), ("cu_rows", _vp), ("batch", _c_int)]
+
+
 # name -> (restype, argtypes); mirrors include/mq.h
 SIGNATURES = {
     "mq_block_elems": (_c_int, [_c_int]),
@@ -98,6 +105,18 @@ SIGNATURES = {
                                  _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _vp]),
     "mq_add_rms_norm_q8_1": (_c_int, [_c_int, _vp, _c_int, _c_int, _vp, _c_int, _vp, _c_float,
                                       _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _vp]),
+    "mq_rope": (_c_int, [_c_int, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_float, _c_int, _c_int,
+                         _c_int, _vp, _c_int, _c_int, _vp]),
+    "mq_kv_q4_page_bytes": (_c_i64, [_c_int, _c_int, _c_int]),
+    "mq_kv_store_q4": (_c_int, [ctypes.POINTER(MqKvQ4), _c_int, _vp, _c_int, _vp, _c_int, _vp,
+                                _c_int, _c_int, _c_float, _vp, _vp, _c_int, _c_int, _c_int, _vp,
+                                _c_int, _c_int, _vp]),
+    "mq_kv_load_q4": (_c_int, [ctypes.POINTER(MqKvQ4), _c_int, _vp, _c_int, _vp, _c_int, _c_int,
+                               _vp]),
+    "mq_attention_q4_workspace_bytes": (_c_i64, [ctypes.POINTER(MqKvQ4), _c_int, _c_int, _c_i64]),
+    "mq_attention_q4": (_c_int, [ctypes.POINTER(MqKvQ4), _c_int, _vp, _c_int, _c_int, _vp, _c_int,
+                                 _c_int, _c_float, _c_int, _c_int, _c_float, _vp, _vp, _c_i64, _vp,
+                                 _c_size, _vp]),
     "mq_gemm_plan_query": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                     ctypes.POINTER(MqGemmPlanInfo)]),
     "mq_strerror": (ctypes.c_char_p, [_c_int]),

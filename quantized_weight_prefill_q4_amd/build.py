@@ -4,7 +4,7 @@ layer operators with the host compiler.
 Usage: ``python -m quantized_weight_prefill_q4_amd.build`` (or ``build_lib()``).
 Each ``csrc/*.hip`` file is compiled to an object under ``_build/`` in
 parallel, then linked into ``quantized_weight_prefill_q4_amd/libmq.so``;
-``csrc/binding.cpp`` becomes the extension module ``_binding.so`` beside it.
+``csrc/binding*.cpp`` become the extension module ``_binding.so`` beside it.
 """
 
 from __future__ import annotations
@@ -24,7 +24,10 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libmq.so")
 BINDING_PATH = os.path.join(PKG, "_binding.so")
 SOURCES = ("mq_api.hip", "dequant.hip", "gemm.hip", "gemm_xf32.hip", "mmq.hip", "rms_norm.hip",
-           "gemm_linear.hip", "gemm_glu.hip", "linear_rows.hip")
+           "gemm_linear.hip", "gemm_glu.hip", "linear_rows.hip", "rope.hip", "kv_q4.hip",
+           "attention_q4.hip")
+
+BINDING_SOURCES = ("binding.cpp", "binding_attention.cpp")
 
 CXX = os.environ.get("CXX", shutil.which("g++") or "c++")
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -65,7 +68,7 @@ def _compile(src: str, verbose: bool) -> str:
 
 
 def _build_binding(verbose: bool) -> str:
-    """csrc/binding.cpp as a CPython extension against the installed torch."""
+    """csrc/binding*.cpp as a CPython extension against the installed torch."""
     import torch
 
     root = os.path.dirname(os.path.abspath(torch.__file__))
@@ -76,7 +79,7 @@ def _build_binding(verbose: bool) -> str:
            "-I", INCLUDE, "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           *(os.path.join(CSRC, s) for s in BINDING_SOURCES), "-o", tmp,
            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -1,0 +1,554 @@
+// Attention over the 4-bit key/value cache (kv_q4.h has its layout).
+//
+// Row i of a sequence with n new rows and len tokens stands at p = len − n + i.
+// For each of its heads, with q the row's query and k_j, v_j the cache's:
+//   s_j = scale · q·k_j;  s_j = cap · tanh(s_j / cap);  s_j −= slope · |p − j|
+//   o   = Σ_j e^(s_j − m) v_j / Σ_j e^(s_j − m),  over the visible j, m their maximum
+// and zeros where none is visible.
+//
+// A workgroup takes R rows (row = token · group + head of the group, so that the
+// query heads of a key/value head share its tiles) of one key/value head and a
+// part of the keys; its four waves take the part's tiles of 32 tokens in turn and
+// their results are joined at the end.  Per tile, in one pass with the running
+// maximum and sum:
+//   Sᵀ[t, n] = K[t, :] · Q[n, :]    matrix instructions 16 x 16 x 32, keys as A
+//   Oᵀ[d, n] += Vᵀ[d, t] · Pᵀ[t, n]  values as A
+// A lane holds of Sᵀ exactly the eight tokens whose weights it has to give as the
+// second product's B operand, because row r of the first product's tile m is
+// token 8·(r/4) + 4·m + r%4: nothing moves between lanes but the maximum of a
+// column.  Codes become f16 in the registers that loaded them.
+//
+// Numerics: q, k and v in f16 (k and v each d·(q − 8) rounded once), products
+// summed in f32; the statistics in f32; a weight e^(s − m) is rounded to f16 as
+// the operand of the second product, times 2^15, so that weights down to 2^-29 of
+// the largest keep 11 bits (the factor leaves with the sum).
+#include "attention_view.h"
+#include "mq_device.h"
+
+namespace mq {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr float kLog2e = 1.44269502f;
+constexpr float kShift = 15.0f;       // weights are held times 2^15
+constexpr int kMaxSplits = 256;
+
+// 1 − 2 / (1 + e^2u), and below 1/4, where that cancels, u − u³/3 + 2u⁵/15 − 17u⁷/315
+// (the next term is 3e-7 of the value at 1/4).
+__device__ __forceinline__ float tanh_f32(float u) {
+    const float e = __builtin_amdgcn_exp2f(u * (2.0f * kLog2e));
+    const float t = u * u;
+    float p = __builtin_fmaf(t, -17.0f / 315.0f, 2.0f / 15.0f);
+    p = __builtin_fmaf(t, p, -1.0f / 3.0f);
+    p = __builtin_fmaf(t * u, p, u);
+    return fabsf(u) < 0.25f ? p : 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+typedef uint32_t q_u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float q_f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight query elements as f16.
+__device__ __forceinline__ half8 load_q8(const void *q, int f32, int64_t at) {
+    if (!f32)
+        return __builtin_bit_cast(
+            half8, (u32x4)*reinterpret_cast<const q_u32x4_a2 *>((const uint16_t *)q + at));
+    const q_f32x4_a4 *p = reinterpret_cast<const q_f32x4_a4 *>((const float *)q + at);
+    const f32x4 x = p[0], y = p[1];
+    return __builtin_bit_cast(half8, u32x4{pack_f16x2(x.x, x.y), pack_f16x2(x.z, x.w),
+                                           pack_f16x2(y.x, y.y), pack_f16x2(y.z, y.w)});
+}
+
+// The eight (q − 8) of a code dword, exact.  A nibble under the exponent of 1024
+// is 1024 + q, one place of four bits higher 1024 + 16·q.
+__device__ __forceinline__ void widen(uint32_t w, half2v h[4]) {
+    const half2v c = {(_Float16)1032.0f, (_Float16)1032.0f};
+    const half2v s = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const half2v o = {(_Float16)-72.0f, (_Float16)-72.0f};
+    const uint32_t u = w >> 8;
+    h[0] = __builtin_bit_cast(half2v, (w & 0x000F000Fu) | 0x64006400u) - c;
+    h[1] = __builtin_elementwise_fma(
+        __builtin_bit_cast(half2v, (w & 0x00F000F0u) | 0x64006400u), s, o);
+    h[2] = __builtin_bit_cast(half2v, (u & 0x000F000Fu) | 0x64006400u) - c;
+    h[3] = __builtin_elementwise_fma(
+        __builtin_bit_cast(half2v, (u & 0x00F000F0u) | 0x64006400u), s, o);
+}
+
+__device__ __forceinline__ half8 join8(const half2v h[4]) {
+    return half8{h[0].x, h[0].y, h[1].x, h[1].y, h[2].x, h[2].y, h[3].x, h[3].y};
+}
+
+__device__ __forceinline__ half2v as_half2(uint32_t w) { return __builtin_bit_cast(half2v, w); }
+
+// A tile as loaded: code dwords of the lane's operands and the scales they need.
+// Lane l is row r = l % 16 of the A operands and their inner octet g = l / 16.
+// Values' operand i holds element d(r, i) of tokens [8g, + 8): d = (D/16)·r + i,
+// where one scale per token serves all of a lane's operands, or for D = 96, whose
+// 16ths straddle blocks, d = 16·i + r.
+template <int NS>
+struct Tile {
+    static constexpr bool kRuns = (NS & (NS - 1)) == 0;
+    static constexpr int kScaleSets = kRuns ? 1 : NS;
+    uint32_t k[2][NS], v[2 * NS];
+    uint32_t ks[2][(NS + 1) / 2];
+    u32x4 vs[kScaleSets];
+};
+
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint32_t *p, uint32_t (&w)[N]) {
+    typedef uint32_t v2 __attribute__((ext_vector_type(2)));
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const u32x4 x = *(const u32x4 *)(p + i);
+            w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+        }
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const v2 x = *(const v2 *)(p + i);
+            w[i] = x.x; w[i + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = p[i];
+    }
+}
+
+template <int NS>
+__device__ __forceinline__ void load_tile(const char *tile, int r, int g, Tile<NS> &t) {
+    constexpr int D = 32 * NS;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        load_dwords((const uint32_t *)tile + ((4 * m + g) * 16 + r) * NS, t.k[m]);
+        const uint16_t *s = (const uint16_t *)(tile + kv_kscale_at(D)) + (16 * m + r) * NS;
+        if constexpr (NS % 2 == 0) {
+            load_dwords((const uint32_t *)s, t.ks[m]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < (NS + 1) / 2; ++i)
+                t.ks[m][i] = s[2 * i] | (2 * i + 1 < NS ? (uint32_t)s[2 * i + 1] << 16 : 0u);
+        }
+    }
+    const uint32_t *vc = (const uint32_t *)(tile + kv_vcode_at(D)) + g * D;
+    const u32x4 *vs = (const u32x4 *)(tile + kv_vscale_at(D)) + g * NS;
+    if constexpr (Tile<NS>::kRuns) {
+        load_dwords(vc + 2 * NS * r, t.v);
+        t.vs[0] = vs[(2 * NS * r) / 32];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2 * NS; ++i) t.v[i] = vc[16 * i + r];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) t.vs[i] = vs[i];
+    }
+}
+
+// The values' operand i.
+template <int NS>
+__device__ __forceinline__ half8 value_operand(const Tile<NS> &t, int i) {
+    const u32x4 s = t.vs[Tile<NS>::kRuns ? 0 : i / 2];
+    half2v h[4];
+    widen(t.v[i], h);
+    h[0] *= as_half2(s.x);
+    h[1] *= as_half2(s.y);
+    h[2] *= as_half2(s.z);
+    h[3] *= as_half2(s.w);
+    return join8(h);
+}
+
+// f16 words whose exponent is all ones (infinities, NaN), as 1.0 / 0.0 each.
+__device__ __forceinline__ uint32_t bad_halves(uint32_t w) {
+    return ((w & 0x7C00u) == 0x7C00u ? 0x3C00u : 0u) |
+           ((w & 0x7C000000u) == 0x7C000000u ? 0x3C000000u : 0u);
+}
+__device__ __forceinline__ uint32_t keep_halves(uint32_t w, bool lo, bool hi) {
+    return (lo ? w & 0xFFFFu : 0u) | (hi ? w & 0xFFFF0000u : 0u);
+}
+
+template <int NS, int NT, bool BIAS>
+__global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
+    constexpr int D = 32 * NS, R = 16 * NT, MT = 2 * NS;   // MT: output tiles of 16 elements
+    constexpr int CH = MT < 8 ? MT : 8;                    // of them joined at a time
+    __shared__ float join[kWaves][CH * 4][64];
+    __shared__ float2 wave_stats[kWaves][R];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    const int split = blockIdx.x % a.splits;
+    const int job = blockIdx.x / a.splits;                 // row tile · heads + head
+    const int head = job % a.kv.heads;
+    View view;
+    if (!find_view<R>(a, job / a.kv.heads, view)) return;
+    const int chunk = part_tiles(view.n, a.splits);
+    const int t_begin = split * chunk;
+    const int t_end = t_begin + chunk < view.n ? t_begin + chunk : view.n;
+    if (t_begin >= t_end && (a.splits > 1 && split > 0)) return;
+
+    // this lane's column in each of the NT column tiles: row 16·c + r
+    half8 q[NT][NS];
+    int pos[NT];
+    Range range[NT];
+    float slope[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        const int64_t row = (int64_t)view.rt * R + 16 * c + r;
+        const int i = (int)(row / a.group), h = head * a.group + (int)(row - (int64_t)i * a.group);
+        const bool live = i < view.rows.n;
+        pos[c] = view.first_pos + i;
+        range[c] = row_range(a, view, pos[c]);
+        slope[c] = BIAS && a.slopes && live ? a.slopes[h] : 0.0f;
+        const int64_t at = (int64_t)(view.rows.first + (live ? i : 0)) * a.ldq +
+                           (int64_t)(live ? h : head * a.group) * D + 8 * g;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) q[c][s] = load_q8(a.q, a.q_f32, at + 32 * s);
+    }
+    f32x4 o[NT][MT];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        m[c] = -__builtin_inff();
+        l[c] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[c][i] = f32x4{0, 0, 0, 0};
+    }
+    const float to_log2 = BIAS ? kLog2e : a.scale * kLog2e;
+
+    auto tile_of = [&](int t) { return t < view.pre ? t : t - view.pre + view.lo; };
+    for (int t = t_begin + wave; t < t_end; t += kWaves) {
+        const int tile = tile_of(t), j0 = tile * kTile;
+        const char *p = kv_tile(a.kv, view.b, head, tile);
+        if (!p) continue;   // no such page: its tokens are not visible
+        Tile<NS> now;
+        load_tile(p, r, g, now);
+        f32x4 s[NT][2];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c) s[c][mt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                half2v h[4];
+                widen(now.k[mt][k], h);
+                const half2v pair = as_half2(now.ks[mt][k / 2]);
+                const _Float16 d = k & 1 ? pair.y : pair.x;
+                const half2v dd = {d, d};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] *= dd;
+                const half8 op = join8(h);
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+                    s[c][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, q[c][k], s[c][mt], 0, 0, 0);
+            }
+        }
+        // element b of s[c][mt]: token j0 + 8g + 4·mt + b
+        const bool edge = !all_visible(a, view, j0);
+        if constexpr (BIAS) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float x = s[c][mt][b] * a.scale;
+                        if (a.cap > 0.0f) x = a.cap * tanh_f32(x * a.inv_cap);
+                        const int j = j0 + 8 * g + 4 * mt + b;
+                        s[c][mt][b] = x - slope[c] * (float)(pos[c] > j ? pos[c] - j : j - pos[c]);
+                    }
+        }
+        uint32_t seen[NT];   // bit 4·mt + b of column c: visible
+        if (edge) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                seen[c] = 0;
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const bool see =
+                            in_range(range[c], view.prefix, j0 + 8 * g + 4 * mt + b);
+                        seen[c] |= (uint32_t)see << (4 * mt + b);
+                        s[c][mt][b] = see ? s[c][mt][b] : -__builtin_inff();
+                    }
+            }
+        }
+        half8 w[NT];
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) top = fmaxf(top, s[c][mt][b]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            top *= to_log2;
+            const float mc = fmaxf(m[c], top);
+            if (__any(mc > m[c])) {
+                const float f = mc == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[c] - mc);
+                l[c] *= f;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) o[c][i] *= f;
+                m[c] = mc;
+            }
+            const float base = mc == -__builtin_inff() ? 0.0f : mc - kShift;
+            float e[8];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    e[4 * mt + b] =
+                        __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][mt][b], to_log2, -base));
+                    l[c] += e[4 * mt + b];
+                }
+            w[c] = __builtin_bit_cast(half8, u32x4{pack_f16x2(e[0], e[1]), pack_f16x2(e[2], e[3]),
+                                                   pack_f16x2(e[4], e[5]), pack_f16x2(e[6], e[7])});
+        }
+        if (edge) {
+            // Weights of unseen tokens are 0, but 0 times an infinite or NaN scale
+            // is not.  Tokens past the sequence (never written, perhaps) lose their
+            // scale; others that are not finite are taken out and given, as NaN,
+            // to the rows that see them.
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < Tile<NS>::kScaleSets; ++i) {
+                const int e0 = view.keys - j0 - 8 * g;   // tokens of this octet that exist
+                now.vs[i].x = keep_halves(now.vs[i].x, e0 > 0, e0 > 1);
+                now.vs[i].y = keep_halves(now.vs[i].y, e0 > 2, e0 > 3);
+                now.vs[i].z = keep_halves(now.vs[i].z, e0 > 4, e0 > 5);
+                now.vs[i].w = keep_halves(now.vs[i].w, e0 > 6, e0 > 7);
+                bad = bad || (bad_halves(now.vs[i].x) | bad_halves(now.vs[i].y) |
+                              bad_halves(now.vs[i].z) | bad_halves(now.vs[i].w));
+            }
+            if (__any(bad)) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const u32x4 s4 = now.vs[Tile<NS>::kRuns ? 0 : i / 2];
+                    const half8 ind = __builtin_bit_cast(
+                        half8, u32x4{bad_halves(s4.x), bad_halves(s4.y), bad_halves(s4.z),
+                                     bad_halves(s4.w)});
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        u32x4 see;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            see[e] = (seen[c] >> (2 * e) & 1 ? 0x3C00u : 0u) |
+                                     (seen[c] >> (2 * e + 1) & 1 ? 0x3C000000u : 0u);
+                        const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            ind, __builtin_bit_cast(half8, see), f32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (hit[b] > 0.0f) o[c][i][b] = __builtin_nanf("");
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < Tile<NS>::kScaleSets; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t x = bad_halves(now.vs[i][e]);
+                        now.vs[i][e] = keep_halves(now.vs[i][e], !(x & 0xFFFFu), !(x >> 16));
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const half8 op = value_operand(now, i);
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+                o[c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, w[c], o[c][i], 0, 0, 0);
+        }
+    }
+
+    // Join the waves: every wave's results at the common maximum.
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        l[c] += __shfl_xor(l[c], 16);
+        l[c] += __shfl_xor(l[c], 32);
+        if (g == 0) wave_stats[wave][16 * c + r] = float2{m[c], l[c]};
+    }
+    __syncthreads();
+    const int64_t part = (int64_t)job * a.splits + split;
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        float mc = -__builtin_inff(), lc = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) mc = fmaxf(mc, wave_stats[i][16 * c + r].x);
+        const float base = mc == -__builtin_inff() ? 0.0f : mc;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const float2 x = wave_stats[i][16 * c + r];
+            lc += x.y * __builtin_amdgcn_exp2f(x.x - base);
+        }
+        const float f = __builtin_amdgcn_exp2f(m[c] - base);
+        const float inv = lc == 0.0f ? 0.0f : 1.0f / lc;
+        const int64_t row = (int64_t)view.rt * R + 16 * c + r;
+        const int i = (int)(row / a.group), h = head * a.group + (int)(row - (int64_t)i * a.group);
+        const bool live = i < view.rows.n;
+        if (a.splits > 1 && wave == 0 && g == 0 && live) {
+            float *st = a.stats + (part * R + 16 * c + r) * 2;
+            st[0] = mc;
+            st[1] = lc;
+        }
+#pragma unroll
+        for (int i0 = 0; i0 < MT; i0 += CH) {
+            if (c > 0 || i0 > 0) __syncthreads();
+#pragma unroll
+            for (int k = 0; k < CH && i0 + k < MT; ++k)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) join[wave][4 * k + b][lane] = o[c][i0 + k][b] * f;
+            __syncthreads();
+            // wave b' = `wave` finishes element row 4g + b' of each tile
+            float x[CH];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+                x[k] = 0.0f;
+                if (i0 + k < MT)
+#pragma unroll
+                    for (int v = 0; v < kWaves; ++v) x[k] += join[v][4 * k + wave][lane];
+            }
+            const int dr = 4 * g + wave;   // row of the output tiles
+            if (live && a.splits > 1) {
+                float *y = a.partial + (part * R + 16 * c + r) * D;
+#pragma unroll
+                for (int k = 0; k < CH; ++k)
+                    if (i0 + k < MT) y[Tile<NS>::kRuns ? MT * dr + i0 + k : 16 * (i0 + k) + dr] = x[k];
+            } else if (live) {
+                uint16_t *y = a.y + (int64_t)(view.rows.first + i) * a.ldy + (int64_t)h * D;
+#pragma unroll
+                for (int k = 0; k < CH; ++k)
+                    if (i0 + k < MT)
+                        y[Tile<NS>::kRuns ? MT * dr + i0 + k : 16 * (i0 + k) + dr] =
+                            (uint16_t)pack_f16x2(x[k] * inv, 0.0f);
+            }
+        }
+    }
+}
+
+// Joins the parts of each row: one wave per row, over the workgroups' layout.
+template <int NS>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int R, int64_t rows) {
+    constexpr int D = 32 * NS;
+    const int lane = threadIdx.x & 63;
+    const int64_t id = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);   // job · R + row
+    if (id >= rows) return;
+    const int64_t job = id / R;
+    const int n = (int)(id - job * R), head = (int)(job % a.kv.heads);
+    View view;
+    const bool any = R == 16 ? find_view<16>(a, job / a.kv.heads, view)
+                   : R == 32 ? find_view<32>(a, job / a.kv.heads, view)
+                             : find_view<64>(a, job / a.kv.heads, view);
+    if (!any) return;
+    const int64_t row = (int64_t)view.rt * R + n;
+    const int i = (int)(row / a.group), h = head * a.group + (int)(row - (int64_t)i * a.group);
+    if (i >= view.rows.n) return;
+    const int chunk = part_tiles(view.n, a.splits);
+    int parts = (view.n + chunk - 1) / chunk;
+    if (parts < 1) parts = 1;   // the first part always writes
+    const float2 *st = (const float2 *)a.stats + job * a.splits * R + n;
+    float m = -__builtin_inff();
+    for (int s = lane; s < parts; s += 64) m = fmaxf(m, st[(int64_t)s * R].x);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    constexpr int E = (D + 63) / 64;
+    float x[E], sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = 0.0f;
+    const float *y = a.partial + (job * a.splits * R + n) * D;
+    for (int s = 0; s < parts; ++s) {
+        const float2 t = st[(int64_t)s * R];
+        const float f = __builtin_amdgcn_exp2f(t.x - base);
+        sum = __builtin_fmaf(t.y, f, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (lane + 64 * e < D)
+                x[e] = __builtin_fmaf(y[(int64_t)s * R * D + lane + 64 * e], f, x[e]);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t *out = a.y + (int64_t)(view.rows.first + i) * a.ldy + (int64_t)h * D;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (lane + 64 * e < D) out[lane + 64 * e] = (uint16_t)pack_f16x2(x[e] * inv, 0.0f);
+}
+
+template <int NS, int NT>
+void launch_rows(const AttnArgs &a, int64_t blocks, bool bias, hipStream_t stream) {
+    if (bias)
+        hipLaunchKernelGGL((attention_kernel<NS, NT, true>), dim3((unsigned)blocks), dim3(256), 0,
+                           stream, a);
+    else
+        hipLaunchKernelGGL((attention_kernel<NS, NT, false>), dim3((unsigned)blocks), dim3(256), 0,
+                           stream, a);
+}
+
+template <int NS>
+hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    const int64_t blocks = p.row_tiles * a.kv.heads * a.splits;
+    // without a cap or bias the scale goes into the exponent's factor, after the
+    // mask's −∞: it has to be positive and in range there
+    const bool bias = a.cap > 0.0f || a.slopes || !(a.scale > 1e-30f && a.scale < 1e30f);
+    if (p.rows == 16)
+        launch_rows<NS, 1>(a, blocks, bias, stream);
+    else if (p.rows == 32)
+        launch_rows<NS, 2>(a, blocks, bias, stream);
+    else if constexpr (NS <= 4)
+        launch_rows<NS, 4>(a, blocks, bias, stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t rows = p.row_tiles * a.kv.heads * p.rows;
+    hipLaunchKernelGGL((attention_join_kernel<NS>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
+                       dim3(256), 0, stream, a, p.rows, rows);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
+    AttnPlan p;
+    const int group = s.q_heads / kv.heads;
+    const int64_t mean = kv.cu ? ((int64_t)kv.M + kv.batch - 1) / kv.batch : kv.rows;
+    const int64_t rows = mean * group;   // of a key/value head and sequence
+    // (64 rows of 256 elements do not fit the registers)
+    p.rows = rows <= 16 ? 16 : rows <= 32 || kv.D > 128 ? 32 : 64;
+    p.row_tiles = kv.cu ? (int64_t)kv.M * group / p.rows + kv.batch
+                        : (rows + p.rows - 1) / p.rows * kv.batch;
+    // Parts of the keys: enough workgroups for every compute unit to hold four
+    const int64_t jobs = p.row_tiles * kv.heads;
+    const int64_t tiles = (s.max_len + kTile - 1) / kTile;
+    int64_t splits = (1024 + jobs - 1) / jobs;
+    if (splits > tiles / kMinTiles) splits = tiles / kMinTiles;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    if (splits < 1) splits = 1;
+    p.splits = (int)splits;
+    p.ws_bytes = splits == 1 ? 0 : jobs * splits * p.rows * (kv.D + 2) * 4;
+    return p;
+}
+
+hipError_t launch_attention(const KvSpec &kv, const AttnSpec &s, const AttnPlan &p, float *ws,
+                            hipStream_t stream) {
+    AttnArgs a;
+    a.kv = kv;
+    a.q = s.q;
+    a.y = s.y;
+    a.ldq = s.ldq;
+    a.ldy = s.ldy;
+    a.scale = s.scale;
+    a.cap = s.cap;
+    a.inv_cap = s.cap > 0.0f ? 1.0f / s.cap : 0.0f;
+    a.q_f32 = s.x_type == kTypeF32;
+    a.q_heads = s.q_heads;
+    a.group = s.q_heads / kv.heads;
+    a.causal = s.causal;
+    a.window = s.window;
+    a.splits = p.splits;
+    a.slopes = s.slopes;
+    a.prefix = s.prefix;
+    a.stats = ws;
+    a.partial = ws + p.row_tiles * kv.heads * p.splits * p.rows * 2;
+    a.per_seq = kv.cu ? 0 : ((int64_t)kv.rows * a.group + p.rows - 1) / p.rows;
+    switch (kv.D) {
+    case 64: return launch_dim<2>(a, p, stream);
+    case 96: return launch_dim<3>(a, p, stream);
+    case 128: return launch_dim<4>(a, p, stream);
+    default: return launch_dim<8>(a, p, stream);
+    }
+}
+
+}  // namespace mq

@@ -354,6 +354,71 @@ int run_linear(int fmt, int x_type, const void *X, int ldx, const void *W, int64
         stream));
 }
 
+// The units of kernels that number a batch's work come to fewer than 2^24 blocks
+// of 256 threads (a launch holds fewer than 2^32 threads).
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;
+
+// Checks of a cache and of the batch of M rows that goes with it; fills `kv`.
+int check_kv(const mq_kv_q4 *c, int M, mq::KvSpec *kv) {
+    if (!c || !c->cache || !c->table || !c->lens) return MQ_ERR_NULL;
+    if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 256)
+        return MQ_ERR_SHAPE;
+    if (c->heads <= 0 || c->heads > MQ_MAX_HEADS || c->page <= 0 || c->page % 32 ||
+        c->page > mq::kMaxLen || c->pages <= 0 || c->batch <= 0 || c->table_width <= 0)
+        return MQ_ERR_SHAPE;
+    if (M <= 0 || M > MQ_MAX_DIM || c->batch > MQ_MAX_DIM) return MQ_ERR_SHAPE;
+    if (!c->cu_rows && M % c->batch) return MQ_ERR_SHAPE;
+    if (M / 8 + 2 * (int64_t)c->batch > kMaxBlocks) return MQ_ERR_SHAPE;
+    if (c->page_bytes < mq_kv_q4_page_bytes(c->heads, c->page, c->head_dim) || c->page_bytes % 16 ||
+        (c->batch > 1 && c->table_ld < c->table_width))
+        return MQ_ERR_LD;
+    if (!aligned16(c->cache) || (uintptr_t)c->table % 4 || (uintptr_t)c->lens % 4 ||
+        (uintptr_t)c->cu_rows % 4)
+        return MQ_ERR_ALIGN;
+    kv->cache = (char *)c->cache;
+    kv->page_bytes = c->page_bytes;
+    kv->table = c->table;
+    kv->lens = c->lens;
+    kv->cu = c->cu_rows;
+    kv->table_ld = c->table_ld;
+    kv->pages = c->pages;
+    kv->heads = c->heads;
+    kv->page = c->page;
+    kv->D = c->head_dim;
+    kv->width = c->table_width;
+    kv->batch = c->batch;
+    kv->rows = M / c->batch;
+    kv->M = M;
+    return MQ_OK;
+}
+Span cache_span(const mq::KvSpec &kv) {
+    return span(kv.cache, kv.page_bytes, mq_kv_q4_page_bytes(kv.heads, kv.page, kv.D), 1, kv.pages);
+}
+int64_t type_bytes(int type) { return type == MQ_F32 ? 4 : 2; }
+
+// A rotation's frequencies: n_rot even and at most the head.
+int check_rotation(const double *freqs, int n_rot, int layout, float mscale, int head_dim) {
+    if (layout != MQ_ROPE_HALF && layout != MQ_ROPE_INTERLEAVED) return MQ_ERR_FORMAT;
+    if (n_rot <= 0 || n_rot % 2 || n_rot > head_dim) return MQ_ERR_SHAPE;
+    if (!(mscale > -3.0e38f && mscale < 3.0e38f)) return MQ_ERR_EPS;
+    if ((uintptr_t)freqs % 8) return MQ_ERR_ALIGN;
+    return MQ_OK;
+}
+
+bool heads_ok(int heads, int head_dim) {
+    return heads > 0 && heads <= MQ_MAX_HEADS && (int64_t)heads * head_dim <= MQ_MAX_K;
+}
+
+// Checks of an attention call that its workspace depends on.
+int check_attention(const mq::KvSpec &kv, int q_heads, int64_t max_len) {
+    if (!heads_ok(q_heads, kv.D) || q_heads % kv.heads || max_len < 0) return MQ_ERR_SHAPE;
+    return MQ_OK;
+}
+int plan_ok(const mq::KvSpec &kv, const mq::AttnPlan &p) {
+    const int64_t jobs = p.row_tiles * kv.heads;
+    return jobs * p.splits <= kMaxBlocks && jobs * p.rows / 4 <= kMaxBlocks;
+}
+
 }  // namespace
 
 extern "C" {
@@ -617,6 +682,132 @@ int mq_add_rms_norm_q8_1(int x_type, const void *X, int ldx, int r_type, const v
     return hip_status(mq::launch_add_rms_norm(n, (hipStream_t)stream));
 }
 
+int mq_rope(int x_type, const void *X, int ldx, const int32_t *positions, const double *freqs,
+            int n_rot, int layout, float mscale, int heads, int head_dim, int y_type, void *Y,
+            int ldy, int M, void *stream) {
+    if (int rc = check_dims(M, 1, 1)) return rc;
+    if (!X || !positions || !freqs || !Y) return MQ_ERR_NULL;
+    if (!type_ok(x_type) || !type_ok(y_type)) return MQ_ERR_TYPE;
+    if (head_dim <= 0 || head_dim > MQ_MAX_ROPE_DIM || !heads_ok(heads, head_dim))
+        return MQ_ERR_SHAPE;
+    if (int rc = check_rotation(freqs, n_rot, layout, mscale, head_dim)) return rc;
+    const int width = heads * head_dim;
+    if (ldx < width || ldy < width) return MQ_ERR_LD;
+    if (!elem_aligned(X, x_type) || !elem_aligned(Y, y_type) || (uintptr_t)positions % 4)
+        return MQ_ERR_ALIGN;
+    const Span x = span(X, ldx, width, type_bytes(x_type), M);
+    const Span y = span(Y, ldy, width, type_bytes(y_type), M);
+    if ((overlap(y, x) && !same_span(y, x)) || overlap(y, span(positions, M, M, 4, 1)) ||
+        overlap(y, span(freqs, n_rot / 2, n_rot / 2, 8, 1)))
+        return MQ_ERR_OVERLAP;
+    const mq::RopeSpec s{X,    Y,        positions, freqs, ldx,    ldy,    M,
+                         heads, head_dim, n_rot,     x_type, y_type, layout == MQ_ROPE_INTERLEAVED,
+                         mscale};
+    return hip_status(mq::launch_rope(s, (hipStream_t)stream));
+}
+
+int64_t mq_kv_q4_page_bytes(int heads, int page, int head_dim) {
+    if (heads <= 0 || heads > MQ_MAX_HEADS || page <= 0 || page % 32 || page > mq::kMaxLen ||
+        (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 256))
+        return MQ_ERR_SHAPE;
+    return (int64_t)heads * (page / 32) * 36 * head_dim;
+}
+
+int mq_kv_store_q4(const mq_kv_q4 *cache, int x_type, const void *K, int ldk, const void *V, int ldv,
+                   const double *freqs, int n_rot, int layout, float mscale,
+                   const int32_t *positions, const void *Q, int ldq, int q_heads, int q_type,
+                   void *QO, int ldqo, int M, void *stream) {
+    mq::KvSpec kv;
+    if (int rc = check_kv(cache, M, &kv)) return rc;
+    if (!K || !V || (Q && !QO)) return MQ_ERR_NULL;
+    if (!type_ok(x_type) || (Q && !type_ok(q_type))) return MQ_ERR_TYPE;
+    if (freqs)
+        if (int rc = check_rotation(freqs, n_rot, layout, mscale, kv.D)) return rc;
+    const int width = kv.heads * kv.D;
+    if (!heads_ok(kv.heads, kv.D) || (Q && !heads_ok(q_heads, kv.D))) return MQ_ERR_SHAPE;
+    if (ldk < width || ldv < width) return MQ_ERR_LD;
+    if (!elem_aligned(K, x_type) || !elem_aligned(V, x_type) || (uintptr_t)positions % 4)
+        return MQ_ERR_ALIGN;
+    const Span k = span(K, ldk, width, type_bytes(x_type), M);
+    const Span v = span(V, ldv, width, type_bytes(x_type), M);
+    const Span c = cache_span(kv);
+    if (overlap(c, k) || overlap(c, v)) return MQ_ERR_OVERLAP;
+    if (Q) {
+        const int qw = q_heads * kv.D;
+        if (ldq < qw || ldqo < qw) return MQ_ERR_LD;
+        if (!elem_aligned(Q, x_type) || !elem_aligned(QO, q_type)) return MQ_ERR_ALIGN;
+        const Span q = span(Q, ldq, qw, type_bytes(x_type), M);
+        const Span o = span(QO, ldqo, qw, type_bytes(q_type), M);
+        if ((overlap(o, q) && !same_span(o, q)) || overlap(o, k) || overlap(o, v) ||
+            overlap(o, c) || overlap(c, q))
+            return MQ_ERR_OVERLAP;
+    }
+    const mq::StoreSpec s{K,   V,    Q,      QO,     positions, freqs,
+                          ldk, ldv,  ldq,    ldqo,   x_type,    q_type,
+                          freqs ? n_rot : 0, q_heads, layout == MQ_ROPE_INTERLEAVED, mscale};
+    return hip_status(mq::launch_kv_store(kv, s, (hipStream_t)stream));
+}
+
+int mq_kv_load_q4(const mq_kv_q4 *cache, int y_type, void *K, int ldk, void *V, int ldv, int M,
+                  void *stream) {
+    mq::KvSpec kv;
+    if (int rc = check_kv(cache, M, &kv)) return rc;
+    if (!K || !V) return MQ_ERR_NULL;
+    if (!type_ok(y_type)) return MQ_ERR_TYPE;
+    const int width = kv.heads * kv.D;
+    if (!heads_ok(kv.heads, kv.D)) return MQ_ERR_SHAPE;
+    if (ldk < width || ldv < width) return MQ_ERR_LD;
+    if (!elem_aligned(K, y_type) || !elem_aligned(V, y_type)) return MQ_ERR_ALIGN;
+    const Span k = span(K, ldk, width, type_bytes(y_type), M);
+    const Span v = span(V, ldv, width, type_bytes(y_type), M);
+    const Span c = cache_span(kv);
+    if (overlap(k, v) || overlap(c, k) || overlap(c, v)) return MQ_ERR_OVERLAP;
+    return hip_status(mq::launch_kv_load(kv, y_type, K, ldk, V, ldv, (hipStream_t)stream));
+}
+
+int64_t mq_attention_q4_workspace_bytes(const mq_kv_q4 *cache, int q_heads, int M,
+                                        int64_t max_len) {
+    mq::KvSpec kv;
+    if (int rc = check_kv(cache, M, &kv)) return rc;
+    if (int rc = check_attention(kv, q_heads, max_len)) return rc;
+    mq::AttnSpec s{};
+    s.q_heads = q_heads;
+    s.max_len = max_len;
+    const mq::AttnPlan p = mq::plan_attention(kv, s);
+    return plan_ok(kv, p) ? p.ws_bytes : MQ_ERR_SHAPE;
+}
+
+int mq_attention_q4(const mq_kv_q4 *cache, int x_type, const void *Q, int ldq, int q_heads,
+                    uint16_t *Y, int ldy, int M, float scale, int causal, int window, float cap,
+                    const float *slopes, const int32_t *prefix, int64_t max_len, void *ws,
+                    size_t ws_bytes, void *stream) {
+    mq::KvSpec kv;
+    if (int rc = check_kv(cache, M, &kv)) return rc;
+    if (!Q || !Y) return MQ_ERR_NULL;
+    if (!type_ok(x_type)) return MQ_ERR_TYPE;
+    if (int rc = check_attention(kv, q_heads, max_len)) return rc;
+    if (!(scale > -3.0e38f && scale < 3.0e38f) || !(cap >= 0.0f && cap < 3.0e38f) || window < 0)
+        return MQ_ERR_EPS;
+    const int width = q_heads * kv.D;
+    if (ldq < width || ldy < width) return MQ_ERR_LD;
+    if (!elem_aligned(Q, x_type) || !elem_aligned(Y, MQ_F16) || (uintptr_t)slopes % 4 ||
+        (uintptr_t)prefix % 4)
+        return MQ_ERR_ALIGN;
+    const mq::AttnSpec s{Q,   Y,   ldq,         ldy,    x_type, q_heads, scale,
+                         cap, causal != 0, window, slopes, prefix,  max_len};
+    const mq::AttnPlan p = mq::plan_attention(kv, s);
+    if (!plan_ok(kv, p)) return MQ_ERR_SHAPE;
+    if (p.ws_bytes > 0 && (!ws || !aligned16(ws) || ws_bytes < (size_t)p.ws_bytes))
+        return MQ_ERR_WORKSPACE;
+    const Span q = span(Q, ldq, width, type_bytes(x_type), M);
+    const Span y = span(Y, ldy, width, 2, M);
+    const Span c = cache_span(kv);
+    const Span w = span(ws, p.ws_bytes, p.ws_bytes, 1, 1);
+    if (overlap(y, q) || overlap(y, c)) return MQ_ERR_OVERLAP;
+    if (p.ws_bytes > 0 && (overlap(w, q) || overlap(w, y) || overlap(w, c))) return MQ_ERR_OVERLAP;
+    return hip_status(mq::launch_attention(kv, s, p, (float *)ws, (hipStream_t)stream));
+}
+
 int mq_gemm_plan_query(int path, int fmt, int M, int N, int K, int split_k,
                        mq_gemm_plan_info *out) {
     if (!out) return MQ_ERR_NULL;
@@ -666,8 +857,8 @@ const char *mq_strerror(int code) {
     switch (code) {
     case MQ_OK: return "success";
     case MQ_ERR_NULL: return "a required pointer is NULL";
-    case MQ_ERR_FORMAT: return "unknown weight format";
-    case MQ_ERR_SHAPE: return "M, N or K out of range, or K not a multiple of the block size";
+    case MQ_ERR_FORMAT: return "unknown weight format or rotary layout";
+    case MQ_ERR_SHAPE: return "a size out of range (M, N, K, heads, pages, batch), or K not a multiple of the block size";
     case MQ_ERR_LD: return "a leading dimension is too small, too large or not a multiple of 8 (4 for f32 rows, 16 for int8 codes)";
     case MQ_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case MQ_ERR_WORKSPACE: return "workspace missing, misaligned or smaller than required";
@@ -675,7 +866,7 @@ const char *mq_strerror(int code) {
     case MQ_ERR_HIP: return "the HIP runtime rejected a launch";
     case MQ_ERR_SCRATCH: return "the K-split partial tiles exceed the static scratch (MQ_NOALLOC_SCRATCH_BYTES)";
     case MQ_ERR_TYPE: return "an element type that is not f32 or f16";
-    case MQ_ERR_EPS: return "eps is negative or not finite";
+    case MQ_ERR_EPS: return "eps, a scale, a cap or a window is negative or not finite";
     case MQ_ERR_OVERLAP: return "an output overlaps another buffer of the call";
     case MQ_ERR_ACT: return "unknown activation";
     default: return "unknown error code";

@@ -161,4 +161,69 @@ struct NormSpec {
 };
 hipError_t launch_add_rms_norm(const NormSpec &n, hipStream_t stream);
 
+// Rotary positions (arguments already validated); x == y: in place.
+struct RopeSpec {
+    const void *x;
+    void *y;
+    const int32_t *pos;
+    const double *freqs;          // n_rot / 2
+    int64_t ldx, ldy;             // elements
+    int M, heads, head_dim, n_rot, x_type, y_type;
+    bool interleaved;
+    float mscale;
+};
+hipError_t launch_rope(const RopeSpec &s, hipStream_t stream);
+
+// The 4-bit key/value cache and the batch whose rows go into or read it, as the
+// kernels take it (kv_q4.h has the layout).
+constexpr int kMaxLen = 1 << 30;  // longest sequence
+struct KvSpec {
+    char *cache;
+    int64_t page_bytes;           // from page to page
+    const int32_t *table;         // [batch][width], rows table_ld apart
+    const int32_t *lens;          // [batch]: tokens, the new rows included
+    const int32_t *cu;            // [batch + 1] first rows, or null: `rows` each
+    int64_t table_ld;
+    int pages, heads, page, D, width, batch, rows, M;
+};
+
+struct StoreSpec {
+    const void *k, *v, *q;        // q may be null
+    void *qo;
+    const int32_t *pos;           // or null
+    const double *freqs;          // or null
+    int64_t ldk, ldv, ldq, ldqo;
+    int x_type, qo_type, n_rot, q_heads;
+    bool interleaved;
+    float mscale;
+};
+hipError_t launch_kv_store(const KvSpec &kv, const StoreSpec &s, hipStream_t stream);
+hipError_t launch_kv_load(const KvSpec &kv, int y_type, void *K, int64_t ldk, void *V, int64_t ldv,
+                          hipStream_t stream);
+
+// Attention over the cache.
+struct AttnSpec {
+    const void *q;
+    uint16_t *y;
+    int64_t ldq, ldy;
+    int x_type, q_heads;
+    float scale, cap;             // cap 0: none
+    bool causal;
+    int window;                   // 0: none
+    const float *slopes;          // [q_heads], or null
+    const int32_t *prefix;        // [batch], or null
+    int64_t max_len;              // a bound of the lengths, for the plan only
+};
+// How a call runs: query rows (of a key/value head's group) per workgroup, and
+// parts that the keys are cut into, whose partial results lie in the workspace.
+struct AttnPlan {
+    int rows;
+    int splits;
+    int64_t row_tiles;            // over the whole batch
+    int64_t ws_bytes;
+};
+AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s);
+hipError_t launch_attention(const KvSpec &kv, const AttnSpec &s, const AttnPlan &p, float *ws,
+                            hipStream_t stream);
+
 }  // namespace mq

@@ -30,7 +30,8 @@ ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh":
 BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
 _ENTRY_POINTS = ("mq_linear_workspace_bytes", "mq_glu_workspace_bytes", "mq_linear_f16cache",
                  "mq_linear_fused", "mq_glu_f16cache", "mq_glu_fused", "mq_add_rms_norm",
-                 "mq_add_rms_norm_q8_1", "mq_row_bytes")
+                 "mq_add_rms_norm_q8_1", "mq_row_bytes", "mq_rope", "mq_kv_store_q4",
+                 "mq_kv_load_q4", "mq_attention_q4", "mq_attention_q4_workspace_bytes")
 
 _raw_stream = torch._C._cuda_getCurrentRawStream if torch.version.hip else None
 _current_device = torch._C._cuda_getDevice if torch.version.hip else None
