@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(PKG, "libmq.so")
 BINDING_PATH = os.path.join(PKG, "_binding.so")
 SOURCES = ("mq_api.hip", "dequant.hip", "gemm.hip", "gemm_xf32.hip", "mmq.hip", "rms_norm.hip",
            "gemm_linear.hip", "gemm_glu.hip", "linear_rows.hip", "rope.hip", "kv_q4.hip",
-           "attention_q4.hip")
+           "attention_q4.hip", "attention_prompt.hip")
 
 BINDING_SOURCES = ("binding.cpp", "binding_attention.cpp")
 

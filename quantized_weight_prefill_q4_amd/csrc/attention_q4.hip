@@ -22,62 +22,13 @@
 // summed in f32; the statistics in f32; a weight e^(s − m) is rounded to f16 as
 // the operand of the second product, times 2^15, so that weights down to 2^-29 of
 // the largest keep 11 bits (the factor leaves with the sum).
-#include "attention_view.h"
-#include "mq_device.h"
+#include "attention_device.h"
 
 namespace mq {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr float kLog2e = 1.44269502f;
-constexpr float kShift = 15.0f;       // weights are held times 2^15
 constexpr int kMaxSplits = 256;
-
-// 1 − 2 / (1 + e^2u), and below 1/4, where that cancels, u − u³/3 + 2u⁵/15 − 17u⁷/315
-// (the next term is 3e-7 of the value at 1/4).
-__device__ __forceinline__ float tanh_f32(float u) {
-    const float e = __builtin_amdgcn_exp2f(u * (2.0f * kLog2e));
-    const float t = u * u;
-    float p = __builtin_fmaf(t, -17.0f / 315.0f, 2.0f / 15.0f);
-    p = __builtin_fmaf(t, p, -1.0f / 3.0f);
-    p = __builtin_fmaf(t * u, p, u);
-    return fabsf(u) < 0.25f ? p : 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e);
-}
-
-typedef uint32_t q_u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
-typedef float q_f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-
-// Eight query elements as f16.
-__device__ __forceinline__ half8 load_q8(const void *q, int f32, int64_t at) {
-    if (!f32)
-        return __builtin_bit_cast(
-            half8, (u32x4)*reinterpret_cast<const q_u32x4_a2 *>((const uint16_t *)q + at));
-    const q_f32x4_a4 *p = reinterpret_cast<const q_f32x4_a4 *>((const float *)q + at);
-    const f32x4 x = p[0], y = p[1];
-    return __builtin_bit_cast(half8, u32x4{pack_f16x2(x.x, x.y), pack_f16x2(x.z, x.w),
-                                           pack_f16x2(y.x, y.y), pack_f16x2(y.z, y.w)});
-}
-
-// The eight (q − 8) of a code dword, exact.  A nibble under the exponent of 1024
-// is 1024 + q, one place of four bits higher 1024 + 16·q.
-__device__ __forceinline__ void widen(uint32_t w, half2v h[4]) {
-    const half2v c = {(_Float16)1032.0f, (_Float16)1032.0f};
-    const half2v s = {(_Float16)0.0625f, (_Float16)0.0625f};
-    const half2v o = {(_Float16)-72.0f, (_Float16)-72.0f};
-    const uint32_t u = w >> 8;
-    h[0] = __builtin_bit_cast(half2v, (w & 0x000F000Fu) | 0x64006400u) - c;
-    h[1] = __builtin_elementwise_fma(
-        __builtin_bit_cast(half2v, (w & 0x00F000F0u) | 0x64006400u), s, o);
-    h[2] = __builtin_bit_cast(half2v, (u & 0x000F000Fu) | 0x64006400u) - c;
-    h[3] = __builtin_elementwise_fma(
-        __builtin_bit_cast(half2v, (u & 0x00F000F0u) | 0x64006400u), s, o);
-}
-
-__device__ __forceinline__ half8 join8(const half2v h[4]) {
-    return half8{h[0].x, h[0].y, h[1].x, h[1].y, h[2].x, h[2].y, h[3].x, h[3].y};
-}
-
-__device__ __forceinline__ half2v as_half2(uint32_t w) { return __builtin_bit_cast(half2v, w); }
 
 // A tile as loaded: code dwords of the lane's operands and the scales they need.
 // Lane l is row r = l % 16 of the A operands and their inner octet g = l / 16.
@@ -92,27 +43,6 @@ struct Tile {
     uint32_t ks[2][(NS + 1) / 2];
     u32x4 vs[kScaleSets];
 };
-
-template <int N>
-__device__ __forceinline__ void load_dwords(const uint32_t *p, uint32_t (&w)[N]) {
-    typedef uint32_t v2 __attribute__((ext_vector_type(2)));
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const u32x4 x = *(const u32x4 *)(p + i);
-            w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
-        }
-    } else if constexpr (N % 2 == 0) {
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const v2 x = *(const v2 *)(p + i);
-            w[i] = x.x; w[i + 1] = x.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = p[i];
-    }
-}
 
 template <int NS>
 __device__ __forceinline__ void load_tile(const char *tile, int r, int g, Tile<NS> &t) {
@@ -153,15 +83,6 @@ __device__ __forceinline__ half8 value_operand(const Tile<NS> &t, int i) {
     h[2] *= as_half2(s.z);
     h[3] *= as_half2(s.w);
     return join8(h);
-}
-
-// f16 words whose exponent is all ones (infinities, NaN), as 1.0 / 0.0 each.
-__device__ __forceinline__ uint32_t bad_halves(uint32_t w) {
-    return ((w & 0x7C00u) == 0x7C00u ? 0x3C00u : 0u) |
-           ((w & 0x7C000000u) == 0x7C000000u ? 0x3C000000u : 0u);
-}
-__device__ __forceinline__ uint32_t keep_halves(uint32_t w, bool lo, bool hi) {
-    return (lo ? w & 0xFFFFu : 0u) | (hi ? w & 0xFFFF0000u : 0u);
 }
 
 template <int NS, int NT, bool BIAS>
@@ -421,46 +342,83 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     }
 }
 
-// Joins the parts of each row: one wave per row, over the workgroups' layout.
-template <int NS>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int R, int64_t rows) {
-    constexpr int D = 32 * NS;
-    const int lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);   // job · R + row
-    if (id >= rows) return;
-    const int64_t job = id / R;
-    const int n = (int)(id - job * R), head = (int)(job % a.kv.heads);
+// Joins the parts of each row (of job · R + row slots): W waves per row, part s by
+// wave s % W.
+template <int NS, int W>
+__global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void attention_join_kernel(AttnArgs a, int R,
+                                                                              int slots) {
+    constexpr int D = 32 * NS, E = (D + 63) / 64, ROWS = (W > 4 ? W : 4) / W;
+    __shared__ float factor[ROWS][kMaxSplits];
+    __shared__ float sums[ROWS][W][E * 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave % W, mine = wave / W;
+    const int slot = blockIdx.x * ROWS + mine;
+    const int job = slot / R, n = slot - job * R, head = job % a.kv.heads;
     View view;
-    const bool any = R == 16 ? find_view<16>(a, job / a.kv.heads, view)
-                   : R == 32 ? find_view<32>(a, job / a.kv.heads, view)
-                             : find_view<64>(a, job / a.kv.heads, view);
-    if (!any) return;
-    const int64_t row = (int64_t)view.rt * R + n;
-    const int i = (int)(row / a.group), h = head * a.group + (int)(row - (int64_t)i * a.group);
-    if (i >= view.rows.n) return;
-    const int chunk = part_tiles(view.n, a.splits);
-    int parts = (view.n + chunk - 1) / chunk;
-    if (parts < 1) parts = 1;   // the first part always writes
-    const float2 *st = (const float2 *)a.stats + job * a.splits * R + n;
-    float m = -__builtin_inff();
-    for (int s = lane; s < parts; s += 64) m = fmaxf(m, st[(int64_t)s * R].x);
+    bool any = slot < slots;
+    if (any)
+        any = R == 16   ? find_view<16>(a, job / a.kv.heads, view)
+              : R == 32 ? find_view<32>(a, job / a.kv.heads, view)
+                        : find_view<128>(a, job / a.kv.heads, view);
+    int i = 0, h = 0;
+    if (any) {
+        const int64_t row = (int64_t)view.rt * R + n;
+        i = (int)(row / a.group);
+        h = head * a.group + (int)(row - (int64_t)i * a.group);
+        any = i < view.rows.n;
+    }
+    if (W >= 4 && !any) return;   // the whole workgroup
+    int parts = 0;
+    float sum = 0.0f;
+    const int64_t base = (int64_t)job * a.splits;
+    if (any) {
+        const int chunk = part_tiles(view.n, a.splits);
+        parts = (view.n + chunk - 1) / chunk;
+        if (parts < 1) parts = 1;   // the first part always writes
+        const float2 *st = (const float2 *)a.stats + base * R + n;
+        float m = -__builtin_inff();
+        float2 t[kMaxSplits / 64];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    const float base = m == -__builtin_inff() ? 0.0f : m;
-    constexpr int E = (D + 63) / 64;
-    float x[E], sum = 0.0f;
+        for (int k = 0; k < kMaxSplits / 64; ++k) {
+            const int s = lane + 64 * k;
+            t[k] = s < parts ? st[(int64_t)s * R] : float2{-__builtin_inff(), 0.0f};
+            m = fmaxf(m, t[k].x);
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+        if (m == -__builtin_inff()) m = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kMaxSplits / 64; ++k) {
+            const float f = __builtin_amdgcn_exp2f(t[k].x - m);
+            sum = __builtin_fmaf(t[k].y, f, sum);
+            if (sub == 0 && lane + 64 * k < parts) factor[mine][lane + 64 * k] = f;
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    }
+    __syncthreads();
+    float x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = 0.0f;
-    const float *y = a.partial + (job * a.splits * R + n) * D;
-    for (int s = 0; s < parts; ++s) {
-        const float2 t = st[(int64_t)s * R];
-        const float f = __builtin_amdgcn_exp2f(t.x - base);
-        sum = __builtin_fmaf(t.y, f, sum);
+    const float *y = a.partial + (base * R + n) * D;
+#pragma unroll 4
+    for (int s = sub; s < parts; s += W) {
+        const float f = factor[mine][s];
 #pragma unroll
         for (int e = 0; e < E; ++e)
             if (lane + 64 * e < D)
                 x[e] = __builtin_fmaf(y[(int64_t)s * R * D + lane + 64 * e], f, x[e]);
     }
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sums[mine][sub][64 * e + lane] = x[e];
+        __syncthreads();
+        if (sub > 0) return;
+#pragma unroll
+        for (int w = 1; w < W; ++w)
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] += sums[mine][w][64 * e + lane];
+    }
+    if (!any) return;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint16_t *out = a.y + (int64_t)(view.rows.first + i) * a.ldy + (int64_t)h * D;
 #pragma unroll
@@ -484,17 +442,24 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) 
     // without a cap or bias the scale goes into the exponent's factor, after the
     // mask's −∞: it has to be positive and in range there
     const bool bias = a.cap > 0.0f || a.slopes || !(a.scale > 1e-30f && a.scale < 1e30f);
-    if (p.rows == 16)
-        launch_rows<NS, 1>(a, blocks, bias, stream);
-    else if (p.rows == 32)
-        launch_rows<NS, 2>(a, blocks, bias, stream);
-    else if constexpr (NS <= 4)
-        launch_rows<NS, 4>(a, blocks, bias, stream);
-    hipError_t e = hipGetLastError();
+    hipError_t e = hipSuccess;
+    if (p.rows == kPromptRows) {
+        e = launch_attention_prompt(a, bias, stream);
+    } else {
+        if (p.rows == 16)
+            launch_rows<NS, 1>(a, blocks, bias, stream);
+        else
+            launch_rows<NS, 2>(a, blocks, bias, stream);
+        e = hipGetLastError();
+    }
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t rows = p.row_tiles * a.kv.heads * p.rows;
-    hipLaunchKernelGGL((attention_join_kernel<NS>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
-                       dim3(256), 0, stream, a, p.rows, rows);
+    const int slots = (int)(p.row_tiles * a.kv.heads * p.rows);
+    if (a.splits <= 8)
+        hipLaunchKernelGGL((attention_join_kernel<NS, 1>), dim3((slots + 3) / 4), dim3(256), 0, stream,
+                           a, p.rows, slots);
+    else
+        hipLaunchKernelGGL((attention_join_kernel<NS, 8>), dim3(slots), dim3(512), 0, stream, a,
+                           p.rows, slots);
     return hipGetLastError();
 }
 
@@ -505,14 +470,15 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
     const int group = s.q_heads / kv.heads;
     const int64_t mean = kv.cu ? ((int64_t)kv.M + kv.batch - 1) / kv.batch : kv.rows;
     const int64_t rows = mean * group;   // of a key/value head and sequence
-    // (64 rows of 256 elements do not fit the registers)
-    p.rows = rows <= 16 ? 16 : rows <= 32 || kv.D > 128 ? 32 : 64;
+    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : kPromptRows;
     p.row_tiles = kv.cu ? (int64_t)kv.M * group / p.rows + kv.batch
                         : (rows + p.rows - 1) / p.rows * kv.batch;
-    // Parts of the keys: enough workgroups for every compute unit to hold four
+    // Parts of the keys, where there are too few workgroups to fill the chip: up to
+    // four per compute unit of the first kernel, two of the second.
     const int64_t jobs = p.row_tiles * kv.heads;
     const int64_t tiles = (s.max_len + kTile - 1) / kTile;
-    int64_t splits = (1024 + jobs - 1) / jobs;
+    const int64_t want = p.rows == kPromptRows ? 512 : 1024;
+    int64_t splits = jobs >= want / 2 ? 1 : (want + jobs - 1) / jobs;
     if (splits > tiles / kMinTiles) splits = tiles / kMinTiles;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
@@ -542,6 +508,7 @@ hipError_t launch_attention(const KvSpec &kv, const AttnSpec &s, const AttnPlan 
     a.prefix = s.prefix;
     a.stats = ws;
     a.partial = ws + p.row_tiles * kv.heads * p.splits * p.rows * 2;
+    a.units = (int)p.row_tiles;
     a.per_seq = kv.cu ? 0 : ((int64_t)kv.rows * a.group + p.rows - 1) / p.rows;
     switch (kv.D) {
     case 64: return launch_dim<2>(a, p, stream);

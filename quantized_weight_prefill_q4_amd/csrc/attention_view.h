@@ -5,9 +5,6 @@
 #include "kv_q4.h"
 
 namespace mq {
-namespace {
-
-constexpr int kMinTiles = 8;   // tiles of a part: fewer do not pay for the join
 
 struct AttnArgs {
     KvSpec kv;
@@ -20,7 +17,15 @@ struct AttnArgs {
     const int32_t *prefix;
     float *stats, *partial;           // workspace: [row tile][head][split][R][2] and [..][R][D]
     int64_t per_seq;                  // row tiles of a sequence (equal rows)
+    int units;                        // row tiles of the batch
 };
+
+// The kernel for many rows (attention_prompt.hip); launches it alone.
+hipError_t launch_attention_prompt(const AttnArgs &a, bool bias, hipStream_t stream);
+
+namespace {
+
+constexpr int kMinTiles = 8;   // tiles of a part: fewer do not pay for the join
 
 // What a workgroup's rows see: tiles [0, pre) and [lo, lo + n − pre).
 struct View {
@@ -64,9 +69,9 @@ MQ_INDEX bool find_view(const AttnArgs &a, int64_t unit, View &v) {
     return true;
 }
 
-// Tiles of a part, and how many parts have any.
+// Tiles of a part: a multiple of four, so that the waves share it evenly.
 MQ_INDEX int part_tiles(int n, int splits) {
-    const int c = (n + splits - 1) / splits;
+    const int c = ((n + splits - 1) / splits + 3) & ~3;
     return c < kMinTiles ? kMinTiles : c;
 }
 

@@ -414,9 +414,9 @@ int check_attention(const mq::KvSpec &kv, int q_heads, int64_t max_len) {
     if (!heads_ok(q_heads, kv.D) || q_heads % kv.heads || max_len < 0) return MQ_ERR_SHAPE;
     return MQ_OK;
 }
-int plan_ok(const mq::KvSpec &kv, const mq::AttnPlan &p) {
+bool plan_ok(const mq::KvSpec &kv, const mq::AttnPlan &p) {
     const int64_t jobs = p.row_tiles * kv.heads;
-    return jobs * p.splits <= kMaxBlocks && jobs * p.rows / 4 <= kMaxBlocks;
+    return jobs * p.splits <= kMaxBlocks && (p.splits == 1 || jobs * p.rows <= kMaxBlocks / 2);
 }
 
 }  // namespace

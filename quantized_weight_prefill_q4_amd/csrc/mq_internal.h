@@ -214,6 +214,7 @@ struct AttnSpec {
     const int32_t *prefix;        // [batch], or null
     int64_t max_len;              // a bound of the lengths, for the plan only
 };
+constexpr int kPromptRows = 128;  // rows per workgroup of the kernel for many rows
 // How a call runs: query rows (of a key/value head's group) per workgroup, and
 // parts that the keys are cut into, whose partial results lie in the workspace.
 struct AttnPlan {

@@ -148,12 +148,12 @@ int main() {
         if (seed % 7 == 0) a.window = INT32_MAX;
         a.prefix = pick(0, 1) ? prefix.data() : nullptr;
         const bool whole = sound && (!ragged || (cu[0] == 0 && cu[kv.batch] == kv.M));
-        for (int R = 16; R <= 64; R *= 2) {
+        for (int R : {16, 32, 128}) {
             a.per_seq = kv.cu ? 0 : ((int64_t)kv.rows * a.group + R - 1) / R;
             const int64_t total = kv.cu ? (int64_t)kv.M * a.group / R + kv.batch : a.per_seq * kv.batch;
             const int rc = R == 16 ? views<16>(kv, a, total, whole, seed)
                          : R == 32 ? views<32>(kv, a, total, whole, seed)
-                                   : views<64>(kv, a, total, whole, seed);
+                                   : views<128>(kv, a, total, whole, seed);
             if (rc) return rc;
         }
     }
