@@ -540,7 +540,8 @@ int mq_kv_load_q4(const mq_kv_q4 *cache, int y_type, void *K, int ldk, void *V, 
  * e^(s − max) are rounded to f16 (2^-12 of each, as far as 2^-29 of the largest) and
  * y once to f16.  A token whose d is infinite or NaN makes the rows that see it not
  * finite, and no others.
- *   Q      : device, x_type, row stride ldq >= q_heads · head_dim.
+ *   Q      : device, x_type, row stride ldq >= q_heads · head_dim; M · (q_heads / heads)
+ *            at most 2^30.
  *   Y      : device f16, row stride ldy likewise.  Q and Y are aligned to their element.
  *   scale  : finite.  cap : finite, >= 0.  window : >= 0.
  *   slopes : device f32, q_heads values, or NULL.

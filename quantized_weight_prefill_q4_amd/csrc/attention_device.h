@@ -8,7 +8,12 @@ namespace mq {
 namespace {
 
 constexpr float kLog2e = 1.44269502f;
-constexpr float kShift = 15.0f;       // weights are held times 2^15
+
+// A row's weights are e^(s − m) with m a maximum that follows the scores only when
+// they exceed it by kSlack (in powers of two): the sums are rescaled rarely.  The f16
+// weights are held times 2^kShift, at most 2^15; the largest of a row is 2^7 at
+// least, so those down to 2^-21 of it keep 11 bits and 2^-32 of it is the step below.
+constexpr float kShift = 7.0f, kSlack = 8.0f;
 
 // 1 − 2 / (1 + e^2u), and below 1/4, where that cancels, u − u³/3 + 2u⁵/15 − 17u⁷/315
 // (the next term is 3e-7 of the value at 1/4).
@@ -25,10 +30,11 @@ typedef uint32_t q_u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float q_f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 // Eight query elements as f16.
-__device__ __forceinline__ half8 load_q8(const void *q, int f32, int64_t at) {
-    if (!f32)
-        return __builtin_bit_cast(
-            half8, (u32x4)*reinterpret_cast<const q_u32x4_a2 *>((const uint16_t *)q + at));
+__device__ __forceinline__ half8 load_q8_f16(const void *q, int64_t at) {
+    return __builtin_bit_cast(half8,
+                              (u32x4)*reinterpret_cast<const q_u32x4_a2 *>((const uint16_t *)q + at));
+}
+__device__ __forceinline__ half8 load_q8_f32(const void *q, int64_t at) {
     const q_f32x4_a4 *p = reinterpret_cast<const q_f32x4_a4 *>((const float *)q + at);
     const f32x4 x = p[0], y = p[1];
     return __builtin_bit_cast(half8, u32x4{pack_f16x2(x.x, x.y), pack_f16x2(x.z, x.w),
@@ -37,17 +43,17 @@ __device__ __forceinline__ half8 load_q8(const void *q, int f32, int64_t at) {
 
 // The eight (q − 8) of a code dword, exact.  A nibble under the exponent of 1024
 // is 1024 + q, one place of four bits higher 1024 + 16·q.
-__device__ __forceinline__ void widen(uint32_t w, half2v h[4]) {
+// (magic() sits in a vector register: an and-or takes one scalar operand, the mask.)
+__device__ __forceinline__ uint32_t magic() { return opaque(0x64006400u); }
+__device__ __forceinline__ void widen(uint32_t w, uint32_t magic, half2v h[4]) {
     const half2v c = {(_Float16)1032.0f, (_Float16)1032.0f};
     const half2v s = {(_Float16)0.0625f, (_Float16)0.0625f};
     const half2v o = {(_Float16)-72.0f, (_Float16)-72.0f};
     const uint32_t u = w >> 8;
-    h[0] = __builtin_bit_cast(half2v, (w & 0x000F000Fu) | 0x64006400u) - c;
-    h[1] = __builtin_elementwise_fma(
-        __builtin_bit_cast(half2v, (w & 0x00F000F0u) | 0x64006400u), s, o);
-    h[2] = __builtin_bit_cast(half2v, (u & 0x000F000Fu) | 0x64006400u) - c;
-    h[3] = __builtin_elementwise_fma(
-        __builtin_bit_cast(half2v, (u & 0x00F000F0u) | 0x64006400u), s, o);
+    h[0] = __builtin_bit_cast(half2v, (w & 0x000F000Fu) | magic) - c;
+    h[1] = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (w & 0x00F000F0u) | magic), s, o);
+    h[2] = __builtin_bit_cast(half2v, (u & 0x000F000Fu) | magic) - c;
+    h[3] = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (u & 0x00F000F0u) | magic), s, o);
 }
 
 __device__ __forceinline__ half8 join8(const half2v h[4]) {
@@ -94,15 +100,82 @@ __device__ __forceinline__ void make_uniform(View &v) {
     v.pre = uniform(v.pre);
     v.lo = uniform(v.lo);
     v.n = uniform(v.n);
+    v.full_pre = uniform(v.full_pre);
+    v.full_lo = uniform(v.full_lo);
+    v.full_hi = uniform(v.full_hi);
 }
 
-// f16 words whose exponent is all ones (infinities, NaN), as 1.0 / 0.0 each.
-__device__ __forceinline__ uint32_t bad_halves(uint32_t w) {
-    return ((w & 0x7C00u) == 0x7C00u ? 0x3C00u : 0u) |
-           ((w & 0x7C000000u) == 0x7C000000u ? 0x3C000000u : 0u);
+// An even share of the batch's tiles for a.target workgroups (all lanes together).
+__device__ __forceinline__ int even_share(const AttnArgs &a, int rows_per_tile) {
+    if (a.splits == 1) return 0;
+    float s = 0.0f;
+    for (int b = threadIdx.x & 63; b < a.kv.batch; b += 64) s += tiles_of_seq(a, b, rows_per_tile);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    const float share = s * (float)a.kv.heads / (float)a.target;
+    return share < 1e9f ? uniform((int)ceilf(share)) : 1000000000;
+}
+
+// The maximum over the lanes that hold the same column: l and l ^ 32, and with 16
+// columns l ^ 16 too.
+__device__ __forceinline__ float max_across32(float v) {
+    const uint32_t x = __builtin_bit_cast(uint32_t, v);
+    const auto p = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+}
+__device__ __forceinline__ float max_across16(float v) {
+    const uint32_t x = __builtin_bit_cast(uint32_t, v);
+    const auto p = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+}
+
+// Values' scales in tiles that are masked in part.  A weight of 0 times an infinity or
+// a NaN is not 0, so scales of tokens past the sequence (never written, perhaps) and
+// scales that are not finite are taken out, and the rows that see one of the latter
+// get a NaN in the elements of its block at the end.
+__device__ __forceinline__ uint32_t bad_halves(uint32_t w) {   // bit 0: the low, 1: the high one
+    return ((w & 0x7C00u) == 0x7C00u ? 1u : 0u) | ((w & 0x7C000000u) == 0x7C000000u ? 2u : 0u);
 }
 __device__ __forceinline__ uint32_t keep_halves(uint32_t w, bool lo, bool hi) {
     return (lo ? w & 0xFFFFu : 0u) | (hi ? w & 0xFFFF0000u : 0u);
+}
+
+// Pair e of an octet's scales as it enters, `tokens` of the octet existing; collects
+// in bad the bits of those taken out that exist.
+__device__ __forceinline__ uint32_t clean_scales(uint32_t s, int tokens, int e, uint32_t &bad) {
+    s = keep_halves(s, tokens > 2 * e, tokens > 2 * e + 1);
+    const uint32_t x = bad_halves(s);
+    bad |= x << (2 * e);
+    return keep_halves(s, !(x & 1), !(x & 2));
+}
+// The blocks (bit per 32 elements) that a row must give NaN in, for the tokens of one
+// octet of a tile that it sees.  Rare: reads the scales again.
+template <int NS>
+__device__ __forceinline__ uint32_t bad_blocks(const char *tile, int octet, int tokens, uint32_t seen) {
+    uint32_t blocks = 0;
+#pragma unroll 1
+    for (int b = 0; b < NS; ++b) {
+        const u32x4 s = ((const u32x4 *)(tile + kv_vscale_at(32 * NS)))[octet * NS + b];
+        uint32_t bad = 0;
+        clean_scales(s.x, tokens, 0, bad);
+        clean_scales(s.y, tokens, 1, bad);
+        clean_scales(s.z, tokens, 2, bad);
+        clean_scales(s.w, tokens, 3, bad);
+        if (bad & seen & 0xFFu) blocks |= 1u << b;
+    }
+    return blocks;
+}
+
+// A pair of f16 weights added to a sum: what is summed is what is multiplied.
+__device__ __forceinline__ float sum_pair(uint32_t w, float sum) {
+    const half2v one = {(_Float16)1.0f, (_Float16)1.0f};
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, w), one, sum, false);
+}
+
+// Two weights as f16.
+__device__ __forceinline__ uint32_t pack_weights(float a, float b) {
+    const half2v v = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, v);
 }
 
 }  // namespace

@@ -20,8 +20,7 @@
 //
 // Numerics: q, k and v in f16 (k and v each d·(q − 8) rounded once), products
 // summed in f32; the statistics in f32; a weight e^(s − m) is rounded to f16 as
-// the operand of the second product, times 2^15, so that weights down to 2^-29 of
-// the largest keep 11 bits (the factor leaves with the sum).
+// the operand of the second product (attention_device.h has its range).
 #include "attention_device.h"
 
 namespace mq {
@@ -74,10 +73,10 @@ __device__ __forceinline__ void load_tile(const char *tile, int r, int g, Tile<N
 
 // The values' operand i.
 template <int NS>
-__device__ __forceinline__ half8 value_operand(const Tile<NS> &t, int i) {
+__device__ __forceinline__ half8 value_operand(const Tile<NS> &t, int i, uint32_t mg) {
     const u32x4 s = t.vs[Tile<NS>::kRuns ? 0 : i / 2];
     half2v h[4];
-    widen(t.v[i], h);
+    widen(t.v[i], mg, h);
     h[0] *= as_half2(s.x);
     h[1] *= as_half2(s.y);
     h[2] *= as_half2(s.z);
@@ -91,17 +90,17 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     constexpr int CH = MT < 8 ? MT : 8;                    // of them joined at a time
     __shared__ float join[kWaves][CH * 4][64];
     __shared__ float2 wave_stats[kWaves][R];
+    __shared__ uint32_t wave_nan[kWaves][R];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4;
-    const int split = blockIdx.x % a.splits;
-    const int job = blockIdx.x / a.splits;                 // row tile · heads + head
-    const int head = job % a.kv.heads;
+    int split, job, head;
+    find_job(a, blockIdx.x, split, job, head);
     View view;
     if (!find_view<R>(a, job / a.kv.heads, view)) return;
-    const int chunk = part_tiles(view.n, a.splits);
-    const int t_begin = split * chunk;
-    const int t_end = t_begin + chunk < view.n ? t_begin + chunk : view.n;
-    if (t_begin >= t_end && (a.splits > 1 && split > 0)) return;
+    const Parts parts = parts_of(a, view.n, even_share(a, R));
+    if (split >= parts.count) return;
+    const int t_begin = split * parts.per;
+    const int t_end = t_begin + parts.per < view.n ? t_begin + parts.per : view.n;
 
     // this lane's column in each of the NT column tiles: row 16·c + r
     half8 q[NT][NS];
@@ -110,27 +109,34 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     float slope[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
-        const int64_t row = (int64_t)view.rt * R + 16 * c + r;
-        const int i = (int)(row / a.group), h = head * a.group + (int)(row - (int64_t)i * a.group);
+        const int row = view.rt * R + 16 * c + r;
+        const int i = (int)((unsigned)row / (unsigned)a.group), h = head * a.group + row - i * a.group;
         const bool live = i < view.rows.n;
         pos[c] = view.first_pos + i;
         range[c] = row_range(a, view, pos[c]);
         slope[c] = BIAS && a.slopes && live ? a.slopes[h] : 0.0f;
         const int64_t at = (int64_t)(view.rows.first + (live ? i : 0)) * a.ldq +
                            (int64_t)(live ? h : head * a.group) * D + 8 * g;
+        if (a.q_f32)
 #pragma unroll
-        for (int s = 0; s < NS; ++s) q[c][s] = load_q8(a.q, a.q_f32, at + 32 * s);
+            for (int s = 0; s < NS; ++s) q[c][s] = load_q8_f32(a.q, at + 32 * s);
+        else
+#pragma unroll
+            for (int s = 0; s < NS; ++s) q[c][s] = load_q8_f16(a.q, at + 32 * s);
     }
     f32x4 o[NT][MT];
     float m[NT], l[NT];
+    uint32_t nan_blocks[NT];   // blocks of the column's row that must become NaN
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         m[c] = -__builtin_inff();
         l[c] = 0.0f;
+        nan_blocks[c] = 0;
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[c][i] = f32x4{0, 0, 0, 0};
     }
     const float to_log2 = BIAS ? kLog2e : a.scale * kLog2e;
+    const uint32_t mg = magic();
 
     auto tile_of = [&](int t) { return t < view.pre ? t : t - view.pre + view.lo; };
     for (int t = t_begin + wave; t < t_end; t += kWaves) {
@@ -147,7 +153,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
                 half2v h[4];
-                widen(now.k[mt][k], h);
+                widen(now.k[mt][k], mg, h);
                 const half2v pair = as_half2(now.ks[mt][k / 2]);
                 const _Float16 d = k & 1 ? pair.y : pair.x;
                 const half2v dd = {d, d};
@@ -160,7 +166,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
             }
         }
         // element b of s[c][mt]: token j0 + 8g + 4·mt + b
-        const bool edge = !all_visible(a, view, j0);
+        const bool edge = !all_visible(view, tile);
         if constexpr (BIAS) {
 #pragma unroll
             for (int c = 0; c < NT; ++c)
@@ -198,79 +204,43 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int b = 0; b < 4; ++b) top = fmaxf(top, s[c][mt][b]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            top *= to_log2;
-            const float mc = fmaxf(m[c], top);
-            if (__any(mc > m[c])) {
+            top = max_across32(max_across16(top)) * to_log2;
+            if (__any(top > m[c] + kSlack)) {
+                const float mc = fmaxf(m[c], top);
                 const float f = mc == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[c] - mc);
                 l[c] *= f;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) o[c][i] *= f;
                 m[c] = mc;
             }
-            const float base = mc == -__builtin_inff() ? 0.0f : mc - kShift;
+            const float base = m[c] == -__builtin_inff() ? 0.0f : m[c] - kShift;
             float e[8];
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < 4; ++b)
                     e[4 * mt + b] =
                         __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][mt][b], to_log2, -base));
-                    l[c] += e[4 * mt + b];
-                }
-            w[c] = __builtin_bit_cast(half8, u32x4{pack_f16x2(e[0], e[1]), pack_f16x2(e[2], e[3]),
-                                                   pack_f16x2(e[4], e[5]), pack_f16x2(e[6], e[7])});
+            l[c] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            w[c] = __builtin_bit_cast(half8, u32x4{pack_weights(e[0], e[1]), pack_weights(e[2], e[3]),
+                                                   pack_weights(e[4], e[5]), pack_weights(e[6], e[7])});
         }
         if (edge) {
-            // Weights of unseen tokens are 0, but 0 times an infinite or NaN scale
-            // is not.  Tokens past the sequence (never written, perhaps) lose their
-            // scale; others that are not finite are taken out and given, as NaN,
-            // to the rows that see them.
-            bool bad = false;
+            uint32_t bad = 0;
+            const int tokens = view.keys - j0 - 8 * g;   // of this octet
 #pragma unroll
-            for (int i = 0; i < Tile<NS>::kScaleSets; ++i) {
-                const int e0 = view.keys - j0 - 8 * g;   // tokens of this octet that exist
-                now.vs[i].x = keep_halves(now.vs[i].x, e0 > 0, e0 > 1);
-                now.vs[i].y = keep_halves(now.vs[i].y, e0 > 2, e0 > 3);
-                now.vs[i].z = keep_halves(now.vs[i].z, e0 > 4, e0 > 5);
-                now.vs[i].w = keep_halves(now.vs[i].w, e0 > 6, e0 > 7);
-                bad = bad || (bad_halves(now.vs[i].x) | bad_halves(now.vs[i].y) |
-                              bad_halves(now.vs[i].z) | bad_halves(now.vs[i].w));
-            }
-            if (__any(bad)) {
+            for (int i = 0; i < Tile<NS>::kScaleSets; ++i)
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const u32x4 s4 = now.vs[Tile<NS>::kRuns ? 0 : i / 2];
-                    const half8 ind = __builtin_bit_cast(
-                        half8, u32x4{bad_halves(s4.x), bad_halves(s4.y), bad_halves(s4.z),
-                                     bad_halves(s4.w)});
+                for (int e = 0; e < 4; ++e)
+                    now.vs[i][e] = clean_scales(now.vs[i][e], tokens, e, bad);
+            if (__any(bad != 0)) {
 #pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        u32x4 see;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            see[e] = (seen[c] >> (2 * e) & 1 ? 0x3C00u : 0u) |
-                                     (seen[c] >> (2 * e + 1) & 1 ? 0x3C000000u : 0u);
-                        const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            ind, __builtin_bit_cast(half8, see), f32x4{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (hit[b] > 0.0f) o[c][i][b] = __builtin_nanf("");
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < Tile<NS>::kScaleSets; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t x = bad_halves(now.vs[i][e]);
-                        now.vs[i][e] = keep_halves(now.vs[i][e], !(x & 0xFFFFu), !(x >> 16));
-                    }
+                for (int c = 0; c < NT; ++c) nan_blocks[c] |= bad_blocks<NS>(p, g, tokens, seen[c]);
             }
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const half8 op = value_operand(now, i);
+            const half8 op = value_operand(now, i, mg);
 #pragma unroll
             for (int c = 0; c < NT; ++c)
                 o[c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, w[c], o[c][i], 0, 0, 0);
@@ -282,10 +252,16 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     for (int c = 0; c < NT; ++c) {
         l[c] += __shfl_xor(l[c], 16);
         l[c] += __shfl_xor(l[c], 32);
-        if (g == 0) wave_stats[wave][16 * c + r] = float2{m[c], l[c]};
+        nan_blocks[c] |= __shfl_xor(nan_blocks[c], 16);
+        nan_blocks[c] |= __shfl_xor(nan_blocks[c], 32);
+        if (g == 0) {
+            wave_stats[wave][16 * c + r] = float2{m[c], l[c]};
+            wave_nan[wave][16 * c + r] = nan_blocks[c];
+        }
     }
     __syncthreads();
     const int64_t part = (int64_t)job * a.splits + split;
+    const bool partial = parts.count > 1;   // else the rows are done
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         float mc = -__builtin_inff(), lc = 0.0f;
@@ -297,12 +273,15 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
             const float2 x = wave_stats[i][16 * c + r];
             lc += x.y * __builtin_amdgcn_exp2f(x.x - base);
         }
+        uint32_t nan = 0;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) nan |= wave_nan[i][16 * c + r];
         const float f = __builtin_amdgcn_exp2f(m[c] - base);
         const float inv = lc == 0.0f ? 0.0f : 1.0f / lc;
-        const int64_t row = (int64_t)view.rt * R + 16 * c + r;
-        const int i = (int)(row / a.group), h = head * a.group + (int)(row - (int64_t)i * a.group);
+        const int row = view.rt * R + 16 * c + r;
+        const int i = (int)((unsigned)row / (unsigned)a.group), h = head * a.group + row - i * a.group;
         const bool live = i < view.rows.n;
-        if (a.splits > 1 && wave == 0 && g == 0 && live) {
+        if (partial && wave == 0 && g == 0 && live) {
             float *st = a.stats + (part * R + 16 * c + r) * 2;
             st[0] = mc;
             st[1] = lc;
@@ -325,7 +304,14 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
                     for (int v = 0; v < kWaves; ++v) x[k] += join[v][4 * k + wave][lane];
             }
             const int dr = 4 * g + wave;   // row of the output tiles
-            if (live && a.splits > 1) {
+            if (nan) {
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const int d = Tile<NS>::kRuns ? MT * dr + i0 + k : 16 * (i0 + k) + dr;
+                    if (nan >> (d / 32) & 1) x[k] = __builtin_nanf("");
+                }
+            }
+            if (live && partial) {
                 float *y = a.partial + (part * R + 16 * c + r) * D;
 #pragma unroll
                 for (int k = 0; k < CH; ++k)
@@ -342,88 +328,133 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     }
 }
 
-// Joins the parts of each row (of job · R + row slots): W waves per row, part s by
-// wave s % W.
-template <int NS, int W>
-__global__ __launch_bounds__(64 * (W > 4 ? W : 4)) void attention_join_kernel(AttnArgs a, int R,
-                                                                              int slots) {
-    constexpr int D = 32 * NS, E = (D + 63) / 64, ROWS = (W > 4 ? W : 4) / W;
-    __shared__ float factor[ROWS][kMaxSplits];
-    __shared__ float sums[ROWS][W][E * 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave % W, mine = wave / W;
-    const int slot = blockIdx.x * ROWS + mine;
-    const int job = slot / R, n = slot - job * R, head = job % a.kv.heads;
+// Joins the parts of the rows that have more than one.
+//   out = Σ_s f_s · o_s / Σ_s f_s · l_s,  f_s = e^(m_s − max m)
+
+template <int NS>
+__device__ __forceinline__ void store_row(const AttnArgs &a, const View &v, int head, int R, int n,
+                                          const float (&x)[(32 * NS + 63) / 64], float sum) {
+    constexpr int D = 32 * NS;
+    const int lane = threadIdx.x & 63;
+    const int row = v.rt * R + n;
+    const int i = (int)((unsigned)row / (unsigned)a.group), h = head * a.group + row - i * a.group;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t *out = a.y + (int64_t)(v.rows.first + i) * a.ldy + (int64_t)h * D;
+#pragma unroll
+    for (int e = 0; e < (D + 63) / 64; ++e)
+        if (lane + 64 * e < D) out[lane + 64 * e] = (uint16_t)pack_f16x2(x[e] * inv, 0.0f);
+}
+
+// Few rows and many parts: a workgroup per row of R per job, part s to wave s % 8.
+template <int NS, int R>
+__global__ __launch_bounds__(512) void attention_join_parts(AttnArgs a) {
+    constexpr int D = 32 * NS, E = (D + 63) / 64, W = 8;
+    __shared__ float factor[kMaxSplits];
+    __shared__ float sums[W][E * 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int job = blockIdx.x / R, n = blockIdx.x % R, head = job % a.kv.heads;
     View view;
-    bool any = slot < slots;
-    if (any)
-        any = R == 16   ? find_view<16>(a, job / a.kv.heads, view)
-              : R == 32 ? find_view<32>(a, job / a.kv.heads, view)
-                        : find_view<128>(a, job / a.kv.heads, view);
-    int i = 0, h = 0;
-    if (any) {
-        const int64_t row = (int64_t)view.rt * R + n;
-        i = (int)(row / a.group);
-        h = head * a.group + (int)(row - (int64_t)i * a.group);
-        any = i < view.rows.n;
-    }
-    if (W >= 4 && !any) return;   // the whole workgroup
-    int parts = 0;
-    float sum = 0.0f;
+    if (!find_view<R>(a, job / a.kv.heads, view)) return;
+    if (view.rt * R + n >= view.rows.n * a.group) return;
+    const Parts parts = parts_of(a, view.n, even_share(a, R));
+    if (parts.count == 1) return;
     const int64_t base = (int64_t)job * a.splits;
-    if (any) {
-        const int chunk = part_tiles(view.n, a.splits);
-        parts = (view.n + chunk - 1) / chunk;
-        if (parts < 1) parts = 1;   // the first part always writes
-        const float2 *st = (const float2 *)a.stats + base * R + n;
-        float m = -__builtin_inff();
-        float2 t[kMaxSplits / 64];
+    const float2 *st = (const float2 *)a.stats + base * R + n;
+    float m = -__builtin_inff(), sum = 0.0f;
+    float2 t[kMaxSplits / 64];
 #pragma unroll
-        for (int k = 0; k < kMaxSplits / 64; ++k) {
-            const int s = lane + 64 * k;
-            t[k] = s < parts ? st[(int64_t)s * R] : float2{-__builtin_inff(), 0.0f};
-            m = fmaxf(m, t[k].x);
-        }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-        if (m == -__builtin_inff()) m = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kMaxSplits / 64; ++k) {
-            const float f = __builtin_amdgcn_exp2f(t[k].x - m);
-            sum = __builtin_fmaf(t[k].y, f, sum);
-            if (sub == 0 && lane + 64 * k < parts) factor[mine][lane + 64 * k] = f;
-        }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    for (int k = 0; k < kMaxSplits / 64; ++k) {
+        const int s = lane + 64 * k;
+        t[k] = s < parts.count ? st[(int64_t)s * R] : float2{-__builtin_inff(), 0.0f};
+        m = fmaxf(m, t[k].x);
     }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (m == -__builtin_inff()) m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 64; ++k) {
+        const float f = __builtin_amdgcn_exp2f(t[k].x - m);
+        sum = __builtin_fmaf(t[k].y, f, sum);
+        if (wave == 0 && lane + 64 * k < parts.count) factor[lane + 64 * k] = f;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
     __syncthreads();
     float x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = 0.0f;
     const float *y = a.partial + (base * R + n) * D;
 #pragma unroll 4
-    for (int s = sub; s < parts; s += W) {
-        const float f = factor[mine][s];
+    for (int s = wave; s < parts.count; s += W) {
+        const float f = factor[s];
 #pragma unroll
         for (int e = 0; e < E; ++e)
             if (lane + 64 * e < D)
                 x[e] = __builtin_fmaf(y[(int64_t)s * R * D + lane + 64 * e], f, x[e]);
     }
-    if constexpr (W > 1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) sums[mine][sub][64 * e + lane] = x[e];
-        __syncthreads();
-        if (sub > 0) return;
+    for (int e = 0; e < E; ++e) sums[wave][64 * e + lane] = x[e];
+    __syncthreads();
+    if (wave > 0) return;
 #pragma unroll
-        for (int w = 1; w < W; ++w)
+    for (int w = 1; w < W; ++w)
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] += sums[mine][w][64 * e + lane];
+        for (int e = 0; e < E; ++e) x[e] += sums[w][64 * e + lane];
+    store_row<NS>(a, view, head, R, n, x, sum);
+}
+
+// Many rows and at most eight parts: a workgroup per 32 rows of a job, eight per wave,
+// whose statistics its lanes hold as row lane / 8, part lane % 8.
+template <int NS, int R>
+__global__ __launch_bounds__(256) void attention_join_rows(AttnArgs a) {
+    constexpr int D = 32 * NS, E = (D + 63) / 64, GROUPS = (R + 31) / 32;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int job = blockIdx.x / GROUPS, head = job % a.kv.heads;
+    const int n0 = (blockIdx.x % GROUPS) * 32 + 8 * wave;
+    View view;
+    if (!find_view<R>(a, job / a.kv.heads, view)) return;
+    const Parts parts = parts_of(a, view.n, even_share(a, R));
+    const int rows = view.rows.n * a.group - view.rt * R;   // of this tile on
+    if (parts.count == 1 || n0 >= rows || n0 >= R) return;
+    const int64_t base = (int64_t)job * a.splits;
+    const int mine = n0 + lane / 8, part = lane % 8;
+    const bool have = part < parts.count && mine < R && mine < rows;
+    const float2 st = have ? ((const float2 *)a.stats)[(base + part) * R + mine]
+                           : float2{-__builtin_inff(), 0.0f};
+    float m = st.x;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    const float f = __builtin_amdgcn_exp2f(st.x - (m == -__builtin_inff() ? 0.0f : m));
+    float sum = st.y * f;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = n0 + i;
+        if (n >= R || n >= rows) break;
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = 0.0f;
+        const float *y = a.partial + (base * R + n) * D;
+        for (int s = 0; s < parts.count; ++s) {
+            const float fs = __shfl(f, 8 * i + s);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (lane + 64 * e < D)
+                    x[e] = __builtin_fmaf(y[(int64_t)s * R * D + lane + 64 * e], fs, x[e]);
+        }
+        store_row<NS>(a, view, head, R, n, x, __shfl(sum, 8 * i));
     }
-    if (!any) return;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t *out = a.y + (int64_t)(view.rows.first + i) * a.ldy + (int64_t)h * D;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (lane + 64 * e < D) out[lane + 64 * e] = (uint16_t)pack_f16x2(x[e] * inv, 0.0f);
+}
+
+template <int NS, int R>
+void launch_join(const AttnArgs &a, hipStream_t stream) {
+    const unsigned jobs = (unsigned)a.units * a.kv.heads;
+    if (a.splits > 8)
+        hipLaunchKernelGGL((attention_join_parts<NS, R>), dim3(jobs * R), dim3(512), 0, stream, a);
+    else
+        hipLaunchKernelGGL((attention_join_rows<NS, R>), dim3(jobs * ((R + 31) / 32)), dim3(256), 0,
+                           stream, a);
 }
 
 template <int NS, int NT>
@@ -443,7 +474,7 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) 
     // mask's −∞: it has to be positive and in range there
     const bool bias = a.cap > 0.0f || a.slopes || !(a.scale > 1e-30f && a.scale < 1e30f);
     hipError_t e = hipSuccess;
-    if (p.rows == kPromptRows) {
+    if (p.rows > 32) {
         e = launch_attention_prompt(a, bias, stream);
     } else {
         if (p.rows == 16)
@@ -453,13 +484,12 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) 
         e = hipGetLastError();
     }
     if (e != hipSuccess || a.splits == 1) return e;
-    const int slots = (int)(p.row_tiles * a.kv.heads * p.rows);
-    if (a.splits <= 8)
-        hipLaunchKernelGGL((attention_join_kernel<NS, 1>), dim3((slots + 3) / 4), dim3(256), 0, stream,
-                           a, p.rows, slots);
+    if (p.rows == 16)
+        launch_join<NS, 16>(a, stream);
+    else if (p.rows == 32)
+        launch_join<NS, 32>(a, stream);
     else
-        hipLaunchKernelGGL((attention_join_kernel<NS, 8>), dim3(slots), dim3(512), 0, stream, a,
-                           p.rows, slots);
+        launch_join<NS, NS <= 4 ? 256 : 128>(a, stream);
     return hipGetLastError();
 }
 
@@ -470,15 +500,17 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
     const int group = s.q_heads / kv.heads;
     const int64_t mean = kv.cu ? ((int64_t)kv.M + kv.batch - 1) / kv.batch : kv.rows;
     const int64_t rows = mean * group;   // of a key/value head and sequence
-    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : kPromptRows;
+    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : attention_prompt_rows(kv.D);
     p.row_tiles = kv.cu ? (int64_t)kv.M * group / p.rows + kv.batch
                         : (rows + p.rows - 1) / p.rows * kv.batch;
-    // Parts of the keys, where there are too few workgroups to fill the chip: up to
-    // four per compute unit of the first kernel, two of the second.
+    // Parts of the keys (parts_of): as many as fill the chip if every sequence is as
+    // long as the bound, and for batches of unequal sequences up to as many more as cost
+    // little when they find nothing to do.
     const int64_t jobs = p.row_tiles * kv.heads;
     const int64_t tiles = (s.max_len + kTile - 1) / kTile;
-    const int64_t want = p.rows == kPromptRows ? 512 : 1024;
-    int64_t splits = jobs >= want / 2 ? 1 : (want + jobs - 1) / jobs;
+    p.target = p.rows > 32 ? 256 : 1024;
+    int64_t splits = p.rows > 32 ? (1024 + jobs - 1) / jobs : 4096 / jobs;
+    if (p.rows > 32 && splits > 8) splits = 8;
     if (splits > tiles / kMinTiles) splits = tiles / kMinTiles;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
@@ -502,14 +534,15 @@ hipError_t launch_attention(const KvSpec &kv, const AttnSpec &s, const AttnPlan 
     a.q_heads = s.q_heads;
     a.group = s.q_heads / kv.heads;
     a.causal = s.causal;
-    a.window = s.window;
+    a.window = s.window < kMaxLen ? s.window : kMaxLen;   // no sequence is longer
     a.splits = p.splits;
+    a.target = p.target;
     a.slopes = s.slopes;
     a.prefix = s.prefix;
     a.stats = ws;
     a.partial = ws + p.row_tiles * kv.heads * p.splits * p.rows * 2;
     a.units = (int)p.row_tiles;
-    a.per_seq = kv.cu ? 0 : ((int64_t)kv.rows * a.group + p.rows - 1) / p.rows;
+    a.per_seq = kv.cu ? 0 : (unsigned)(((int64_t)kv.rows * a.group + p.rows - 1) / p.rows);
     switch (kv.D) {
     case 64: return launch_dim<2>(a, p, stream);
     case 96: return launch_dim<3>(a, p, stream);

@@ -12,15 +12,17 @@ struct AttnArgs {
     uint16_t *y;
     int64_t ldq, ldy;
     float scale, cap, inv_cap;        // cap 0: none
-    int q_f32, q_heads, group, causal, window, splits;
+    int q_f32, q_heads, group, causal, window;
+    int splits, target;               // parts of the keys: at most, workgroups to fill
     const float *slopes;
     const int32_t *prefix;
     float *stats, *partial;           // workspace: [row tile][head][split][R][2] and [..][R][D]
-    int64_t per_seq;                  // row tiles of a sequence (equal rows)
+    unsigned per_seq;                 // row tiles of a sequence (equal rows)
     int units;                        // row tiles of the batch
 };
 
-// The kernel for many rows (attention_prompt.hip); launches it alone.
+// The kernel for many rows (attention_prompt.hip), and how many a workgroup takes.
+int attention_prompt_rows(int D);
 hipError_t launch_attention_prompt(const AttnArgs &a, bool bias, hipStream_t stream);
 
 namespace {
@@ -35,44 +37,91 @@ struct View {
     int first_pos;            // of the sequence's first new row (may be negative)
     int p_min, p_max;         // of the row tile's rows
     int pre, lo, n;
+    int full_pre, full_lo, full_hi;   // tiles [0, full_pre) and [full_lo, full_hi): all rows
+                                      // see all of them
 };
 
 template <int R>
-MQ_INDEX bool find_view(const AttnArgs &a, int64_t unit, View &v) {
-    int64_t within;
+MQ_INDEX bool find_view(const AttnArgs &a, int unit, View &v) {
+    int within;
     v.b = find_seq(a.kv, unit, a.group, R, 1, a.per_seq, &within);
     v.rows = seq_rows(a.kv, v.b);
-    const int64_t total = (int64_t)v.rows.n * a.group;
-    if (within < 0 || within * R >= total) return false;
-    v.rt = (int)within;
+    const int total = v.rows.n * a.group;
+    if (within < 0 || (int64_t)within * R >= total) return false;
+    v.rt = within;
     v.len = seq_len(a.kv, v.b);
     v.keys = seq_keys(a.kv, v.len);
     v.first_pos = v.len - v.rows.n;
-    const int64_t last = (within + 1) * R < total ? (within + 1) * R : total;
-    v.p_min = v.first_pos + (int)(within * R / a.group);
-    v.p_max = v.first_pos + (int)((last - 1) / a.group);
+    const int first = within * R, last = total - first < R ? total - 1 : first + R - 1;
+    v.p_min = v.first_pos + (int)((unsigned)first / (unsigned)a.group);
+    v.p_max = v.first_pos + (int)((unsigned)last / (unsigned)a.group);
     v.prefix = a.prefix ? clampi(a.prefix[v.b], 0, v.keys) : 0;
-    int64_t lo = 0, hi = v.keys;
+    // positions lie within 2^30 of 0, the window is cut to 2^30: no sum passes an int
+    int lo = 0, hi = v.keys, from = 0, to = v.keys;
     if (a.window) {
-        lo = (int64_t)v.p_min - a.window + 1;
+        lo = v.p_min - a.window + 1;
+        from = v.p_max - a.window + 1;
+        if (v.p_max + a.window < hi) hi = v.p_max + a.window;
+        if (v.p_min + a.window < to) to = v.p_min + a.window;
         if (lo < 0) lo = 0;
-        if ((int64_t)v.p_max + a.window < hi) hi = (int64_t)v.p_max + a.window;
+        if (from < 0) from = 0;
     }
-    if (a.causal && (int64_t)v.p_max + 1 < hi) hi = (int64_t)v.p_max + 1;
+    if (a.causal) {
+        if (v.p_max + 1 < hi) hi = v.p_max + 1;
+        if (v.p_min + 1 < to) to = v.p_min + 1;
+    }
     if (hi < v.prefix) hi = v.prefix;
     if (hi < 0) hi = 0;
+    if (to < 0) to = 0;
     v.pre = (v.prefix + kTile - 1) / kTile;
-    v.lo = (int)(lo / kTile);
-    const int end = (int)((hi + kTile - 1) / kTile);
+    v.lo = lo / kTile;
+    const int end = (hi + kTile - 1) / kTile;
     if (v.pre >= v.lo) v.pre = v.lo = 0;
     v.n = v.pre + (end > v.lo ? end - v.lo : 0);
+    v.full_pre = v.prefix / kTile;
+    v.full_lo = (from + kTile - 1) / kTile;
+    v.full_hi = to / kTile;
     return true;
 }
 
-// Tiles of a part: a multiple of four, so that the waves share it evenly.
-MQ_INDEX int part_tiles(int n, int splits) {
-    const int c = ((n + splits - 1) / splits + 3) & ~3;
-    return c < kMinTiles ? kMinTiles : c;
+// The keys of a row tile in parts, each a workgroup's, of `per` tiles (a multiple of
+// four: the waves share a part evenly): about as many tiles as a part holds if all
+// tiles of the batch are dealt to a.target workgroups (even_share), at least kMinTiles,
+// and at most a.splits parts.  One part needs no joining.
+struct Parts {
+    int per, count;
+};
+MQ_INDEX Parts parts_of(const AttnArgs &a, int n, int share) {
+    int c = (share + 3) & ~3;
+    if (c < kMinTiles) c = kMinTiles;
+    int want = (n + c / 2) / c;
+    if (want > a.splits) want = a.splits;
+    if (want < 1) want = 1;
+    int per = ((n + want - 1) / want + 3) & ~3;
+    if (per < kMinTiles) per = kMinTiles;
+    const int count = (n + per - 1) / per;
+    return Parts{per, count < 1 ? 1 : count};
+}
+// A workgroup's part and job (row tile · heads + head).  Workgroups go to the eight
+// XCDs in turn, and many have no part: with the parts outermost those that have are
+// neighbours and fill all XCDs (with the parts innermost, four of which two are
+// empty, half the chip stands idle: a 2048-row prompt 166 us against 88).  The last
+// parts first: only the longest jobs have them.
+MQ_INDEX void find_job(const AttnArgs &a, unsigned block, int &split, int &job, int &head) {
+    const unsigned jobs = (unsigned)a.units * a.kv.heads;
+    split = a.splits - 1 - (int)(block / jobs);
+    job = (int)(block % jobs);
+    head = job % a.kv.heads;
+}
+
+// Tiles that the row tiles of sequence b read, about, per head.
+MQ_INDEX float tiles_of_seq(const AttnArgs &a, int b, int rows_per_tile) {
+    const SeqRows r = seq_rows(a.kv, b);
+    int keys = seq_keys(a.kv, seq_len(a.kv, b));
+    if (a.causal) keys -= r.n / 2;
+    if (a.window && keys > a.window + r.n) keys = a.window + r.n;
+    if (keys < 0) keys = 0;
+    return (float)((r.n * a.group + rows_per_tile - 1) / rows_per_tile) * (float)(keys / kTile + 1);
 }
 
 // The tokens that the row at position p sees: [lo, hi), and those before the prefix.
@@ -82,9 +131,8 @@ struct Range {
 MQ_INDEX Range row_range(const AttnArgs &a, const View &v, int p) {
     Range r{0, v.keys};
     if (a.window) {
-        const int64_t lo = (int64_t)p - a.window + 1, hi = (int64_t)p + a.window;
-        if (lo > 0) r.lo = (int)lo;
-        if (hi < r.hi) r.hi = (int)hi;
+        if (p - a.window + 1 > 0) r.lo = p - a.window + 1;
+        if (p + a.window < r.hi) r.hi = p + a.window;
     }
     if (a.causal && p + 1 < r.hi) r.hi = p + 1;
     return r;
@@ -94,13 +142,9 @@ MQ_INDEX bool in_range(const Range &r, int prefix, int j) {
     return ((j >= r.lo) & (j < r.hi)) | (j < prefix);
 }
 
-// Whether every row of the workgroup sees all of tokens [j, j + 32).
-MQ_INDEX bool all_visible(const AttnArgs &a, const View &v, int j) {
-    const int last = j + kTile - 1;
-    if (last >= v.keys) return false;
-    if (last < v.prefix) return true;
-    if (a.causal && last > v.p_min) return false;
-    return !a.window || (j > v.p_max - a.window && last < (int64_t)v.p_min + a.window);
+// Whether every row of the workgroup sees all of a tile.
+MQ_INDEX bool all_visible(const View &v, int tile) {
+    return tile < v.full_pre || (tile >= v.full_lo && tile < v.full_hi);
 }
 
 }  // namespace

@@ -68,19 +68,21 @@ MQ_INDEX int seq_keys(const KvSpec &kv, int len) {
     return len < room ? len : (int)room;
 }
 
-// A sequence's work in units of `per` (rows times rows_scale, or positions) is
+// A sequence's work in units of `per` (rows times scale, or positions) is
 // numbered with those of the others: sequence b's units begin at
 // cu[b]·scale / per + extra·b, which leaves it at least as many as it needs.
 // Finds the sequence of a unit, and the unit's number within it (negative before
-// the first row, beyond what the sequence needs behind its last).
-MQ_INDEX int64_t unit_base(const KvSpec &kv, int b, int scale, int per, int extra) {
-    return (int64_t)clampi(kv.cu[b], 0, kv.M) * scale / per + (int64_t)extra * b;
+// the first row, beyond what the sequence needs behind its last).  The host refuses
+// batches whose rows times scale, or units, pass an int: 64-bit divisions are a
+// hundred instructions each, fetched cold by every workgroup.
+MQ_INDEX int unit_base(const KvSpec &kv, int b, int scale, unsigned per, int extra) {
+    return (int)((unsigned)(clampi(kv.cu[b], 0, kv.M) * scale) / per) + extra * b;
 }
-MQ_INDEX int find_seq(const KvSpec &kv, int64_t unit, int scale, int per, int extra,
-                      int64_t per_seq, int64_t *within) {
+MQ_INDEX int find_seq(const KvSpec &kv, int unit, int scale, unsigned per, int extra,
+                      unsigned per_seq, int *within) {
     if (!kv.cu) {
-        const int b = (int)(unit / per_seq);
-        *within = unit - b * per_seq;
+        const int b = kv.batch == 1 ? 0 : (int)((unsigned)unit / per_seq);
+        *within = unit - b * (int)per_seq;
         return b;
     }
     int lo = 0, hi = kv.batch - 1;   // the last b whose base is at most unit
@@ -103,23 +105,23 @@ struct Octet {
     int b, p0, e_lo, e_hi, keys;
     int64_t row0;
 };
-MQ_INDEX bool find_octet(const KvSpec &kv, int64_t unit, int64_t per_seq, Octet &o) {
-    int64_t within;
+MQ_INDEX bool find_octet(const KvSpec &kv, int unit, unsigned per_seq, Octet &o) {
+    int within;
     o.b = find_seq(kv, unit, 1, 8, 2, per_seq, &within);
     const SeqRows rows = seq_rows(kv, o.b);
     const int len = seq_len(kv, o.b), start = len - rows.n;
-    const int64_t p0 = 8 * ((start > 0 ? start / 8 : 0) + within);
-    if (within < 0 || p0 >= len) return false;
-    o.p0 = (int)p0;
+    // (within is below 2^24 + 2, start below 2^30)
+    o.p0 = 8 * ((start > 0 ? start / 8 : 0) + within);
+    if (within < 0 || o.p0 >= len) return false;
     o.e_lo = start > o.p0 ? start - o.p0 : 0;
     o.e_hi = len - o.p0 < 8 ? len - o.p0 : 8;
     o.keys = seq_keys(kv, len);
     o.row0 = (int64_t)rows.first + o.p0 - start;
     return true;
 }
-inline int64_t units_per_seq(const KvSpec &kv) { return (int64_t)kv.rows / 8 + 2; }
+inline unsigned units_per_seq(const KvSpec &kv) { return kv.rows / 8 + 2; }
 inline int64_t total_units(const KvSpec &kv) {
-    return kv.cu ? (int64_t)kv.M / 8 + 2 * (int64_t)kv.batch : units_per_seq(kv) * kv.batch;
+    return kv.cu ? (int64_t)kv.M / 8 + 2 * (int64_t)kv.batch : (int64_t)units_per_seq(kv) * kv.batch;
 }
 
 // The tile of tokens [32·tile, + 32) of sequence b's head, or null where the

@@ -32,7 +32,7 @@ struct StoreArgs {
     int64_t ldk, ldv, ldq, ldqo;
     int x_type, qo_type, n_rot, interleaved, q_heads, q_part, in_place;
     float mscale;
-    int64_t per_seq;       // units of each sequence (equal rows)
+    unsigned per_seq;      // units of each sequence (equal rows)
 };
 
 struct Top {
@@ -185,7 +185,8 @@ __global__ __launch_bounds__(kThreads) void kv_store_kernel(StoreArgs a) {
 struct LoadArgs {
     KvSpec kv;
     void *k, *v;
-    int64_t ldk, ldv, per_seq;
+    int64_t ldk, ldv;
+    unsigned per_seq;
     int y_type;
 };
 

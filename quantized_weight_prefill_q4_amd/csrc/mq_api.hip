@@ -412,11 +412,13 @@ bool heads_ok(int heads, int head_dim) {
 // Checks of an attention call that its workspace depends on.
 int check_attention(const mq::KvSpec &kv, int q_heads, int64_t max_len) {
     if (!heads_ok(q_heads, kv.D) || q_heads % kv.heads || max_len < 0) return MQ_ERR_SHAPE;
+    // the kernels number a key/value head's rows, and work beyond them, as ints
+    if ((int64_t)kv.M * (q_heads / kv.heads) > (1 << 30)) return MQ_ERR_SHAPE;
     return MQ_OK;
 }
 bool plan_ok(const mq::KvSpec &kv, const mq::AttnPlan &p) {
     const int64_t jobs = p.row_tiles * kv.heads;
-    return jobs * p.splits <= kMaxBlocks && (p.splits == 1 || jobs * p.rows <= kMaxBlocks / 2);
+    return jobs * p.splits <= kMaxBlocks / 2 && (p.splits == 1 || jobs * p.rows <= kMaxBlocks / 2);
 }
 
 }  // namespace

@@ -214,12 +214,12 @@ struct AttnSpec {
     const int32_t *prefix;        // [batch], or null
     int64_t max_len;              // a bound of the lengths, for the plan only
 };
-constexpr int kPromptRows = 128;  // rows per workgroup of the kernel for many rows
 // How a call runs: query rows (of a key/value head's group) per workgroup, and
-// parts that the keys are cut into, whose partial results lie in the workspace.
+// the parts that the keys are cut into, whose partial results lie in the workspace.
 struct AttnPlan {
     int rows;
-    int splits;
+    int splits;                   // at most
+    int target;                   // workgroups that the keys are dealt to
     int64_t row_tiles;            // over the whole batch
     int64_t ws_bytes;
 };

@@ -8,9 +8,9 @@ Tolerance, per output element; e = 2^-11 is f16's half step, u = 2^-24.
            hardware's exponential adds 2u: a weight and the sum of weights are each off
            by at most e^(δ + 2u) − 1
   output   weights and values enter as f16: 2e of Σ w|v|; the sums of L terms in f32, L·u;
-           weights below 2^-39 of the largest may vanish: L·2^-39·max|v|
+           weights are held to 2^-32 of the largest (f16 at 2^7 and more for it): L·2^-32·max|v|
   rounding e of the value, 2^-25 below the smallest normal
-Together: S·(2·(e^(δ + 2u) − 1)·1.01 + 2e·1.01 + 2·L·u) + L·2^-39·max|v| + e·|y| + 2^-25, S =
+Together: S·(2·(e^(δ + 2u) − 1)·1.01 + 2e·1.01 + 2·L·u) + L·2^-32·max|v| + e·|y| + 2^-25, S =
 Σ w|v|.  (The cap's tanh is good to 3e-7 of its value and has slope at most 1.)"""
 
 import numpy as np
@@ -60,7 +60,7 @@ def expect(s, q, H, b, positions, rows, scale, causal, window, cap, slopes, pref
             top = big + (abs(slopes[h]) * dist if slopes is not None else 0)
             delta = big * (E + (D + 16) * U) + 8 * U * top + 2 * U
             w = 2 * np.expm1(delta) * 1.01 + 2 * E * 1.01 + 2 * L * U
-            tol[:, h] = S[:, h] * w[:, None] + L * 2.0 ** -39 * np.abs(np.nan_to_num(v)).max()
+            tol[:, h] = S[:, h] * w[:, None] + L * 2.0 ** -32 * np.abs(np.nan_to_num(v)).max()
     return y, tol + E * np.abs(y) + 2.0 ** -25
 
 

@@ -62,16 +62,20 @@ static int views(const KvSpec &kv, const AttnArgs &a, int64_t units, bool sound,
                 const int64_t far = p > j ? (int64_t)p - j : (int64_t)j - p;
                 CHECK(see == (((!a.causal || j <= p) && (!a.window || far < a.window)) || j < v.prefix));
                 if (see) CHECK(in[j / kTile]);
-                if (!see && in[j / kTile]) CHECK(!all_visible(a, v, j / kTile * kTile));
+                if (!see && in[j / kTile]) CHECK(!all_visible(v, j / kTile));
             }
         }
         for (int tile = 0; tile * kTile < v.keys; ++tile)
-            if ((tile + 1) * kTile > v.keys) CHECK(!all_visible(a, v, tile * kTile));
-        // the parts are the tiles, once each
-        for (int splits = 1; splits < 9; ++splits) {
-            const int c = part_tiles(v.n, splits);
-            CHECK((int64_t)c * splits >= v.n);
-        }
+            if ((tile + 1) * kTile > v.keys) CHECK(!all_visible(v, tile));
+        // the parts are the tiles, once each, in no more than were planned for
+        for (int splits = 1; splits < 20; ++splits)
+            for (int share : {0, 1, 3, 9, 40, 1000000000}) {
+                AttnArgs s = a;
+                s.splits = splits;
+                const Parts p = parts_of(s, v.n, share);
+                CHECK(p.count >= 1 && p.count <= splits && p.per % 4 == 0 && p.per >= kMinTiles);
+                CHECK((int64_t)p.count * p.per >= v.n && (v.n == 0 || (int64_t)(p.count - 1) * p.per < v.n));
+            }
     }
     if (sound)
         for (int x : seen) CHECK(x == 1);
@@ -118,7 +122,8 @@ int main() {
         kv.lens = lens.data();
         kv.cu = ragged ? cu.data() : nullptr;
         std::vector<int> rows(kv.M);
-        const int64_t per = units_per_seq(kv), units = total_units(kv);
+        const unsigned per = units_per_seq(kv);
+        const int64_t units = total_units(kv);
         for (int64_t u = 0; u < units; ++u) {
             Octet o;
             if (!find_octet(kv, u, per, o)) continue;
@@ -145,15 +150,18 @@ int main() {
         a.group = pick(1, 9);
         a.causal = pick(0, 1);
         a.window = pick(0, 1) ? pick(1, 200) : 0;
-        if (seed % 7 == 0) a.window = INT32_MAX;
+        if (seed % 7 == 0) a.window = kMaxLen;
         a.prefix = pick(0, 1) ? prefix.data() : nullptr;
+        for (int b = 0; b < kv.batch; ++b)
+            for (int R : {16, 256}) CHECK(tiles_of_seq(a, b, R) >= 0.0f);
         const bool whole = sound && (!ragged || (cu[0] == 0 && cu[kv.batch] == kv.M));
-        for (int R : {16, 32, 128}) {
+        for (int R : {16, 32, 128, 256}) {
             a.per_seq = kv.cu ? 0 : ((int64_t)kv.rows * a.group + R - 1) / R;
-            const int64_t total = kv.cu ? (int64_t)kv.M * a.group / R + kv.batch : a.per_seq * kv.batch;
+            const int64_t total = kv.cu ? (int64_t)kv.M * a.group / R + kv.batch : (int64_t)a.per_seq * kv.batch;
             const int rc = R == 16 ? views<16>(kv, a, total, whole, seed)
                          : R == 32 ? views<32>(kv, a, total, whole, seed)
-                                   : views<128>(kv, a, total, whole, seed);
+                         : R == 128 ? views<128>(kv, a, total, whole, seed)
+                                    : views<256>(kv, a, total, whole, seed);
             if (rc) return rc;
         }
     }
