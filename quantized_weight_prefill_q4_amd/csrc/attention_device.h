@@ -109,9 +109,13 @@ __device__ __forceinline__ void make_uniform(View &v) {
 __device__ __forceinline__ int even_share(const AttnArgs &a, int rows_per_tile) {
     if (a.splits == 1) return 0;
     float s = 0.0f;
-    for (int b = threadIdx.x & 63; b < a.kv.batch; b += 64) s += tiles_of_seq(a, b, rows_per_tile);
+    if (a.kv.batch == 1) {
+        s = tiles_of_seq(a, 0, rows_per_tile);
+    } else {
+        for (int b = threadIdx.x & 63; b < a.kv.batch; b += 64) s += tiles_of_seq(a, b, rows_per_tile);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+        for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    }
     const float share = s * (float)a.kv.heads / (float)a.target;
     return share < 1e9f ? uniform((int)ceilf(share)) : 1000000000;
 }
@@ -127,6 +131,12 @@ __device__ __forceinline__ float max_across16(float v) {
     const uint32_t x = __builtin_bit_cast(uint32_t, v);
     const auto p = __builtin_amdgcn_permlane16_swap(x, x, false, false);
     return fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+}
+
+// The score where its bit is set, else −∞ (two instructions: no condition registers).
+__device__ __forceinline__ float masked(float s, uint32_t bits, int bit) {
+    const uint32_t keep = (uint32_t)((int32_t)(bits << (31 - bit)) >> 31);
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, s) & keep) | (0xFF800000u & ~keep));
 }
 
 // Values' scales in tiles that are masked in part.  A weight of 0 times an infinity or

@@ -31,6 +31,13 @@ __device__ __forceinline__ half8 load_operand(const u32x4 *p) {
     return __builtin_bit_cast(half8, *p);
 }
 
+// What the wave's lanes wrote to LDS is there for all of them.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <int V>
 struct Int {
     static constexpr int value = V;
@@ -55,13 +62,16 @@ template <int NS, int WAVES, bool BIAS>
 __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a) {
     constexpr int D = 32 * NS, KS = 2 * NS;   // KS: k-steps of the first product
     constexpr int ROWS = 32 * WAVES, PW = (KS + WAVES - 1) / WAVES;
+    constexpr int kRowChunks = D / 8 + 1;   // 16 bytes each; odd: no bank conflicts
     typedef KeyCodes<NS, PW> Keys;
     typedef ValueCodes<NS, PW> Values;
     constexpr bool kRuns = Values::kRuns, kWhole = PW * WAVES == KS;
     static_assert(KS % PW == 0 && (!kRuns || NS % PW == 0), "a wave's operands share their scales");
     __shared__ u32x4 kops[2][KS][64], vops[2][KS][64];   // [buffer][operand][lane]
-    // of a tile masked in part: tokens whose scale is not finite, by token half, block, h
-    __shared__ uint8_t bad_tokens[2][2][NS][2];
+    // of a tile masked in part: tokens whose scale is not finite, a byte by h and token half
+    __shared__ uint32_t bad_tokens[2][NS];
+    // a wave's rows of queries on their way in and of results on their way out
+    __shared__ u32x4 rows_of_wave[WAVES][32 * kRowChunks];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int r = lane & 31, h = lane >> 5;
     int split, job, head;
@@ -85,17 +95,6 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     const int pos = view.first_pos + qi;
     const Range range = row_range(a, view, pos);
     const float slope = BIAS && a.slopes && live ? a.slopes[qh] : 0.0f;
-    half8 q[KS];
-    {
-        const int64_t at = (int64_t)(view.rows.first + (live ? qi : 0)) * a.ldq +
-                           (int64_t)(live ? qh : head * a.group) * D + 8 * h;
-        if (a.q_f32)
-#pragma unroll
-            for (int s = 0; s < KS; ++s) q[s] = load_q8_f32(a.q, at + 16 * s);
-        else
-#pragma unroll
-            for (int s = 0; s < KS; ++s) q[s] = load_q8_f16(a.q, at + 16 * s);
-    }
     f32x16 o[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i)
@@ -113,9 +112,10 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     const char *const first_tile = a.kv.cache + (int64_t)head * per_page * kv_tile_bytes(D);
     int ahead_t, ahead_tile, page, off;   // off: tile within the page
     int id;
+    auto tile_of = [&](int t) { return t < view.pre ? t : t - view.pre + view.lo; };
     auto go = [&](int t) {
         ahead_t = t;
-        ahead_tile = t < view.pre ? t : t - view.pre + view.lo;
+        ahead_tile = tile_of(t);
         page = ahead_tile / per_page;
         off = ahead_tile - page * per_page;
     };
@@ -123,12 +123,15 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     // Bits of the tiles in the pipeline, this one's first: no such page, or behind the
     // part (all masked); masked in part or wholly.
     uint32_t holes = 0, edges = 0;
-    auto place = [&](int bit) {   // the bytes of the next tile (of the cache's first without)
-        const int p = uniform(id);
+    auto place = [&](int tile, int p, int o, int bit) {   // (of the cache's first tile without)
         const bool hole = (unsigned)p >= (unsigned)a.kv.pages;
-        const char *at = first_tile + (hole ? 0 : p) * a.kv.page_bytes + off * kv_tile_bytes(D);
+        const char *at = first_tile + (hole ? 0 : p) * a.kv.page_bytes + o * kv_tile_bytes(D);
         holes |= (hole ? 1u : 0u) << bit;
-        edges |= (hole || !all_visible(view, ahead_tile) ? 1u : 0u) << bit;
+        edges |= (hole || !all_visible(view, tile) ? 1u : 0u) << bit;
+        return at;
+    };
+    auto place_next = [&](int bit) {
+        const char *at = place(ahead_tile, uniform(id), off, bit);
         ++ahead_t;
         ++ahead_tile;
         if (++off == per_page) {
@@ -190,7 +193,6 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         if (kWhole || PW * wave < KS)   // [half][element tile]
             vops[buf][PW * wave + k][lane] = __builtin_bit_cast(u32x4, join8(w));
     };
-    auto tile_of = [&](int t) { return t < view.pre ? t : t - view.pre + view.lo; };
     // Takes scales out of a tile that is masked in part (clean_scales).
     auto clean_values = [&](Values &c, int t, bool hole, int buf) {
 #pragma unroll
@@ -200,7 +202,8 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
             uint32_t bad = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) c.s[k][e] = clean_scales(c.s[k][e], tokens, e, bad);
-            bad_tokens[buf][u][kRuns ? NS * r / 32 : (s0 + k) % NS][h] = (uint8_t)bad;
+            ((uint8_t *)&bad_tokens[buf][kRuns ? NS * r / 32 : (s0 + k) % NS])[2 * h + u] =
+                (uint8_t)bad;
         }
     };
     auto read_keys = [&](int buf, half8 (&op)[KS]) {
@@ -208,16 +211,52 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         for (int k = 0; k < KS; ++k) op[k] = load_operand(&kops[buf][k][lane]);
     };
 
-    // Fill the pipeline.
+    // Fill the pipeline.  The page numbers of the first four tiles are asked for at once,
+    // by four lanes, then the queries.
+    const int front_t = t_begin + (lane & 3), front = tile_of(front_t);
+    const int front_page = (int)((unsigned)front / (unsigned)per_page);
+    const int front_off = front - front_page * per_page;
+    const int front_id = front_t < t_end ? table[front_page] : -1;
+    // Global memory is read and written along the rows, 16 bytes a lane: lanes of 32
+    // different rows would cost a cycle each (a 256-row workgroup: 4 us of 2.5 + 8).
+    u32x4 *const stage = rows_of_wave[wave];
+    half8 q[KS];
+    const int64_t q_row = (int64_t)(view.rows.first + (live ? qi : 0)) * a.ldq +
+                          (int64_t)(live ? qh : head * a.group) * D;
+    int64_t q_at[KS];
+    half8 q_in[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        const int chunk = 64 * k + lane, n = chunk / (D / 8);
+        q_at[k] = __shfl(q_row, n) + 8 * (chunk - n * (D / 8));
+    }
+    if (a.q_f32)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) q_in[k] = load_q8_f32(a.q, q_at[k]);
+    else
+#pragma unroll
+        for (int k = 0; k < KS; ++k) q_in[k] = load_q8_f16(a.q, q_at[k]);
+    auto place_front = [&](int k) {
+        return place(__builtin_amdgcn_readlane(front, k), __builtin_amdgcn_readlane(front_id, k),
+                     __builtin_amdgcn_readlane(front_off, k), k);
+    };
     Keys ka, kb;
     Values va, vb;
-    go(t_begin);
-    ask();
-    const char *p0 = place(0), *p1 = place(1), *p2 = place(2), *p3 = place(3);
+    const char *p0 = place_front(0), *p1 = place_front(1), *p2 = place_front(2), *p3 = place_front(3);
     fetch_keys(p0, ka);
     fetch_values(p0, va);
     fetch_keys(p1, kb);
     fetch_values(p1, vb);
+    go(t_begin + 4);
+    ask();
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        const int chunk = 64 * k + lane, n = chunk / (D / 8);
+        stage[chunk + n] = __builtin_bit_cast(u32x4, q_in[k]);
+    }
+    wave_sync();
+#pragma unroll
+    for (int s = 0; s < KS; ++s) q[s] = load_operand(&stage[r * kRowChunks + 2 * s + h]);
 #pragma unroll
     for (int k = 0; k < PW; ++k) expand_key(ka, k, 0);
     if (edges & 1) clean_values(va, t_begin, holes & 1, 0);
@@ -256,19 +295,18 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         }
         if (edges & 1) {
             const int j0 = tile_of(t) * kTile;
-            const bool hole = holes & 1;
-            uint32_t seen = 0;
+            // bits 0 to 15: elements of s
+            uint32_t seen = holes & 1 ? 0u : visible_bits(range, view.prefix, j0) >> (8 * h);
+            seen = (seen & 0xFFu) | (seen >> 8 & 0xFF00u);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const bool see =
-                    in_range(range, view.prefix, j0 + 8 * h + 16 * (e >> 3) + (e & 7)) & !hole;
-                seen |= (uint32_t)see << e;
-                s[e] = see ? s[e] : -__builtin_inff();
-            }
-#pragma unroll 1
-            for (int b = 0; b < NS; ++b) {
-                const uint32_t bad = bad_tokens[BUF][0][b][h] | (uint32_t)bad_tokens[BUF][1][b][h] << 8;
-                nan_blocks |= (bad & seen ? 1u : 0u) << b;
+            for (int e = 0; e < 16; ++e) s[e] = masked(s[e], seen, e);
+            uint32_t bad[NS], any = 0;
+#pragma unroll
+            for (int b = 0; b < NS; ++b) any |= bad[b] = bad_tokens[BUF][b];
+            if (uniform(any)) {
+#pragma unroll
+                for (int b = 0; b < NS; ++b)
+                    nan_blocks |= (bad[b] >> (16 * h) & seen & 0xFFFFu ? 1u : 0u) << b;
             }
         }
         // operands are read some way ahead of their use
@@ -333,7 +371,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         holes >>= 1;
         edges >>= 1;
         fetch_values(p3, vc);
-        p3 = place(3);
+        p3 = place_next(3);
         fetch_keys(p3, kc);
         s = ahead;
         __syncthreads();
@@ -344,37 +382,80 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         step(Int<1>{}, t, kb, va);
     }
 
-    l += __shfl_xor(l, 32);
-    nan_blocks |= __shfl_xor(nan_blocks, 32);
-    if (!live) return;
-    // register 4a + b of o[i]: row ρ = 8a + 4h + b, element NS·ρ + i (or 32·i + ρ)
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t part = ((int64_t)job * a.splits + split) * ROWS + slot;
-    const bool partial = parts.count > 1;   // else the row is done
-    if (partial && h == 0) {
-        a.stats[2 * part] = m;
-        a.stats[2 * part + 1] = l;
-    }
-    uint16_t *y = a.y + (int64_t)(view.rows.first + qi) * a.ldy + (int64_t)qh * D;
-    float *py = a.partial + part * D;
+    // The row's place is computed again: the loop has no registers to keep it in.
+    const int lane_again = (int)opaque((uint32_t)lane);
+    {
+        const int lane = lane_again, r = lane & 31, h = lane >> 5, slot = 32 * wave + r;
+        const int row = view.rt * ROWS + slot, qi = (int)((unsigned)row / (unsigned)a.group);
+        const int qh = head * a.group + row - qi * a.group;
+        l += __shfl_xor(l, 32);
+        nan_blocks |= __shfl_xor(nan_blocks, 32);
+        // register 4a + b of o[i]: row ρ = 8a + 4h + b, element NS·ρ + i (or 32·i + ρ)
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t part = ((int64_t)job * a.splits + split) * ROWS + slot;
+        const bool partial = parts.count > 1;   // else the row is done
+        const int total = view.rows.n * a.group;
+        if (partial && h == 0 && row < total) {
+            a.stats[2 * part] = m;
+            a.stats[2 * part + 1] = l;
+        }
+        if (__any(nan_blocks != 0)) {
 #pragma unroll
-    for (int ra = 0; ra < 4; ++ra) {
-        float x[4 * NS];   // kRuns: elements NS·(8a + 4h) + [0, 4·NS)
+            for (int i = 0; i < NS; ++i)
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+                for (int e = 0; e < 16; ++e) {
+                    const int rho = 8 * (e / 4) + 4 * h + e % 4, d = kRuns ? NS * rho + i : 32 * i + rho;
+                    if (nan_blocks >> (d / 32) & 1) o[i][e] = __builtin_nanf("");
+                }
+        }
+        // quads of a row's elements: number j of o's registers 4·ra .. 4·ra + 3 is
+        // kRuns: elements NS·(8·ra + 4·h) + 4·j and on, else 32·j + 8·ra + 4·h and on
+        auto quad = [&](int ra, int j) {
+            f32x4 x;
 #pragma unroll
-            for (int i = 0; i < NS; ++i) x[kRuns ? NS * b + i : 4 * i + b] = o[i][4 * ra + b];
-        const int rho = 8 * ra + 4 * h;
+            for (int e = 0; e < 4; ++e)
+                x[e] = kRuns ? o[(4 * j + e) % NS][4 * ra + (4 * j + e) / NS] : o[j][4 * ra + e];
+            return x;
+        };
+        if (partial) {   // half the elements at a time: f32 rows are twice as long
+            f32x4 *const py = (f32x4 *)(a.partial + (part - slot + 32 * wave) * D);
 #pragma unroll
-        for (int e = 0; e < 4 * NS; e += 4) {
-            const int d = kRuns ? NS * rho + e : 32 * (e / 4) + rho;
-            if (nan_blocks >> (d / 32) & 1) x[e] = x[e + 1] = x[e + 2] = x[e + 3] = __builtin_nanf("");
-            if (partial) {
-                *(f32x4 *)(py + d) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
-            } else {
-                typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
-                *(u2 *)(y + d) = u2{pack_f16x2(x[e] * inv, x[e + 1] * inv),
-                                    pack_f16x2(x[e + 2] * inv, x[e + 3] * inv)};
+            for (int half = 0; half < 2; ++half) {
+                wave_sync();
+#pragma unroll
+                for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+                    for (int j = 0; j < NS; ++j)
+                        stage[r * kRowChunks + (kRuns ? NS * (2 * rb + h) + j : 4 * j + 2 * rb + h)] =
+                            __builtin_bit_cast(u32x4, quad(2 * half + rb, j));
+                wave_sync();
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const int chunk = 64 * k + lane, n = chunk / (D / 8), c = chunk - n * (D / 8);
+                    if (row - r + n < total)
+                        py[n * (D / 4) + (kRuns ? half * (D / 8) + c : 8 * (c / 4) + 4 * half + c % 4)] =
+                            __builtin_bit_cast(f32x4, stage[chunk + n]);
+                }
+            }
+        } else {
+            const int64_t mine = (int64_t)(view.rows.first + qi) * a.ldy + (int64_t)qh * D;
+            typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+            wave_sync();
+#pragma unroll
+            for (int ra = 0; ra < 4; ++ra)
+#pragma unroll
+                for (int j = 0; j < NS; ++j) {
+                    const f32x4 x = quad(ra, j);
+                    const int at = kRuns ? NS * (2 * ra + h) + j : 8 * j + 2 * ra + h;
+                    ((u2 *)&stage[r * kRowChunks])[at] =
+                        u2{pack_f16x2(x[0] * inv, x[1] * inv), pack_f16x2(x[2] * inv, x[3] * inv)};
+                }
+            wave_sync();
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const int chunk = 64 * k + lane, n = chunk / (D / 8), c = chunk - n * (D / 8);
+                const int64_t at = __shfl(mine, n) + 8 * c;
+                if (row - r + n < total) *(q_u32x4_a2 *)(a.y + at) = stage[chunk + n];
             }
         }
     }

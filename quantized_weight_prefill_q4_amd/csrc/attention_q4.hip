@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kMaxSplits = 256;
+constexpr int kJoinRows = 32;   // rows of a workgroup that joins few parts
 
 // A tile as loaded: code dwords of the lane's operands and the scales they need.
 // Lane l is row r = l % 16 of the A operands and their inner octet g = l / 16.
@@ -184,16 +185,11 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
         if (edge) {
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
-                seen[c] = 0;
+                seen[c] = visible_bits(range[c], view.prefix, j0) >> (8 * g);
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const bool see =
-                            in_range(range[c], view.prefix, j0 + 8 * g + 4 * mt + b);
-                        seen[c] |= (uint32_t)see << (4 * mt + b);
-                        s[c][mt][b] = see ? s[c][mt][b] : -__builtin_inff();
-                    }
+                    for (int b = 0; b < 4; ++b) s[c][mt][b] = masked(s[c][mt][b], seen[c], 4 * mt + b);
             }
         }
         half8 w[NT];
@@ -403,58 +399,69 @@ __global__ __launch_bounds__(512) void attention_join_parts(AttnArgs a) {
     store_row<NS>(a, view, head, R, n, x, sum);
 }
 
-// Many rows and at most eight parts: a workgroup per 32 rows of a job, eight per wave,
-// whose statistics its lanes hold as row lane / 8, part lane % 8.
+// Many rows and few parts: a workgroup per 32 rows of a job (or its R), four elements
+// per thread, four parts at a time with a running maximum.
 template <int NS, int R>
 __global__ __launch_bounds__(256) void attention_join_rows(AttnArgs a) {
-    constexpr int D = 32 * NS, E = (D + 63) / 64, GROUPS = (R + 31) / 32;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int job = blockIdx.x / GROUPS, head = job % a.kv.heads;
-    const int n0 = (blockIdx.x % GROUPS) * 32 + 8 * wave;
+    constexpr int D = 32 * NS, Q = D / 4, PASS = 256 / Q;   // threads per row, rows per pass
+    constexpr int ROWS = R < kJoinRows ? R : kJoinRows, P = 4;
+    const int job = blockIdx.x / (R / ROWS), head = job % a.kv.heads;
     View view;
     if (!find_view<R>(a, job / a.kv.heads, view)) return;
     const Parts parts = parts_of(a, view.n, even_share(a, R));
+    if (parts.count == 1) return;
+    const int n0 = (blockIdx.x % (R / ROWS)) * ROWS, e = threadIdx.x % Q * 4;
     const int rows = view.rows.n * a.group - view.rt * R;   // of this tile on
-    if (parts.count == 1 || n0 >= rows || n0 >= R) return;
-    const int64_t base = (int64_t)job * a.splits;
-    const int mine = n0 + lane / 8, part = lane % 8;
-    const bool have = part < parts.count && mine < R && mine < rows;
-    const float2 st = have ? ((const float2 *)a.stats)[(base + part) * R + mine]
-                           : float2{-__builtin_inff(), 0.0f};
-    float m = st.x;
+    const int end = n0 + ROWS < rows ? n0 + ROWS : rows;
+    const int64_t base = (int64_t)job * a.splits * R;
+    for (int n = n0 + threadIdx.x / Q; n < end && threadIdx.x < Q * PASS; n += PASS) {
+        float m = -__builtin_inff(), sum = 0.0f;
+        f32x4 x = {0, 0, 0, 0};
+        for (int s0 = 0; s0 < parts.count; s0 += P) {
+            float2 st[P];
+            f32x4 y[P];
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    const float f = __builtin_amdgcn_exp2f(st.x - (m == -__builtin_inff() ? 0.0f : m));
-    float sum = st.y * f;
+            for (int k = 0; k < P; ++k) {   // parts beyond the last: that, with no weight
+                const int s = s0 + k < parts.count ? s0 + k : parts.count - 1;
+                const int64_t at = base + (int64_t)s * R + n;
+                st[k] = ((const float2 *)a.stats)[at];
+                y[k] = *(const f32x4 *)(a.partial + at * D + e);
+            }
+            float top = m;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+            for (int k = 0; k < P; ++k) top = fmaxf(top, st[k].x);
+            const float shift = top == -__builtin_inff() ? 0.0f : top;
+            const float f = __builtin_amdgcn_exp2f(m - shift);
+            m = top;
+            sum *= f;
+            x *= f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int n = n0 + i;
-        if (n >= R || n >= rows) break;
-        float x[E];
+            for (int k = 0; k < P; ++k) {
+                if (s0 + k >= parts.count) break;
+                const float w = __builtin_amdgcn_exp2f(st[k].x - shift);
+                sum = __builtin_fmaf(st[k].y, w, sum);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = 0.0f;
-        const float *y = a.partial + (base * R + n) * D;
-        for (int s = 0; s < parts.count; ++s) {
-            const float fs = __shfl(f, 8 * i + s);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (lane + 64 * e < D)
-                    x[e] = __builtin_fmaf(y[(int64_t)s * R * D + lane + 64 * e], fs, x[e]);
+                for (int i = 0; i < 4; ++i) x[i] = __builtin_fmaf(y[k][i], w, x[i]);
+            }
         }
-        store_row<NS>(a, view, head, R, n, x, __shfl(sum, 8 * i));
+        const int row = view.rt * R + n;
+        const int i = (int)((unsigned)row / (unsigned)a.group), h = head * a.group + row - i * a.group;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
+        *(u2 *)(a.y + (int64_t)(view.rows.first + i) * a.ldy + (int64_t)h * D + e) =
+            u2{pack_f16x2(x[0] * inv, x[1] * inv), pack_f16x2(x[2] * inv, x[3] * inv)};
     }
 }
 
 template <int NS, int R>
 void launch_join(const AttnArgs &a, hipStream_t stream) {
     const unsigned jobs = (unsigned)a.units * a.kv.heads;
-    if (a.splits > 8)
+    constexpr int ROWS = R < kJoinRows ? R : kJoinRows;
+    if (a.splits > 16)
         hipLaunchKernelGGL((attention_join_parts<NS, R>), dim3(jobs * R), dim3(512), 0, stream, a);
     else
-        hipLaunchKernelGGL((attention_join_rows<NS, R>), dim3(jobs * ((R + 31) / 32)), dim3(256), 0,
-                           stream, a);
+        hipLaunchKernelGGL((attention_join_rows<NS, R>), dim3(jobs * (R / ROWS)), dim3(256), 0, stream,
+                           a);
 }
 
 template <int NS, int NT>
@@ -511,6 +518,10 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
     p.target = p.rows > 32 ? 256 : 1024;
     int64_t splits = p.rows > 32 ? (1024 + jobs - 1) / jobs : 4096 / jobs;
     if (p.rows > 32 && splits > 8) splits = 8;
+    if (kv.batch == 1) {   // the longest of the jobs, against the mean: causal rows see less
+        const int64_t mean = s.causal && s.max_len > kv.M ? s.max_len - kv.M / 2 : s.max_len / 2 + 1;
+        splits = (p.target * s.max_len + jobs * mean / 2) / (jobs * mean);
+    }
     if (splits > tiles / kMinTiles) splits = tiles / kMinTiles;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;

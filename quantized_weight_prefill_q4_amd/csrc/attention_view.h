@@ -92,8 +92,7 @@ struct Parts {
     int per, count;
 };
 MQ_INDEX Parts parts_of(const AttnArgs &a, int n, int share) {
-    int c = (share + 3) & ~3;
-    if (c < kMinTiles) c = kMinTiles;
+    const int c = share < kMinTiles ? kMinTiles : share;
     int want = (n + c / 2) / c;
     if (want > a.splits) want = a.splits;
     if (want < 1) want = 1;
@@ -137,9 +136,10 @@ MQ_INDEX Range row_range(const AttnArgs &a, const View &v, int p) {
     if (a.causal && p + 1 < r.hi) r.hi = p + 1;
     return r;
 }
-// (without branches: eight of these per lane and column of a tile)
-MQ_INDEX bool in_range(const Range &r, int prefix, int j) {
-    return ((j >= r.lo) & (j < r.hi)) | (j < prefix);
+// The 32 tokens from j0 on that a row with this range sees, a bit each.
+MQ_INDEX uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+MQ_INDEX uint32_t visible_bits(const Range &r, int prefix, int j0) {
+    return (bits_below(r.hi - j0) & ~bits_below(r.lo - j0)) | bits_below(prefix - j0);
 }
 
 // Whether every row of the workgroup sees all of a tile.

@@ -58,7 +58,8 @@ static int views(const KvSpec &kv, const AttnArgs &a, int64_t units, bool sound,
             const int p = v.first_pos + (int)i;
             CHECK(p >= v.p_min && p <= v.p_max);
             for (int j = 0; j < v.keys; ++j) {
-                const bool see = in_range(row_range(a, v, p), v.prefix, j);
+                const bool see =
+                    visible_bits(row_range(a, v, p), v.prefix, j / kTile * kTile) >> (j % kTile) & 1;
                 const int64_t far = p > j ? (int64_t)p - j : (int64_t)j - p;
                 CHECK(see == (((!a.causal || j <= p) && (!a.window || far < a.window)) || j < v.prefix));
                 if (see) CHECK(in[j / kTile]);
