@@ -17,11 +17,17 @@
 // Matrix and vector instructions overlap within a wave: in one step the scores of
 // the next tile are multiplied while this tile's weights are computed, and this
 // tile's values while later operands are expanded (keys two tiles ahead, values
-// one; codes loaded two steps before, page numbers three).  Two LDS buffers each,
-// one barrier per step.  A wave issues one instruction in some four cycles, so a
-// step's time is near its number of instructions: what is the same for all lanes
-// and steps is kept out of the loop, what only tiles masked in part need behind
-// one branch.
+// one).  The codes go to LDS as they lie, 16 bytes a lane (each wave loading its own
+// operands' codes is five loads of 2 to 16 bytes a lane instead of one), three tiles
+// ahead of their use and loaded two steps before.  One barrier per step.
+//
+// What bounds it: with all compute units at work the clock falls to 2.0 to 2.2 GHz, and
+// a step of 256 rows by 32 tokens (D = 128) takes 2480 cycles, of which the matrix
+// instructions fill 1024: 0.86 PFLOP/s, where a large matrix product alone reaches 1.17.
+// Tried without gain: two tiles per barrier (the same 2480), waves of a SIMD half a
+// step apart by a second barrier (2900), 128 rows per workgroup and two workgroups per
+// unit (16512 tokens by 512 rows 261 us against 192), 64 rows per wave (operands in
+// accumulation registers have to be copied).
 #include "attention_device.h"
 
 namespace mq {
@@ -38,36 +44,38 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+#define MQ_INLINE __attribute__((always_inline))
+
 template <int V>
 struct Int {
     static constexpr int value = V;
 };
 
-// One wave's share of a tile's expansion, as loaded: PW key operands (k-steps PW·wave
-// + k) and PW value operands (number PW·wave + k of those by token half and tile of
-// elements).  Waves past the last operand have none.
+// One wave's share of a tile's keys or values, as loaded: PW operands (number PW·member
+// + k: k-steps of the keys; values by token half and tile of elements) and the scales of
+// their pairs.  Waves past the last operand have none.
 template <int NS, int PW>
-struct KeyCodes {
-    static constexpr int BLOCKS = (PW + 1) / 2;   // scales: one per two k-steps
-    uint32_t c[PW], s[BLOCKS];
-};
-template <int NS, int PW>
-struct ValueCodes {
-    static constexpr bool kRuns = (NS & (NS - 1)) == 0;
+struct Codes {
+    static constexpr bool kRuns = (NS & (NS - 1)) == 0;   // one set of scales serves all values
+    static constexpr int SETS = kRuns ? (PW + 1) / 2 : PW;
+    static constexpr int key_set(int k) { return kRuns ? k / 2 : k; }
+    static constexpr int value_set(int k) { return kRuns ? 0 : k; }
     uint32_t c[PW];
-    u32x4 s[kRuns ? 1 : PW];
+    u32x4 s[SETS];
 };
 
 template <int NS, int WAVES, bool BIAS>
 __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a) {
     constexpr int D = 32 * NS, KS = 2 * NS;   // KS: k-steps of the first product
-    constexpr int ROWS = 32 * WAVES, PW = (KS + WAVES - 1) / WAVES;
+    constexpr int ROWS = 32 * WAVES;
+    constexpr int PW = (KS + WAVES - 1) / WAVES;   // operands that a wave expands
+    constexpr int CHUNKS = kv_tile_bytes(D) / 16, PIECES = (CHUNKS + 64 * WAVES - 1) / (64 * WAVES);
     constexpr int kRowChunks = D / 8 + 1;   // 16 bytes each; odd: no bank conflicts
-    typedef KeyCodes<NS, PW> Keys;
-    typedef ValueCodes<NS, PW> Values;
-    constexpr bool kRuns = Values::kRuns, kWhole = PW * WAVES == KS;
+    typedef Codes<NS, PW> Share;
+    constexpr bool kRuns = Share::kRuns, kWhole = PW * WAVES == KS;
     static_assert(KS % PW == 0 && (!kRuns || NS % PW == 0), "a wave's operands share their scales");
-    __shared__ u32x4 kops[2][KS][64], vops[2][KS][64];   // [buffer][operand][lane]
+    __shared__ u32x4 ops[2][2][KS][64];   // [keys, values][buffer][operand][lane]
+    __shared__ u32x4 raw[3][CHUNKS];   // tiles as they lie in the cache
     // of a tile masked in part: tokens whose scale is not finite, a byte by h and token half
     __shared__ uint32_t bad_tokens[2][NS];
     // a wave's rows of queries on their way in and of results on their way out
@@ -82,7 +90,9 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     View view;
     if (!find_view<ROWS>(a, unit, view)) return;
     make_uniform(view);
-    const Parts parts = parts_of(a, view.n, even_share(a, ROWS));
+    Parts parts = parts_of(a, view.n, even_share(a, ROWS));
+    parts.per = uniform(parts.per);
+    parts.count = uniform(parts.count);
     if (split >= parts.count) return;
     const int t_begin = split * parts.per;
     const int t_end = t_begin + parts.per < view.n ? t_begin + parts.per : view.n;
@@ -153,15 +163,32 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     const uint32_t kscale_at = kv_kscale_at(D) + 2 * (token_place * NS + s0 / 2);
     const uint32_t vcode_at = kv_vcode_at(D) + 4 * (o8 * D + NS * r + s0 % NS);
     const uint32_t vscale_at = kv_vscale_at(D) + 16 * (o8 * NS + NS * r / 32);
-    auto fetch_keys = [&](const char *p, Keys &c) {
+    auto load_piece = [&](const char *p, u32x4 (&x)[PIECES]) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int chunk = 64 * (WAVES * i + wave) + lane;
+            if (chunk < CHUNKS) x[i] = ((const u32x4 *)p)[chunk];
+        }
+    };
+    auto store_piece = [&](const u32x4 (&x)[PIECES], u32x4 *to) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int chunk = 64 * (WAVES * i + wave) + lane;
+            if (chunk < CHUNKS) to[chunk] = x[i];
+        }
+    };
+    auto read_key_codes = [&](const u32x4 *tile, Share &c) {
+        const char *const p = (const char *)tile;
 #pragma unroll
         for (int k = 0; k < PW; ++k)
             c.c[k] = *(const uint32_t *)(p + kcode_at + 128 * NS * (k & 1) + 4 * (k / 2));
 #pragma unroll
-        for (int k = 0; k < Keys::BLOCKS; ++k)
-            c.s[k] = *(const uint16_t *)(p + kscale_at + 2 * k);
+        for (int k = 0; k < PW; ++k)
+            if (k == 0 || Share::key_set(k) > Share::key_set(k - 1))
+                c.s[Share::key_set(k)].x = *(const uint16_t *)(p + kscale_at + 2 * (k / 2));
     };
-    auto fetch_values = [&](const char *p, Values &c) {
+    auto read_value_codes = [&](const u32x4 *tile, Share &c) {
+        const char *const p = (const char *)tile;
         if constexpr (kRuns) {
             load_dwords((const uint32_t *)(p + vcode_at), c.c);
             c.s[0] = *(const u32x4 *)(p + vscale_at);
@@ -174,29 +201,18 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
             }
         }
     };
-    // Operand k of the wave's share, into LDS.
-    auto expand_key = [&](const Keys &c, int k, int buf) {
-        half2v w[4];
-        widen(c.c[k], mg, w);
-        const _Float16 d = as_half2(c.s[k / 2]).x;
-        const half2v dd = {d, d};
+    // A key's scale is one for all elements: in all pairs, as the values' are by token.
+    auto spread_scales = [&](Share &c) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] *= dd;
-        if (kWhole || PW * wave < KS)
-            kops[buf][PW * wave + k][lane] = __builtin_bit_cast(u32x4, join8(w));
-    };
-    auto expand_value = [&](const Values &c, int k, int buf) {
-        half2v w[4];
-        widen(c.c[k], mg, w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] *= as_half2(c.s[kRuns ? 0 : k][e]);
-        if (kWhole || PW * wave < KS)   // [half][element tile]
-            vops[buf][PW * wave + k][lane] = __builtin_bit_cast(u32x4, join8(w));
+        for (int k = 0; k < Share::SETS; ++k) {
+            c.s[k].x |= c.s[k].x << 16;
+            c.s[k].y = c.s[k].z = c.s[k].w = c.s[k].x;
+        }
     };
     // Takes scales out of a tile that is masked in part (clean_scales).
-    auto clean_values = [&](Values &c, int t, bool hole, int buf) {
+    auto clean_values = [&](Share &c, int t, bool hole, int buf) {
 #pragma unroll
-        for (int k = 0; k < (kRuns ? 1 : PW); ++k) {
+        for (int k = 0; k <= Share::value_set(PW - 1); ++k) {
             const int u = (s0 + k) / NS;
             const int tokens = hole ? 0 : view.keys - tile_of(t) * kTile - 8 * (2 * u + h);
             uint32_t bad = 0;
@@ -206,14 +222,22 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
                 (uint8_t)bad;
         }
     };
+    // Operand k of a share, into LDS.
+    auto expand = [&](const Share &c, int k, int set, u32x4 (*to)[64]) {
+        half2v w[4];
+        widen(c.c[k], mg, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] *= as_half2(c.s[set][e]);
+        if (kWhole || PW * wave < KS) to[PW * wave + k][lane] = __builtin_bit_cast(u32x4, join8(w));
+    };
     auto read_keys = [&](int buf, half8 (&op)[KS]) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) op[k] = load_operand(&kops[buf][k][lane]);
+        for (int k = 0; k < KS; ++k) op[k] = load_operand(&ops[0][buf][k][lane]);
     };
 
-    // Fill the pipeline.  The page numbers of the first four tiles are asked for at once,
-    // by four lanes, then the queries.
-    const int front_t = t_begin + (lane & 3), front = tile_of(front_t);
+    // Fill the pipeline.  The page numbers of the first tiles are asked for at once,
+    // by as many lanes, then the queries.
+    const int front_t = t_begin + (lane & 7), front = tile_of(front_t);
     const int front_page = (int)((unsigned)front / (unsigned)per_page);
     const int front_off = front - front_page * per_page;
     const int front_id = front_t < t_end ? table[front_page] : -1;
@@ -240,15 +264,18 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         return place(__builtin_amdgcn_readlane(front, k), __builtin_amdgcn_readlane(front_id, k),
                      __builtin_amdgcn_readlane(front_off, k), k);
     };
-    Keys ka, kb;
-    Values va, vb;
-    const char *p0 = place_front(0), *p1 = place_front(1), *p2 = place_front(2), *p3 = place_front(3);
-    fetch_keys(p0, ka);
-    fetch_values(p0, va);
-    fetch_keys(p1, kb);
-    fetch_values(p1, vb);
-    go(t_begin + 4);
-    ask();
+    u32x4 pa[PIECES], pb[PIECES];   // the wave's share of two tiles on their way to LDS
+    {
+        u32x4 first[3][PIECES];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) load_piece(place_front(k), first[k]);
+        load_piece(place_front(3), pa);
+        load_piece(place_front(4), pb);
+        go(t_begin + 5);
+        ask();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) store_piece(first[k], raw[k]);
+    }
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
         const int chunk = 64 * k + lane, n = chunk / (D / 8);
@@ -257,16 +284,23 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     wave_sync();
 #pragma unroll
     for (int s = 0; s < KS; ++s) q[s] = load_operand(&stage[r * kRowChunks + 2 * s + h]);
+    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < PW; ++k) expand_key(ka, k, 0);
-    if (edges & 1) clean_values(va, t_begin, holes & 1, 0);
+    for (int i = 0; i < 2; ++i) {
+        Share c;
+        read_key_codes(raw[i], c);
+        spread_scales(c);
 #pragma unroll
-    for (int k = 0; k < PW; ++k) expand_value(va, k, 0);
+        for (int k = 0; k < PW; ++k) expand(c, k, Share::key_set(k), ops[0][i]);
+    }
+    {
+        Share c;
+        read_value_codes(raw[0], c);
+        if (edges & 1) clean_values(c, t_begin, holes & 1, 0);
 #pragma unroll
-    for (int k = 0; k < PW; ++k) expand_key(kb, k, 1);
-    fetch_keys(p2, ka);
-    fetch_values(p2, va);
-    fetch_keys(p3, kb);
+        for (int k = 0; k < PW; ++k) expand(c, k, Share::value_set(k), ops[1][0]);
+    }
+    int raw1 = 1, raw2 = 2, raw3 = 0;   // raw buffers of the next three tiles
     __syncthreads();
     f32x16 s;
     half8 kop[KS];
@@ -277,42 +311,45 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     for (int k = 0; k < KS; ++k)
         s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kop[k], q[k], s, 0, 0, 0);
     __syncthreads();
-    // One step.  kc, vc: codes of the keys two tiles ahead and the values one ahead,
-    // loaded by now or soon; BUF: this tile's buffers.
-    auto step = [&](auto parity, int t, Keys &kc, Values &vc) {
-        constexpr int BUF = decltype(parity)::value;
-        if (edges & 2) clean_values(vc, t + 1, holes & 2, BUF ^ 1);
-        // element 8u + 4v + b of s: token j0 + 16u + 8h + 4v + b
-        if constexpr (BIAS) {
-            const int j0 = tile_of(t) * kTile;
+    constexpr int kAhead = KS < 4 ? KS : 4;   // operands are read as far ahead of their use
+    uint32_t w[8];   // a tile's weights by pairs
+    // The elements of s that the lane's row sees, a bit each, in a tile masked in part.
+    auto seen_bits = [&](int t) {
+        const uint32_t seen =
+            holes & 1 ? 0u : visible_bits(range, view.prefix, tile_of(t) * kTile) >> (8 * h);
+        return (seen & 0xFFu) | (seen >> 8 & 0xFF00u);
+    };
+    // Marks blocks of the row that saw a value with a scale that is not finite.
+    auto mark_bad = [&](int buf, int t) {
+        uint32_t bad[NS], any = 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float x = s[e] * a.scale;
-                if (a.cap > 0.0f) x = a.cap * tanh_f32(x * a.inv_cap);
-                const int j = j0 + 16 * (e >> 3) + 8 * h + (e & 7);
-                s[e] = x - slope * (float)(pos > j ? pos - j : j - pos);
-            }
+        for (int b = 0; b < NS; ++b) any |= bad[b] = bad_tokens[buf][b];
+        if (uniform(any)) {
+            const uint32_t seen = seen_bits(t);
+#pragma unroll
+            for (int b = 0; b < NS; ++b)
+                nan_blocks |= (bad[b] >> (16 * h) & seen ? 1u : 0u) << b;
+        }
+    };
+    // The weights of tile t from its scores, beside the scores of the next.
+    auto weigh = [&](auto parity, int t) MQ_INLINE {
+        constexpr int BUF = decltype(parity)::value;
+        if constexpr (BIAS) {
+            float x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = s[e];
+            bias_scores(a, x, slope, pos - tile_of(t) * kTile - 8 * h,
+                        [](int e) { return 16 * (e >> 3) + (e & 7); });
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = x[e];
         }
         if (edges & 1) {
-            const int j0 = tile_of(t) * kTile;
-            // bits 0 to 15: elements of s
-            uint32_t seen = holes & 1 ? 0u : visible_bits(range, view.prefix, j0) >> (8 * h);
-            seen = (seen & 0xFFu) | (seen >> 8 & 0xFF00u);
+            const uint32_t seen = seen_bits(t);
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = masked(s[e], seen, e);
-            uint32_t bad[NS], any = 0;
-#pragma unroll
-            for (int b = 0; b < NS; ++b) any |= bad[b] = bad_tokens[BUF][b];
-            if (uniform(any)) {
-#pragma unroll
-                for (int b = 0; b < NS; ++b)
-                    nan_blocks |= (bad[b] >> (16 * h) & seen & 0xFFFFu ? 1u : 0u) << b;
-            }
         }
-        // operands are read some way ahead of their use
-        constexpr int kAhead = KS < 4 ? KS : 4;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) kop[k] = load_operand(&kops[BUF ^ 1][k][lane]);
+        for (int k = 0; k < kAhead; ++k) kop[k] = load_operand(&ops[0][BUF ^ 1][k][lane]);
         float top = s[0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
@@ -330,15 +367,12 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         // right before its use): between two matrix instructions, what they leave time for.
         // The next tile's scores beside this one's weights and the reading of its values.
         f32x16 ahead;
-        half8 vop[KS];
-        uint32_t w[8];   // weights by pairs
 #pragma unroll
         for (int e = 0; e < 16; ++e) ahead[e] = 0.0f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             ahead = __builtin_amdgcn_mfma_f32_32x32x16_f16(kop[k], q[k], ahead, 0, 0, 0);
-            if (k + kAhead < KS) kop[k + kAhead] = load_operand(&kops[BUF ^ 1][k + kAhead][lane]);
-            vop[k] = load_operand(&vops[BUF][k][lane]);
+            if (k + kAhead < KS) kop[k + kAhead] = load_operand(&ops[0][BUF ^ 1][k + kAhead][lane]);
 #pragma unroll
             for (int x = 0; x < 8; ++x)
                 if (x * KS / 8 == k) {
@@ -347,39 +381,63 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
                     const float e1 =
                         __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * x + 1], to_log2, -base));
                     w[x] = pack_weights(e0, e1);
+                    asm volatile("" : "+v"(w[x]));   // here, not where it is used
                     l = sum_pair(w[x], l);
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
-        // this tile's values beside the expansion
+        s = ahead;
+    };
+    // Their products with its values, beside the expansion of keys kc (two tiles ahead) and
+    // values vc (one).
+    auto multiply = [&](auto parity, const Share &kc, const Share &vc) MQ_INLINE {
+        constexpr int BUF = decltype(parity)::value;
+        half8 vop[KS];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) vop[k] = load_operand(&ops[1][BUF][k][lane]);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {   // operand [half][element tile]
             const int u = k / NS, i = k % NS;
             const u32x4 x = {w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]};
             o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vop[k], __builtin_bit_cast(half8, x), o[i],
                                                           0, 0, 0);
+            if (k + kAhead < KS) vop[k + kAhead] = load_operand(&ops[1][BUF][k + kAhead][lane]);
 #pragma unroll
             for (int y = 0; y < 2 * PW; ++y)
                 if (y * KS / (2 * PW) == k) {
                     if (y < PW)
-                        expand_key(kc, y, BUF);
+                        expand(kc, y, Share::key_set(y), ops[0][BUF]);
                     else
-                        expand_value(vc, y - PW, BUF ^ 1);
+                        expand(vc, y - PW, Share::value_set(y - PW), ops[1][BUF ^ 1]);
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    // One step.  p: of tile t + 3, to LDS now; that of tile t + 5 is loaded.
+    auto step = [&](auto parity, int t, u32x4 (&p)[PIECES]) MQ_INLINE {
+        constexpr int BUF = decltype(parity)::value;
+        weigh(parity, t);
+        if (edges & 1) mark_bad(BUF, t);
+        Share kc, vc;
+        read_key_codes(raw[raw2], kc);
+        read_value_codes(raw[raw1], vc);
+        spread_scales(kc);
+        if (edges & 2) clean_values(vc, t + 1, holes & 2, BUF ^ 1);
+        multiply(parity, kc, vc);
+        store_piece(p, raw[raw3]);
         holes >>= 1;
         edges >>= 1;
-        fetch_values(p3, vc);
-        p3 = place_next(3);
-        fetch_keys(p3, kc);
-        s = ahead;
+        load_piece(place_next(4), p);
+        const int next = raw1;
+        raw1 = raw2;
+        raw2 = raw3;
+        raw3 = next;
         __syncthreads();
     };
     for (int t = t_begin; t < t_end; ++t) {
-        step(Int<0>{}, t, ka, vb);
+        step(Int<0>{}, t, pa);
         if (++t >= t_end) break;
-        step(Int<1>{}, t, kb, va);
+        step(Int<1>{}, t, pb);
     }
 
     // The row's place is computed again: the loop has no registers to keep it in.

@@ -170,16 +170,14 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
         const bool edge = !all_visible(view, tile);
         if constexpr (BIAS) {
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
+            for (int c = 0; c < NT; ++c) {
+                float x[8];
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                for (int e = 0; e < 8; ++e) x[e] = s[c][e / 4][e % 4];
+                bias_scores(a, x, slope[c], pos[c] - j0 - 8 * g, [](int e) { return e; });
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        float x = s[c][mt][b] * a.scale;
-                        if (a.cap > 0.0f) x = a.cap * tanh_f32(x * a.inv_cap);
-                        const int j = j0 + 8 * g + 4 * mt + b;
-                        s[c][mt][b] = x - slope[c] * (float)(pos[c] > j ? pos[c] - j : j - pos[c]);
-                    }
+                for (int e = 0; e < 8; ++e) s[c][e / 4][e % 4] = x[e];
+            }
         }
         uint32_t seen[NT];   // bit 4·mt + b of column c: visible
         if (edge) {

@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kTile = 32;
 
-MQ_INDEX int kv_tile_bytes(int D) { return 36 * D; }
+MQ_INDEX constexpr int kv_tile_bytes(int D) { return 36 * D; }
 
 // Keys' codes at 0; then
 MQ_INDEX int kv_kscale_at(int D) { return 16 * D; }
