@@ -4,6 +4,8 @@
 #include "attention_view.h"
 #include "mq_device.h"
 
+#define MQ_INLINE __attribute__((always_inline))   // on a lambda that is used more than once
+
 namespace mq {
 namespace {
 
@@ -148,6 +150,70 @@ __device__ __forceinline__ int even_share(const AttnArgs &a, int rows_per_tile) 
     }
     const float share = s * (float)a.kv.heads / (float)a.target;
     return uniform(share < 1e9f ? (int)ceilf(share) : 1000000000);
+}
+
+// The work of a workgroup of the kernel for few rows, or (BY_JOB) of the one that joins
+// the parts of a job: number `index`.  All lanes of a wave together, a sequence each.
+struct Work {
+    View view;          // of the row tile, with pre, lo and n of the sequence's rows
+    int head, split;
+    Parts parts;
+    int first;          // number of the job's first part
+};
+template <int R, bool BY_JOB>
+__device__ __forceinline__ bool find_work(const AttnArgs &a, int index, Work &w) {
+    const int lane = threadIdx.x & 63, batch = a.kv.batch;
+    SeqWork mine = seq_work<R>(a, lane < batch ? lane : batch - 1);
+    int share = 0;
+    if (a.splits > 1) {
+        float cost = lane < batch ? mine.cost : 0.0f;
+        for (int b = lane + 64; b < batch; b += 64) cost += seq_work<R>(a, b).cost;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2)
+            if (o < batch) cost += __shfl_xor(cost, o);
+        share = uniform(share_of(a, cost));
+    }
+    int jobs0 = 0, items0 = 0;
+    for (int b0 = 0; b0 < batch; b0 += 64) {
+        if (b0 > 0) mine = seq_work<R>(a, b0 + lane < batch ? b0 + lane : batch - 1);
+        const Parts parts = parts_of(a, mine.span.n, share);
+        const bool here = b0 + lane < batch;
+        const int jobs = here ? mine.jobs : 0, items = here ? items_of(mine, parts) : 0;
+        int job_sum = jobs, item_sum = items;   // of the lanes up to this one
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            if (o < batch) {
+                const int x = __shfl_up(job_sum, o), y = __shfl_up(item_sum, o);
+                if (lane >= o) {
+                    job_sum += x;
+                    item_sum += y;
+                }
+            }
+        }
+        const uint64_t past = __ballot(BY_JOB ? jobs0 + job_sum > index : items0 + item_sum > index);
+        if (past) {
+            const int l = uniform(__builtin_ctzll(past));
+            const int job_base = jobs0 + __builtin_amdgcn_readlane(job_sum - jobs, l);
+            const int item_base = items0 + __builtin_amdgcn_readlane(item_sum - items, l);
+            w.parts.per = __builtin_amdgcn_readlane(parts.per, l);
+            w.parts.count = __builtin_amdgcn_readlane(parts.count, l);
+            const int within = BY_JOB ? (index - job_base) * w.parts.count : index - item_base;
+            const int job = (int)((unsigned)within / (unsigned)w.parts.count);
+            w.split = within - job * w.parts.count;
+            w.first = item_base + job * w.parts.count;
+            const int rt = (int)((unsigned)job / (unsigned)a.kv.heads);
+            w.head = job - rt * a.kv.heads;
+            w.view.b = b0 + l;
+            const bool found = tile_view<R>(a, rt, w.view);
+            w.view.pre = __builtin_amdgcn_readlane(mine.span.pre, l);
+            w.view.lo = __builtin_amdgcn_readlane(mine.span.lo, l);
+            w.view.n = __builtin_amdgcn_readlane(mine.span.n, l);
+            return found;
+        }
+        jobs0 = clampi(jobs0 + __builtin_amdgcn_readlane(job_sum, 63), 0, 1 << 30);
+        items0 = clampi(items0 + __builtin_amdgcn_readlane(item_sum, 63), 0, 1 << 30);
+    }
+    return false;
 }
 
 // The maximum over the lanes that hold the same column: l and l ^ 32, and with 16

@@ -44,8 +44,6 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-#define MQ_INLINE __attribute__((always_inline))
-
 template <int V>
 struct Int {
     static constexpr int value = V;

@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kMaxSplits = 256;
+constexpr int kFewRowsTarget = 768;   // workgroups: three on each unit
 constexpr int kJoinRows = 32;   // rows of a workgroup that joins few parts
 
 // A tile as loaded: code dwords of the lane's operands and the scales they need.
@@ -39,54 +40,73 @@ template <int NS>
 struct Tile {
     static constexpr bool kRuns = (NS & (NS - 1)) == 0;
     static constexpr int kScaleSets = kRuns ? 1 : NS;
-    uint32_t k[2][NS], v[2 * NS];
-    uint32_t ks[2][(NS + 1) / 2];
-    u32x4 vs[kScaleSets];
+    static constexpr int KS2 = (NS + 1) / 2;
+    // (vectors: arrays that live on from one trip of a loop to the next went to memory)
+    typedef uint32_t Codes __attribute__((ext_vector_type(2 * NS)));
+    typedef uint32_t KeyScales __attribute__((ext_vector_type(2 * KS2)));
+    typedef uint32_t ValueScales __attribute__((ext_vector_type(4 * kScaleSets)));
+    Codes k, v;           // [m][block], [operand]
+    KeyScales ks;         // [m][pair of blocks]
+    ValueScales vs;       // [set][pair of tokens]
 };
 
 template <int NS>
 __device__ __forceinline__ void load_tile(const char *tile, int r, int g, Tile<NS> &t) {
-    constexpr int D = 32 * NS;
+    constexpr int D = 32 * NS, KS2 = Tile<NS>::KS2;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-        load_dwords((const uint32_t *)tile + ((4 * m + g) * 16 + r) * NS, t.k[m]);
+        uint32_t k[NS], ks[KS2];
+        load_dwords((const uint32_t *)tile + ((4 * m + g) * 16 + r) * NS, k);
         const uint16_t *s = (const uint16_t *)(tile + kv_kscale_at(D)) + (16 * m + r) * NS;
         if constexpr (NS % 2 == 0) {
-            load_dwords((const uint32_t *)s, t.ks[m]);
+            load_dwords((const uint32_t *)s, ks);
         } else {
 #pragma unroll
-            for (int i = 0; i < (NS + 1) / 2; ++i)
-                t.ks[m][i] = s[2 * i] | (2 * i + 1 < NS ? (uint32_t)s[2 * i + 1] << 16 : 0u);
+            for (int i = 0; i < KS2; ++i)
+                ks[i] = s[2 * i] | (2 * i + 1 < NS ? (uint32_t)s[2 * i + 1] << 16 : 0u);
         }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) t.k[m * NS + i] = k[i];
+#pragma unroll
+        for (int i = 0; i < KS2; ++i) t.ks[m * KS2 + i] = ks[i];
     }
     const uint32_t *vc = (const uint32_t *)(tile + kv_vcode_at(D)) + g * D;
     const u32x4 *vs = (const u32x4 *)(tile + kv_vscale_at(D)) + g * NS;
+    uint32_t v[2 * NS];
     if constexpr (Tile<NS>::kRuns) {
-        load_dwords(vc + 2 * NS * r, t.v);
-        t.vs[0] = vs[(2 * NS * r) / 32];
+        load_dwords(vc + 2 * NS * r, v);
+        vs += (2 * NS * r) / 32;
     } else {
 #pragma unroll
-        for (int i = 0; i < 2 * NS; ++i) t.v[i] = vc[16 * i + r];
+        for (int i = 0; i < 2 * NS; ++i) v[i] = vc[16 * i + r];
+    }
 #pragma unroll
-        for (int i = 0; i < NS; ++i) t.vs[i] = vs[i];
+    for (int i = 0; i < 2 * NS; ++i) t.v[i] = v[i];
+#pragma unroll
+    for (int i = 0; i < Tile<NS>::kScaleSets; ++i) {
+        const u32x4 x = vs[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t.vs[4 * i + e] = x[e];
     }
 }
 
 // The values' operand i.
 template <int NS>
 __device__ __forceinline__ half8 value_operand(const Tile<NS> &t, int i, uint32_t mg) {
-    const u32x4 s = t.vs[Tile<NS>::kRuns ? 0 : i / 2];
+    const int set = Tile<NS>::kRuns ? 0 : i / 2;
     half2v h[4];
     widen(t.v[i], mg, h);
-    h[0] *= as_half2(s.x);
-    h[1] *= as_half2(s.y);
-    h[2] *= as_half2(s.z);
-    h[3] *= as_half2(s.w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] *= as_half2(t.vs[4 * set + e]);
     return join8(h);
 }
 
+// Waves per SIMD that the registers have to leave room for.
+template <int NS, int NT>
+constexpr int kWavesPerSimd = NS * NT <= 4 ? 3 : NS * NT <= 8 ? 2 : 1;
+
 template <int NS, int NT, bool BIAS>
-__global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel(AttnArgs a) {
     constexpr int D = 32 * NS, R = 16 * NT, MT = 2 * NS;   // MT: output tiles of 16 elements
     constexpr int CH = MT < 8 ? MT : 8;                    // of them joined at a time
     __shared__ float join[kWaves][CH * 4][64];
@@ -94,14 +114,12 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     __shared__ uint32_t wave_nan[kWaves][R];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4;
-    int split, job, head;
-    find_job(a, blockIdx.x, split, job, head);
-    View view;
-    if (!find_view<R>(a, job / a.kv.heads, view)) return;
-    const Parts parts = parts_of(a, view.n, even_share(a, R));
-    if (split >= parts.count) return;
-    const int t_begin = split * parts.per;
-    const int t_end = t_begin + parts.per < view.n ? t_begin + parts.per : view.n;
+    Work work;
+    if (!find_work<R, false>(a, blockIdx.x, work)) return;
+    View &view = work.view;
+    make_uniform(view);
+    const int head = work.head, t_begin = work.split * work.parts.per;
+    const int t_end = t_begin + work.parts.per < view.n ? t_begin + work.parts.per : view.n;
 
     // this lane's column in each of the NT column tiles: row 16·c + r
     half8 q[NT][NS];
@@ -140,12 +158,11 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     const uint32_t mg = magic();
 
     auto tile_of = [&](int t) { return t < view.pre ? t : t - view.pre + view.lo; };
-    for (int t = t_begin + wave; t < t_end; t += kWaves) {
+    const int per_page = a.kv.page / kTile;
+    const char *const first_tile = a.kv.cache + (int64_t)head * per_page * kv_tile_bytes(D);
+    // The work on one tile; hole: there is no such page, its tokens are not visible.
+    auto use_tile = [&](Tile<NS> &now, const char *p, int t, bool hole) MQ_INLINE {
         const int tile = tile_of(t), j0 = tile * kTile;
-        const char *p = kv_tile(a.kv, view.b, head, tile);
-        if (!p) continue;   // no such page: its tokens are not visible
-        Tile<NS> now;
-        load_tile(p, r, g, now);
         f32x4 s[NT][2];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
@@ -154,8 +171,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
                 half2v h[4];
-                widen(now.k[mt][k], mg, h);
-                const half2v pair = as_half2(now.ks[mt][k / 2]);
+                widen(now.k[mt * NS + k], mg, h);
+                const half2v pair = as_half2(now.ks[mt * Tile<NS>::KS2 + k / 2]);
                 const _Float16 d = k & 1 ? pair.y : pair.x;
                 const half2v dd = {d, d};
 #pragma unroll
@@ -167,7 +184,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
             }
         }
         // element b of s[c][mt]: token j0 + 8g + 4·mt + b
-        const bool edge = !all_visible(view, tile);
+        const bool edge = hole || !all_visible(view, tile);
         if constexpr (BIAS) {
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
@@ -183,7 +200,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
         if (edge) {
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
-                seen[c] = visible_bits(range[c], view.prefix, j0) >> (8 * g);
+                seen[c] = hole ? 0u : visible_bits(range[c], view.prefix, j0) >> (8 * g);
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -221,12 +238,12 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
         }
         if (edge) {
             uint32_t bad = 0;
-            const int tokens = view.keys - j0 - 8 * g;   // of this octet
+            const int tokens = hole ? 0 : view.keys - j0 - 8 * g;   // of this octet
 #pragma unroll
             for (int i = 0; i < Tile<NS>::kScaleSets; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    now.vs[i][e] = clean_scales(now.vs[i][e], tokens, e, bad);
+                    now.vs[4 * i + e] = clean_scales(now.vs[4 * i + e], tokens, e, bad);
             if (__any(bad != 0)) {
 #pragma unroll
                 for (int c = 0; c < NT; ++c) nan_blocks[c] |= bad_blocks<NS>(p, g, tokens, seen[c]);
@@ -239,6 +256,40 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
             for (int c = 0; c < NT; ++c)
                 o[c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, w[c], o[c][i], 0, 0, 0);
         }
+    };
+    // The wave's tiles: where they lie is looked up 64 at a time, one a lane, and each is
+    // loaded while the one before is worked on.
+    for (int t0 = t_begin + wave; t0 < t_end; t0 += 64 * kWaves) {
+        int64_t at = -1;
+        if (t0 + kWaves * lane < t_end) {
+            const int tile = tile_of(t0 + kWaves * lane);
+            const int page = (int)((unsigned)tile / (unsigned)per_page);
+            const int id = a.kv.table[view.b * a.kv.table_ld + page];
+            if ((unsigned)id < (unsigned)a.kv.pages)
+                at = id * a.kv.page_bytes + (tile - page * per_page) * kv_tile_bytes(D);
+        }
+        auto place = [&](int k, bool &hole) {   // (of the cache's first tile without)
+            const int64_t x = (int64_t)__builtin_amdgcn_readlane((int)(at >> 32), k) << 32 |
+                              (uint32_t)__builtin_amdgcn_readlane((int)at, k);
+            hole = x < 0;
+            return first_tile + (hole ? 0 : x);
+        };
+        const int left = (t_end - t0 + kWaves - 1) / kWaves, n = left < 64 ? left : 64;
+        bool hole;
+        const char *p = place(0, hole);
+        Tile<NS> now;
+        load_tile(p, r, g, now);
+        for (int k = 0; k + 1 < n; ++k) {
+            bool next_hole;
+            const char *next_p = place(k + 1, next_hole);
+            Tile<NS> next;
+            load_tile(next_p, r, g, next);
+            use_tile(now, p, t0 + kWaves * k, hole);
+            now = next;
+            p = next_p;
+            hole = next_hole;
+        }
+        use_tile(now, p, t0 + kWaves * (n - 1), hole);
     }
 
     // Join the waves: every wave's results at the common maximum.
@@ -254,8 +305,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
         }
     }
     __syncthreads();
-    const int64_t part = (int64_t)job * a.splits + split;
-    const bool partial = parts.count > 1;   // else the rows are done
+    const int64_t part = blockIdx.x;
+    const bool partial = work.parts.count > 1;   // else the rows are done
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         float mc = -__builtin_inff(), lc = 0.0f;
@@ -346,13 +397,15 @@ __global__ __launch_bounds__(512) void attention_join_parts(AttnArgs a) {
     __shared__ float factor[kMaxSplits];
     __shared__ float sums[W][E * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int job = blockIdx.x / R, n = blockIdx.x % R, head = job % a.kv.heads;
-    View view;
-    if (!find_view<R>(a, job / a.kv.heads, view)) return;
+    const int n = blockIdx.x % R;
+    Work work;
+    if (!find_work<R, true>(a, blockIdx.x / R, work)) return;
+    const View &view = work.view;
+    const Parts &parts = work.parts;
+    const int head = work.head;
     if (view.rt * R + n >= view.rows.n * a.group) return;
-    const Parts parts = parts_of(a, view.n, even_share(a, R));
-    if (parts.count == 1) return;
-    const int64_t base = (int64_t)job * a.splits;
+    if (parts.count == 1 || work.first + parts.count > a.items) return;
+    const int64_t base = work.first;
     const float2 *st = (const float2 *)a.stats + base * R + n;
     float m = -__builtin_inff(), sum = 0.0f;
     float2 t[kMaxSplits / 64];
@@ -403,15 +456,25 @@ template <int NS, int R>
 __global__ __launch_bounds__(256) void attention_join_rows(AttnArgs a) {
     constexpr int D = 32 * NS, Q = D / 4, PASS = 256 / Q;   // threads per row, rows per pass
     constexpr int ROWS = R < kJoinRows ? R : kJoinRows, P = 4;
-    const int job = blockIdx.x / (R / ROWS), head = job % a.kv.heads;
-    View view;
-    if (!find_view<R>(a, job / a.kv.heads, view)) return;
-    const Parts parts = parts_of(a, view.n, even_share(a, R));
+    const int job = blockIdx.x / (R / ROWS);
+    Work work;
+    if constexpr (R > 32) {   // the kernel for many rows: a.splits places for each job
+        work.head = job % a.kv.heads;
+        work.first = job * a.splits;
+        if (!find_view<R>(a, job / a.kv.heads, work.view)) return;
+        work.parts = parts_of(a, work.view.n, even_share(a, R));
+    } else {
+        if (!find_work<R, true>(a, job, work)) return;
+        if (work.first + work.parts.count > a.items) return;
+    }
+    const View &view = work.view;
+    const Parts &parts = work.parts;
+    const int head = work.head;
     if (parts.count == 1) return;
     const int n0 = (blockIdx.x % (R / ROWS)) * ROWS, e = threadIdx.x % Q * 4;
     const int rows = view.rows.n * a.group - view.rt * R;   // of this tile on
     const int end = n0 + ROWS < rows ? n0 + ROWS : rows;
-    const int64_t base = (int64_t)job * a.splits * R;
+    const int64_t base = (int64_t)work.first * R;
     for (int n = n0 + threadIdx.x / Q; n < end && threadIdx.x < Q * PASS; n += PASS) {
         float m = -__builtin_inff(), sum = 0.0f;
         f32x4 x = {0, 0, 0, 0};
@@ -455,26 +518,25 @@ template <int NS, int R>
 void launch_join(const AttnArgs &a, hipStream_t stream) {
     const unsigned jobs = (unsigned)a.units * a.kv.heads;
     constexpr int ROWS = R < kJoinRows ? R : kJoinRows;
-    if (a.splits > 16)
-        hipLaunchKernelGGL((attention_join_parts<NS, R>), dim3(jobs * R), dim3(512), 0, stream, a);
-    else
-        hipLaunchKernelGGL((attention_join_rows<NS, R>), dim3(jobs * (R / ROWS)), dim3(256), 0, stream,
-                           a);
+    if constexpr (R <= 32) {
+        if (a.splits > 8 && jobs * R <= 512) {
+            hipLaunchKernelGGL((attention_join_parts<NS, R>), dim3(jobs * R), dim3(512), 0, stream, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((attention_join_rows<NS, R>), dim3(jobs * (R / ROWS)), dim3(256), 0, stream, a);
 }
 
 template <int NS, int NT>
-void launch_rows(const AttnArgs &a, int64_t blocks, bool bias, hipStream_t stream) {
+void launch_rows(const AttnArgs &a, bool bias, hipStream_t stream) {
     if (bias)
-        hipLaunchKernelGGL((attention_kernel<NS, NT, true>), dim3((unsigned)blocks), dim3(256), 0,
-                           stream, a);
+        hipLaunchKernelGGL((attention_kernel<NS, NT, true>), dim3(a.items), dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((attention_kernel<NS, NT, false>), dim3((unsigned)blocks), dim3(256), 0,
-                           stream, a);
+        hipLaunchKernelGGL((attention_kernel<NS, NT, false>), dim3(a.items), dim3(256), 0, stream, a);
 }
 
 template <int NS>
 hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
-    const int64_t blocks = p.row_tiles * a.kv.heads * a.splits;
     // without a cap or bias the scale goes into the exponent's factor, after the
     // mask's −∞: it has to be positive and in range there
     const bool bias = a.cap > 0.0f || a.slopes || !(a.scale > 1e-30f && a.scale < 1e30f);
@@ -483,9 +545,9 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) 
         e = launch_attention_prompt(a, bias, stream);
     } else {
         if (p.rows == 16)
-            launch_rows<NS, 1>(a, blocks, bias, stream);
+            launch_rows<NS, 1>(a, bias, stream);
         else
-            launch_rows<NS, 2>(a, blocks, bias, stream);
+            launch_rows<NS, 2>(a, bias, stream);
         e = hipGetLastError();
     }
     if (e != hipSuccess || a.splits == 1) return e;
@@ -508,23 +570,36 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
     p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : attention_prompt_rows(kv.D);
     p.row_tiles = kv.cu ? (int64_t)kv.M * group / p.rows + kv.batch
                         : (rows + p.rows - 1) / p.rows * kv.batch;
-    // Parts of the keys (parts_of): as many as fill the chip if every sequence is as
-    // long as the bound, and for batches of unequal sequences up to as many more as cost
-    // little when they find nothing to do.
+    // Parts of the keys.  (The workspace's size is asked for without the mask: none of this
+    // may depend on it.)
     const int64_t jobs = p.row_tiles * kv.heads;
-    const int64_t tiles = (s.max_len + kTile - 1) / kTile;
-    p.target = p.rows > 32 ? 256 : 1024;
-    int64_t splits = p.rows > 32 ? (1024 + jobs - 1) / jobs : 4096 / jobs;
-    if (p.rows > 32 && splits > 8) splits = 8;
-    if (kv.batch == 1) {   // the longest of the jobs, against the mean: causal rows see less
-        const int64_t mean = s.causal && s.max_len > kv.M ? s.max_len - kv.M / 2 : s.max_len / 2 + 1;
-        splits = (p.target * s.max_len + jobs * mean / 2) / (jobs * mean);
+    const int64_t max_len = s.max_len < kMaxLen ? s.max_len : kMaxLen;
+    const int64_t tiles = (max_len + kTile - 1) / kTile;
+    int64_t splits;
+    if (p.rows <= 32) {   // dealt out over the batch (find_work)
+        p.target = kFewRowsTarget;
+        splits = kMaxSplits;
+    } else if (kv.batch == 1) {   // the longest of the jobs against their mean, if causal
+        p.target = 256;
+        const double mean = max_len > kv.M ? max_len - kv.M / 2 : max_len / 2 + 1;
+        splits = (int64_t)(p.target / (double)jobs * (max_len / mean) + 0.5);
+    } else {
+        p.target = 256;
+        splits = (1024 + jobs - 1) / jobs;
+        if (splits > 8) splits = 8;
     }
-    if (splits > tiles / kMinTiles) splits = tiles / kMinTiles;
+    // Parts of four tiles, one a wave, where the few jobs leave most of the chip idle (one
+    // token over 4096, four heads: 10.0 us against 10.8 with eight); with more jobs they
+    // cost more to join than they give (8 sequences of 5 rows, heads of 256: 20.1 against
+    // 17.3).
+    p.min_tiles = p.rows <= 32 && jobs <= 64 ? 4 : 8;
+    if (splits > tiles / p.min_tiles) splits = tiles / p.min_tiles;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
     p.splits = (int)splits;
-    p.ws_bytes = splits == 1 ? 0 : jobs * splits * p.rows * (kv.D + 2) * 4;
+    p.items = jobs * splits;
+    if (p.rows <= 32 && p.items > jobs + p.target + 8) p.items = jobs + p.target + 8;
+    p.ws_bytes = splits == 1 ? 0 : p.items * p.rows * (kv.D + 2) * 4;
     return p;
 }
 
@@ -546,10 +621,12 @@ hipError_t launch_attention(const KvSpec &kv, const AttnSpec &s, const AttnPlan 
     a.window = s.window < kMaxLen ? s.window : kMaxLen;   // no sequence is longer
     a.splits = p.splits;
     a.target = p.target;
+    a.min_tiles = p.min_tiles;
     a.slopes = s.slopes;
     a.prefix = s.prefix;
     a.stats = ws;
-    a.partial = ws + p.row_tiles * kv.heads * p.splits * p.rows * 2;
+    a.items = (int)p.items;
+    a.partial = ws + p.items * p.rows * 2;
     a.units = (int)p.row_tiles;
     a.per_seq = kv.cu ? 0 : (unsigned)(((int64_t)kv.rows * a.group + p.rows - 1) / p.rows);
     switch (kv.D) {

@@ -14,9 +14,12 @@ struct AttnArgs {
     float scale, cap, inv_cap;        // cap 0: none
     int q_f32, q_heads, group, causal, window;
     int splits, target;               // parts of the keys: at most, workgroups to fill
+    int min_tiles;                    // of a part: fewer do not pay for the join
+    int items;                        // workgroups of the kernel for few rows
     const float *slopes;
     const int32_t *prefix;
-    float *stats, *partial;           // workspace: [row tile][head][split][R][2] and [..][R][D]
+    float *stats, *partial;           // workspace: [part][R][2] and [part][R][D], those of a
+                                      // row tile and head side by side
     unsigned per_seq;                 // row tiles of a sequence (equal rows)
     int units;                        // row tiles of the batch
 };
@@ -26,8 +29,6 @@ int attention_prompt_rows(int D);
 hipError_t launch_attention_prompt(const AttnArgs &a, bool bias, hipStream_t stream);
 
 namespace {
-
-constexpr int kMinTiles = 8;   // tiles of a part: fewer do not pay for the join
 
 // What a workgroup's rows see: tiles [0, pre) and [lo, lo + n − pre).
 struct View {
@@ -41,18 +42,12 @@ struct View {
                                       // see all of them
 };
 
-template <int R>
-MQ_INDEX bool find_view(const AttnArgs &a, int unit, View &v) {
-    int within;
-    v.b = find_seq(a.kv, unit, a.group, R, 1, a.per_seq, &within);
-    v.rows = seq_rows(a.kv, v.b);
-    const int total = v.rows.n * a.group;
-    if (within < 0 || (int64_t)within * R >= total) return false;
-    v.rt = within;
+// What rows [first, last] of sequence v.b see (rows of a key/value head: token · group +
+// query head); v.rows is known.
+MQ_INDEX void set_view(const AttnArgs &a, View &v, int first, int last) {
     v.len = seq_len(a.kv, v.b);
     v.keys = seq_keys(a.kv, v.len);
     v.first_pos = v.len - v.rows.n;
-    const int first = within * R, last = total - first < R ? total - 1 : first + R - 1;
     v.p_min = v.first_pos + (int)((unsigned)first / (unsigned)a.group);
     v.p_max = v.first_pos + (int)((unsigned)last / (unsigned)a.group);
     v.prefix = a.prefix ? clampi(a.prefix[v.b], 0, v.keys) : 0;
@@ -81,23 +76,39 @@ MQ_INDEX bool find_view(const AttnArgs &a, int unit, View &v) {
     v.full_pre = v.prefix / kTile;
     v.full_lo = (from + kTile - 1) / kTile;
     v.full_hi = to / kTile;
+}
+
+// The view of row tile `rt` of sequence v.b, false without such rows.
+template <int R>
+MQ_INDEX bool tile_view(const AttnArgs &a, int rt, View &v) {
+    v.rows = seq_rows(a.kv, v.b);
+    const int total = v.rows.n * a.group;
+    if (rt < 0 || (int64_t)rt * R >= total) return false;
+    v.rt = rt;
+    set_view(a, v, rt * R, total - rt * R < R ? total - 1 : rt * R + R - 1);
     return true;
+}
+template <int R>
+MQ_INDEX bool find_view(const AttnArgs &a, int unit, View &v) {
+    int within;
+    v.b = find_seq(a.kv, unit, a.group, R, 1, a.per_seq, &within);
+    return tile_view<R>(a, within, v);
 }
 
 // The keys of a row tile in parts, each a workgroup's, of `per` tiles (a multiple of
 // four: the waves share a part evenly): about as many tiles as a part holds if all
-// tiles of the batch are dealt to a.target workgroups (even_share), at least kMinTiles,
+// tiles of the batch are dealt to a.target workgroups (even_share), at least a.min_tiles,
 // and at most a.splits parts.  One part needs no joining.
 struct Parts {
     int per, count;
 };
 MQ_INDEX Parts parts_of(const AttnArgs &a, int n, int share) {
-    const int c = share < kMinTiles ? kMinTiles : share;
+    const int c = share < a.min_tiles ? a.min_tiles : share;
     int want = (n + c / 2) / c;
     if (want > a.splits) want = a.splits;
     if (want < 1) want = 1;
     int per = ((n + want - 1) / want + 3) & ~3;
-    if (per < kMinTiles) per = kMinTiles;
+    if (per < a.min_tiles) per = a.min_tiles;
     const int count = (n + per - 1) / per;
     return Parts{per, count < 1 ? 1 : count};
 }
@@ -121,6 +132,42 @@ MQ_INDEX float tiles_of_seq(const AttnArgs &a, int b, int rows_per_tile) {
     if (a.window && keys > a.window + r.n) keys = a.window + r.n;
     if (keys < 0) keys = 0;
     return (float)((r.n * a.group + rows_per_tile - 1) / rows_per_tile) * (float)(keys / kTile + 1);
+}
+
+// The kernel for few rows deals a sequence's keys out as a whole: all its row tiles
+// (one, mostly) have the same parts, of the tiles that any of its rows sees.  Parts are
+// numbered with those of the sequences before, job by job (row tile · heads + head):
+// every number below `items` of the last sequence is a workgroup's work, and there are
+// at most jobs + a.target of them, plus the sum's rounding (plan_attention).
+struct SeqWork {
+    View span;    // pre, lo and n of all rows
+    int jobs;
+    float cost;   // tiles to read
+};
+template <int R>
+MQ_INDEX SeqWork seq_work(const AttnArgs &a, int b) {
+    SeqWork w;
+    w.span.b = b;
+    w.span.rows = seq_rows(a.kv, b);
+    const int total = w.span.rows.n * a.group;
+    if (total == 0) {
+        w.span.pre = w.span.lo = w.span.n = w.span.keys = w.jobs = 0;
+        w.cost = 0.0f;
+        return w;
+    }
+    set_view(a, w.span, 0, total - 1);
+    w.jobs = (total + R - 1) / R * a.kv.heads;
+    w.cost = (float)w.jobs * (float)w.span.n;
+    return w;
+}
+MQ_INDEX int share_of(const AttnArgs &a, float cost) {
+    const float share = ceilf(cost / (float)a.target);
+    return share < 1e9f ? (int)share : 1000000000;
+}
+constexpr int kMostItems = 1 << 24;   // of a sequence or a call (the host's limit too)
+MQ_INDEX int items_of(const SeqWork &w, const Parts &p) {
+    const int64_t n = (int64_t)w.jobs * p.count;
+    return n < kMostItems ? (int)n : kMostItems;
 }
 
 // The tokens that the row at position p sees: [lo, hi), and those before the prefix.

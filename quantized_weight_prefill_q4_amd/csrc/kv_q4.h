@@ -85,14 +85,26 @@ MQ_INDEX int find_seq(const KvSpec &kv, int unit, int scale, unsigned per, int e
         *within = unit - b * (int)per_seq;
         return b;
     }
-    int lo = 0, hi = kv.batch - 1;   // the last b whose base is at most unit
-    while (lo < hi) {
+    int lo = 0;   // the last b whose base is at most unit
+#ifdef __HIP_DEVICE_COMPILE__
+    // 64 of them at a time, one a lane: a search by halves waits for a load in each step
+    for (int n = kv.batch; n > 1;) {
+        const int step = (n + 63) / 64, at = (int)(threadIdx.x & 63) * step;
+        const uint64_t below =
+            __ballot(at < n && unit_base(kv, at < n ? lo + at : lo, scale, per, extra) <= unit);
+        const int found = 63 - __builtin_clzll(below | 1);
+        lo += found * step;
+        n = n - found * step < step ? n - found * step : step;
+    }
+#else
+    for (int hi = kv.batch - 1; lo < hi;) {
         const int mid = (lo + hi + 1) >> 1;
         if (unit_base(kv, mid, scale, per, extra) <= unit)
             lo = mid;
         else
             hi = mid - 1;
     }
+#endif
     *within = unit - unit_base(kv, lo, scale, per, extra);
     return lo;
 }

@@ -418,7 +418,7 @@ int check_attention(const mq::KvSpec &kv, int q_heads, int64_t max_len) {
 }
 bool plan_ok(const mq::KvSpec &kv, const mq::AttnPlan &p) {
     const int64_t jobs = p.row_tiles * kv.heads;
-    return jobs * p.splits <= kMaxBlocks / 2 && (p.splits == 1 || jobs * p.rows <= kMaxBlocks / 2);
+    return p.items <= kMaxBlocks / 2 && (p.splits == 1 || jobs * p.rows <= kMaxBlocks / 2);
 }
 
 }  // namespace

@@ -220,7 +220,9 @@ struct AttnPlan {
     int rows;
     int splits;                   // at most
     int target;                   // workgroups that the keys are dealt to
+    int min_tiles;                // tiles of a part
     int64_t row_tiles;            // over the whole batch
+    int64_t items;                // workgroups, each with a part of a row tile's keys
     int64_t ws_bytes;
 };
 AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s);

@@ -73,13 +73,54 @@ static int views(const KvSpec &kv, const AttnArgs &a, int64_t units, bool sound,
             for (int share : {0, 1, 3, 9, 40, 1000000000}) {
                 AttnArgs s = a;
                 s.splits = splits;
+                s.min_tiles = splits % 2 ? 4 : 8;
                 const Parts p = parts_of(s, v.n, share);
-                CHECK(p.count >= 1 && p.count <= splits && p.per % 4 == 0 && p.per >= kMinTiles);
+                CHECK(p.count >= 1 && p.count <= splits && p.per % 4 == 0 && p.per >= s.min_tiles);
                 CHECK((int64_t)p.count * p.per >= v.n && (v.n == 0 || (int64_t)(p.count - 1) * p.per < v.n));
             }
     }
     if (sound)
         for (int x : seen) CHECK(x == 1);
+    return 0;
+}
+
+// The kernel for few rows: no more parts than it has workgroups and room for, and every
+// tile that a row tile reads is in its sequence's span.
+template <int R>
+static int works(const KvSpec &kv, AttnArgs a, bool sound, int seed) {
+    const int64_t most_jobs = ((int64_t)kv.M * a.group / R + kv.batch) * kv.heads;
+    for (int target : {1, 5, 40, 768})
+        for (int splits : {1, 2, 256}) {
+            a.target = target;
+            a.splits = splits;
+            a.min_tiles = target % 2 ? 4 : 8;
+            float cost = 0.0f;
+            for (int b = 0; b < kv.batch; ++b) cost += seq_work<R>(a, b).cost;
+            const int share = share_of(a, cost);
+            int64_t jobs = 0, items = 0;
+            for (int b = 0; b < kv.batch; ++b) {
+                const SeqWork w = seq_work<R>(a, b);
+                const Parts p = parts_of(a, w.span.n, share);
+                CHECK(w.jobs >= 0 && w.jobs % kv.heads == 0);
+                jobs += w.jobs;
+                items += items_of(w, p);
+                std::vector<char> in(w.span.keys / kTile + 2, 0);
+                for (int t = 0; t < w.span.n; ++t)
+                    in[t < w.span.pre ? t : t - w.span.pre + w.span.lo] = 1;
+                for (int rt = 0; rt * kv.heads < w.jobs; ++rt) {
+                    View v;
+                    v.b = b;
+                    CHECK(tile_view<R>(a, rt, v));
+                    for (int t = 0; t < v.n; ++t) CHECK(in[t < v.pre ? t : t - v.pre + v.lo]);
+                }
+                View v;
+                v.b = b;
+                CHECK(!tile_view<R>(a, w.jobs / kv.heads, v) && !tile_view<R>(a, -1, v));
+            }
+            if (!sound) continue;
+            CHECK(jobs <= most_jobs);
+            CHECK(splits > 1 ? items <= most_jobs + target + 8 : items == jobs);
+        }
     return 0;
 }
 
@@ -164,6 +205,9 @@ int main() {
                          : R == 128 ? views<128>(kv, a, total, whole, seed)
                                     : views<256>(kv, a, total, whole, seed);
             if (rc) return rc;
+            if (R <= 32)
+                if (const int rc = R == 16 ? works<16>(kv, a, whole, seed) : works<32>(kv, a, whole, seed))
+                    return rc;
         }
     }
     // the byte layout: every nibble and scale of a tile has one place
