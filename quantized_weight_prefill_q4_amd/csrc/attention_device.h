@@ -61,16 +61,19 @@ __device__ __forceinline__ void bias_scores(const AttnArgs &a, float (&s)[N], fl
 typedef uint32_t q_u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float q_f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
-// Eight query elements as f16.
-__device__ __forceinline__ half8 load_q8_f16(const void *q, int64_t at) {
-    return __builtin_bit_cast(half8,
-                              (u32x4)*reinterpret_cast<const q_u32x4_a2 *>((const uint16_t *)q + at));
+// Eight query elements as f16; of f32 ones, what that rounding leaves as f16 too.
+__device__ __forceinline__ half8 load_q8(const uint16_t *q, int64_t at) {
+    return __builtin_bit_cast(half8, (u32x4)*reinterpret_cast<const q_u32x4_a2 *>(q + at));
 }
-__device__ __forceinline__ half8 load_q8_f32(const void *q, int64_t at) {
-    const q_f32x4_a4 *p = reinterpret_cast<const q_f32x4_a4 *>((const float *)q + at);
+__device__ __forceinline__ void load_q8(const float *q, int64_t at, half8 &high, half8 &low) {
+    const q_f32x4_a4 *p = reinterpret_cast<const q_f32x4_a4 *>(q + at);
     const f32x4 x = p[0], y = p[1];
-    return __builtin_bit_cast(half8, u32x4{pack_f16x2(x.x, x.y), pack_f16x2(x.z, x.w),
-                                           pack_f16x2(y.x, y.y), pack_f16x2(y.z, y.w)});
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float v = e < 4 ? x[e & 3] : y[e & 3];
+        high[e] = (_Float16)v;
+        low[e] = (_Float16)(v - (float)high[e]);
+    }
 }
 
 // The eight (q − 8) of a code dword, exact.  A nibble under the exponent of 1024
@@ -270,6 +273,13 @@ __device__ __forceinline__ uint32_t bad_blocks(const char *tile, int octet, int 
         if (bad & seen & 0xFFu) blocks |= 1u << b;
     }
     return blocks;
+}
+
+// A key's scale as two f16 whose products with a code are exact: seven bits of it (times
+// four of the code), and the four bits that are left.
+__device__ __forceinline__ void split_scales(uint32_t d, half2v &high, half2v &low) {
+    high = as_half2(d & 0xFFF0FFF0u);
+    low = as_half2(d) - high;
 }
 
 // A pair of f16 weights added to a sum: what is summed is what is multiplied.

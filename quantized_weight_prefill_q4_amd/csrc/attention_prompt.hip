@@ -62,7 +62,7 @@ struct Codes {
     u32x4 s[SETS];
 };
 
-template <int NS, int WAVES, bool BIAS>
+template <int NS, int WAVES, bool BIAS, bool WIDE>
 __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a) {
     constexpr int D = 32 * NS, KS = 2 * NS;   // KS: k-steps of the first product
     constexpr int ROWS = 32 * WAVES;
@@ -72,12 +72,14 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     typedef Codes<NS, PW> Share;
     constexpr bool kRuns = Share::kRuns, kWhole = PW * WAVES == KS;
     static_assert(KS % PW == 0 && (!kRuns || NS % PW == 0), "a wave's operands share their scales");
-    __shared__ u32x4 ops[2][2][KS][64];   // [keys, values][buffer][operand][lane]
+    // operands: [buffer][keys, what their rounding left, values][operand][lane], and in the
+    // same place a wave's rows of queries on their way in and of results on their way out
+    constexpr int OPS = 2 * 3 * KS * 64, ROWS_LDS = WAVES * 32 * kRowChunks;
+    __shared__ u32x4 lds[OPS > ROWS_LDS ? OPS : ROWS_LDS];
+    u32x4(*const ops)[3][KS][64] = (u32x4(*)[3][KS][64])lds;
     __shared__ u32x4 raw[3][CHUNKS];   // tiles as they lie in the cache
     // of a tile masked in part: tokens whose scale is not finite, a byte by h and token half
     __shared__ uint32_t bad_tokens[2][NS];
-    // a wave's rows of queries on their way in and of results on their way out
-    __shared__ u32x4 rows_of_wave[WAVES][32 * kRowChunks];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int r = lane & 31, h = lane >> 5;
     int split, job, head;
@@ -199,14 +201,6 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
             }
         }
     };
-    // A key's scale is one for all elements: in all pairs, as the values' are by token.
-    auto spread_scales = [&](Share &c) {
-#pragma unroll
-        for (int k = 0; k < Share::SETS; ++k) {
-            c.s[k].x |= c.s[k].x << 16;
-            c.s[k].y = c.s[k].z = c.s[k].w = c.s[k].x;
-        }
-    };
     // Takes scales out of a tile that is masked in part (clean_scales).
     auto clean_values = [&](Share &c, int t, bool hole, int buf) {
 #pragma unroll
@@ -221,17 +215,31 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         }
     };
     // Operand k of a share, into LDS.
-    auto expand = [&](const Share &c, int k, int set, u32x4 (*to)[64]) {
+    auto expand_key = [&](const Share &c, int k, int buf) {
+        half2v w[4], low[4], dh, dl;
+        widen(c.c[k], mg, w);
+        split_scales(c.s[Share::key_set(k)].x, dh, dl);
+        const half2v hh = {dh.x, dh.x}, ll = {dl.x, dl.x};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            low[e] = w[e] * ll;
+            w[e] *= hh;
+        }
+        if (kWhole || PW * wave < KS) {
+            ops[buf][0][PW * wave + k][lane] = __builtin_bit_cast(u32x4, join8(w));
+            ops[buf][1][PW * wave + k][lane] = __builtin_bit_cast(u32x4, join8(low));
+        }
+    };
+    auto expand_value = [&](const Share &c, int k, int buf) {
         half2v w[4];
         widen(c.c[k], mg, w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] *= as_half2(c.s[set][e]);
-        if (kWhole || PW * wave < KS) to[PW * wave + k][lane] = __builtin_bit_cast(u32x4, join8(w));
+        for (int e = 0; e < 4; ++e) w[e] *= as_half2(c.s[Share::value_set(k)][e]);
+        if (kWhole || PW * wave < KS)   // [half][element tile]
+            ops[buf][2][PW * wave + k][lane] = __builtin_bit_cast(u32x4, join8(w));
     };
-    auto read_keys = [&](int buf, half8 (&op)[KS]) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) op[k] = load_operand(&ops[0][buf][k][lane]);
-    };
+    // K-step k of the first product, its operands one after the other.
+    auto key_operand = [&](int buf, int i) { return load_operand(&ops[buf][i & 1][i / 2][lane]); };
 
     // Fill the pipeline.  The page numbers of the first tiles are asked for at once,
     // by as many lanes, then the queries.
@@ -241,23 +249,24 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     const int front_id = front_t < t_end ? table[front_page] : -1;
     // Global memory is read and written along the rows, 16 bytes a lane: lanes of 32
     // different rows would cost a cycle each (a 256-row workgroup: 4 us of 2.5 + 8).
-    u32x4 *const stage = rows_of_wave[wave];
+    u32x4 *const stage = lds + wave * 32 * kRowChunks;
     half8 q[KS];
     const int64_t q_row = (int64_t)(view.rows.first + (live ? qi : 0)) * a.ldq +
                           (int64_t)(live ? qh : head * a.group) * D;
     int64_t q_at[KS];
-    half8 q_in[KS];
+    half8 q_in[KS], q_low_in[WIDE ? KS : 1];
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
         const int chunk = 64 * k + lane, n = chunk / (D / 8);
         q_at[k] = __shfl(q_row, n) + 8 * (chunk - n * (D / 8));
     }
-    if (a.q_f32)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) q_in[k] = load_q8_f32(a.q, q_at[k]);
-    else
-#pragma unroll
-        for (int k = 0; k < KS; ++k) q_in[k] = load_q8_f16(a.q, q_at[k]);
+    for (int k = 0; k < KS; ++k) {
+        if constexpr (WIDE)
+            load_q8((const float *)a.q, q_at[k], q_in[k], q_low_in[k]);
+        else
+            q_in[k] = load_q8((const uint16_t *)a.q, q_at[k]);
+    }
     auto place_front = [&](int k) {
         return place(__builtin_amdgcn_readlane(front, k), __builtin_amdgcn_readlane(front_id, k),
                      __builtin_amdgcn_readlane(front_off, k), k);
@@ -274,42 +283,51 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
 #pragma unroll
         for (int k = 0; k < 3; ++k) store_piece(first[k], raw[k]);
     }
+    half8 q_low[WIDE ? KS : 1];
+    auto turn = [&](const half8 (&in)[KS], half8 (&out)[KS]) MQ_INLINE {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-        const int chunk = 64 * k + lane, n = chunk / (D / 8);
-        stage[chunk + n] = __builtin_bit_cast(u32x4, q_in[k]);
+        for (int k = 0; k < KS; ++k) {
+            const int chunk = 64 * k + lane, n = chunk / (D / 8);
+            stage[chunk + n] = __builtin_bit_cast(u32x4, in[k]);
+        }
+        wave_sync();
+#pragma unroll
+        for (int s = 0; s < KS; ++s) out[s] = load_operand(&stage[r * kRowChunks + 2 * s + h]);
+    };
+    turn(q_in, q);
+    if constexpr (WIDE) {
+        wave_sync();
+        turn(q_low_in, q_low);
     }
-    wave_sync();
-#pragma unroll
-    for (int s = 0; s < KS; ++s) q[s] = load_operand(&stage[r * kRowChunks + 2 * s + h]);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         Share c;
         read_key_codes(raw[i], c);
-        spread_scales(c);
 #pragma unroll
-        for (int k = 0; k < PW; ++k) expand(c, k, Share::key_set(k), ops[0][i]);
+        for (int k = 0; k < PW; ++k) expand_key(c, k, i);
     }
     {
         Share c;
         read_value_codes(raw[0], c);
         if (edges & 1) clean_values(c, t_begin, holes & 1, 0);
 #pragma unroll
-        for (int k = 0; k < PW; ++k) expand(c, k, Share::value_set(k), ops[1][0]);
+        for (int k = 0; k < PW; ++k) expand_value(c, k, 0);
     }
     int raw1 = 1, raw2 = 2, raw3 = 0;   // raw buffers of the next three tiles
     __syncthreads();
     f32x16 s;
-    half8 kop[KS];
-    read_keys(0, kop);
 #pragma unroll
     for (int e = 0; e < 16; ++e) s[e] = 0.0f;
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kop[k], q[k], s, 0, 0, 0);
+    for (int i = 0; i < 2 * KS; ++i) {
+        const half8 op = key_operand(0, i);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(op, q[i / 2], s, 0, 0, 0);
+        if constexpr (WIDE)
+            if (i % 2 == 0) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(op, q_low[i / 2], s, 0, 0, 0);
+    }
     __syncthreads();
-    constexpr int kAhead = KS < 4 ? KS : 4;   // operands are read as far ahead of their use
+    constexpr int kAhead = 4;   // operands are read as far ahead of their use
     uint32_t w[8];   // a tile's weights by pairs
     // The elements of s that the lane's row sees, a bit each, in a tile masked in part.
     auto seen_bits = [&](int t) {
@@ -346,8 +364,9 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = masked(s[e], seen, e);
         }
+        half8 kop[2 * KS];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) kop[k] = load_operand(&ops[0][BUF ^ 1][k][lane]);
+        for (int i = 0; i < kAhead; ++i) kop[i] = key_operand(BUF ^ 1, i);
         float top = s[0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
@@ -369,8 +388,15 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         for (int e = 0; e < 16; ++e) ahead[e] = 0.0f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-            ahead = __builtin_amdgcn_mfma_f32_32x32x16_f16(kop[k], q[k], ahead, 0, 0, 0);
-            if (k + kAhead < KS) kop[k + kAhead] = load_operand(&ops[0][BUF ^ 1][k + kAhead][lane]);
+#pragma unroll
+            for (int i = 2 * k; i < 2 * k + 2; ++i) {
+                ahead = __builtin_amdgcn_mfma_f32_32x32x16_f16(kop[i], q[k], ahead, 0, 0, 0);
+                if constexpr (WIDE)
+                    if (i == 2 * k)
+                        ahead =
+                            __builtin_amdgcn_mfma_f32_32x32x16_f16(kop[i], q_low[k], ahead, 0, 0, 0);
+                if (i + kAhead < 2 * KS) kop[i + kAhead] = key_operand(BUF ^ 1, i + kAhead);
+            }
 #pragma unroll
             for (int x = 0; x < 8; ++x)
                 if (x * KS / 8 == k) {
@@ -392,21 +418,21 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         constexpr int BUF = decltype(parity)::value;
         half8 vop[KS];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) vop[k] = load_operand(&ops[1][BUF][k][lane]);
+        for (int k = 0; k < kAhead; ++k) vop[k] = load_operand(&ops[BUF][2][k][lane]);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {   // operand [half][element tile]
             const int u = k / NS, i = k % NS;
             const u32x4 x = {w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]};
             o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vop[k], __builtin_bit_cast(half8, x), o[i],
                                                           0, 0, 0);
-            if (k + kAhead < KS) vop[k + kAhead] = load_operand(&ops[1][BUF][k + kAhead][lane]);
+            if (k + kAhead < KS) vop[k + kAhead] = load_operand(&ops[BUF][2][k + kAhead][lane]);
 #pragma unroll
-            for (int y = 0; y < 2 * PW; ++y)
-                if (y * KS / (2 * PW) == k) {
-                    if (y < PW)
-                        expand(kc, y, Share::key_set(y), ops[0][BUF]);
+            for (int z = 0; z < 2 * PW; ++z)
+                if (z * KS / (2 * PW) == k) {
+                    if (z < PW)
+                        expand_key(kc, z, BUF);
                     else
-                        expand(vc, y - PW, Share::value_set(y - PW), ops[1][BUF ^ 1]);
+                        expand_value(vc, z - PW, BUF ^ 1);
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -419,7 +445,6 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         Share kc, vc;
         read_key_codes(raw[raw2], kc);
         read_value_codes(raw[raw1], vc);
-        spread_scales(kc);
         if (edges & 2) clean_values(vc, t + 1, holes & 2, BUF ^ 1);
         multiply(parity, kc, vc);
         store_piece(p, raw[raw3]);
@@ -520,10 +545,12 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
 template <int NS, int WAVES>
 hipError_t launch(const AttnArgs &a, bool bias, hipStream_t stream) {
     const dim3 grid((unsigned)(a.units * a.kv.heads * a.splits)), block(64 * WAVES);
-    if (bias)
-        hipLaunchKernelGGL((attention_prompt_kernel<NS, WAVES, true>), grid, block, 0, stream, a);
+    if (a.q_f32)   // (with the scores' general form: one kernel less)
+        hipLaunchKernelGGL((attention_prompt_kernel<NS, WAVES, true, true>), grid, block, 0, stream, a);
+    else if (bias)
+        hipLaunchKernelGGL((attention_prompt_kernel<NS, WAVES, true, false>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((attention_prompt_kernel<NS, WAVES, false>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((attention_prompt_kernel<NS, WAVES, false, false>), grid, block, 0, stream, a);
     return hipGetLastError();
 }
 

@@ -29,7 +29,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kMaxSplits = 256;
 constexpr int kFewRowsTarget = 768;   // workgroups: three on each unit
-constexpr int kJoinRows = 32;   // rows of a workgroup that joins few parts
 
 // A tile as loaded: code dwords of the lane's operands and the scales they need.
 // Lane l is row r = l % 16 of the A operands and their inner octet g = l / 16.
@@ -105,7 +104,7 @@ __device__ __forceinline__ half8 value_operand(const Tile<NS> &t, int i, uint32_
 template <int NS, int NT>
 constexpr int kWavesPerSimd = NS * NT <= 4 ? 3 : NS * NT <= 8 ? 2 : 1;
 
-template <int NS, int NT, bool BIAS>
+template <int NS, int NT, bool BIAS, bool WIDE>
 __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel(AttnArgs a) {
     constexpr int D = 32 * NS, R = 16 * NT, MT = 2 * NS;   // MT: output tiles of 16 elements
     constexpr int CH = MT < 8 ? MT : 8;                    // of them joined at a time
@@ -122,7 +121,7 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
     const int t_end = t_begin + work.parts.per < view.n ? t_begin + work.parts.per : view.n;
 
     // this lane's column in each of the NT column tiles: row 16·c + r
-    half8 q[NT][NS];
+    half8 q[NT][NS], q_low[NT][WIDE ? NS : 1];
     int pos[NT];
     Range range[NT];
     float slope[NT];
@@ -136,12 +135,13 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
         slope[c] = BIAS && a.slopes && live ? a.slopes[h] : 0.0f;
         const int64_t at = (int64_t)(view.rows.first + (live ? i : 0)) * a.ldq +
                            (int64_t)(live ? h : head * a.group) * D + 8 * g;
-        if (a.q_f32)
 #pragma unroll
-            for (int s = 0; s < NS; ++s) q[c][s] = load_q8_f32(a.q, at + 32 * s);
-        else
-#pragma unroll
-            for (int s = 0; s < NS; ++s) q[c][s] = load_q8_f16(a.q, at + 32 * s);
+        for (int s = 0; s < NS; ++s) {
+            if constexpr (WIDE)
+                load_q8((const float *)a.q, at + 32 * s, q[c][s], q_low[c][s]);
+            else
+                q[c][s] = load_q8((const uint16_t *)a.q, at + 32 * s);
+        }
     }
     f32x4 o[NT][MT];
     float m[NT], l[NT];
@@ -170,17 +170,26 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
             for (int c = 0; c < NT; ++c) s[c][mt] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
-                half2v h[4];
+                half2v h[4], low[4], dh, dl;
                 widen(now.k[mt * NS + k], mg, h);
-                const half2v pair = as_half2(now.ks[mt * Tile<NS>::KS2 + k / 2]);
-                const _Float16 d = k & 1 ? pair.y : pair.x;
-                const half2v dd = {d, d};
+                split_scales(now.ks[mt * Tile<NS>::KS2 + k / 2], dh, dl);
+                const _Float16 x = k & 1 ? dh.y : dh.x, y = k & 1 ? dl.y : dl.x;
+                const half2v xx = {x, x}, yy = {y, y};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] *= dd;
-                const half8 op = join8(h);
+                for (int e = 0; e < 4; ++e) {
+                    low[e] = h[e] * yy;
+                    h[e] *= xx;
+                }
+                const half8 op = join8(h), op_low = join8(low);
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
+                for (int c = 0; c < NT; ++c) {
                     s[c][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, q[c][k], s[c][mt], 0, 0, 0);
+                    s[c][mt] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_f16(op_low, q[c][k], s[c][mt], 0, 0, 0);
+                    if constexpr (WIDE)
+                        s[c][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, q_low[c][k], s[c][mt],
+                                                                          0, 0, 0);
+                }
             }
         }
         // element b of s[c][mt]: token j0 + 8g + 4·mt + b
@@ -232,9 +241,13 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
                 for (int b = 0; b < 4; ++b)
                     e[4 * mt + b] =
                         __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][mt][b], to_log2, -base));
-            l[c] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-            w[c] = __builtin_bit_cast(half8, u32x4{pack_weights(e[0], e[1]), pack_weights(e[2], e[3]),
-                                                   pack_weights(e[4], e[5]), pack_weights(e[6], e[7])});
+            uint32_t pairs[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pairs[i] = pack_weights(e[2 * i], e[2 * i + 1]);
+                l[c] = sum_pair(pairs[i], l[c]);
+            }
+            w[c] = __builtin_bit_cast(half8, u32x4{pairs[0], pairs[1], pairs[2], pairs[3]});
         }
         if (edge) {
             uint32_t bad = 0;
@@ -450,13 +463,13 @@ __global__ __launch_bounds__(512) void attention_join_parts(AttnArgs a) {
     store_row<NS>(a, view, head, R, n, x, sum);
 }
 
-// Many rows and few parts: a workgroup per 32 rows of a job (or its R), four elements
-// per thread, four parts at a time with a running maximum.
+// Many rows and few parts: a workgroup per a.join_rows rows of a job, four elements per
+// thread, four parts at a time with a running maximum.
 template <int NS, int R>
 __global__ __launch_bounds__(256) void attention_join_rows(AttnArgs a) {
     constexpr int D = 32 * NS, Q = D / 4, PASS = 256 / Q;   // threads per row, rows per pass
-    constexpr int ROWS = R < kJoinRows ? R : kJoinRows, P = 4;
-    const int job = blockIdx.x / (R / ROWS);
+    constexpr int P = 4;
+    const int groups = R / a.join_rows, job = (int)((unsigned)blockIdx.x / (unsigned)groups);
     Work work;
     if constexpr (R > 32) {   // the kernel for many rows: a.splits places for each job
         work.head = job % a.kv.heads;
@@ -471,9 +484,9 @@ __global__ __launch_bounds__(256) void attention_join_rows(AttnArgs a) {
     const Parts &parts = work.parts;
     const int head = work.head;
     if (parts.count == 1) return;
-    const int n0 = (blockIdx.x % (R / ROWS)) * ROWS, e = threadIdx.x % Q * 4;
+    const int n0 = ((int)blockIdx.x - job * groups) * a.join_rows, e = threadIdx.x % Q * 4;
     const int rows = view.rows.n * a.group - view.rt * R;   // of this tile on
-    const int end = n0 + ROWS < rows ? n0 + ROWS : rows;
+    const int end = n0 + a.join_rows < rows ? n0 + a.join_rows : rows;
     const int64_t base = (int64_t)work.first * R;
     for (int n = n0 + threadIdx.x / Q; n < end && threadIdx.x < Q * PASS; n += PASS) {
         float m = -__builtin_inff(), sum = 0.0f;
@@ -515,24 +528,28 @@ __global__ __launch_bounds__(256) void attention_join_rows(AttnArgs a) {
 }
 
 template <int NS, int R>
-void launch_join(const AttnArgs &a, hipStream_t stream) {
+void launch_join(AttnArgs a, hipStream_t stream) {
     const unsigned jobs = (unsigned)a.units * a.kv.heads;
-    constexpr int ROWS = R < kJoinRows ? R : kJoinRows;
     if constexpr (R <= 32) {
         if (a.splits > 8 && jobs * R <= 512) {
             hipLaunchKernelGGL((attention_join_parts<NS, R>), dim3(jobs * R), dim3(512), 0, stream, a);
             return;
         }
     }
-    hipLaunchKernelGGL((attention_join_rows<NS, R>), dim3(jobs * (R / ROWS)), dim3(256), 0, stream, a);
+    a.join_rows = R <= 32 ? R : jobs <= 32 ? 8 : 32;
+    hipLaunchKernelGGL((attention_join_rows<NS, R>), dim3(jobs * (R / a.join_rows)), dim3(256), 0,
+                       stream, a);
 }
 
 template <int NS, int NT>
 void launch_rows(const AttnArgs &a, bool bias, hipStream_t stream) {
-    if (bias)
-        hipLaunchKernelGGL((attention_kernel<NS, NT, true>), dim3(a.items), dim3(256), 0, stream, a);
+    const dim3 grid(a.items), block(256);
+    if (a.q_f32)   // (with the scores' general form: one kernel less)
+        hipLaunchKernelGGL((attention_kernel<NS, NT, true, true>), grid, block, 0, stream, a);
+    else if (bias)
+        hipLaunchKernelGGL((attention_kernel<NS, NT, true, false>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((attention_kernel<NS, NT, false>), dim3(a.items), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attention_kernel<NS, NT, false, false>), grid, block, 0, stream, a);
 }
 
 template <int NS>
@@ -579,14 +596,19 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
     if (p.rows <= 32) {   // dealt out over the batch (find_work)
         p.target = kFewRowsTarget;
         splits = kMaxSplits;
-    } else if (kv.batch == 1) {   // the longest of the jobs against their mean, if causal
-        p.target = 256;
-        const double mean = max_len > kv.M ? max_len - kv.M / 2 : max_len / 2 + 1;
-        splits = (int64_t)(p.target / (double)jobs * (max_len / mean) + 0.5);
     } else {
         p.target = 256;
         splits = (1024 + jobs - 1) / jobs;
-        if (splits > 8) splits = 8;
+        if (kv.batch == 1) {   // the longest of the jobs against their mean, if causal
+            const double mean = max_len > kv.M ? max_len - kv.M / 2 : max_len / 2 + 1;
+            splits = (int64_t)(p.target / (double)jobs * (max_len / mean) + 0.5);
+        }
+        // few jobs: the parts' time falls with their number and the join's grows, equal at
+        // some 2·√tiles (128 rows over 19500 tokens 66 us with 8 parts, 34 with 32; over
+        // 131000 tokens 130 with 32, 75 with 128)
+        int64_t most = 8;
+        while (most * jobs < 512 && most * most < 4 * tiles) ++most;
+        if (splits > most) splits = most;
     }
     // Parts of four tiles, one a wave, where the few jobs leave most of the chip idle (one
     // token over 4096, four heads: 10.0 us against 10.8 with eight); with more jobs they

@@ -16,6 +16,7 @@ struct AttnArgs {
     int splits, target;               // parts of the keys: at most, workgroups to fill
     int min_tiles;                    // of a part: fewer do not pay for the join
     int items;                        // workgroups of the kernel for few rows
+    int join_rows;                    // rows of a workgroup of the join
     const float *slopes;
     const int32_t *prefix;
     float *stats, *partial;           // workspace: [part][R][2] and [part][R][D], those of a

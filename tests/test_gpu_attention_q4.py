@@ -2,16 +2,20 @@
 the cache holds (exact, through the load).
 
 Tolerance, per output element; e = 2^-11 is f16's half step, u = 2^-24.
-  scores   k enters as f16(d·(q − 8)): e of each product; D products are summed in f32
-           (D·u of Σ|q·k|), and scaling, cap, bias and the exponent's argument round a few
-           times more: δ = scale·max_j Σ|q·k_j|·(e + (D + 16)·u) + 8u·max_j|s_j|, and the
-           hardware's exponential adds 2u: a weight and the sum of weights are each off
-           by at most e^(δ + 2u) − 1
+  scores   k enters exactly, as two f16 numbers (7 and 4 bits of the scale times the code);
+           f32 queries as two as well, of which the product of the low parts is left out
+           (2^-11 · 2^-7 of the product) and what is below 2^-24 (half a step, 2^-25·Σ|k|).
+           At most 3·D products are summed in f32 ((3D)·u of Σ|q·k|), and scaling, cap, bias
+           and the exponent's argument round a few times more; a cap of at most 128 adds
+           2^-21 of it (1/(1 + e^2u) is good to 2^-22 and counts twice the cap).
+           δ = scale·max_j Σ|q·k_j|·(2^-18 [f32] + (3D + 16)·u) + scale·2^-25·max_j Σ|k_j| [f32]
+             + 8u·(max_j|s_j| + cap), and the hardware's exponential adds 2u: a weight and the
+           sum of weights are each off by at most e^(δ + 2u) − 1
   output   weights and values enter as f16: 2e of Σ w|v|; the sums of L terms in f32, L·u;
            weights are held to 2^-32 of the largest (f16 at 2^7 and more for it): L·2^-32·max|v|
   rounding e of the value, 2^-25 below the smallest normal
 Together: S·(2·(e^(δ + 2u) − 1)·1.01 + 2e·1.01 + 2·L·u) + L·2^-32·max|v| + e·|y| + 2^-25, S =
-Σ w|v|.  (The cap's tanh is good to 3e-7 of its value and has slope at most 1.)"""
+Σ w|v|."""
 
 import numpy as np
 import pytest
@@ -43,7 +47,8 @@ def filled(D, Hkv, page, rows, lens, seed=0, ragged=True, stride=0, gain=1.0):
     return s
 
 
-def expect(s, q, H, b, positions, rows, scale, causal, window, cap, slopes, prefix, keys=None):
+def expect(s, q, H, b, positions, rows, scale, causal, window, cap, slopes, prefix, keys=None,
+           wide=False):
     """(y, tolerance) of sequence b's rows."""
     D = s.D
     at = slice(s.tok[b], s.tok[b + 1]) if keys is None else np.asarray(keys) + s.tok[b]
@@ -58,7 +63,9 @@ def expect(s, q, H, b, positions, rows, scale, causal, window, cap, slopes, pref
         for h in range(H):
             big = abs(scale) * (np.abs(qq[:, h]) @ np.abs(np.nan_to_num(k[:, h // G])).T).max(1)
             top = big + (abs(slopes[h]) * dist if slopes is not None else 0)
-            delta = big * (E + (D + 16) * U) + 8 * U * top + 2 * U
+            delta = big * ((3 * D + 16) * U + (2.0 ** -18 if wide else 0)) + 8 * U * (top + cap) + 2 * U
+            if wide:
+                delta = delta + abs(scale) * 2.0 ** -25 * np.abs(np.nan_to_num(k[:, h // G])).sum(1).max()
             w = 2 * np.expm1(delta) * 1.01 + 2 * E * 1.01 + 2 * L * U
             tol[:, h] = S[:, h] * w[:, None] + L * 2.0 ** -32 * np.abs(np.nan_to_num(v)).max()
     return y, tol + E * np.abs(y) + 2.0 ** -25
@@ -82,7 +89,7 @@ def check(s, H, xt="f16", seed=1, pad=0, lead=0, gain=1.0, causal=True, window=0
                         window=window, cap=cap, slopes=sl, prefix=pf, max_len=max_len,
                         out=out[:, :W])
     assert bool((out[:, W:] == 77).all())
-    qs = to_host(q.half()).astype(np.float64).reshape(s.M, H, s.D)
+    qs = to_host(q).astype(np.float64).reshape(s.M, H, s.D)
     got = to_host(y).astype(np.float64).reshape(s.M, H, s.D)
     sc = oa.default_scale(s.D) if scale is None else scale
     worst = 0.0
@@ -91,7 +98,8 @@ def check(s, H, xt="f16", seed=1, pad=0, lead=0, gain=1.0, causal=True, window=0
             continue
         rows = slice(s.cu_np[b], s.cu_np[b] + r)
         ref, tol = expect(s, qs, H, b, np.arange(n - r, n), rows, sc, causal, window, cap, slopes,
-                          0 if prefix is None else min(max(prefix[b], 0), n))
+                          0 if prefix is None else min(max(prefix[b], 0), n),
+                          wide=xt == "f32")
         ratio = np.abs(got[rows] - ref) / tol
         assert np.isfinite(got[rows]).all(), b
         worst = max(worst, float(ratio.max()))
