@@ -7,27 +7,33 @@
 // each of its waves (eight; four for heads of 256, which need the registers of two)
 // and goes through the keys 32 tokens at a time: each wave expands its share of the
 // tile's operands into LDS and reads all of them.
-//   Sᵀ[t, n] = K[t, :] · Q[n, :]    matrix instructions 32 x 32 x 16, keys as A
+//   Sᵀ[t, n] = K[t, :] · Q[n, :]    matrix instructions 32 x 32 x 16, keys as A, twice:
+//                                   both parts of the keys; f32 queries' low part a third
 //   Oᵀ[d, n] += Vᵀ[d, t] · Pᵀ[t, n]  values as A
 // Operands lie in LDS as the lanes hold them, 16 bytes per lane in lane order: no
 // bank conflicts on either side.  Row ρ = 8a + 4h + b of a key operand is token
 // 16·(a/2) + 8h + 4·(a%2) + b, which puts the eight tokens that a lane has to give
 // to the second product's step u into its own registers 8u .. 8u + 7.
 //
-// Matrix and vector instructions overlap within a wave: in one step the scores of
-// the next tile are multiplied while this tile's weights are computed, and this
-// tile's values while later operands are expanded (keys two tiles ahead, values
-// one).  The codes go to LDS as they lie, 16 bytes a lane (each wave loading its own
-// operands' codes is five loads of 2 to 16 bytes a lane instead of one), three tiles
-// ahead of their use and loaded two steps before.  One barrier per step.
+// In one step the scores of the next tile are multiplied while this tile's weights are
+// computed, and this tile's values while later operands are expanded (keys two tiles
+// ahead, values one).  The codes go to LDS as they lie, 16 bytes a lane (each wave
+// loading its own operands' codes is five loads of 2 to 16 bytes a lane instead of
+// one), three tiles ahead of their use and loaded two steps before.  One barrier per
+// step.
 //
 // What bounds it: with all compute units at work the clock falls to 2.0 to 2.2 GHz, and
-// a step of 256 rows by 32 tokens (D = 128) takes 2480 cycles, of which the matrix
-// instructions fill 1024: 0.86 PFLOP/s, where a large matrix product alone reaches 1.17.
-// Tried without gain: two tiles per barrier (the same 2480), waves of a SIMD half a
-// step apart by a second barrier (2900), 128 rows per workgroup and two workgroups per
-// unit (16512 tokens by 512 rows 261 us against 192), 64 rows per wave (operands in
-// accumulation registers have to be copied).
+// a step of 256 rows by 32 tokens (D = 128) takes some 2900 cycles, of which the matrix
+// instructions fill 1536 and the vector instructions of a SIMD's two waves 1450: they
+// overlap little, whatever their order.  Starting a workgroup takes 10000 cycles (three
+// loads one after the other: lengths, page numbers, tiles), ending it 3900.
+// Tried without gain, all with keys as one f16 (then 2480 cycles a step): two tiles per
+// barrier (the same), waves of a SIMD half a step apart by a second barrier (2900), 128
+// rows per workgroup and two workgroups per unit (512 rows over 16512 tokens 261 us
+// against 192), 64 rows per wave (operands in accumulation registers have to be copied).
+// The second part of the keys is 500 of the cycles: without it, 67 us for a 2048-token
+// prompt instead of 77, and an error against 64 bits of 2.2 times the output's rounding
+// instead of 1.4.
 #include "attention_device.h"
 
 namespace mq {
@@ -440,7 +446,11 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     // One step.  p: of tile t + 3, to LDS now; that of tile t + 5 is loaded.
     auto step = [&](auto parity, int t, u32x4 (&p)[PIECES]) MQ_INLINE {
         constexpr int BUF = decltype(parity)::value;
+        // the wave with more vector instructions before the other of its SIMD (88.7 -> 84.0
+        // us for a 2048-token prompt; the other way round 86.6)
+        __builtin_amdgcn_s_setprio(1);
         weigh(parity, t);
+        __builtin_amdgcn_s_setprio(0);
         if (edges & 1) mark_bad(BUF, t);
         Share kc, vc;
         read_key_codes(raw[raw2], kc);

@@ -6,21 +6,33 @@
 //   o   = Σ_j e^(s_j − m) v_j / Σ_j e^(s_j − m),  over the visible j, m their maximum
 // and zeros where none is visible.
 //
-// A workgroup takes R rows (row = token · group + head of the group, so that the
-// query heads of a key/value head share its tiles) of one key/value head and a
-// part of the keys; its four waves take the part's tiles of 32 tokens in turn and
-// their results are joined at the end.  Per tile, in one pass with the running
-// maximum and sum:
-//   Sᵀ[t, n] = K[t, :] · Q[n, :]    matrix instructions 16 x 16 x 32, keys as A
+// Few rows of a key/value head (up to 32, this file; more in attention_prompt.hip): the
+// time is that of reading the cache.  A workgroup takes R rows (16 or 32; row = token ·
+// group + head of the group, so that the query heads of a key/value head share its
+// tiles) of one key/value head and a part of the keys; its four waves take the part's
+// tiles of 32 tokens in turn, each loading one tile ahead, and their results are joined
+// at the end.  Per tile, in one pass with the running maximum and sum:
+//   Sᵀ[t, n] = K[t, :] · Q[n, :]    matrix instructions 16 x 16 x 32, keys as A, twice:
+//                                   both parts of the keys; f32 queries' low part a third
 //   Oᵀ[d, n] += Vᵀ[d, t] · Pᵀ[t, n]  values as A
 // A lane holds of Sᵀ exactly the eight tokens whose weights it has to give as the
 // second product's B operand, because row r of the first product's tile m is
 // token 8·(r/4) + 4·m + r%4: nothing moves between lanes but the maximum of a
 // column.  Codes become f16 in the registers that loaded them.
 //
-// Numerics: q, k and v in f16 (k and v each d·(q − 8) rounded once), products
-// summed in f32; the statistics in f32; a weight e^(s − m) is rounded to f16 as
-// the operand of the second product (attention_device.h has its range).
+// Numerics: the keys d·(q − 8) enter as two f16 numbers whose sum they are, f32 queries
+// likewise as two (the product of both low parts is left out: 2^-18); one f16 number
+// would leave a score of s off by 2^-12·s or so and its weight by as much, which is more
+// than the output's own rounding.  Products are summed in f32, statistics are f32.  The
+// second product's operands are f16: values d·(q − 8) and weights e^(s − m), each rounded
+// once (attention_device.h has the weights' range), errors of either sign that the sum
+// over the tokens averages.
+//
+// What bounds it, at one token of 32 heads (8 key/value heads, D = 128) over 131072
+// tokens, 151 MB: 33 us when the cache lies in the chip's last-level cache, of which the
+// vector instructions that expand the codes (some 350 a tile and wave) are 20, and 38
+// from memory (4.0 TB/s; a large copy 4.8); the join 5.  Short contexts: the chain of
+// loads (lengths, page numbers, tiles) and two launches, 10 us over 4096 tokens.
 #include "attention_device.h"
 
 namespace mq {
@@ -28,7 +40,10 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kMaxSplits = 256;
-constexpr int kFewRowsTarget = 768;   // workgroups: three on each unit
+// Workgroups that the keys are dealt to: the three that fit on each unit.  (One token over
+// 131072: 41.6 us with 512, 43 with 768, 46.5 with 1024; 64 sequences of up to 8000 52.6,
+// 51.2, 51.3.)
+constexpr int kFewRowsTarget = 768;
 
 // A tile as loaded: code dwords of the lane's operands and the scales they need.
 // Lane l is row r = l % 16 of the A operands and their inner octet g = l / 16.
@@ -597,6 +612,8 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
         p.target = kFewRowsTarget;
         splits = kMaxSplits;
     } else {
+        // one workgroup per unit (512 rows over 16512 tokens 229 us; 274 with 200, 331 with
+        // 300, 245 with 512)
         p.target = 256;
         splits = (1024 + jobs - 1) / jobs;
         if (kv.batch == 1) {   // the longest of the jobs against their mean, if causal
