@@ -23,17 +23,19 @@
 // step.
 //
 // What bounds it: with all compute units at work the clock falls to 2.0 to 2.2 GHz, and
-// a step of 256 rows by 32 tokens (D = 128) takes some 2900 cycles, of which the matrix
-// instructions fill 1536 and the vector instructions of a SIMD's two waves 1450: they
-// overlap little, whatever their order.  Starting a workgroup takes 10000 cycles (three
-// loads one after the other: lengths, page numbers, tiles), ending it 3900.
-// Tried without gain, all with keys as one f16 (then 2480 cycles a step): two tiles per
-// barrier (the same), waves of a SIMD half a step apart by a second barrier (2900), 128
-// rows per workgroup and two workgroups per unit (512 rows over 16512 tokens 261 us
-// against 192), 64 rows per wave (operands in accumulation registers have to be copied).
-// The second part of the keys is 500 of the cycles: without it, 67 us for a 2048-token
-// prompt instead of 77, and an error against 64 bits of 2.2 times the output's rounding
-// instead of 1.4.
+// a step of 256 rows by 32 tokens (D = 128) takes some 2800 cycles, 1.35 us, of which the
+// matrix instructions fill 1536.  The mix alone (24 of them, 24 LDS reads, 96 vector
+// instructions and 24 exponentials a wave and one barrier, without dependencies) takes
+// 1.05 us on the full chip and 0.86 on one unit: power and issue, not latency.  Starting a
+// workgroup takes 9000 cycles (three loads one after the other: lengths, page numbers,
+// tiles), ending it 3900.
+// Tried without gain: the values' products a step later, beside the maximum (the same);
+// with keys as one f16 (then 2480 cycles a step): two tiles per barrier (the same), waves
+// of a SIMD half a step apart by a second barrier (2900), 128 rows per workgroup and two
+// workgroups per unit (512 rows over 16512 tokens 261 us against 192), 64 rows per wave
+// (operands in accumulation registers have to be copied).
+// The second part of the keys costs 10 us of a 2048-token prompt's 75; with one f16 the
+// error against 64 bits is 2.2 times the output's rounding instead of 1.4.
 #include "attention_device.h"
 
 namespace mq {
@@ -121,43 +123,32 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     const float to_log2 = BIAS ? kLog2e : a.scale * kLog2e;
     const uint32_t mg = magic();
 
-    // The tiles in turn: [0, pre), then from lo on.  ahead_tile: the tile whose codes are
-    // loaded next, and where it lies; its page number has been asked for.
+    // The tiles in turn: [0, pre), then from lo on.  Where they lie is looked up 64 at a
+    // time, one a lane (a page walked in scalar instructions, one waiting for the other, was
+    // 500 cycles of a step): byte offsets, and a bit each for those masked in part or wholly
+    // and for holes among them (no such page, or behind the part).
     const int per_page = a.kv.page / kTile;
     const int32_t *const table = a.kv.table + view.b * a.kv.table_ld;
     const char *const first_tile = a.kv.cache + (int64_t)head * per_page * kv_tile_bytes(D);
-    int ahead_t, ahead_tile, page, off;   // off: tile within the page
-    int id;
     auto tile_of = [&](int t) { return t < view.pre ? t : t - view.pre + view.lo; };
-    auto go = [&](int t) {
-        ahead_t = t;
-        ahead_tile = tile_of(t);
-        page = ahead_tile / per_page;
-        off = ahead_tile - page * per_page;
+    int64_t place_at;
+    uint64_t hole_bits, edge_bits;
+    auto look_up = [&](int t0) {
+        const int t = t0 + lane, tile = tile_of(t);
+        const int page = (int)((unsigned)tile / (unsigned)per_page);
+        const int id = t < t_end ? table[page] : -1;
+        const bool hole = (unsigned)id >= (unsigned)a.kv.pages;
+        place_at = hole ? 0   // (the cache's first tile)
+                        : id * a.kv.page_bytes + (tile - page * per_page) * kv_tile_bytes(D);
+        hole_bits = __ballot(hole);
+        edge_bits = __ballot(hole || !all_visible(view, tile));
     };
-    auto ask = [&]() { id = ahead_t < t_end ? table[page] : -1; };
-    // Bits of the tiles in the pipeline, this one's first: no such page, or behind the
-    // part (all masked); masked in part or wholly.
-    uint32_t holes = 0, edges = 0;
-    auto place = [&](int tile, int p, int o, int bit) {   // (of the cache's first tile without)
-        const bool hole = (unsigned)p >= (unsigned)a.kv.pages;
-        const char *at = first_tile + (hole ? 0 : p) * a.kv.page_bytes + o * kv_tile_bytes(D);
-        holes |= (hole ? 1u : 0u) << bit;
-        edges |= (hole || !all_visible(view, tile) ? 1u : 0u) << bit;
-        return at;
+    auto place = [&](int k) {
+        return first_tile + ((int64_t)__builtin_amdgcn_readlane((int)(place_at >> 32), k) << 32 |
+                             (uint32_t)__builtin_amdgcn_readlane((int)place_at, k));
     };
-    auto place_next = [&](int bit) {
-        const char *at = place(ahead_tile, uniform(id), off, bit);
-        ++ahead_t;
-        ++ahead_tile;
-        if (++off == per_page) {
-            off = 0;
-            ++page;
-        }
-        if (ahead_t == view.pre) go(ahead_t);
-        ask();
-        return at;
-    };
+    // Bits of the tiles in the pipeline, this one's first.
+    uint32_t holes, edges;
 
     // Lane's token of a key operand: row r = 8·ra + 4·rh + rb.  K-step s takes octet 2s + h
     // of the token's elements, which lies in block s / 2.  Byte offsets within a tile:
@@ -247,12 +238,8 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     // K-step k of the first product, its operands one after the other.
     auto key_operand = [&](int buf, int i) { return load_operand(&ops[buf][i & 1][i / 2][lane]); };
 
-    // Fill the pipeline.  The page numbers of the first tiles are asked for at once,
-    // by as many lanes, then the queries.
-    const int front_t = t_begin + (lane & 7), front = tile_of(front_t);
-    const int front_page = (int)((unsigned)front / (unsigned)per_page);
-    const int front_off = front - front_page * per_page;
-    const int front_id = front_t < t_end ? table[front_page] : -1;
+    // Fill the pipeline.
+    look_up(t_begin);
     // Global memory is read and written along the rows, 16 bytes a lane: lanes of 32
     // different rows would cost a cycle each (a 256-row workgroup: 4 us of 2.5 + 8).
     u32x4 *const stage = lds + wave * 32 * kRowChunks;
@@ -273,19 +260,15 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         else
             q_in[k] = load_q8((const uint16_t *)a.q, q_at[k]);
     }
-    auto place_front = [&](int k) {
-        return place(__builtin_amdgcn_readlane(front, k), __builtin_amdgcn_readlane(front_id, k),
-                     __builtin_amdgcn_readlane(front_off, k), k);
-    };
     u32x4 pa[PIECES], pb[PIECES];   // the wave's share of two tiles on their way to LDS
     {
         u32x4 first[3][PIECES];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) load_piece(place_front(k), first[k]);
-        load_piece(place_front(3), pa);
-        load_piece(place_front(4), pb);
-        go(t_begin + 5);
-        ask();
+        for (int k = 0; k < 3; ++k) load_piece(place(k), first[k]);
+        load_piece(place(3), pa);
+        load_piece(place(4), pb);
+        holes = (uint32_t)hole_bits & 31;
+        edges = (uint32_t)edge_bits & 31;
 #pragma unroll
         for (int k = 0; k < 3; ++k) store_piece(first[k], raw[k]);
     }
@@ -446,21 +429,23 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     // One step.  p: of tile t + 3, to LDS now; that of tile t + 5 is loaded.
     auto step = [&](auto parity, int t, u32x4 (&p)[PIECES]) MQ_INLINE {
         constexpr int BUF = decltype(parity)::value;
+        Share kc, vc;
+        read_key_codes(raw[raw2], kc);
+        read_value_codes(raw[raw1], vc);
         // the wave with more vector instructions before the other of its SIMD (88.7 -> 84.0
         // us for a 2048-token prompt; the other way round 86.6)
         __builtin_amdgcn_s_setprio(1);
         weigh(parity, t);
         __builtin_amdgcn_s_setprio(0);
         if (edges & 1) mark_bad(BUF, t);
-        Share kc, vc;
-        read_key_codes(raw[raw2], kc);
-        read_value_codes(raw[raw1], vc);
         if (edges & 2) clean_values(vc, t + 1, holes & 2, BUF ^ 1);
         multiply(parity, kc, vc);
         store_piece(p, raw[raw3]);
-        holes >>= 1;
-        edges >>= 1;
-        load_piece(place_next(4), p);
+        const int k = (t + 5 - t_begin) & 63;
+        if (k == 0) look_up(t + 5);
+        load_piece(place(k), p);
+        holes = holes >> 1 | (uint32_t)(hole_bits >> k & 1) << 4;
+        edges = edges >> 1 | (uint32_t)(edge_bits >> k & 1) << 4;
         const int next = raw1;
         raw1 = raw2;
         raw2 = raw3;
