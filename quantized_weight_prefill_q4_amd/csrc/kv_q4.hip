@@ -8,12 +8,13 @@
 // NaN as its d.  The queries of the same rows are rotated by the same launch: a
 // single token's layer is launch-bound.
 //
-// A workgroup takes one head of eight consecutive positions [8u, 8u + 8) of one
-// sequence, the tokens that share the values' dwords: it alone writes them, so
-// neighbours' codes in a dword that a call fills in part are merged without
-// atomics.
+// A workgroup takes eight consecutive positions [8u, 8u + 8) of one sequence, the tokens
+// that share the values' dwords, of one head or a few: it alone writes them, so neighbours'
+// codes in a dword that a call fills in part are merged without atomics.
 //
-// Both directions move bytes.
+// Both directions move bytes: 1750 rows of f32 (32 query heads, 8 key/value heads of 128)
+// in 15 us, 4.3 TB/s.  Few rows wait for three loads and the f64 angles one after the
+// other, 5.8 us.
 #include "kv_q4.h"
 #include "rotary.h"
 
@@ -33,10 +34,7 @@ struct StoreArgs {
     int x_type, qo_type, n_rot, interleaved, q_heads, q_part, in_place;
     float mscale;
     unsigned per_seq;      // units of each sequence (equal rows)
-};
-
-struct Top {
-    float a, v;   // magnitude, signed value
+    int kv_part;           // key/value heads of a workgroup
 };
 
 // The eight elements [8·oct, + 8) of row x of a head, rotated.
@@ -101,9 +99,14 @@ __device__ __forceinline__ uint16_t quantize_q4(const float v[8], int q[8]) {
         for (int e = 0; e < 8; ++e) q[e] = 8;
         return 0x7E00;
     }
+    // x/d from the correctly rounded 1/d, one residual exact by fma: correctly rounded too
+    // (Markstein), in three instructions where a division is eleven.  (A quotient so small
+    // that the residual underflows gives 8 either way.)
+    const float inv = d == 0.0f ? 0.0f : 1.0f / d;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float t = d == 0.0f ? 8.0f : floorf(v[e] / d + 8.5f);
+        const float x = v[e] * inv;
+        const float t = floorf(__builtin_fmaf(__builtin_fmaf(-x, d, v[e]), inv, x) + 8.5f);
         q[e] = (int)fminf(fmaxf(t, 0.0f), 15.0f);
     }
     return d == 0.0f ? 0 : bits;
@@ -125,11 +128,11 @@ __global__ __launch_bounds__(kThreads) void kv_store_kernel(StoreArgs a) {
             cs[e][j] = rotation(a.pos ? a.pos[row0 + e] : p0 + e, a.freqs[j], a.mscale);
     }
     __syncthreads();
-    const int y = blockIdx.y;
-    if (y >= kv.heads) {   // queries
+    const int kv_blocks = (kv.heads + a.kv_part - 1) / a.kv_part;
+    if ((int)blockIdx.y >= kv_blocks) {   // queries
         const HeadItems h = head_items(D, a.freqs ? a.n_rot : 0, a.in_place);
         const int per_head = h.rot + h.copy;
-        const int h0 = (y - kv.heads) * a.q_part;
+        const int h0 = ((int)blockIdx.y - kv_blocks) * a.q_part;
         const int heads = a.q_heads - h0 < a.q_part ? a.q_heads - h0 : a.q_part;
         const int per_row = per_head * heads;
         for (int i = threadIdx.x; i < (e_hi - e_lo) * per_row; i += kThreads) {
@@ -142,43 +145,49 @@ __global__ __launch_bounds__(kThreads) void kv_store_kernel(StoreArgs a) {
         return;
     }
     const int hi = o.keys - p0 < e_hi ? o.keys - p0 : e_hi;   // beyond the table: no place
-    char *tile = p0 < o.keys ? kv_tile(kv, o.b, y, p0 / kTile) : nullptr;
+    char *tile = p0 < o.keys ? kv_tile(kv, o.b, 0, p0 / kTile) : nullptr;
     if (!tile) return;
     const int t0 = p0 & (kTile - 1);
-    for (int i = threadIdx.x; i < 16 * octs; i += kThreads) {
-        const bool value = i >= 8 * octs;
-        const int k = value ? i - 8 * octs : i;
-        const int e = k / octs, oct = k - e * octs;
-        if (e < e_lo || e >= hi) continue;   // the block's four threads together
-        const int64_t row = row0 + e;
-        float x[8];
-        if (value)
-            load_eight(a.v, a.x_type, row * a.ldv + (int64_t)y * D + 8 * oct, x);
-        else
-            load_rotated(a, a.k, row * a.ldk + (int64_t)y * D, oct, cs[e], x);
-        int q[8];
-        const uint16_t d = quantize_q4(x, q);
-        if (value) {
+    const int y0 = blockIdx.y * a.kv_part, y1 = y0 + a.kv_part < kv.heads ? y0 + a.kv_part : kv.heads;
+    const int64_t head_bytes = (int64_t)(kv.page / kTile) * kv_tile_bytes(D);
+    tile += y0 * head_bytes;
+    for (int y = y0; y < y1; ++y, tile += head_bytes) {
+        if (y > y0) __syncthreads();   // codes are read
+        for (int i = threadIdx.x; i < 16 * octs; i += kThreads) {
+            const bool value = i >= 8 * octs;
+            const int k = value ? i - 8 * octs : i;
+            const int e = k / octs, oct = k - e * octs;
+            if (e < e_lo || e >= hi) continue;   // the block's four threads together
+            const int64_t row = row0 + e;
+            float x[8];
+            if (value)
+                load_eight(a.v, a.x_type, row * a.ldv + (int64_t)y * D + 8 * oct, x);
+            else
+                load_rotated(a, a.k, row * a.ldk + (int64_t)y * D, oct, cs[e], x);
+            int q[8];
+            const uint16_t d = quantize_q4(x, q);
+            if (value) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) codes[e][8 * oct + j] = (uint8_t)q[j];
-            if ((oct & 3) == 0)
-                ((uint16_t *)(tile + kv_vscale_at(D)))[((t0 >> 3) * NS + (oct >> 2)) * 8 + e] = d;
-        } else {
-            uint32_t w = 0;
+                for (int j = 0; j < 8; ++j) codes[e][8 * oct + j] = (uint8_t)q[j];
+                if ((oct & 3) == 0)
+                    ((uint16_t *)(tile + kv_vscale_at(D)))[((t0 >> 3) * NS + (oct >> 2)) * 8 + e] = d;
+            } else {
+                uint32_t w = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w |= (uint32_t)q[j] << kv_shift(j);
-            ((uint32_t *)tile)[kv_key_dword(t0 + e, oct, NS)] = w;
-            if ((oct & 3) == 0)
-                ((uint16_t *)(tile + kv_kscale_at(D)))[kv_key_place(t0 + e) * NS + (oct >> 2)] = d;
+                for (int j = 0; j < 8; ++j) w |= (uint32_t)q[j] << kv_shift(j);
+                ((uint32_t *)tile)[kv_key_dword(t0 + e, oct, NS)] = w;
+                if ((oct & 3) == 0)
+                    ((uint16_t *)(tile + kv_kscale_at(D)))[kv_key_place(t0 + e) * NS + (oct >> 2)] = d;
+            }
         }
-    }
-    __syncthreads();
-    uint32_t *vc = (uint32_t *)(tile + kv_vcode_at(D)) + (t0 >> 3) * D;
-    for (int d = threadIdx.x; d < D; d += kThreads) {
-        uint32_t w = e_lo == 0 && hi == 8 ? 0 : vc[d];
-        for (int e = e_lo; e < hi; ++e)
-            w = (w & ~(15u << kv_shift(e))) | ((uint32_t)codes[e][d] << kv_shift(e));
-        vc[d] = w;
+        __syncthreads();
+        uint32_t *vc = (uint32_t *)(tile + kv_vcode_at(D)) + (t0 >> 3) * D;
+        for (int d = threadIdx.x; d < D; d += kThreads) {
+            uint32_t w = e_lo == 0 && hi == 8 ? 0 : vc[d];
+            for (int e = e_lo; e < hi; ++e)
+                w = (w & ~(15u << kv_shift(e))) | ((uint32_t)codes[e][d] << kv_shift(e));
+            vc[d] = w;
+        }
     }
 }
 
@@ -255,7 +264,13 @@ hipError_t launch_kv_store(const KvSpec &kv, const StoreSpec &s, hipStream_t str
     // query heads of a workgroup: enough work for its threads
     a.q_part = 8;
     const int q_blocks = (a.q_heads + a.q_part - 1) / a.q_part;
-    const dim3 grid((unsigned)total_units(kv), (unsigned)(kv.heads + q_blocks));
+    // key/value heads of a workgroup: the look-up and the angles are then made once for
+    // them (1750 rows of 8 heads, keys, values and queries and the load behind: 23.6 us with
+    // one, 21.0 with two, 22.7 with four; 131072 rows 352, 287, 258 without queries)
+    const int64_t work = total_units(kv) * kv.heads;
+    a.kv_part = work < 1500 ? 1 : work < 4096 ? 2 : 4;
+    const int kv_blocks = (kv.heads + a.kv_part - 1) / a.kv_part;
+    const dim3 grid((unsigned)total_units(kv), (unsigned)(kv_blocks + q_blocks));
     hipLaunchKernelGGL(kv_store_kernel, grid, dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }

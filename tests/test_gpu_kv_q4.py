@@ -142,6 +142,33 @@ def test_one_row_each_and_equal_rows():
     _check(128, 8, 256, [700], [1500], "f16", ragged=False, freqs=f, H=8)
 
 
+def test_prompts_whose_workgroups_take_several_heads():
+    f = mq.rope_freqs(64, device=dev())
+    _check(64, 5, 64, [2700], [2750], "f32", ragged=False, freqs=f, H=5)      # two heads each
+    _check(64, 5, 64, [4000, 3001], [4000, 3100], "f16", freqs=f, H=5)        # four and one
+    _check(128, 8, 128, [2100, 3100], [2111, 3100], "f32")
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(4)
+    rows = [int(r) for r in rng.integers(0, 4, 200)]
+    _check(64, 2, 32, rows, [r + int(p) for r, p in zip(rows, rng.integers(0, 70, 200))], "f16")
+
+
+def test_codes_of_all_magnitudes():
+    """The quotient x/d is the correctly rounded one: blocks from 10^-9 to 10^4."""
+    announce("kv_store_q4 magnitudes")
+    s = Batch(128, 8, 64, [2048], [2048], 5, ragged=False)
+    size = 10.0 ** (torch.rand(2048, 8 * 128 // 32, device=dev(), dtype=torch.float64) * 13 - 9)
+    size = size.float().repeat_interleave(32, dim=1)
+    k, v = (rows_of(2048, 8 * 128, torch.float32, i) * size for i in (1, 2))
+    v = torch.where(torch.rand(v.shape, device=dev()) < 0.1, v * 1e-30, v)   # and tiny ones in them
+    mq.kv_store_q4(k, v, s.cache, s.table, s.lens_t)
+    want = oa.quantize_q4(to_host(k).reshape(-1, 8, 128)) + oa.quantize_q4(to_host(v).reshape(-1, 8, 128))
+    for g, w in zip(s.tokens()[0], want):
+        assert np.array_equal(g, w, equal_nan=g.dtype.kind == "f")
+
+
 def test_positions_of_their_own():
     f = mq.rope_freqs(96, device=dev())
     pos = ints([5, 900000, -3, 17, 2, 1])
