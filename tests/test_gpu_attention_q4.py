@@ -135,6 +135,37 @@ def test_long_sequences_in_parts(length):
     check(s, 8, xt="f32")
 
 
+def test_many_and_unequal_sequences():
+    """More sequences than lanes of a wave, empty ones among them, and one much longer than
+    the others: the keys are dealt out over the batch."""
+    rng = np.random.default_rng(3)
+    rows = [int(r) for r in rng.integers(0, 4, 150)]
+    lens = [r + int(p) for r, p in zip(rows, rng.integers(0, 400, 150))]
+    s = filled(64, 1, 32, rows, lens, seed=21)
+    check(s, 5)
+    check(s, 5, xt="f32", window=100, max_len=100)
+    lens = [int(n) for n in rng.integers(1, 90, 70)]
+    s = filled(64, 2, 32, [1] * 70, lens, seed=22, ragged=False)
+    check(s, 4, max_len=1 << 20)
+    for at in (0, 30, 66):
+        lens[at] = 9000
+        s = filled(64, 1, 64, [1] * 67, lens[:67], seed=23 + at, ragged=False)
+        check(s, 4)
+        lens[at] = 50
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_many_rows_in_parts(D):
+    s = filled(D, 1, 64, [70], [1700], seed=31 + D, ragged=False)
+    check(s, 4)
+    check(s, 4, xt="f32", causal=False, max_len=100)
+    s = filled(D, 2, 32, [100, 3, 40], [2100, 3, 900], seed=32 + D)
+    check(s, 6)
+    check(s, 6, xt="f32", cap=20.0, window=700)
+    s = filled(D, 1, 32, [8], [6000], seed=33 + D, ragged=False)     # few jobs, many parts
+    check(s, 16)
+
+
 @pytest.mark.parametrize("D,rows,lens", [(128, [1, 1, 1], [300, 40, 1]), (96, [40, 7], [333, 7]),
                                          (256, [20, 3], [150, 90]), (64, [200], [200])])
 @pytest.mark.parametrize("kw", [
