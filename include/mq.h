@@ -543,7 +543,8 @@ int mq_kv_load_q4(const mq_kv_q4 *cache, int y_type, void *K, int ldk, void *V, 
  *   Q      : device, x_type, row stride ldq >= q_heads · head_dim; M · (q_heads / heads)
  *            at most 2^30.
  *   Y      : device f16, row stride ldy likewise.  Q and Y are aligned to their element.
- *   scale  : finite.  cap : finite, >= 0.  window : >= 0.
+ *   scale  : finite; scores are expected below 2^24 in magnitude, where f32 has their
+ *            units.  cap : finite, >= 0.  window : >= 0.
  *   slopes : device f32, q_heads values, or NULL.
  *   prefix : device int32, batch values, or NULL.
  *   max_len: a bound of lens, for the launch plan alone (results do not depend on its

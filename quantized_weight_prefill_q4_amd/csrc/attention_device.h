@@ -38,11 +38,12 @@ constexpr float kQuickCap = 128.0f;
 template <int N, class At>
 __device__ __forceinline__ void bias_scores(const AttnArgs &a, float (&s)[N], float slope, int to,
                                             At at) {
-    if (a.cap > kQuickCap) {
+    const float k = a.scale * a.inv_cap * (2.0f * kLog2e);
+    if (a.cap > kQuickCap || (a.cap > 0.0f && !(fabsf(k) < 1e30f))) {
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] = a.cap * tanh_f32(s[i] * a.scale * a.inv_cap);
     } else if (a.cap > 0.0f) {
-        const float k = a.scale * a.inv_cap * (2.0f * kLog2e), c2 = -2.0f * a.cap;
+        const float c2 = -2.0f * a.cap;
 #pragma unroll
         for (int i = 0; i < N; ++i)
             s[i] = __builtin_fmaf(

@@ -125,11 +125,11 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
 
     // The tiles in turn: [0, pre), then from lo on.  Where they lie is looked up 64 at a
     // time, one a lane (a page walked in scalar instructions, one waiting for the other, was
-    // 500 cycles of a step): byte offsets, and a bit each for those masked in part or wholly
+    // 500 cycles of a step): byte offsets (the cache's
+    // first tile where there is none), and a bit each for those masked in part or wholly
     // and for holes among them (no such page, or behind the part).
     const int per_page = a.kv.page / kTile;
     const int32_t *const table = a.kv.table + view.b * a.kv.table_ld;
-    const char *const first_tile = a.kv.cache + (int64_t)head * per_page * kv_tile_bytes(D);
     auto tile_of = [&](int t) { return t < view.pre ? t : t - view.pre + view.lo; };
     int64_t place_at;
     uint64_t hole_bits, edge_bits;
@@ -138,13 +138,12 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         const int page = (int)((unsigned)tile / (unsigned)per_page);
         const int id = t < t_end ? table[page] : -1;
         const bool hole = (unsigned)id >= (unsigned)a.kv.pages;
-        place_at = hole ? 0   // (the cache's first tile)
-                        : id * a.kv.page_bytes + (tile - page * per_page) * kv_tile_bytes(D);
+        place_at = hole ? 0 : kv_tile_at(a.kv, head, id, tile - page * per_page);
         hole_bits = __ballot(hole);
         edge_bits = __ballot(hole || !all_visible(view, tile));
     };
     auto place = [&](int k) {
-        return first_tile + ((int64_t)__builtin_amdgcn_readlane((int)(place_at >> 32), k) << 32 |
+        return a.kv.cache + ((int64_t)__builtin_amdgcn_readlane((int)(place_at >> 32), k) << 32 |
                              (uint32_t)__builtin_amdgcn_readlane((int)place_at, k));
     };
     // Bits of the tiles in the pipeline, this one's first.

@@ -174,7 +174,6 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
 
     auto tile_of = [&](int t) { return t < view.pre ? t : t - view.pre + view.lo; };
     const int per_page = a.kv.page / kTile;
-    const char *const first_tile = a.kv.cache + (int64_t)head * per_page * kv_tile_bytes(D);
     // The work on one tile; hole: there is no such page, its tokens are not visible.
     auto use_tile = [&](Tile<NS> &now, const char *p, int t, bool hole) MQ_INLINE {
         const int tile = tile_of(t), j0 = tile * kTile;
@@ -294,13 +293,13 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
             const int page = (int)((unsigned)tile / (unsigned)per_page);
             const int id = a.kv.table[view.b * a.kv.table_ld + page];
             if ((unsigned)id < (unsigned)a.kv.pages)
-                at = id * a.kv.page_bytes + (tile - page * per_page) * kv_tile_bytes(D);
+                at = kv_tile_at(a.kv, head, id, tile - page * per_page);
         }
         auto place = [&](int k, bool &hole) {   // (of the cache's first tile without)
             const int64_t x = (int64_t)__builtin_amdgcn_readlane((int)(at >> 32), k) << 32 |
                               (uint32_t)__builtin_amdgcn_readlane((int)at, k);
             hole = x < 0;
-            return first_tile + (hole ? 0 : x);
+            return (const char *)a.kv.cache + (hole ? 0 : x);
         };
         const int left = (t_end - t0 + kWaves - 1) / kWaves, n = left < 64 ? left : 64;
         bool hole;
@@ -652,7 +651,8 @@ hipError_t launch_attention(const KvSpec &kv, const AttnSpec &s, const AttnPlan 
     a.ldy = s.ldy;
     a.scale = s.scale;
     a.cap = s.cap;
-    a.inv_cap = s.cap > 0.0f ? 1.0f / s.cap : 0.0f;
+    // (a cap below 1e-30 is as good as 0: finite all the same)
+    a.inv_cap = s.cap > 1e-30f ? 1.0f / s.cap : s.cap > 0.0f ? 1e30f : 0.0f;
     a.q_f32 = s.x_type == kTypeF32;
     a.q_heads = s.q_heads;
     a.group = s.q_heads / kv.heads;

@@ -136,14 +136,18 @@ inline int64_t total_units(const KvSpec &kv) {
     return kv.cu ? (int64_t)kv.M / 8 + 2 * (int64_t)kv.batch : (int64_t)units_per_seq(kv) * kv.batch;
 }
 
+// Bytes from the cache's start to a tile: number `off` of a page's.
+MQ_INDEX int64_t kv_tile_at(const KvSpec &kv, int head, int page, int off) {
+    return page * kv.page_bytes +
+           ((int64_t)head * (kv.page / kTile) + off) * kv_tile_bytes(kv.D);
+}
 // The tile of tokens [32·tile, + 32) of sequence b's head, or null where the
 // table names no page of the cache.
 MQ_INDEX char *kv_tile(const KvSpec &kv, int b, int head, int tile) {
     const int per = kv.page / kTile, p = tile / per;
     const int id = kv.table[b * kv.table_ld + p];
     if ((unsigned)id >= (unsigned)kv.pages) return nullptr;
-    return kv.cache + id * kv.page_bytes +
-           ((int64_t)head * per + (tile - p * per)) * kv_tile_bytes(kv.D);
+    return kv.cache + kv_tile_at(kv, head, id, tile - p * per);
 }
 
 }  // namespace

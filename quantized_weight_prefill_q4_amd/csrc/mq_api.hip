@@ -416,10 +416,7 @@ int check_attention(const mq::KvSpec &kv, int q_heads, int64_t max_len) {
     if ((int64_t)kv.M * (q_heads / kv.heads) > (1 << 30)) return MQ_ERR_SHAPE;
     return MQ_OK;
 }
-bool plan_ok(const mq::KvSpec &kv, const mq::AttnPlan &p) {
-    const int64_t jobs = p.row_tiles * kv.heads;
-    return p.items <= kMaxBlocks / 2 && (p.splits == 1 || jobs * p.rows <= kMaxBlocks / 2);
-}
+bool plan_ok(const mq::AttnPlan &p) { return p.items <= kMaxBlocks / 2; }
 
 }  // namespace
 
@@ -776,7 +773,7 @@ int64_t mq_attention_q4_workspace_bytes(const mq_kv_q4 *cache, int q_heads, int 
     s.q_heads = q_heads;
     s.max_len = max_len;
     const mq::AttnPlan p = mq::plan_attention(kv, s);
-    return plan_ok(kv, p) ? p.ws_bytes : MQ_ERR_SHAPE;
+    return plan_ok(p) ? p.ws_bytes : MQ_ERR_SHAPE;
 }
 
 int mq_attention_q4(const mq_kv_q4 *cache, int x_type, const void *Q, int ldq, int q_heads,
@@ -798,7 +795,7 @@ int mq_attention_q4(const mq_kv_q4 *cache, int x_type, const void *Q, int ldq, i
     const mq::AttnSpec s{Q,   Y,   ldq,         ldy,    x_type, q_heads, scale,
                          cap, causal != 0, window, slopes, prefix,  max_len};
     const mq::AttnPlan p = mq::plan_attention(kv, s);
-    if (!plan_ok(kv, p)) return MQ_ERR_SHAPE;
+    if (!plan_ok(p)) return MQ_ERR_SHAPE;
     if (p.ws_bytes > 0 && (!ws || !aligned16(ws) || ws_bytes < (size_t)p.ws_bytes))
         return MQ_ERR_WORKSPACE;
     const Span q = span(Q, ldq, width, type_bytes(x_type), M);

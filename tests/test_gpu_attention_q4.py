@@ -66,7 +66,7 @@ def expect(s, q, H, b, positions, rows, scale, causal, window, cap, slopes, pref
             delta = big * ((3 * D + 16) * U + (2.0 ** -18 if wide else 0)) + 8 * U * (top + cap) + 2 * U
             if wide:
                 delta = delta + abs(scale) * 2.0 ** -25 * np.abs(np.nan_to_num(k[:, h // G])).sum(1).max()
-            w = 2 * np.expm1(delta) * 1.01 + 2 * E * 1.01 + 2 * L * U
+            w = 2 * np.expm1(np.minimum(delta, 50)) * 1.01 + 2 * E * 1.01 + 2 * L * U
             tol[:, h] = S[:, h] * w[:, None] + L * 2.0 ** -32 * np.abs(np.nan_to_num(v)).max()
     return y, tol + E * np.abs(y) + 2.0 ** -25
 
@@ -125,6 +125,15 @@ def test_several_rows(D, rows):
     check(s, 14, xt="f32", causal=False)
 
 
+def test_one_sequence_of_many_rows_among_single_tokens():
+    """The kernel for few rows on a sequence of many: its row tiles share their parts."""
+    s = filled(128, 2, 32, [150] + [1] * 30, [700] + [40 + b for b in range(30)], seed=41)
+    check(s, 8)
+    check(s, 8, xt="f32", window=60)
+    s = filled(64, 1, 64, [1, 90, 2, 1, 0, 1], [3, 3000, 200, 1, 7, 64], seed=42)
+    check(s, 1, prefix=[130] * 6)
+
+
 @pytest.mark.parametrize("length", [2000, 5003, 20000])
 def test_long_sequences_in_parts(length):
     s = filled(128, 2, 256, [1], [length], seed=length % 97, ragged=False)
@@ -170,7 +179,7 @@ def test_many_rows_in_parts(D):
                                          (256, [20, 3], [150, 90]), (64, [200], [200])])
 @pytest.mark.parametrize("kw", [
     dict(window=1), dict(window=33), dict(window=128, causal=False), dict(window=2, causal=False),
-    dict(cap=5.0), dict(cap=1000.0, gain=4.0), dict(slopes=True), dict(slopes=True, causal=False),
+    dict(cap=5.0), dict(cap=1000.0, gain=4.0), dict(cap=1e-39), dict(cap=1.0, scale=1e36), dict(slopes=True), dict(slopes=True, causal=False),
     dict(prefix=20), dict(prefix=20, window=16), dict(prefix=10000), dict(prefix=-4),
     dict(causal=False), dict(scale=0.0), dict(scale=-0.3),
     dict(window=40, cap=3.0, slopes=True, prefix=37)])

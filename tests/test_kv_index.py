@@ -210,6 +210,15 @@ int main() {
                     return rc;
         }
     }
+    {   // a page of more than 2^31 bytes
+        const int seed = 0;
+        KvSpec kv{};
+        kv.page = 1 << 29;
+        kv.heads = 2;
+        kv.D = 256;
+        kv.page_bytes = (int64_t)2 * (kv.page / 32) * 36 * 256;
+        CHECK(kv_tile_at(kv, 1, 3, (1 << 24) - 1) == 4 * kv.page_bytes - 36 * 256);
+    }
     // the byte layout: every nibble and scale of a tile has one place
     for (int D : {64, 96, 128, 256}) {
         const int seed = D, NS = D / 32;
