@@ -537,8 +537,8 @@ int mq_kv_load_q4(const mq_kv_q4 *cache, int y_type, void *K, int ldk, void *V, 
  * every j < prefix[b].  A row that sees nothing gives zeros.
  * Scores are exact but for f32 sums (f32 queries: 2^-18 of each product; a query beyond
  * 65504 makes its row not finite); statistics are f32.  In the second product the values
- * d·(q − 8) and the weights e^(s − max) are rounded to f16 each (2^-12 of the weight down
- * to 2^-21 of the largest, 2^-32 of that below) and y once to f16.  A token whose d is infinite or NaN makes the rows that see
+ * d·(q − 8) are rounded once to f16 and the weights e^(s − max) to 22 bits (2^-32 of the
+ * largest where that is more), and y once to f16.  A token whose d is infinite or NaN makes the rows that see
  * it not finite, and no others.
  *   Q      : device, x_type, row stride ldq >= q_heads · head_dim; M · (q_heads / heads)
  *            at most 2^30.

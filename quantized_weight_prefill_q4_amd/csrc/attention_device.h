@@ -13,8 +13,9 @@ constexpr float kLog2e = 1.44269502f;
 
 // A row's weights are e^(s − m) with m a maximum that follows the scores only when
 // they exceed it by kSlack (in powers of two): the sums are rescaled rarely.  The f16
-// weights are held times 2^kShift, at most 2^15; the largest of a row is 2^7 at
-// least, so those down to 2^-21 of it keep 11 bits and 2^-32 of it is the step below.
+// parts of a weight are held times 2^kShift, at most 2^15; the largest of a row is 2^7 at
+// least, so those down to 2^-21 of it keep the first part's 11 bits, and 2^-31 of it is the
+// step of either part.
 constexpr float kShift = 7.0f, kSlack = 8.0f;
 
 // tanh u = 1 − 2 / (1 + e^2u), and below 1/4, where that cancels,
@@ -283,16 +284,13 @@ __device__ __forceinline__ void split_scales(uint32_t d, half2v &high, half2v &l
     low = as_half2(d) - high;
 }
 
-// A pair of f16 weights added to a sum: what is summed is what is multiplied.
-__device__ __forceinline__ float sum_pair(uint32_t w, float sum) {
-    const half2v one = {(_Float16)1.0f, (_Float16)1.0f};
-    return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, w), one, sum, false);
-}
-
-// Two weights as f16.
-__device__ __forceinline__ uint32_t pack_weights(float a, float b) {
-    const half2v v = {(_Float16)a, (_Float16)b};
-    return __builtin_bit_cast(uint32_t, v);
+// Two weights as f16, and what that rounding left of them as f16 (exact differences).
+__device__ __forceinline__ void pack_weights(float a, float b, uint32_t &high, uint32_t &low) {
+    const half2v h = {(_Float16)a, (_Float16)b};
+    const half2v l = {(_Float16)__builtin_fmaf((float)h.x, -1.0f, a),
+                      (_Float16)__builtin_fmaf((float)h.y, -1.0f, b)};
+    high = __builtin_bit_cast(uint32_t, h);
+    low = __builtin_bit_cast(uint32_t, l);
 }
 
 }  // namespace

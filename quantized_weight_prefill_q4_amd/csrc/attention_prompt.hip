@@ -9,7 +9,7 @@
 // tile's operands into LDS and reads all of them.
 //   Sᵀ[t, n] = K[t, :] · Q[n, :]    matrix instructions 32 x 32 x 16, keys as A, twice:
 //                                   both parts of the keys; f32 queries' low part a third
-//   Oᵀ[d, n] += Vᵀ[d, t] · Pᵀ[t, n]  values as A
+//   Oᵀ[d, n] += Vᵀ[d, t] · Pᵀ[t, n]  values as A, twice: both parts of the weights
 // Operands lie in LDS as the lanes hold them, 16 bytes per lane in lane order: no
 // bank conflicts on either side.  Row ρ = 8a + 4h + b of a key operand is token
 // 16·(a/2) + 8h + 4·(a%2) + b, which puts the eight tokens that a lane has to give
@@ -22,20 +22,20 @@
 // one), three tiles ahead of their use and loaded two steps before.  One barrier per
 // step.
 //
-// What bounds it: with all compute units at work the clock falls to 2.0 to 2.2 GHz, and
-// a step of 256 rows by 32 tokens (D = 128) takes some 2800 cycles, 1.35 us, of which the
-// matrix instructions fill 1536.  The mix alone (24 of them, 24 LDS reads, 96 vector
-// instructions and 24 exponentials a wave and one barrier, without dependencies) takes
-// 1.05 us on the full chip and 0.86 on one unit: power and issue, not latency.  Starting a
-// workgroup takes 9000 cycles (three loads one after the other: lengths, page numbers,
+// What bounds it: the matrix instructions.  A step of 256 rows by 32 tokens (D = 128) takes
+// 3270 cycles, at the 2.0 to 2.1 GHz that the power limit leaves with all compute units at
+// work, and they fill 2048; over long contexts (512 rows over 16512 tokens, 266 us without a
+// cap) they run at 1.06 PFLOP/s, where a large matrix product alone reaches 1.17.  Starting
+// a workgroup takes 9000 cycles (three loads one after the other: lengths, page numbers,
 // tiles), ending it 3900.
-// Tried without gain: the values' products a step later, beside the maximum (the same);
-// with keys as one f16 (then 2480 cycles a step): two tiles per barrier (the same), waves
-// of a SIMD half a step apart by a second barrier (2900), 128 rows per workgroup and two
-// workgroups per unit (512 rows over 16512 tokens 261 us against 192), 64 rows per wave
-// (operands in accumulation registers have to be copied).
-// The second part of the keys costs 10 us of a 2048-token prompt's 75; with one f16 the
-// error against 64 bits is 2.2 times the output's rounding instead of 1.4.
+// What the parts cost there: keys and weights as one f16 each 188 us, keys as two 225, both
+// 266; the error against 64 bits, in units of the output's own rounding, is 2.4, 1.5 and
+// 1.25.
+// Tried without gain: the values' products a step later, beside the maximum (within 3%
+// either way); with one f16 each (then 2480 cycles a step): two tiles per barrier (the
+// same), waves of a SIMD half a step apart by a second barrier (2900), 128 rows per
+// workgroup and two workgroups per unit (261 us against 192), 64 rows per wave (operands in
+// accumulation registers have to be copied).
 #include "attention_device.h"
 
 namespace mq {
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
     }
     __syncthreads();
     constexpr int kAhead = 4;   // operands are read as far ahead of their use
-    uint32_t w[8];   // a tile's weights by pairs
+    uint32_t w[8], w_low[8];   // a tile's weights by pairs
     // The elements of s that the lane's row sees, a bit each, in a tile masked in part.
     auto seen_bits = [&](int t) {
         const uint32_t seen =
@@ -392,9 +392,9 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
                         __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * x], to_log2, -base));
                     const float e1 =
                         __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * x + 1], to_log2, -base));
-                    w[x] = pack_weights(e0, e1);
-                    asm volatile("" : "+v"(w[x]));   // here, not where it is used
-                    l = sum_pair(w[x], l);
+                    l += e0 + e1;
+                    pack_weights(e0, e1, w[x], w_low[x]);
+                    asm volatile("" : "+v"(w[x]), "+v"(w_low[x]));   // here, not where they are used
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -411,9 +411,12 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         for (int k = 0; k < KS; ++k) {   // operand [half][element tile]
             const int u = k / NS, i = k % NS;
             const u32x4 x = {w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]};
+            const u32x4 y = {w_low[4 * u], w_low[4 * u + 1], w_low[4 * u + 2], w_low[4 * u + 3]};
             o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vop[k], __builtin_bit_cast(half8, x), o[i],
                                                           0, 0, 0);
             if (k + kAhead < KS) vop[k + kAhead] = load_operand(&ops[BUF][2][k + kAhead][lane]);
+            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vop[k], __builtin_bit_cast(half8, y), o[i],
+                                                          0, 0, 0);
 #pragma unroll
             for (int z = 0; z < 2 * PW; ++z)
                 if (z * KS / (2 * PW) == k) {
@@ -431,8 +434,8 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
         Share kc, vc;
         read_key_codes(raw[raw2], kc);
         read_value_codes(raw[raw1], vc);
-        // the wave with more vector instructions before the other of its SIMD (88.7 -> 84.0
-        // us for a 2048-token prompt; the other way round 86.6)
+        // the wave with more vector instructions before the other of its SIMD (101 -> 96 us
+        // for a 2048-token prompt)
         __builtin_amdgcn_s_setprio(1);
         weigh(parity, t);
         __builtin_amdgcn_s_setprio(0);

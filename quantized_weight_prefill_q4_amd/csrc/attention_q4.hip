@@ -14,24 +14,23 @@
 // at the end.  Per tile, in one pass with the running maximum and sum:
 //   Sᵀ[t, n] = K[t, :] · Q[n, :]    matrix instructions 16 x 16 x 32, keys as A, twice:
 //                                   both parts of the keys; f32 queries' low part a third
-//   Oᵀ[d, n] += Vᵀ[d, t] · Pᵀ[t, n]  values as A
+//   Oᵀ[d, n] += Vᵀ[d, t] · Pᵀ[t, n]  values as A, twice: both parts of the weights
 // A lane holds of Sᵀ exactly the eight tokens whose weights it has to give as the
 // second product's B operand, because row r of the first product's tile m is
 // token 8·(r/4) + 4·m + r%4: nothing moves between lanes but the maximum of a
 // column.  Codes become f16 in the registers that loaded them.
 //
-// Numerics: the keys d·(q − 8) enter as two f16 numbers whose sum they are, f32 queries
-// likewise as two (the product of both low parts is left out: 2^-18); one f16 number
-// would leave a score of s off by 2^-12·s or so and its weight by as much, which is more
-// than the output's own rounding.  Products are summed in f32, statistics are f32.  The
-// second product's operands are f16: values d·(q − 8) and weights e^(s − m), each rounded
-// once (attention_device.h has the weights' range), errors of either sign that the sum
-// over the tokens averages.
+// Numerics: the keys d·(q − 8) enter as two f16 numbers whose sum they are, f32 queries as
+// two (the product of both low parts is left out: 2^-18), the weights e^(s − m) as two
+// (2^-22 of the weight).  Products are summed in f32, statistics are f32.  The values
+// d·(q − 8) enter as one f16, rounded once: errors of either sign that the sum over the
+// tokens averages, 0.75 of the output's own rounding in effect.  One f16 for the keys would
+// add 1.6 of it, and one for the weights 0.8.
 //
 // What bounds it, at one token of 32 heads (8 key/value heads, D = 128) over 131072
-// tokens, 151 MB: 33 us when the cache lies in the chip's last-level cache, of which the
-// vector instructions that expand the codes (some 350 a tile and wave) are 20, and 38
-// from memory (4.0 TB/s; a large copy 4.8); the join 5.  Short contexts: the chain of
+// tokens, 151 MB: 36 us when the cache lies in the chip's last-level cache, of which the
+// vector instructions that expand the codes (some 400 a tile and wave) are 23, and 39
+// from memory (3.9 TB/s; a large copy 4.8); the join 5.  Short contexts: the chain of
 // loads (lengths, page numbers, tiles) and two launches, 10 us over 4096 tokens.
 #include "attention_device.h"
 
@@ -230,7 +229,7 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
                     for (int b = 0; b < 4; ++b) s[c][mt][b] = masked(s[c][mt][b], seen[c], 4 * mt + b);
             }
         }
-        half8 w[NT];
+        half8 w[NT], w_low[NT];
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
             float top = -__builtin_inff();
@@ -255,13 +254,12 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
                 for (int b = 0; b < 4; ++b)
                     e[4 * mt + b] =
                         __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][mt][b], to_log2, -base));
-            uint32_t pairs[4];
+            l[c] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            uint32_t high[4], low[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                pairs[i] = pack_weights(e[2 * i], e[2 * i + 1]);
-                l[c] = sum_pair(pairs[i], l[c]);
-            }
-            w[c] = __builtin_bit_cast(half8, u32x4{pairs[0], pairs[1], pairs[2], pairs[3]});
+            for (int i = 0; i < 4; ++i) pack_weights(e[2 * i], e[2 * i + 1], high[i], low[i]);
+            w[c] = __builtin_bit_cast(half8, u32x4{high[0], high[1], high[2], high[3]});
+            w_low[c] = __builtin_bit_cast(half8, u32x4{low[0], low[1], low[2], low[3]});
         }
         if (edge) {
             uint32_t bad = 0;
@@ -280,8 +278,10 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
         for (int i = 0; i < MT; ++i) {
             const half8 op = value_operand(now, i, mg);
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
+            for (int c = 0; c < NT; ++c) {
                 o[c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, w[c], o[c][i], 0, 0, 0);
+                o[c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, w_low[c], o[c][i], 0, 0, 0);
+            }
         }
     };
     // The wave's tiles: where they lie is looked up 64 at a time, one a lane, and each is

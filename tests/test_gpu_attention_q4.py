@@ -11,10 +11,11 @@ Tolerance, per output element; e = 2^-11 is f16's half step, u = 2^-24.
            δ = scale·max_j Σ|q·k_j|·(2^-18 [f32] + (3D + 16)·u) + scale·2^-25·max_j Σ|k_j| [f32]
              + 8u·(max_j|s_j| + cap), and the hardware's exponential adds 2u: a weight and the
            sum of weights are each off by at most e^(δ + 2u) − 1
-  output   weights and values enter as f16: 2e of Σ w|v|; the sums of L terms in f32, L·u;
-           weights are held to 2^-32 of the largest (f16 at 2^7 and more for it): L·2^-32·max|v|
+  output   values enter as f16: e of Σ w|v|; weights as two f16 numbers: 2^-22 of it; the
+           sums of L terms in f32, L·u; weights are held to 2^-32 of the largest (f16 at 2^7
+           and more for it): L·2^-32·max|v|
   rounding e of the value, 2^-25 below the smallest normal
-Together: S·(2·(e^(δ + 2u) − 1)·1.01 + 2e·1.01 + 2·L·u) + L·2^-32·max|v| + e·|y| + 2^-25, S =
+Together: S·(2·(e^(δ + 2u) − 1)·1.01 + (e + 2^-21)·1.01 + 2·L·u) + L·2^-32·max|v| + e·|y| + 2^-25, S =
 Σ w|v|."""
 
 import numpy as np
@@ -66,7 +67,7 @@ def expect(s, q, H, b, positions, rows, scale, causal, window, cap, slopes, pref
             delta = big * ((3 * D + 16) * U + (2.0 ** -18 if wide else 0)) + 8 * U * (top + cap) + 2 * U
             if wide:
                 delta = delta + abs(scale) * 2.0 ** -25 * np.abs(np.nan_to_num(k[:, h // G])).sum(1).max()
-            w = 2 * np.expm1(np.minimum(delta, 50)) * 1.01 + 2 * E * 1.01 + 2 * L * U
+            w = 2 * np.expm1(np.minimum(delta, 50)) * 1.01 + (E + 2.0 ** -21) * 1.01 + 2 * L * U
             tol[:, h] = S[:, h] * w[:, None] + L * 2.0 ** -32 * np.abs(np.nan_to_num(v)).max()
     return y, tol + E * np.abs(y) + 2.0 ** -25
 
