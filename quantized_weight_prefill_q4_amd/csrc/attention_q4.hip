@@ -29,7 +29,7 @@
 //
 // What bounds it, at one token of 32 heads (8 key/value heads, D = 128) over 131072
 // tokens, 151 MB: 36 us when the cache lies in the chip's last-level cache, of which the
-// vector instructions that expand the codes (some 400 a tile and wave) are 23, and 39
+// vector instructions that expand the codes (430 a tile and wave) are 23, and 39
 // from memory (3.9 TB/s; a large copy 4.8); the join 5.  Short contexts: the chain of
 // loads (lengths, page numbers, tiles) and two launches, 10 us over 4096 tokens.
 #include "attention_device.h"
