@@ -6,7 +6,7 @@
 //   o   = Σ_j e^(s_j − m) v_j / Σ_j e^(s_j − m),  over the visible j, m their maximum
 // and zeros where none is visible.
 //
-// Few rows of a key/value head (up to 32, this file; more in attention_prompt.hip): the
+// Few rows of a key/value head (this file; more in attention_prompt.hip): the
 // time is that of reading the cache.  A workgroup takes R rows (16 or 32; row = token ·
 // group + head of the group, so that the query heads of a key/value head share its
 // tiles) of one key/value head and a part of the keys; its four waves take the part's
@@ -116,7 +116,7 @@ __device__ __forceinline__ half8 value_operand(const Tile<NS> &t, int i, uint32_
 
 // Waves per SIMD that the registers have to leave room for.
 template <int NS, int NT>
-constexpr int kWavesPerSimd = NS * NT <= 4 ? 3 : NS * NT <= 8 ? 2 : 1;
+constexpr int kWavesPerSimd = NS * NT <= 4 ? 3 : 2;
 
 template <int NS, int NT, bool BIAS, bool WIDE>
 __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel(AttnArgs a) {
@@ -577,17 +577,17 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) 
     } else {
         if (p.rows == 16)
             launch_rows<NS, 1>(a, bias, stream);
-        else
+        else if constexpr (NS <= 4)
             launch_rows<NS, 2>(a, bias, stream);
         e = hipGetLastError();
     }
     if (e != hipSuccess || a.splits == 1) return e;
     if (p.rows == 16)
         launch_join<NS, 16>(a, stream);
-    else if (p.rows == 32)
-        launch_join<NS, 32>(a, stream);
-    else
+    else if (p.rows > 32)
         launch_join<NS, NS <= 4 ? 256 : 128>(a, stream);
+    else if constexpr (NS <= 4)
+        launch_join<NS, 32>(a, stream);
     return hipGetLastError();
 }
 
@@ -598,7 +598,21 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
     const int group = s.q_heads / kv.heads;
     const int64_t mean = kv.cu ? ((int64_t)kv.M + kv.batch - 1) / kv.batch : kv.rows;
     const int64_t rows = mean * group;   // of a key/value head and sequence
-    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : attention_prompt_rows(kv.D);
+    // Rows of a workgroup.  Up to 16 rows one column tile, up to 64 two (up to 128 where
+    // contexts may be long), for heads of 256 one up to 96 (their second does not fit the
+    // registers), and beyond that the kernel for many rows.  One sequence over 30000 tokens /
+    // 32 sequences over 3000 / over 200, 8 key/value heads (4 of 256), us:
+    //   D = 128  24 rows  16: 27.5 / 59.7 / 13.5   32: 30.6 / 50.4 / 13.9
+    //            40 rows                           32: 37.3 / 78.8 / 19.0   256: 72.8 / 179 / 22.1
+    //            64 rows  16: 43.8 / 103 / 23.3    32: 38.9 / 83.6 / 25.4   256: 73.9 / 180 / 22.1
+    //           128 rows                           32: 84.7 / 151 / 40.0    256: 77.0 / 189 / 23.0
+    //   D = 64   96 rows                           32: 49.3 / 71.2 / 14.8   256: 58.6 / 134 / 17.1
+    //   D = 256  32 rows  16: 37.4 / 62.1 / 15.8   32: 38.7 / 85.2 / 20.5
+    //            96 rows  16: 57.3 / 140 / 31.8                             128: 90.0 / 150 / 29.2
+    //           128 rows  16: 70.5 / 184 / 39.4                             128: 92.4 / 150 / 30.1
+    const bool wide = kv.D == 256;
+    const int64_t most = wide ? 96 : s.max_len < 1024 ? 64 : 128;
+    p.rows = rows <= 16 ? 16 : rows > most ? attention_prompt_rows(kv.D) : wide ? 16 : 32;
     p.row_tiles = kv.cu ? (int64_t)kv.M * group / p.rows + kv.batch
                         : (rows + p.rows - 1) / p.rows * kv.batch;
     // Parts of the keys.  (The workspace's size is asked for without the mask: none of this
@@ -620,7 +634,7 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
             splits = (int64_t)(p.target / (double)jobs * (max_len / mean) + 0.5);
         }
         // few jobs: the parts' time falls with their number and the join's grows, equal at
-        // some 2·√tiles (128 rows over 19500 tokens 66 us with 8 parts, 34 with 32; over
+        // some 2·√tiles (128 rows of one head of 64, 19500 tokens 66 us with 8 parts, 34 with 32; over
         // 131000 tokens 130 with 32, 75 with 128)
         int64_t most = 8;
         while (most * jobs < 512 && most * most < 4 * tiles) ++most;

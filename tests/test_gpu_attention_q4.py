@@ -165,6 +165,15 @@ def test_many_and_unequal_sequences():
 
 
 @pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("rows", [11, 16, 22, 32, 33, 43])
+def test_between_few_and_many_rows(D, rows):
+    s = filled(D, 2, 32, [rows] * 2, [rows + 37, 1800], seed=rows + D, ragged=False)
+    check(s, 6)                                    # 33 to 99 rows of a key/value head
+    check(s, 6, max_len=1000)
+    check(s, 6, xt="f32", window=500, slopes=[0.1] * 6)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
 def test_many_rows_in_parts(D):
     s = filled(D, 1, 64, [70], [1700], seed=31 + D, ragged=False)
     check(s, 4)
