@@ -209,6 +209,52 @@ def test_large_and_small_scores():
     check(s, 4, gain=8.0)
     check(s, 4, gain=1e-3)
     check(s, 4, gain=8.0, scale=1.0)
+    s = filled(128, 1, 32, [1, 70], [300, 150], seed=6, gain=1e-5)     # scales below f16's normals
+    for xt in ("f16", "f32"):
+        check(s, 4, xt=xt, scale=2e4)
+    check(s, 4, xt="f32", gain=1e-4, scale=1e8)
+
+
+def test_other_streams_and_two_graphs_on_one_workspace():
+    """Two captured calls of different kernels share a workspace; each replay is compared."""
+    announce("attention_q4 two graphs, one workspace")
+    D, H = 128, 8
+    s1 = filled(D, 2, 64, [1, 1, 1], [3000, 5, 1200], seed=51)
+    s2 = filled(D, 2, 64, [90, 20], [2000, 700], seed=52)
+    q1, q2 = (rows_of(s.M, H * D, torch.float16, 53) for s in (s1, s2))
+    need = [mq.attention_workspace_bytes(s.cache, len(s.lens), H, s.M, 4096, ragged=True)
+            for s in (s1, s2)]
+    assert min(need) > 0
+    ws = torch.full((max(need),), 255, dtype=torch.uint8, device=dev())
+    run = [lambda s=s, q=q: mq.attention_q4(q, s.cache, s.table, s.lens_t, cu_rows=s.cu,
+                                            max_len=4096, ws=ws) for s, q in ((s1, q1), (s2, q2))]
+    eager = [f().clone() for f in run]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for f, y in zip(run, eager):
+            assert torch.equal(f(), y)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for f in run:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = f()
+        graphs.append((g, y))
+    for _ in range(4):
+        for (g, y), want in zip(graphs, eager):
+            y.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+            run[1]()
+            ws.fill_(255)
+    # shorter sequences between replays: the parts follow the lengths on the device
+    s1.lens_t.copy_(ints([40, 5, 900]))
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    got = graphs[0][1].clone()
+    assert torch.equal(got, run[0]())
 
 
 def test_strides_and_odd_rows():
