@@ -286,10 +286,12 @@ __device__ __forceinline__ void split_scales(uint32_t d, half2v &high, half2v &l
 
 // Two weights as f16, and what that rounding left of them as f16 (exact differences).
 __device__ __forceinline__ void pack_weights(float a, float b, uint32_t &high, uint32_t &low) {
-    const half2v h = {(_Float16)a, (_Float16)b};
+    const half2v v = {(_Float16)a, (_Float16)b};
+    // (opaque: the pair is converted once, not each half again for its difference)
+    high = opaque(__builtin_bit_cast(uint32_t, v));
+    const half2v h = as_half2(high);
     const half2v l = {(_Float16)__builtin_fmaf((float)h.x, -1.0f, a),
                       (_Float16)__builtin_fmaf((float)h.y, -1.0f, b)};
-    high = __builtin_bit_cast(uint32_t, h);
     low = __builtin_bit_cast(uint32_t, l);
 }
 

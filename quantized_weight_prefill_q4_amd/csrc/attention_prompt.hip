@@ -1,5 +1,7 @@
 // Attention over the 4-bit cache for many query rows (attention_q4.hip has the
-// definition and the numerics, which are the same here).
+// definition and the numerics; here the keys d·(q − 8) enter as two f16 numbers whose sum
+// they are, which keeps blocks in one sum, and f32 queries lose 2^-18 of a product, that of
+// both low parts).
 //
 // With many rows the work is the matrix products and the exponentials: 4·D
 // operations and one exponential per visible pair, and the expansion of the codes

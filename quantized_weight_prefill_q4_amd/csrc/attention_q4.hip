@@ -12,26 +12,28 @@
 // tiles) of one key/value head and a part of the keys; its four waves take the part's
 // tiles of 32 tokens in turn, each loading one tile ahead, and their results are joined
 // at the end.  Per tile, in one pass with the running maximum and sum:
-//   Sᵀ[t, n] = K[t, :] · Q[n, :]    matrix instructions 16 x 16 x 32, keys as A, twice:
-//                                   both parts of the keys; f32 queries' low part a third
+//   Sᵀ[t, n] = Σ_b d_b[t] · (q − 8)[t, b] · Q[n, b]   over the blocks b of 32 elements:
+//                                   matrix instructions 16 x 16 x 32, a block's codes as A,
+//                                   times its scale in f32; f32 queries' low part a second
 //   Oᵀ[d, n] += Vᵀ[d, t] · Pᵀ[t, n]  values as A, twice: both parts of the weights
 // A lane holds of Sᵀ exactly the eight tokens whose weights it has to give as the
 // second product's B operand, because row r of the first product's tile m is
 // token 8·(r/4) + 4·m + r%4: nothing moves between lanes but the maximum of a
 // column.  Codes become f16 in the registers that loaded them.
 //
-// Numerics: the keys d·(q − 8) enter as two f16 numbers whose sum they are, f32 queries as
-// two (the product of both low parts is left out: 2^-18), the weights e^(s − m) as two
-// (2^-22 of the weight).  Products are summed in f32, statistics are f32.  The values
-// d·(q − 8) enter as one f16, rounded once: errors of either sign that the sum over the
-// tokens averages, 0.75 of the output's own rounding in effect.  One f16 for the keys would
-// add 1.6 of it, and one for the weights 0.8.
+// Numerics: the keys' codes are exact in f16 and their scales multiply f32 sums; f32
+// queries enter as two f16 numbers, the weights e^(s − m) as two (2^-22 of the weight).
+// Products are summed in f32, statistics are f32.  The values d·(q − 8) enter as one f16,
+// rounded once: errors of either sign that the sum over the tokens averages, 0.75 of the
+// output's own rounding in effect.  Keys rounded to one f16 would add 1.6 of it, weights
+// 0.8.
 //
 // What bounds it, at one token of 32 heads (8 key/value heads, D = 128) over 131072
-// tokens, 151 MB: 36 us when the cache lies in the chip's last-level cache, of which the
-// vector instructions that expand the codes (430 a tile and wave) are 23, and 39
-// from memory (3.9 TB/s; a large copy 4.8); the join 5.  Short contexts: the chain of
-// loads (lengths, page numbers, tiles) and two launches, 10 us over 4096 tokens.
+// tokens, 151 MB: 33.5 us when the cache lies in the chip's last-level cache, of which the
+// vector instructions that expand the codes (350 a tile and wave) are 19, and 37 from
+// memory (4.1 TB/s; a large copy 4.8); the join 5.  (Keys as two f16 parts, eight more
+// matrix and 100 more vector instructions a tile: 36.)  Short contexts: the chain of loads
+// (lengths, page numbers, tiles) and two launches, 10 us over 4096 tokens.
 #include "attention_device.h"
 
 namespace mq {
@@ -115,11 +117,11 @@ __device__ __forceinline__ half8 value_operand(const Tile<NS> &t, int i, uint32_
 }
 
 // Waves per SIMD that the registers have to leave room for.
-template <int NS, int NT>
-constexpr int kWavesPerSimd = NS * NT <= 4 ? 3 : 2;
+template <int NS, int NT, bool WIDE>
+constexpr int kWavesPerSimd = NS * NT <= 4 ? 3 : NS * NT == 8 && NT == 1 && WIDE ? 1 : 2;
 
 template <int NS, int NT, bool BIAS, bool WIDE>
-__global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT, WIDE>)) void attention_kernel(AttnArgs a) {
     constexpr int D = 32 * NS, R = 16 * NT, MT = 2 * NS;   // MT: output tiles of 16 elements
     constexpr int CH = MT < 8 ? MT : 8;                    // of them joined at a time
     __shared__ float join[kWaves][CH * 4][64];
@@ -179,29 +181,34 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT>)) void attention_kernel
         f32x4 s[NT][2];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
+            // scales of the lane's four tokens: row 4g + b of the operand is lane 4g + b's
+            uint32_t d[Tile<NS>::KS2][4];
+#pragma unroll
+            for (int i = 0; i < Tile<NS>::KS2; ++i)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    d[i][b] = __builtin_amdgcn_ds_bpermute(
+                        16 * g + 4 * b, now.ks[mt * Tile<NS>::KS2 + i]);
 #pragma unroll
             for (int c = 0; c < NT; ++c) s[c][mt] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
-                half2v h[4], low[4], dh, dl;
+                half2v h[4];
                 widen(now.k[mt * NS + k], mg, h);
-                split_scales(now.ks[mt * Tile<NS>::KS2 + k / 2], dh, dl);
-                const _Float16 x = k & 1 ? dh.y : dh.x, y = k & 1 ? dl.y : dl.x;
-                const half2v xx = {x, x}, yy = {y, y};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    low[e] = h[e] * yy;
-                    h[e] *= xx;
-                }
-                const half8 op = join8(h), op_low = join8(low);
+                const half8 op = join8(h);
 #pragma unroll
                 for (int c = 0; c < NT; ++c) {
-                    s[c][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, q[c][k], s[c][mt], 0, 0, 0);
-                    s[c][mt] =
-                        __builtin_amdgcn_mfma_f32_16x16x32_f16(op_low, q[c][k], s[c][mt], 0, 0, 0);
+                    f32x4 x = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, q[c][k], f32x4{0, 0, 0, 0}, 0,
+                                                                     0, 0);
                     if constexpr (WIDE)
-                        s[c][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, q_low[c][k], s[c][mt],
-                                                                          0, 0, 0);
+                        x = __builtin_amdgcn_mfma_f32_16x16x32_f16(op, q_low[c][k], x, 0, 0, 0);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const half2v pair = as_half2(d[k / 2][b]);
+                        s[c][mt][b] =
+                            __builtin_fmaf((float)(k & 1 ? pair.y : pair.x), x[b], s[c][mt][b]);
+                    }
+                    asm volatile("" : "+v"(s[c][mt]));   // here, not where they are used
                 }
             }
         }
@@ -668,7 +675,6 @@ hipError_t launch_attention(const KvSpec &kv, const AttnSpec &s, const AttnPlan 
     // (a cap below 1e-30 is as good as 0: finite all the same)
     a.inv_cap = s.cap > 1e-30f ? 1.0f / s.cap : s.cap > 0.0f ? 1e30f : 0.0f;
     a.q_f32 = s.x_type == kTypeF32;
-    a.q_heads = s.q_heads;
     a.group = s.q_heads / kv.heads;
     a.causal = s.causal;
     a.window = s.window < kMaxLen ? s.window : kMaxLen;   // no sequence is longer

@@ -12,7 +12,7 @@ struct AttnArgs {
     uint16_t *y;
     int64_t ldq, ldy;
     float scale, cap, inv_cap;        // cap 0: none
-    int q_f32, q_heads, group, causal, window;
+    int q_f32, group, causal, window;
     int splits, target;               // parts of the keys: at most, workgroups to fill
     int min_tiles;                    // of a part: fewer do not pay for the join
     int items;                        // workgroups of the kernel for few rows
