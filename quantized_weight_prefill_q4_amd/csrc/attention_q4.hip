@@ -30,9 +30,9 @@
 //
 // What bounds it, at one token of 32 heads (8 key/value heads, D = 128) over 131072
 // tokens, 151 MB: 33.5 us when the cache lies in the chip's last-level cache, of which the
-// vector instructions that expand the codes (350 a tile and wave) are 19, and 37 from
+// vector instructions that expand the codes (380 a tile and wave) are 20, and 37 from
 // memory (4.1 TB/s; a large copy 4.8); the join 5.  (Keys as two f16 parts, eight more
-// matrix and 100 more vector instructions a tile: 36.)  Short contexts: the chain of loads
+// matrix and 50 more vector instructions a tile: 36.)  Short contexts: the chain of loads
 // (lengths, page numbers, tiles) and two launches, 10 us over 4096 tokens.
 #include "attention_device.h"
 
