@@ -396,22 +396,20 @@ def test_appending_token_by_token_is_the_prompt():
             parts.append(layer(s, x[at:at + c], h0[at:at + c], at + c))
             at += c
         results.append((s, [torch.cat(p) for p in zip(*parts)]))
-    s, (q, a, y) = results[0]
-    lk, lv = mq.kv_load_q4(s.cache, s.table, s.lens_t, n, out_dtype=torch.float32)
-    s.k, s.v = (to_host(t).astype(np.float64).reshape(n, Hkv, D) for t in (lk, lv))
-    s.tok = [0, n]
-    for t, (qt, at, yt) in results:
-        # the product's sums may differ with the row count by their last bits, so a
-        # piece's cache may differ in a code: compared where the bytes are the same
+    w = mq.dequant_to_f16(wo, fmt, hidden, H * D)[:, :H * D].double()
+    for s, (qt, at, yt) in results:
+        # (the product's sums may differ with the row count by their last bits, and a
+        # piece's cache in a code: each against its own)
+        lk, lv = mq.kv_load_q4(s.cache, s.table, s.lens_t, n, out_dtype=torch.float32)
+        s.k, s.v = (to_host(t).astype(np.float64).reshape(n, Hkv, D) for t in (lk, lv))
+        s.tok = [0, n]
         qs = to_host(qt).astype(np.float64).reshape(n, H, D)
-        if torch.equal(t.bytes, s.bytes):
-            ref, tol = expect(s, qs, H, 0, np.arange(n), slice(0, n), oa.default_scale(D), True, 0,
-                              0.0, None, 0)
-            assert (np.abs(to_host(at).astype(np.float64).reshape(n, H, D) - ref) <= tol).all()
-        assert bool(torch.isfinite(yt).all())
-        assert torch.equal(yt[:1], mq.linear_fused(at[:1], wo, fmt, hidden, H * D, residual=h0[:1])) \
-            or float((yt[0] - y[0]).abs().max()) < 1e-2 * float(y.abs().max())
-    assert torch.equal(results[0][0].bytes, s.bytes)
+        ref, tol = expect(s, qs, H, 0, np.arange(n), slice(0, n), oa.default_scale(D), True, 0,
+                          0.0, None, 0)
+        assert (np.abs(to_host(at).astype(np.float64).reshape(n, H, D) - ref) <= tol).all()
+        # the o product's own bound, 1e-3 of the sum of magnitudes
+        want = h0.double() + at.double() @ w.T
+        assert bool(((yt - want).abs() <= 1e-3 * (at.double().abs() @ w.abs().T) + 1e-5).all())
 
 
 def test_deterministic_on_streams_and_in_graphs():
