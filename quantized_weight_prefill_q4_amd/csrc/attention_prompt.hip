@@ -59,9 +59,9 @@ struct Int {
     static constexpr int value = V;
 };
 
-// One wave's share of a tile's keys or values, as loaded: PW operands (number PW·member
+// One wave's share of a tile's keys or values, as loaded: PW operands (number PW·wave
 // + k: k-steps of the keys; values by token half and tile of elements) and the scales of
-// their pairs.  Waves past the last operand have none.
+// their pairs (a key's is one, in x).  Waves past the last operand have none.
 template <int NS, int PW>
 struct Codes {
     static constexpr bool kRuns = (NS & (NS - 1)) == 0;   // one set of scales serves all values

@@ -178,6 +178,7 @@ def test_many_rows_in_parts(D):
     s = filled(D, 1, 64, [70], [1700], seed=31 + D, ragged=False)
     check(s, 4)
     check(s, 4, xt="f32", causal=False, max_len=100)
+    check(s, 4, causal=False)
     s = filled(D, 2, 32, [100, 3, 40], [2100, 3, 900], seed=32 + D)
     check(s, 6)
     check(s, 6, xt="f32", cap=20.0, window=700)
