@@ -512,7 +512,7 @@ int64_t mq_kv_q4_page_bytes(int heads, int page, int head_dim);
  * buffer of the call.  Rows at negative positions (lens[b] smaller than the
  * sequence's rows) are left out, their queries included.  Two sequences whose
  * tables give the same page for rows of this call overwrite each other there in
- * no particular order.
+ * no particular order; one without rows in the call touches no page.
  * Errors: those of mq_rope, MQ_ERR_SHAPE also for M not a multiple of batch without
  * cu_rows, MQ_ERR_LD also for page_bytes and table_ld. */
 int mq_kv_store_q4(const mq_kv_q4 *cache, int x_type, const void *K, int ldk, const void *V, int ldv,

@@ -109,8 +109,8 @@ MQ_INDEX int find_seq(const KvSpec &kv, int unit, int scale, unsigned per, int e
     return lo;
 }
 
-// Eight positions [p0, p0 + 8) of sequence b, of which [e_lo, e_hi) are rows of the
-// batch (position p0 + e is row row0 + e); positions at or past keys have no place.
+// Eight positions [p0, p0 + 8) of sequence b, of which [e_lo, e_hi), one at least, are rows
+// of the batch (position p0 + e is row row0 + e); positions at or past keys have no place.
 // Units of eight positions are numbered as above; n rows from any position on
 // touch at most n/8 + 2.  Rows at negative positions are in no unit.
 struct Octet {
@@ -127,6 +127,9 @@ MQ_INDEX bool find_octet(const KvSpec &kv, int unit, unsigned per_seq, Octet &o)
     if (within < 0 || o.p0 >= len) return false;
     o.e_lo = start > o.p0 ? start - o.p0 : 0;
     o.e_hi = len - o.p0 < 8 ? len - o.p0 : 8;
+    // a sequence without rows has its end in an octet, and no work there: the store would
+    // put the dwords of other tokens back as it read them, over another workgroup's
+    if (o.e_lo >= o.e_hi) return false;
     o.keys = seq_keys(kv, len);
     o.row0 = (int64_t)rows.first + o.p0 - start;
     return true;

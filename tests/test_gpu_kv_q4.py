@@ -303,6 +303,30 @@ def test_far_pages():
     assert np.array_equal(to_host(outs[1][1]), want.astype(np.float16))
 
 
+def test_sequences_without_rows_share_pages_with_others():
+    """A slot without rows in the call whose length ends inside an octet (a finished request,
+    a waiting fork) names a page that another sequence is stored into: the page is what that
+    sequence leaves."""
+    announce("kv_store_q4 idle slots over a page in use")
+    for D, Hkv, n, idle in ((128, 8, 20, [13]), (64, 2, 32, [1, 7, 9, 15, 18, 25, 31, 33]),
+                            (256, 4, 24, [5, 13, 21] * 40), (96, 3, 31, [30] * 70)):
+        s = Batch(D, Hkv, 32, [n], [n], D, False)
+        k, v = (rows_of(n, Hkv * D, torch.float16, i) for i in (1, 2))
+        mq.kv_store_q4(k, v, s.cache, s.table, s.lens_t)
+        want = s.bytes.clone()
+        B = len(idle)
+        table = s.table.repeat(2 * B + 1, 1)
+        lens = ints(idle + [n] + idle)
+        cu = ints([0] * (B + 1) + [n] * (B + 1))
+        lk, lv = mq.kv_load_q4(s.cache, s.table, s.lens_t, n)
+        for _ in range(10):
+            s.bytes.fill_(255)
+            mq.kv_store_q4(k, v, s.cache, table, lens, cu_rows=cu)
+            assert torch.equal(s.bytes, want), D
+        a, b = mq.kv_load_q4(s.cache, table, lens, n, cu_rows=cu)
+        assert torch.equal(a, lk) and torch.equal(b, lv)
+
+
 def test_streams_and_graphs():
     announce("kv_store_q4 on another stream, captured and replayed")
     D, H, Hkv = 128, 4, 2

@@ -254,3 +254,91 @@ def test_indexes_stay_in_bounds(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", (r.stdout, r.stderr[-2000:])
+
+
+EMPTY = r"""
+#include <stdio.h>
+#include <random>
+#include <vector>
+#include "kv_q4.h"
+using namespace mq;
+
+int main() {
+    // a sequence without rows, of every length: none of its units has work
+    for (int len = 0; len < 70; ++len)
+        for (int at = 0; at < 3; ++at) {
+            int table[12], lens[3] = {20, 20, 20}, cu[4] = {0, 20, 40, 60};
+            for (int &t : table) t = 0;
+            lens[at] = len;
+            for (int b = at + 1; b < 4; ++b) cu[b] -= 20;
+            KvSpec kv{};
+            kv.batch = 3;
+            kv.page = 32;
+            kv.width = kv.table_ld = 4;
+            kv.pages = 1;
+            kv.heads = 1;
+            kv.D = 64;
+            kv.table = table;
+            kv.lens = lens;
+            kv.cu = cu;
+            kv.M = 40;
+            int rows = 0;
+            for (int64_t u = 0; u < total_units(kv); ++u) {
+                Octet o;
+                if (!find_octet(kv, u, units_per_seq(kv), o)) continue;
+                if (o.b == at || o.e_lo >= o.e_hi) {
+                    printf("length %d at %d: unit %d, positions %d + [%d, %d)\n", len, at, (int)u, o.p0,
+                           o.e_lo, o.e_hi);
+                    return 1;
+                }
+                rows += o.e_hi - o.e_lo;
+            }
+            if (rows != 40) {
+                printf("length %d at %d: %d rows\n", len, at, rows);
+                return 1;
+            }
+        }
+    // whatever lens and cu_rows hold, every unit with work has a row
+    for (int seed = 0; seed < 20000; ++seed) {
+        std::mt19937 rng(seed);
+        auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
+        const int odd[] = {-1, INT32_MIN, INT32_MAX, 1 << 30, -7, 3, 1000000};
+        KvSpec kv{};
+        kv.batch = pick(1, 5);
+        kv.page = 32;
+        kv.width = pick(1, 4);
+        kv.M = pick(1, 60);
+        std::vector<int> lens(kv.batch), cu(kv.batch + 1);
+        for (int &x : lens) x = pick(0, 3) ? pick(0, 200) : odd[pick(0, 6)];
+        for (int &x : cu) x = pick(0, 3) ? pick(0, kv.M) : odd[pick(0, 6)];
+        kv.lens = lens.data();
+        kv.cu = cu.data();
+        for (int64_t u = 0; u < total_units(kv); ++u) {
+            Octet o;
+            if (find_octet(kv, u, 0, o) && o.e_lo >= o.e_hi) {
+                printf("seed %d: a unit without rows\n", seed);
+                return 1;
+            }
+        }
+    }
+    printf("ok\n");
+    return 0;
+}
+"""
+
+
+def test_sequences_without_rows_have_no_octets(tmp_path):
+    """The store reads and rewrites whole dwords of an octet: one without rows must be
+    nobody's work, or it puts old values back over those that another sequence stores."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None or not os.path.exists("/opt/rocm/include/hip/hip_runtime.h"):
+        pytest.skip("no host compiler or HIP headers")
+    src, exe = tmp_path / "empty.cpp", tmp_path / "empty"
+    src.write_text(EMPTY)
+    r = subprocess.run([cxx, "-std=c++17", "-O1", "-g", "-w", "-fsanitize=address,undefined",
+                        "-fno-sanitize-recover=undefined", "-D__HIP_PLATFORM_AMD__",
+                        "-I", "/opt/rocm/include", "-I", CSRC, str(src), "-o", str(exe)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", (r.stdout, r.stderr[-2000:])
