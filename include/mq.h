@@ -500,7 +500,8 @@ int64_t mq_kv_q4_page_bytes(int heads, int page, int head_dim);
  * freqs is given, and rotates the rows' queries beside them when Q is.
  * Per block, v its first element of largest magnitude: d = f16(v / −8), q =
  * clamp(floor(x/d + 8.5), 0, 15), 8 where d is 0; all in f32.  A block with an
- * infinity or NaN, or whose d overflows f16, gets NaN as its d.
+ * infinity or NaN, or with an element of magnitude 65520 or more after its rotation
+ * (|d| > 8188: f16 does not hold 8·d), gets NaN as its d.
  *   K, V      : device, x_type, row strides ldk, ldv >= heads · head_dim.
  *   freqs, n_rot, layout, mscale : as mq_rope; freqs == NULL: no rotation (the other
  *               three ignored).

@@ -56,7 +56,7 @@ def quantize_q4(x: np.ndarray):
     top = np.take_along_axis(b, at[..., None], -1)[..., 0]
     with np.errstate(over="ignore", invalid="ignore", divide="ignore"):
         d = (top / np.float32(-8)).astype(np.float16)
-        bad |= ~np.isfinite(d)
+        bad |= ~(np.abs(d.astype(np.float32)) <= 8188)   # d·(q − 8) has to be an f16 number
         df = d.astype(np.float32)[..., None]
         q = np.floor(b / df + np.float32(8.5))
     q = np.where((df == 0) | bad[..., None], 8, np.clip(np.nan_to_num(q), 0, 15))

@@ -243,9 +243,11 @@ __device__ __forceinline__ float masked(float s, uint32_t bits, int bit) {
 // Values' scales in tiles that are masked in part.  A weight of 0 times an infinity or
 // a NaN is not 0, so scales of tokens past the sequence (never written, perhaps) and
 // scales that are not finite are taken out, and the rows that see one of the latter
-// get a NaN in the elements of its block at the end.
+// get a NaN in the elements of its block at the end.  Likewise finite ones from 8192 on
+// (the three upper bits of the exponent): their products are infinite in f16.  The store
+// writes none (kMostScale), but a token that no row sees may never have been stored.
 __device__ __forceinline__ uint32_t bad_halves(uint32_t w) {   // bit 0: the low, 1: the high one
-    return ((w & 0x7C00u) == 0x7C00u ? 1u : 0u) | ((w & 0x7C000000u) == 0x7C000000u ? 2u : 0u);
+    return ((w & 0x7000u) == 0x7000u ? 1u : 0u) | ((w & 0x70000000u) == 0x70000000u ? 2u : 0u);
 }
 __device__ __forceinline__ uint32_t keep_halves(uint32_t w, bool lo, bool hi) {
     return (lo ? w & 0xFFFFu : 0u) | (hi ? w & 0xFFFF0000u : 0u);

@@ -27,6 +27,7 @@ namespace mq {
 namespace {
 
 constexpr int kTile = 32;
+constexpr float kMostScale = 8188.0f;   // of a block: 8 of it are f16's largest number
 
 MQ_INDEX constexpr int kv_tile_bytes(int D) { return 36 * D; }
 

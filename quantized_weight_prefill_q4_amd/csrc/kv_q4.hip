@@ -4,8 +4,9 @@
 // blocks of 32 elements: with v the first of the elements of largest magnitude,
 //   d = f16(v / −8),   q = clamp(floor(x/d + 8.5), 0, 15)   (8 where d is 0)
 // so v itself is code 0 and the range is used whole.  All in f32 (the f16 d
-// widened).  A block with an infinity or a NaN, or whose d overflows f16, gets a
-// NaN as its d.  The queries of the same rows are rotated by the same launch: a
+// widened).  A block with an infinity or a NaN, or with |d| > 8188 (an element of 65520 or
+// more), gets a NaN as its d: what attention multiplies are f16 numbers d·(q − 8), and f16
+// ends at 65504 = 8 · 8188.  The queries of the same rows are rotated by the same launch: a
 // single token's layer is launch-bound.
 //
 // A workgroup takes eight consecutive positions [8u, 8u + 8) of one sequence, the tokens
@@ -94,7 +95,7 @@ __device__ __forceinline__ uint16_t quantize_q4(const float v[8], int q[8]) {
     }
     uint16_t bits = (uint16_t)pack_f16x2(top / -8.0f, 0.0f);
     const float d = f16_bits_to_f32(bits);
-    if (any || !(fabsf(d) < __builtin_inff())) {
+    if (any || !(fabsf(d) <= kMostScale)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = 8;
         return 0x7E00;

@@ -348,6 +348,66 @@ def test_infinities_and_nan_stay_with_the_rows_that_see_them(D):
     assert torch.equal(y[same], clean.view(n, H, D)[same])
 
 
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("n", [20, 100])               # few and many rows of a key/value head
+def test_blocks_beyond_f16_stay_with_the_rows_that_see_them(D, n):
+    """Keys and values that f32 holds and f16 does not: NaN in the rows that see them, in both
+    kernels, and no bit changed in the rows before."""
+    announce("attention_q4 blocks beyond f16", D, n)
+    H, Hkv = 4, 2
+    s = filled(D, Hkv, 32, [n], [n], seed=11, ragged=False)
+    q = rows_of(n, H * D, torch.float16, 12)
+    clean = mq.attention_q4(q, s.cache, s.table, s.lens_t).view(n, H, D)
+    k, v = (rows_of(1, Hkv * D, torch.float32, i).contiguous() for i in (13, 14))
+    keep = s.bytes.clone()
+    for size in (65520.0, -1e5, 524000.0):
+        for t in (0, 17, n - 1):
+            for which in "kv":
+                kk, vv = k.clone(), v.clone()
+                (kk if which == "k" else vv)[0, D + 5] = size     # head 1 of token t
+                mq.kv_store_q4(kk, vv, s.cache, s.table, ints([t + 1]))
+                y = mq.attention_q4(q, s.cache, s.table, s.lens_t).view(n, H, D)
+                assert torch.equal(y[:t], clean[:t]), (size, t, which)
+                bad = ~torch.isfinite(y)
+                assert not bool(bad[:, :2].any())
+                if which == "k":
+                    assert bool(bad[t:, 2:].all())
+                else:
+                    assert bool(bad[t:, 2:, :32].all()) and not bool(bad[..., 32:].any())
+                s.bytes.copy_(keep)
+    # and the largest that are stored: right in both kernels
+    kk, vv = k.clone(), v.clone()
+    kk[0, D + 5], vv[0, D + 5] = 65519.0, -65519.0
+    mq.kv_store_q4(kk, vv, s.cache, s.table, ints([18]))
+    lk, lv = mq.kv_load_q4(s.cache, s.table, s.lens_t, n, out_dtype=torch.float32)
+    s.k, s.v = (to_host(t).astype(np.float64).reshape(n, Hkv, D) for t in (lk, lv))
+    assert abs(s.k[17, 1, 5]) == 65504 and abs(s.v[17, 1, 5]) == 65504
+    check(s, H, scale=2.0 ** -16)
+    check(s, H, xt="f32", scale=2.0 ** -16, causal=False)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("byte", [0x70, 0xF7, 0x7B, 0xFF])
+def test_tokens_never_stored_stay_out_of_rows_that_do_not_see_them(D, byte):
+    """Scales of 9088, −30000, 61000 (finite: their products with a code are not) and NaN in
+    the bytes behind the tokens that the rows see."""
+    announce("attention_q4 tokens never stored", D, byte)
+    n, past = 45, 70
+    s = filled(D, 1, 32, [n], [n], seed=byte, ragged=False)
+    raw = Batch(D, 1, 32, [n + past], [n + past], byte, False)
+    raw.bytes.fill_(byte)
+    k, v = rows_of(n, D, torch.float16, 100 + byte), rows_of(n, D, torch.float16, 101 + byte)
+    mq.kv_store_q4(k, v, raw.cache, raw.table, ints([n]))
+    for H, rows in ((1, n + past), (4, n + past), (8, 80)):
+        q = rows_of(rows, H * D, torch.float16, 3)
+        y = mq.attention_q4(q, raw.cache, raw.table, ints([n + past]))
+        at = np.arange(n + past - rows, n)             # positions of the rows before the bytes
+        ref, tol = expect(s, to_host(q).astype(np.float64).reshape(rows, H, D), H, 0, at,
+                          slice(0, len(at)), oa.default_scale(D), True, 0, 0.0, None, 0)
+        got = to_host(y).astype(np.float64).reshape(rows, H, D)[:len(at)]
+        assert (np.abs(got - ref) <= tol).all(), (H, rows)
+
+
 def test_far_pages():
     """A cache past 2^32 bytes."""
     D, Hkv, page = 128, 8, 256

@@ -218,6 +218,39 @@ def test_special_blocks():
     assert bool(torch.isnan(lv[5, 32:]).all()) and bool(torch.isfinite(lv[5, :32]).all())
 
 
+def test_blocks_end_where_f16_does():
+    """Elements up to 65519 are stored, a block with a larger one is NaN; for keys that is the
+    element after its rotation, f16's own largest numbers included."""
+    announce("kv_store_q4 blocks at the end of f16")
+    tops = [60000.0, 65504.0, 65519.0, 65519.99609375, 65520.0, 65536.0, 1e5, 524000.0]
+    s = Batch(64, 1, 32, [16], [16], 6, False)
+    k = rows_of(16, 64, torch.float32, 7).contiguous() * 1000
+    v = rows_of(16, 64, torch.float32, 8).contiguous() * 1000
+    for i, top in enumerate(tops):
+        for j, sign in enumerate((-1, 1)):
+            k[i + 8 * j, 5], v[i + 8 * j, 40] = sign * top, -sign * top
+    mq.kv_store_q4(k, v, s.cache, s.table, s.lens_t)
+    want = oa.quantize_q4(to_host(k)[:, None]) + oa.quantize_q4(to_host(v)[:, None])
+    for g, w in zip(s.tokens()[0], want):
+        assert np.array_equal(g, w, equal_nan=g.dtype != np.uint8)
+    lk, lv = mq.kv_load_q4(s.cache, s.table, s.lens_t, 16)
+    nan = torch.tensor([t >= 65520 for t in tops] * 2, device=dev())
+    for t, block in ((lk, 0), (lv, 1)):
+        t = t.view(16, 2, 32)
+        assert torch.equal(torch.isnan(t[:, block]).all(1), nan)
+        assert bool(torch.isfinite(t[:, block][~nan]).all()) and bool(torch.isfinite(t[:, 1 - block]).all())
+    # f16 keys turned past f16's end: (a, a) by an eighth of a turn is (0, 1.41·a)
+    f = torch.full((32,), np.pi / 4, dtype=torch.float64, device=dev())
+    k = torch.zeros(2, 64, dtype=torch.float16, device=dev())
+    k[:, [3, 35]] = 46000.0
+    k[1, [3, 35]] = 47000.0
+    one = ints([1, 1])
+    mq.kv_store_q4(k, k, s.cache, s.table, ints([2]), freqs=f, positions=one)
+    lk, lv = mq.kv_load_q4(s.cache, s.table, ints([2]), 2)
+    assert float(lk[0, 35]) > 65000 and bool(torch.isfinite(lk[0]).all())
+    assert bool(torch.isnan(lk[1, 32:]).all()) and bool(torch.isfinite(lv).all())
+
+
 def test_in_place_queries_in_one_buffer():
     """q, k and v as columns of one activation, q rotated where it stands."""
     announce("kv_store_q4 in one buffer")

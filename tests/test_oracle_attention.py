@@ -55,6 +55,21 @@ def test_blocks_by_hand():
         assert np.isnan(d[0]) and (q == 8).all()
 
 
+def test_blocks_end_where_f16_does():
+    """65504 = 8 · 8188 is f16's largest number; 65520 is the first that rounds beyond it."""
+    b = np.linspace(-1000, 1000, 32, dtype=np.float32)
+    for sign in (-1, 1):
+        for top in (65504.0, 65519.0, np.nextafter(np.float32(65520), np.float32(0))):
+            b[9] = sign * top
+            q, d = oa.quantize_q4(b)
+            assert d[0] == -sign * 8188 and q[9] == 0
+            assert np.isfinite(oa.values(q, d).astype(np.float16)).all()
+        for top in (65520.0, 65536.0, 1e5, 524000.0):     # of these d alone would be finite
+            b[9] = sign * top
+            q, d = oa.quantize_q4(b)
+            assert np.isnan(d[0]) and (q == 8).all()
+
+
 def test_blocks_are_within_half_a_step():
     rng = np.random.default_rng(2)
     x = rng.standard_normal((50, 96)).astype(np.float32)
