@@ -29,7 +29,9 @@ __device__ __forceinline__ float tanh_f32(float u) {
     return fabsf(u) < 0.25f ? p : 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// Products to scores: scale and cap, and the bias of N tokens, of which number i is
+__device__ __forceinline__ float finite(float v) { return fminf(fmaxf(v, -3.0e38f), 3.0e38f); }
+
+// Products to scores: scale (a.scale, over what the row's queries were multiplied by) and cap, and the bias of N tokens, of which number i is
 // `to − at(i)` positions before the row's.
 // The cancellation of tanh's quotient is of no account where the cap is small: the
 // score is off by 2^-21 of the cap at most, 2^-14 for kQuickCap, which is 2^-14 of a
@@ -37,21 +39,21 @@ __device__ __forceinline__ float tanh_f32(float u) {
 // rows over 16512 tokens 294 us to 232.)
 constexpr float kQuickCap = 128.0f;
 template <int N, class At>
-__device__ __forceinline__ void bias_scores(const AttnArgs &a, float (&s)[N], float slope, int to,
-                                            At at) {
-    const float k = a.scale * a.inv_cap * (2.0f * kLog2e);
-    if (a.cap > kQuickCap || (a.cap > 0.0f && !(fabsf(k) < 1e30f))) {
+__device__ __forceinline__ void bias_scores(const AttnArgs &a, float (&s)[N], float scale,
+                                            float slope, int to, At at) {
+    if (a.cap > kQuickCap) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = a.cap * tanh_f32(s[i] * a.scale * a.inv_cap);
+        for (int i = 0; i < N; ++i) s[i] = a.cap * tanh_f32(s[i] * scale * a.inv_cap);
     } else if (a.cap > 0.0f) {
-        const float c2 = -2.0f * a.cap;
+        // (finite: a score of 0 stays one)
+        const float c2 = -2.0f * a.cap, k = finite(scale * a.inv_cap * (2.0f * kLog2e));
 #pragma unroll
         for (int i = 0; i < N; ++i)
             s[i] = __builtin_fmaf(
                 c2, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[i] * k)), a.cap);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] *= a.scale;
+        for (int i = 0; i < N; ++i) s[i] *= scale;
     }
     if (a.slopes) {
         const float d = (float)to;   // (rounded beyond 2^24, like the distance itself)
@@ -63,18 +65,38 @@ __device__ __forceinline__ void bias_scores(const AttnArgs &a, float (&s)[N], fl
 typedef uint32_t q_u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float q_f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
-// Eight query elements as f16; of f32 ones, what that rounding leaves as f16 too.
+// Eight query elements.
 __device__ __forceinline__ half8 load_q8(const uint16_t *q, int64_t at) {
     return __builtin_bit_cast(half8, (u32x4)*reinterpret_cast<const q_u32x4_a2 *>(q + at));
 }
-__device__ __forceinline__ void load_q8(const float *q, int64_t at, half8 &high, half8 &low) {
+__device__ __forceinline__ void load_q8(const float *q, int64_t at, float (&v)[8]) {
     const q_f32x4_a4 *p = reinterpret_cast<const q_f32x4_a4 *>(q + at);
     const f32x4 x = p[0], y = p[1];
 #pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < 4 ? x[e & 3] : y[e & 3];
+}
+__device__ __forceinline__ float largest_of(const float (&v)[8], float m) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+    return m;
+}
+// f32 queries enter as two f16 numbers, of 22 bits together, down to f16's last step.  So
+// that f16's range is no limit, a row goes in times a power of two that puts its largest
+// element between 2^14 and 2^15 (the last step is then 2^-39 of it or less), and its
+// scores' scale takes it out again, both exactly.  (The scale is then each lane's own: with
+// f32 queries up to 4% of the time, for heads of 256, elsewhere 0 to 3%.)
+__device__ __forceinline__ int query_shift(float largest) {
+    return 15 - __builtin_amdgcn_frexp_expf(largest);   // (of 0, infinity and NaN: 15)
+}
+__device__ __forceinline__ float shifted_scale(float scale, int shift) {
+    return finite(__builtin_amdgcn_ldexpf(scale, -shift));
+}
+__device__ __forceinline__ void split_q8(const float (&v)[8], int shift, half8 &high, half8 &low) {
+#pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float v = e < 4 ? x[e & 3] : y[e & 3];
-        high[e] = (_Float16)v;
-        low[e] = (_Float16)(v - (float)high[e]);
+        const float x = __builtin_amdgcn_ldexpf(v[e], shift);
+        high[e] = (_Float16)x;
+        low[e] = (_Float16)(x - (float)high[e]);
     }
 }
 

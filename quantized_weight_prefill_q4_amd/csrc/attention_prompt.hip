@@ -249,17 +249,37 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
                           (int64_t)(live ? qh : head * a.group) * D;
     int64_t q_at[KS];
     half8 q_in[KS], q_low_in[WIDE ? KS : 1];
+    float scale = a.scale;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
         const int chunk = 64 * k + lane, n = chunk / (D / 8);
         q_at[k] = __shfl(q_row, n) + 8 * (chunk - n * (D / 8));
     }
+    if constexpr (WIDE) {
+        float x[KS][8];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-        if constexpr (WIDE)
-            load_q8((const float *)a.q, q_at[k], q_in[k], q_low_in[k]);
-        else
-            q_in[k] = load_q8((const uint16_t *)a.q, q_at[k]);
+        for (int k = 0; k < KS; ++k) load_q8((const float *)a.q, q_at[k], x[k]);
+        // the largest of each chunk, and by them that of the lane's row
+        float *const tops = (float *)stage;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) tops[64 * k + lane] = largest_of(x[k], 0.0f);
+        wave_sync();
+        f32x4 top = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const f32x4 t = ((const f32x4 *)tops)[r * (D / 32) + i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], t[e]);
+        }
+        const int shift = query_shift(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+        scale = shifted_scale(a.scale, shift);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+            split_q8(x[k], __shfl(shift, (64 * k + lane) / (D / 8)), q_in[k], q_low_in[k]);
+        wave_sync();   // the place is used again
+    } else {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) q_in[k] = load_q8((const uint16_t *)a.q, q_at[k]);
     }
     u32x4 pa[PIECES], pb[PIECES];   // the wave's share of two tiles on their way to LDS
     {
@@ -344,7 +364,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_prompt_kernel(AttnArgs a
             float x[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = s[e];
-            bias_scores(a, x, slope, pos - tile_of(t) * kTile - 8 * h,
+            bias_scores(a, x, scale, slope, pos - tile_of(t) * kTile - 8 * h,
                         [](int e) { return 16 * (e >> 3) + (e & 7); });
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = x[e];

@@ -22,7 +22,7 @@
 // column.  Codes become f16 in the registers that loaded them.
 //
 // Numerics: the keys' codes are exact in f16 and their scales multiply f32 sums; f32
-// queries enter as two f16 numbers, the weights e^(s − m) as two (2^-22 of the weight).
+// queries enter as two f16 numbers (their row scaled into f16's range: split_q8), the weights e^(s − m) as two (2^-22 of the weight).
 // Products are summed in f32, statistics are f32.  The values d·(q − 8) enter as one f16,
 // rounded once: errors of either sign that the sum over the tokens averages, 0.75 of the
 // output's own rounding in effect.  Keys rounded to one f16 would add 1.6 of it, weights
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT, WIDE>)) void attention_
     half8 q[NT][NS], q_low[NT][WIDE ? NS : 1];
     int pos[NT];
     Range range[NT];
-    float slope[NT];
+    float slope[NT], scale[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const int row = view.rt * R + 16 * c + r;
@@ -151,12 +151,20 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT, WIDE>)) void attention_
         slope[c] = BIAS && a.slopes && live ? a.slopes[h] : 0.0f;
         const int64_t at = (int64_t)(view.rows.first + (live ? i : 0)) * a.ldq +
                            (int64_t)(live ? h : head * a.group) * D + 8 * g;
+        scale[c] = a.scale;
+        if constexpr (WIDE) {
+            float x[NS][8], top = 0.0f;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            if constexpr (WIDE)
-                load_q8((const float *)a.q, at + 32 * s, q[c][s], q_low[c][s]);
-            else
-                q[c][s] = load_q8((const uint16_t *)a.q, at + 32 * s);
+            for (int s = 0; s < NS; ++s) load_q8((const float *)a.q, at + 32 * s, x[s]);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) top = largest_of(x[s], top);
+            const int shift = query_shift(max_across32(max_across16(top)));
+            scale[c] = shifted_scale(a.scale, shift);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) split_q8(x[s], shift, q[c][s], q_low[c][s]);
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) q[c][s] = load_q8((const uint16_t *)a.q, at + 32 * s);
         }
     }
     f32x4 o[NT][MT];
@@ -220,7 +228,7 @@ __global__ __launch_bounds__(256, (kWavesPerSimd<NS, NT, WIDE>)) void attention_
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = s[c][e / 4][e % 4];
-                bias_scores(a, x, slope[c], pos[c] - j0 - 8 * g, [](int e) { return e; });
+                bias_scores(a, x, scale[c], slope[c], pos[c] - j0 - 8 * g, [](int e) { return e; });
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s[c][e / 4][e % 4] = x[e];
             }

@@ -216,6 +216,59 @@ def test_large_and_small_scores():
     check(s, 4, xt="f32", gain=1e-4, scale=1e8)
 
 
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("rows", [1, 5, 40, 200])
+def test_f32_queries_of_any_magnitude(D, rows):
+    """Queries times a power of two, with the scale divided by it, give the same bits: f16's
+    range does not show, whatever the other rows of the call are like (of other rows' scores
+    the moments follow at which sums are rescaled: results are then within the tolerance)."""
+    announce("attention_q4 f32 queries of any magnitude", D, rows)
+    s = filled(D, 2, 32, [rows], [rows + 50], seed=3, ragged=False)
+    kw = [dict(), dict(cap=5.0), dict(cap=500.0, slopes=torch.ones(4, device=dev()))]
+    q, y = check(s, 4, xt="f32", scale=0.125, seed=5)
+    run = lambda q, scale, kw: mq.attention_q4(q, s.cache, s.table, s.lens_t, scale=scale, **kw)
+    want = [run(q, 0.125, k) for k in kw]
+    assert torch.equal(want[0], y)
+    qs = to_host(q).astype(np.float64).reshape(rows, 4, D)
+    ref, tol = expect(s, qs, 4, 0, np.arange(50, rows + 50), slice(0, rows), 0.125, True, 0, 0.0,
+                      None, 0, wide=True)
+
+    def near(t, mine):
+        got = to_host(t).astype(np.float64).reshape(rows, 4, D)
+        return bool((np.abs(got - ref) <= tol)[mine].all())
+
+    powers = (-110, -60, -30, -15, -4, 3, 12, 20, 60, 110)
+    for p in powers:
+        for k, w in zip(kw, want):
+            assert torch.equal(run(q * 2.0 ** p, 2.0 ** (-3 - p), k), w), (p, k)
+    if rows > 1:
+        own = [powers[i % len(powers)] for i in range(rows)]
+        mixed = q * torch.tensor([2.0 ** p for p in own], device=dev())[:, None]
+        for p in powers:
+            mine = [i for i in range(rows) if own[i] == p]
+            # (rows of a larger magnitude: scores far beyond 2^24, nobody's result)
+            assert near(run(mixed, 2.0 ** (-3 - p), {}), mine), p
+    # the elements of a row far below its largest: what they contribute is below its last bits
+    tiny = q.clone()
+    tiny[:, 1::2] *= 2.0 ** -60
+    none = q.clone()
+    none[:, 1::2] = 0
+    assert torch.equal(run(tiny, 0.125, {}), run(none, 0.125, {}))
+    # rows of zeros, and of one infinity or NaN
+    odd = q.clone()
+    odd[0] = 0
+    if rows > 2:
+        odd[1, 3], odd[2, D + 3] = float("inf"), float("nan")
+    z = run(odd, 0.125, {})
+    assert bool(torch.isfinite(z[0]).all())
+    if rows > 2:
+        assert near(z, slice(3, rows))
+        bad = ~torch.isfinite(z.view(rows, 4, D))
+        assert bool(bad[1, 0].all()) and bool(bad[2, 1].all())
+        bad[1, 0] = bad[2, 1] = False
+        assert not bool(bad.any())
+
+
 def test_other_streams_and_two_graphs_on_one_workspace():
     """Two captured calls of different kernels share a workspace; each replay is compared."""
     announce("attention_q4 two graphs, one workspace")
