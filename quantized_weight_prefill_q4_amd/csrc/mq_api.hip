@@ -396,6 +396,16 @@ Span cache_span(const mq::KvSpec &kv) {
 }
 int64_t type_bytes(int type) { return type == MQ_F32 ? 4 : 2; }
 
+// Whether an output lies over n values of a vector that the call reads (null: none).
+bool over(const Span &out, const void *p, int64_t n, int64_t elem) {
+    return p && overlap(out, span(p, n, n, elem, 1));
+}
+// ... over what says where the batch's rows and tokens are.
+bool over_batch(const Span &out, const mq::KvSpec &kv) {
+    return overlap(out, span(kv.table, kv.table_ld, kv.width, 4, kv.batch)) ||
+           over(out, kv.lens, kv.batch, 4) || over(out, kv.cu, (int64_t)kv.batch + 1, 4);
+}
+
 // A rotation's frequencies: n_rot even and at most the head.
 int check_rotation(const double *freqs, int n_rot, int layout, float mscale, int head_dim) {
     if (layout != MQ_ROPE_HALF && layout != MQ_ROPE_INTERLEAVED) return MQ_ERR_FORMAT;
@@ -730,7 +740,11 @@ int mq_kv_store_q4(const mq_kv_q4 *cache, int x_type, const void *K, int ldk, co
     const Span k = span(K, ldk, width, type_bytes(x_type), M);
     const Span v = span(V, ldv, width, type_bytes(x_type), M);
     const Span c = cache_span(kv);
-    if (overlap(c, k) || overlap(c, v)) return MQ_ERR_OVERLAP;
+    const int pairs = freqs ? n_rot / 2 : 0;
+    auto over_tables = [&](const Span &out) {
+        return over_batch(out, kv) || over(out, positions, M, 4) || over(out, freqs, pairs, 8);
+    };
+    if (overlap(c, k) || overlap(c, v) || over_tables(c)) return MQ_ERR_OVERLAP;
     if (Q) {
         const int qw = q_heads * kv.D;
         if (ldq < qw || ldqo < qw) return MQ_ERR_LD;
@@ -738,7 +752,7 @@ int mq_kv_store_q4(const mq_kv_q4 *cache, int x_type, const void *K, int ldk, co
         const Span q = span(Q, ldq, qw, type_bytes(x_type), M);
         const Span o = span(QO, ldqo, qw, type_bytes(q_type), M);
         if ((overlap(o, q) && !same_span(o, q)) || overlap(o, k) || overlap(o, v) ||
-            overlap(o, c) || overlap(c, q))
+            overlap(o, c) || overlap(c, q) || over_tables(o))
             return MQ_ERR_OVERLAP;
     }
     const mq::StoreSpec s{K,   V,    Q,      QO,     positions, freqs,
@@ -760,7 +774,8 @@ int mq_kv_load_q4(const mq_kv_q4 *cache, int y_type, void *K, int ldk, void *V, 
     const Span k = span(K, ldk, width, type_bytes(y_type), M);
     const Span v = span(V, ldv, width, type_bytes(y_type), M);
     const Span c = cache_span(kv);
-    if (overlap(k, v) || overlap(c, k) || overlap(c, v)) return MQ_ERR_OVERLAP;
+    if (overlap(k, v) || overlap(c, k) || overlap(c, v) || over_batch(k, kv) || over_batch(v, kv))
+        return MQ_ERR_OVERLAP;
     return hip_status(mq::launch_kv_load(kv, y_type, K, ldk, V, ldv, (hipStream_t)stream));
 }
 
@@ -802,8 +817,12 @@ int mq_attention_q4(const mq_kv_q4 *cache, int x_type, const void *Q, int ldq, i
     const Span y = span(Y, ldy, width, 2, M);
     const Span c = cache_span(kv);
     const Span w = span(ws, p.ws_bytes, p.ws_bytes, 1, 1);
-    if (overlap(y, q) || overlap(y, c)) return MQ_ERR_OVERLAP;
-    if (p.ws_bytes > 0 && (overlap(w, q) || overlap(w, y) || overlap(w, c))) return MQ_ERR_OVERLAP;
+    auto over_tables = [&](const Span &out) {
+        return over_batch(out, kv) || over(out, slopes, q_heads, 4) || over(out, prefix, kv.batch, 4);
+    };
+    if (overlap(y, q) || overlap(y, c) || over_tables(y)) return MQ_ERR_OVERLAP;
+    if (p.ws_bytes > 0 && (overlap(w, q) || overlap(w, y) || overlap(w, c) || over_tables(w)))
+        return MQ_ERR_OVERLAP;
     return hip_status(mq::launch_attention(kv, s, p, (float *)ws, (hipStream_t)stream));
 }
 

@@ -165,6 +165,38 @@ def test_attention_refuses(L, bad, code):
     assert _attn(L, **bad) == code
 
 
+LIST = K + 0x8000000       # of the call's lists, where a test gives one a place of its own
+
+
+@pytest.mark.parametrize("name", ["table", "lens", "cu_rows", "pos", "freqs", "slopes", "prefix"])
+def test_outputs_over_a_list_of_the_call_are_refused(L, name):
+    """An output may not overlap what the kernels read beside it: the lists that say where rows
+    and tokens are, positions, frequencies, slopes and prefixes.  By its last element too."""
+    size = {"table": 2 * 3 * 4, "lens": 8, "cu_rows": 12, "pos": 24, "freqs": 512, "slopes": 16,
+            "prefix": 8}[name]
+    lists = {name: LIST}
+    end = LIST + size
+    plan = dict(table_width=3, max_len=1 << 20)
+    ws = dict(wsb=1 << 40, Y=Y, **plan)
+    row = 6 * 512 * 2                                   # bytes of a Q, QO or Y of M rows
+    if name not in ("slopes", "prefix"):
+        for qo in (LIST, end - 4 - end % 2, LIST - row + 4):
+            assert _store(L, QO=qo, **lists) == _lib.MQ_ERR_OVERLAP, hex(qo)
+        for c in (LIST, (end - 1) & ~15, LIST + 16 - 4 * 18432):
+            assert _store(L, cache=c, Q=None, **lists) == _lib.MQ_ERR_OVERLAP, hex(c)
+    if name in ("table", "lens", "cu_rows"):
+        for p in (LIST, end - 4, LIST - 6 * 256 * 2 + 4):
+            assert _load(L, K=p, V=V, **lists) == _lib.MQ_ERR_OVERLAP
+            assert _load(L, K=Y, V=p, **lists) == _lib.MQ_ERR_OVERLAP
+    if name not in ("pos", "freqs"):
+        for y in (LIST, end - 4, LIST - row + 4):
+            assert _attn(L, Y=y, **lists) == _lib.MQ_ERR_OVERLAP
+        need = L.mq_attention_q4_workspace_bytes(_kv(plan), 4, 6, 1 << 20)
+        assert need > 0
+        for w in (LIST, (end - 1) & ~15, LIST + 16 - need):
+            assert _attn(L, ws=w, **ws, **lists) == _lib.MQ_ERR_OVERLAP
+
+
 def test_sizes(L):
     assert mq.kv_page_bytes(8, 64, 128) == 8 * 2 * 36 * 128
     for bad in ((0, 64, 128), (8, 33, 128), (8, 64, 100), (1 << 32, 64, 128)):

@@ -318,6 +318,42 @@ def test_strides_and_odd_rows():
         check(s, 3, xt=xt, pad=512)
 
 
+def test_lists_beside_the_outputs():
+    """Outputs may not overlap the lists that a call reads, but one buffer may hold both: lists
+    in the columns between an output's rows, and right behind its last."""
+    announce("lists beside the outputs")
+    D, H, M = 64, 4, 3
+    s = filled(D, 2, 32, [1] * M, [40, 3, 65], seed=44, ragged=False)
+    q = rows_of(M, H * D, torch.float16, 45)
+    f = mq.rope_freqs(D, device=dev())
+    k, v = rows_of(M, 2 * D, torch.float16, 46), rows_of(M, 2 * D, torch.float16, 47)
+    row = H * D + 16
+    y = mq.attention_q4(q, s.cache, s.table, s.lens_t)
+    buf = torch.zeros(M * row + 4 * s.table.numel(), dtype=torch.float16, device=dev())
+    out = buf[:M * row].view(M, row)[:, :H * D]
+    lens = buf[H * D:H * D + 2 * M].view(torch.int32)       # between rows 0 and 1
+    table = buf[M * row - 16:M * row - 16 + 2 * s.table.numel()].view(torch.int32).view_as(s.table)
+    lens.copy_(s.lens_t)
+    table.copy_(s.table)
+    assert torch.equal(mq.attention_q4(q, s.cache, table, lens, out=out), y)
+    want = mq.kv_store_q4(k, v, s.cache, s.table, s.lens_t, freqs=f, q=q)
+    bytes1 = s.bytes.clone()
+    assert torch.equal(mq.kv_store_q4(k, v, s.cache, table, lens, freqs=f, q=q, q_out=out), want)
+    assert torch.equal(s.bytes, bytes1)
+    lk, lv = mq.kv_load_q4(s.cache, s.table, s.lens_t, M)
+    mq.kv_load_q4(s.cache, table, lens, M, k_out=out[:, :2 * D], v_out=out[:, 2 * D:])
+    assert torch.equal(out, torch.cat((lk, lv), 1))
+    assert torch.equal(lens, s.lens_t) and torch.equal(table, s.table)
+    over = buf[:2 * M].view(torch.int32)                    # and under the first row
+    over.copy_(s.lens_t)
+    for call in (lambda: mq.attention_q4(q, s.cache, table, over, out=out),
+                 lambda: mq.kv_store_q4(k, v, s.cache, table, over, freqs=f, q=q, q_out=out),
+                 lambda: mq.kv_load_q4(s.cache, table, over, M, k_out=out[:, :2 * D])):
+        with pytest.raises(mq.MQError) as e:
+            call()
+        assert e.value.code == mq._lib.MQ_ERR_OVERLAP
+
+
 def test_rows_that_see_nothing_and_rows_of_nobody():
     announce("attention_q4 rows that see nothing")
     D, H = 64, 4
