@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 
 import torch
 
@@ -128,6 +129,9 @@ def attention_workspace_bytes(cache: torch.Tensor, batch: int, q_heads: int, row
     page where the call gives none)."""
     if cache.dim() != 4 or cache.size(3) % 36:
         raise ValueError("cache must be [pages, heads, page / 32, 36 * head_dim]")
+    max_len = operator.index(max_len)
+    if not -(1 << 63) <= max_len < 1 << 63:   # (ctypes would pass its low 64 bits)
+        raise OverflowError(f"max_len must fit in 64 bits, got {max_len}")
     one = 16   # an aligned address: the plan reads no memory
     kv = MqKvQ4(cache=one, page_bytes=1 << 62, pages=1, heads=_as_int(cache.size(1)),
                 page=_as_int(32 * cache.size(2)), head_dim=_as_int(cache.size(3) // 36), table=one,

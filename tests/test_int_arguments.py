@@ -55,6 +55,25 @@ def test_queries(query):
             assert e.value.code == (_lib.MQ_ERR_SPLIT if i == 3 else _lib.MQ_ERR_SHAPE)
 
 
+def test_bounds_of_lengths():
+    """max_len is 64 bits wide: what does not fit is refused by the size query as by the call."""
+    c = mq.kv_cache_q4(3, 2, 64, 128, device="cpu")
+    need = mq.attention_workspace_bytes(c, 1, 4, 1, 1 << 30)
+    assert need > 0
+    for fits in ((1 << 30) + 1, WRAPS, (1 << 63) - 1):
+        assert mq.attention_workspace_bytes(c, 1, 4, 1, fits) == need
+    for wraps in (1 << 63, 1 << 64, (1 << 64) + 40, -(1 << 64) + 40):
+        with pytest.raises(OverflowError):
+            mq.attention_workspace_bytes(c, 1, 4, 1, wraps)
+    for bad in (40.0, None, "40"):
+        with pytest.raises(TypeError):
+            mq.attention_workspace_bytes(c, 1, 4, 1, bad)
+    for neg in (-1, -(1 << 63)):
+        with pytest.raises(mq.MQError) as e:
+            mq.attention_workspace_bytes(c, 1, 4, 1, neg)
+        assert e.value.code == _lib.MQ_ERR_SHAPE
+
+
 def test_formats():
     for fmt in (WRAPS + _lib.MQ_Q4_K, _lib.MQ_Q4_K - WRAPS):
         for query in (lambda: mq.row_bytes(fmt, 256), lambda: mq.block_bytes(fmt),
