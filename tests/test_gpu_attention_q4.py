@@ -204,6 +204,55 @@ def test_masks_and_scores(D, rows, lens, kw):
     check(s, 6, **kw)
 
 
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("rows", [3, 100])             # few and many rows of a key/value head
+@pytest.mark.parametrize("kw", [
+    dict(scale=1.0), dict(scale=-1.0), dict(scale=0.7), dict(scale=1.0, slopes=True),
+    dict(cap=1.0, scale=1e36), dict(cap=3.0, scale=-1e30), dict(cap=1e-39, scale=0.5),
+    dict(cap=1e-3, scale=1e-4), dict(cap=8.0, scale=0.02), dict(cap=128.0, scale=0.5),
+    dict(cap=129.0, scale=0.5), dict(cap=1000.0, scale=0.5), dict(cap=5000.0, scale=1e-3),
+    dict(cap=50.0, scale=0.05, slopes=True, window=40)])
+def test_scores_that_f32_sums_exactly(D, rows, kw):
+    """Queries and keys of small whole numbers: every sum of products is exact, so that the
+    tolerance holds what scale, cap, bias and exponential round and nothing else:
+      δ = 8u·(max|s| + cap) + 2^-21·cap [tanh's quotient: 2/(1 + e) within 2^-21.8 of 1] + 2u,
+    at most 2^-9, far from letting a wrong sign, cap or maximum pass."""
+    announce("attention_q4 exact sums", D, rows, kw)
+    H, Hkv, n = 4, 2, rows + 61
+    rng = np.random.default_rng(D + rows)
+    s = Batch(D, Hkv, 32, [rows], [n], D, False)
+    k = rng.integers(-7, 8, (n, Hkv * D)).astype(np.float32)
+    k[:, ::32] = -8                                    # so d is 1 and the codes are the numbers
+    v = rows_of(n, Hkv * D, torch.float32, 9)
+    mq.kv_store_q4(torch.from_numpy(k).to(dev()), v, s.cache, s.table, s.lens_t)
+    lk, lv = mq.kv_load_q4(s.cache, s.table, s.lens_t, n, out_dtype=torch.float32)
+    s.k, s.v = (to_host(t).astype(np.float64).reshape(n, Hkv, D) for t in (lk, lv))
+    assert np.array_equal(s.k.reshape(n, -1), k)
+    q = rng.integers(-3, 4, (rows, H * D))
+    qs = q.astype(np.float64).reshape(rows, H, D)
+    a = dict(cap=0.0, slopes=None, window=0) | kw
+    if a["slopes"]:
+        a["slopes"] = [0.5, 0.25, 2.0, 0.125]
+    a["scale"] = float(np.float32(a["scale"]))
+    a["cap"] = float(np.float32(a["cap"]))
+    at = np.arange(n - rows, n)
+    y, S = oa.attention_ref(qs, s.k, s.v, at, a["scale"], True, a["window"], a["cap"], a["slopes"], 0)
+    top = max(float(np.abs(qs[:, h] @ s.k[:, h // 2].T).max()) for h in range(H)) * abs(a["scale"])
+    if a["cap"]:
+        top = min(top, a["cap"])
+    top += 2.0 * n if a["slopes"] else 0
+    delta = 8 * U * (top + a["cap"]) + 2.0 ** -21 * a["cap"] + 2 * U
+    assert delta <= (2.0 ** -9 if a["cap"] <= 1000 else 2.0 ** -7)
+    tol = S * (2 * np.expm1(delta) * 1.01 + (E + 2.0 ** -21) * 1.01 + 2 * n * U) + \
+        n * 2.0 ** -32 * np.abs(s.v).max() + E * np.abs(y) + 2.0 ** -25
+    sl = None if a["slopes"] is None else torch.tensor(a["slopes"], device=dev())
+    for xt in ("f16", "f32"):
+        got = mq.attention_q4(torch.from_numpy(q).to(dev()).to(T[xt]), s.cache, s.table, s.lens_t,
+                              scale=a["scale"], cap=a["cap"], window=a["window"], slopes=sl)
+        err = np.abs(to_host(got).astype(np.float64).reshape(rows, H, D) - y)
+        assert (err <= tol).all(), (xt, float((err / tol).max()))
+
+
 def test_large_and_small_scores():
     """Scores far apart and far from 0: the running maximum and its rescaling."""
     s = filled(128, 1, 32, [1, 9], [700, 150], seed=5, gain=20.0)
