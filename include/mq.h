@@ -537,11 +537,11 @@ int mq_kv_load_q4(const mq_kv_q4 *cache, int y_type, void *K, int ldk, void *V, 
  * A row sees j where (not causal, or j <= p) and (window 0, or |p − j| < window), and
  * every j < prefix[b].  A row that sees nothing gives zeros.
  * Scores are exact but for f32 sums and, with f32 queries of any magnitude, 2^-18 of each
- * product and 2^-39 of the row's largest query times the sum of |k|; a cap of at most 128
- * adds 2^-21 of itself.  Statistics are f32.  In the second product the values
- * d·(q − 8) are rounded once to f16 and the weights e^(s − max) to 22 bits (2^-32 of the
- * largest where that is more), and y once to f16.  A token whose d is infinite or NaN makes the rows that see
- * it not finite, and no others.
+ * product and 2^-39 of the row's largest query times the sum of |k|; a cap adds up to 2^-21
+ * of itself.  Statistics are f32.  In the second product the values d·(q − 8) are rounded
+ * once to f16 and the weights e^(s − max) to 22 bits (2^-32 of the largest where that is
+ * more), and y once to f16.  A token whose d is infinite or NaN makes the rows that see it
+ * not finite, and no others; so does a query that is not finite with its own row.
  *   Q      : device, x_type, row stride ldq >= q_heads · head_dim; M · (q_heads / heads)
  *            at most 2^30.
  *   Y      : device f16, row stride ldy likewise.  Q and Y are aligned to their element.

@@ -12,6 +12,11 @@ gives the page of each sequence's tokens, ``lens`` (int32 [B]) how many tokens e
 has, the batch's own rows included: a sequence's n rows are its last n tokens.  They
 are rows ``cu_rows[b]`` to ``cu_rows[b + 1]`` of the activations (int32 [B + 1]), or
 without it equally many for each, in order.
+
+Rows that are no sequence's (before ``cu_rows[0]``, behind ``cu_rows[B]``) are not written,
+nor, by the store and the load, those of tokens before a sequence's first (``lens`` smaller
+than its rows): a given output keeps there what it held, and a new one holds there what its
+memory held.
 """
 
 from __future__ import annotations
@@ -106,7 +111,8 @@ def kv_store_q4(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, table: to
     """Quantizes k and v [M, heads * head_dim] (f32 or f16) into the cache at the last
     positions of their sequences; with freqs the keys are rotated first (as rope
     does, by their positions in the sequence or by ``positions``, int32 [M]), and q
-    [M, q_heads * head_dim] beside them.  Returns the rotated q in q_dtype (or q_out,
+    [M, q_heads * head_dim] beside them.  A block of 32 with an element that is not finite or,
+    rotated, beyond f16's range (65520 and more) reads back as NaN.  Returns the rotated q in q_dtype (or q_out,
     which may be q itself), None without q."""
     return _on_device(k, _binding().kv_store, "mq_kv_store_q4",
                       (k, v, cache, table, lens, cu_rows, freqs, _layout(layout), mscale, positions,
@@ -156,7 +162,9 @@ def attention_q4(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens
     the tokens up to its own (all of its sequence's if not causal), with a window
     only those nearer than that, and always the first prefix[b] (int32 [B]).  Rows
     that see nothing are zeros.  max_len: a bound of lens where the table holds much
-    more, for the launch plan.  ws: a workspace of attention_workspace_bytes."""
+    more, for the launch plan.  ws: a workspace of attention_workspace_bytes.  The launch
+    is planned for the mean number of rows: long prompts and single tokens are faster in
+    a call each."""
     return _on_device(q, _binding().attend, "mq_attention_q4",
                       (q, cache, table, lens, cu_rows, scale, causal, window, cap, slopes, prefix,
                        max_len, out, ws))

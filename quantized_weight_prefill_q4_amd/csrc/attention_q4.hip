@@ -30,8 +30,8 @@
 //
 // What bounds it, at one token of 32 heads (8 key/value heads, D = 128) over 131072
 // tokens, 151 MB: 33.5 us when the cache lies in the chip's last-level cache, of which the
-// vector instructions that expand the codes (380 a tile and wave) are 20, and 37 from
-// memory (4.1 TB/s; a large copy 4.8); the join 5.  (Keys as two f16 parts, eight more
+// vector instructions that expand the codes (380 a tile and wave) are 20, and 35 from
+// memory (4.3 TB/s; a large copy 4.8); the join 5.6.  (Keys as two f16 parts, eight more
 // matrix and 50 more vector instructions a tile: 36.)  Short contexts: the chain of loads
 // (lengths, page numbers, tiles) and two launches, 10 us over 4096 tokens.
 #include "attention_device.h"
@@ -42,8 +42,8 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kMaxSplits = 256;
 // Workgroups that the keys are dealt to: the three that fit on each unit.  (One token over
-// 131072: 41.6 us with 512, 43 with 768, 46.5 with 1024; 64 sequences of up to 8000 52.6,
-// 51.2, 51.3.)
+// 131072: 40.6 us with 512, 40.3 with 768, 42.4 with 1024; 64 sequences of up to 8000 54.0,
+// 49.5, 46.6.)
 constexpr int kFewRowsTarget = 768;
 
 // A tile as loaded: code dwords of the lane's operands and the scales they need.
@@ -611,20 +611,22 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) 
 AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
     AttnPlan p;
     const int group = s.q_heads / kv.heads;
+    // (row counts are on the device: one plan for all, by their mean.  A prompt of 2048 rows
+    // beside 60 single tokens of up to 8000: 467 us so, 129 in two calls.)
     const int64_t mean = kv.cu ? ((int64_t)kv.M + kv.batch - 1) / kv.batch : kv.rows;
     const int64_t rows = mean * group;   // of a key/value head and sequence
     // Rows of a workgroup.  Up to 16 rows one column tile, up to 64 two (up to 128 where
     // contexts may be long), for heads of 256 one up to 96 (their second does not fit the
     // registers), and beyond that the kernel for many rows.  One sequence over 30000 tokens /
     // 32 sequences over 3000 / over 200, 8 key/value heads (4 of 256), us:
-    //   D = 128  24 rows  16: 27.5 / 59.7 / 13.5   32: 30.6 / 50.4 / 13.9
-    //            40 rows                           32: 37.3 / 78.8 / 19.0   256: 72.8 / 179 / 22.1
-    //            64 rows  16: 43.8 / 103 / 23.3    32: 38.9 / 83.6 / 25.4   256: 73.9 / 180 / 22.1
-    //           128 rows                           32: 84.7 / 151 / 40.0    256: 77.0 / 189 / 23.0
-    //   D = 64   96 rows                           32: 49.3 / 71.2 / 14.8   256: 58.6 / 134 / 17.1
-    //   D = 256  32 rows  16: 37.4 / 62.1 / 15.8   32: 38.7 / 85.2 / 20.5
-    //            96 rows  16: 57.3 / 140 / 31.8                             128: 90.0 / 150 / 29.2
-    //           128 rows  16: 70.5 / 184 / 39.4                             128: 92.4 / 150 / 30.1
+    //   D = 128  24 rows  16: 25.7 / 54.3 / 12.2   32: 30.2 / 49.1 / 12.4   256: 72.3 / 168 / 18.5
+    //            40 rows  16: 32.7 / 72.1 / 14.8   32: 35.8 / 74.6 / 17.1   256: 67.7 / 168 / 19.1
+    //            64 rows  16: 39.8 / 90.5 / 22.5   32: 37.1 / 77.7 / 22.7   256: 68.3 / 172 / 19.4
+    //           128 rows  16: 63.4 / 159 / 35.7    32: 86.0 / 134 / 36.6    256: 71.2 / 176 / 20.5
+    //   D = 64   96 rows  16: 35.5 / 76.5 / 15.4   32: 46.3 / 62.3 / 12.4   256: 53.6 / 115 / 14.4
+    //   D = 256  32 rows  16: 35.6 / 58.1 / 14.1                            128: 83.1 / 132 / 26.0
+    //            96 rows  16: 55.1 / 126 / 30.0                             128: 89.3 / 143 / 27.0
+    //           128 rows  16: 70.2 / 157 / 34.1                             128: 90.7 / 141 / 27.3
     const bool wide = kv.D == 256;
     const int64_t most = wide ? 96 : s.max_len < 1024 ? 64 : 128;
     p.rows = rows <= 16 ? 16 : rows > most ? attention_prompt_rows(kv.D) : wide ? 16 : 32;
@@ -640,8 +642,8 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
         p.target = kFewRowsTarget;
         splits = kMaxSplits;
     } else {
-        // one workgroup per unit (512 rows over 16512 tokens 229 us; 274 with 200, 331 with
-        // 300, 245 with 512)
+        // one workgroup per unit (512 rows over 16512 tokens 254 us; 270 with 200, 343 with
+        // 300, 269 with 512)
         p.target = 256;
         splits = (1024 + jobs - 1) / jobs;
         if (kv.batch == 1) {   // the longest of the jobs against their mean, if causal
@@ -649,16 +651,16 @@ AttnPlan plan_attention(const KvSpec &kv, const AttnSpec &s) {
             splits = (int64_t)(p.target / (double)jobs * (max_len / mean) + 0.5);
         }
         // few jobs: the parts' time falls with their number and the join's grows, equal at
-        // some 2·√tiles (128 rows of one head of 64, 19500 tokens 66 us with 8 parts, 34 with 32; over
-        // 131000 tokens 130 with 32, 75 with 128)
+        // some 2·√tiles (256 rows of one head of 64 over 19500 tokens 90 us with 8 parts, 39 with
+        // 50; over 131000 tokens 514 with 8, 82 with 128)
         int64_t most = 8;
         while (most * jobs < 512 && most * most < 4 * tiles) ++most;
         if (splits > most) splits = most;
     }
     // Parts of four tiles, one a wave, where the few jobs leave most of the chip idle (one
-    // token over 4096, four heads: 10.0 us against 10.8 with eight); with more jobs they
-    // cost more to join than they give (8 sequences of 5 rows, heads of 256: 20.1 against
-    // 17.3).
+    // token over 4096, four heads: 10.3 us against 11.5 with eight); with more jobs they
+    // cost more to join than they give (8 sequences of 5 rows, heads of 256: 19.8 against
+    // 18.4).
     p.min_tiles = p.rows <= 32 && jobs <= 64 ? 4 : 8;
     if (splits > tiles / p.min_tiles) splits = tiles / p.min_tiles;
     if (splits > kMaxSplits) splits = kMaxSplits;
