@@ -512,8 +512,8 @@ int64_t mq_kv_q4_page_bytes(int heads, int page, int head_dim);
  * All are aligned to their element.  Neither QO nor the cache may overlap another
  * buffer of the call.  Rows at negative positions (lens[b] smaller than the
  * sequence's rows) are left out, their queries included.  Two sequences whose
- * tables give the same page for rows of this call overwrite each other there in
- * no particular order; one without rows in the call touches no page.
+ * tables give the same page for rows of this call, or one that names a page twice,
+ * overwrite there in no particular order; one without rows in the call touches no page.
  * Errors: those of mq_rope, MQ_ERR_SHAPE also for M not a multiple of batch without
  * cu_rows, MQ_ERR_LD also for page_bytes and table_ld. */
 int mq_kv_store_q4(const mq_kv_q4 *cache, int x_type, const void *K, int ldk, const void *V, int ldv,
@@ -541,7 +541,7 @@ int mq_kv_load_q4(const mq_kv_q4 *cache, int y_type, void *K, int ldk, void *V, 
  * of itself.  Statistics are f32.  In the second product the values d·(q − 8) are rounded
  * once to f16 and the weights e^(s − max) to 22 bits (2^-32 of the largest where that is
  * more), and y once to f16.  A token whose d is infinite or NaN makes the rows that see it
- * not finite, and no others; so does a query that is not finite with its own row.
+ * not finite, and no others; a query that is not finite touches its own row alone.
  *   Q      : device, x_type, row stride ldq >= q_heads · head_dim; M · (q_heads / heads)
  *            at most 2^30.
  *   Y      : device f16, row stride ldy likewise.  Q and Y are aligned to their element.

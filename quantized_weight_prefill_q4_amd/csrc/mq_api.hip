@@ -402,7 +402,10 @@ bool over(const Span &out, const void *p, int64_t n, int64_t elem) {
 }
 // ... over what says where the batch's rows and tokens are.
 bool over_batch(const Span &out, const mq::KvSpec &kv) {
-    return overlap(out, span(kv.table, kv.table_ld, kv.width, 4, kv.batch)) ||
+    // (the table's rows, or all of it as one: it may lie between an output's rows as a whole)
+    const int64_t all = (kv.batch - 1) * kv.table_ld + kv.width;
+    return (overlap(out, span(kv.table, kv.table_ld, kv.width, 4, kv.batch)) &&
+            over(out, kv.table, all, 4)) ||
            over(out, kv.lens, kv.batch, 4) || over(out, kv.cu, (int64_t)kv.batch + 1, 4);
 }
 

@@ -393,6 +393,17 @@ def test_lists_beside_the_outputs():
     mq.kv_load_q4(s.cache, table, lens, M, k_out=out[:, :2 * D], v_out=out[:, 2 * D:])
     assert torch.equal(out, torch.cat((lk, lv), 1))
     assert torch.equal(lens, s.lens_t) and torch.equal(table, s.table)
+    # lists between the pages of a strided cache
+    p = Batch(D, 2, 32, [1] * M, [40, 3, 65], 44, False, stride=4096)
+    p.bytes[:, :-4096] = s.bytes
+    gap = p.bytes[0, -4096:].view(torch.int32)
+    lens2, table2 = gap[:M], gap[64:64 + s.table.numel()].view_as(s.table)
+    lens2.copy_(s.lens_t)
+    table2.copy_(s.table)
+    assert torch.equal(mq.kv_store_q4(k, v, p.cache, table2, lens2, freqs=f, q=q), want)
+    assert torch.equal(p.bytes[:, :-4096], s.bytes) and torch.equal(table2, s.table)
+    assert torch.equal(mq.attention_q4(q, p.cache, table2, lens2),
+                       mq.attention_q4(q, s.cache, s.table, s.lens_t))
     over = buf[:2 * M].view(torch.int32)                    # and under the first row
     over.copy_(s.lens_t)
     for call in (lambda: mq.attention_q4(q, s.cache, table, over, out=out),
