@@ -111,9 +111,9 @@ def kv_store_q4(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, table: to
     """Quantizes k and v [M, heads * head_dim] (f32 or f16) into the cache at the last
     positions of their sequences; with freqs the keys are rotated first (as rope
     does, by their positions in the sequence or by ``positions``, int32 [M]), and q
-    [M, q_heads * head_dim] beside them.  A block of 32 with an element that is not finite or,
-    rotated, beyond f16's range (65520 and more) reads back as NaN.  Returns the rotated q in q_dtype (or q_out,
-    which may be q itself), None without q."""
+    [M, q_heads * head_dim] beside them.  A block of 32 with an element that is not finite
+    or, rotated, beyond f16's range (65520 and more) reads back as NaN.  Returns the
+    rotated q in q_dtype (or q_out, which may be q itself), None without q."""
     return _on_device(k, _binding().kv_store, "mq_kv_store_q4",
                       (k, v, cache, table, lens, cu_rows, freqs, _layout(layout), mscale, positions,
                        q, _out_type(q_dtype), q_out))

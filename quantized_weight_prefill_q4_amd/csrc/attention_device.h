@@ -31,8 +31,9 @@ __device__ __forceinline__ float tanh_f32(float u) {
 
 __device__ __forceinline__ float finite(float v) { return fminf(fmaxf(v, -3.0e38f), 3.0e38f); }
 
-// Products to scores: scale (a.scale, over what the row's queries were multiplied by) and cap, and the bias of N tokens, of which number i is
-// `to − at(i)` positions before the row's.
+// Products to scores: scale (a.scale, over what the row's queries were multiplied by) and
+// cap, and the bias of N tokens, of which number i is `to − at(i)` positions before the
+// row's.
 // The cancellation of tanh's quotient is of no account where the cap is small: the
 // score is off by 2^-21 of the cap at most, 2^-14 for kQuickCap, which changes a weight by
 // an eighth of the half step that the output is rounded to.  (Five instructions per score

@@ -27,12 +27,12 @@
 // What bounds it: the matrix instructions.  A step of 256 rows by 32 tokens (D = 128) takes
 // 3270 cycles, at the 2.0 to 2.1 GHz that the power limit leaves with all compute units at
 // work, and they fill 2048; over long contexts (512 rows over 16512 tokens, 254 us without a
-// cap, 9 of them the join's) they run at 1.1 PFLOP/s, where a large matrix product alone reaches 1.17.  Starting
-// a workgroup takes 9000 cycles (three loads one after the other: lengths, page numbers,
-// tiles), ending it 3900.
-// What the parts cost there: keys and weights as one f16 each 188 us, keys as two 225, both
-// 266 (measured one after the other, with a cap's code beside them); the error against 64 bits, in units of the output's own rounding, is 2.4, 1.5 and
-// 1.25.
+// cap, 9 of them the join's) they run at 1.1 PFLOP/s, where a large matrix product alone
+// reaches 1.17.  Starting a workgroup takes 9000 cycles (three loads one after the other:
+// lengths, page numbers, tiles), ending it 3900.
+// What the parts cost there, in one measurement: keys and weights as one f16 each 188 us,
+// keys as two 225, both 266; the error against 64 bits, in units of the output's own
+// rounding, is 2.4, 1.5 and 1.25.
 // Tried without gain: the values' products a step later, beside the maximum (within 3%
 // either way); with one f16 each (then 2480 cycles a step): two tiles per barrier (the
 // same), waves of a SIMD half a step apart by a second barrier (2900), 128 rows per

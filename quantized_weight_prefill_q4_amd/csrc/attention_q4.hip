@@ -22,8 +22,8 @@
 // column.  Codes become f16 in the registers that loaded them.
 //
 // Numerics: the keys' codes are exact in f16 and their scales multiply f32 sums; f32
-// queries enter as two f16 numbers (their row scaled into f16's range: split_q8), the weights e^(s − m) as two (2^-22 of the weight).
-// Products are summed in f32, statistics are f32.  The values d·(q − 8) enter as one f16,
+// queries enter as two f16 numbers (their row scaled into f16's range: split_q8), the
+// weights e^(s − m) as two (2^-22 of the weight).  Products are summed in f32, statistics are f32.  The values d·(q − 8) enter as one f16,
 // rounded once: errors of either sign that the sum over the tokens averages, 0.75 of the
 // output's own rounding in effect.  Keys rounded to one f16 would add 1.6 of it, weights
 // 0.8.
